@@ -243,6 +243,155 @@ int conv4d_forward_cl(gemm_handle_t h, const void* x, int64_t C_in, const int64_
 int conv4d_forward_tc(gemm_handle_t h, const void* x, int64_t C_in, const int64_t in_dims[4], const void* w,
                       int64_t C_out, const int64_t k_dims[4], float* y, int64_t ldy, int dtype, void* stream);
 
+/* ------------------------------------------------------------------ linear layers
+ *
+ * The product of gemm_run as a layer of a neural network uses it, on the tensor cores:
+ * bias, activation and residual in the epilogue, one weight matrix or one per group of
+ * rows (the experts of a mixture-of-experts block), and the gradients.  W is K x N
+ * row-major as B is in gemm_run.
+ *
+ * Operands are bf16 or fp16 (GEMM_F32 is GEMM_ERR_UNSUPPORTED: these run on the tensor
+ * cores only).  Products of 16-bit values accumulate in fp32 as in gemm_run; bias,
+ * activation and residual are applied in fp32 and the result is rounded once.  Results
+ * are deterministic.  Calls on one handle share its workspace: calls on different streams
+ * must not overlap in time.  Once a call of the largest sizes has grown the workspace,
+ * calls allocate nothing and can be captured in a CUDA graph. */
+
+typedef enum {
+    GEMM_ACT_NONE = 0,
+    GEMM_ACT_RELU = 1,
+    GEMM_ACT_GELU = 2,      /* z Phi(z) = z (1 + erf(z / sqrt 2)) / 2 */
+    GEMM_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    GEMM_ACT_SILU = 4,      /* z / (1 + e^-z) */
+    GEMM_ACT_SWIGLU = 5     /* silu(z[0..N-1]) * z[N..2N-1]: W has 2 N columns, gate then up */
+} gemm_act_t;
+
+/* The arguments of gemm_linear. */
+typedef struct gemm_linear_args {
+    int64_t M, K, N;
+    const void* X;
+    int64_t ldx;
+    const void* W;
+    int64_t ldw;
+    int64_t w_stride;
+    const void* bias;
+    const void* R;
+    int64_t ldr;
+    void* Z;
+    int64_t ldz;
+    void* Y;
+    int64_t ldy;
+    int64_t groups;
+    const int32_t* offsets;
+    int dtype, y_dtype, act;
+} gemm_linear_args;
+
+/* Z = X W + bias,  Y = act(Z) + R, with Nw = N columns of W (2 N for GEMM_ACT_SWIGLU).
+ *   X [M][K], W [K][Nw], bias [Nw], Z [M][Nw]: type `dtype`; R and Y [M][N]: type `y_dtype`
+ *   (`dtype` or GEMM_F32).  bias, R and Z may be NULL; Z keeps the activation's input for
+ *   gemm_linear_backward.  R may be Y itself.
+ *   groups > 0: rows offsets[g] .. offsets[g+1]-1 of X (and of Y, Z, R) use the weight
+ *   matrix W + g * w_stride (elements) and the bias bias + g * Nw; `offsets` is device
+ *   memory, groups + 1 non-decreasing values from 0 to at most M, read by the kernel (no
+ *   host synchronisation).  Rows from offsets[groups] on are not written.  groups == 0: one
+ *   matrix for all rows; offsets and w_stride are ignored.
+ * X and W must be 16-byte aligned with ldx, ldw (and w_stride) multiples of 8; N a multiple
+ * of 8 for GEMM_ACT_SWIGLU; the others aligned to their elements (GEMM_ERR_ALIGNMENT).
+ * GEMM_ERR_UNSUPPORTED for more than 1024 groups or sizes of 2^31 - 1024 and more.
+ * M == 0 or N == 0: nothing is done.  K == 0: Y = act(bias) + R.
+ * The pages have no counterpart to it: it is the layer large language models are built of. */
+int gemm_linear(gemm_handle_t h, const gemm_linear_args* args, void* stream);
+
+/* The arguments of gemm_linear_backward. */
+typedef struct gemm_linear_grad_args {
+    int64_t M, K, N;
+    const void* dY;
+    int64_t lddy;
+    const void* X;
+    int64_t ldx;
+    const void* W;
+    int64_t ldw;
+    int64_t w_stride;
+    const void* Z;
+    int64_t ldz;
+    void* dX;
+    int64_t lddx;
+    void* dW;
+    int64_t lddw;
+    int64_t dw_stride;
+    float* db;
+    int64_t groups;
+    const int32_t* offsets;
+    int dtype, dw_dtype, act;
+} gemm_linear_grad_args;
+
+/* The gradients of gemm_linear:
+ *     dZ = dY act'(Z),  dX = dZ W^T,  dW = X^T dZ,  db = column sums of dZ
+ * (the residual's gradient is dY itself).  dX, dW and db may each be NULL: not computed.
+ *   dY [M][N], X, W, Z [M][Nw] as in the forward call, of type `dtype`; Z is the
+ *   activation's input (unread for GEMM_ACT_NONE).  dX [M][K]: `dtype`.  dW [K][Nw] (per
+ *   group at dw_stride elements): `dw_dtype`, `dtype` or GEMM_F32.  db [Nw] (per group
+ *   contiguous): fp32.  All are overwritten; a group without rows gets zeros.
+ * dZ is rounded once to `dtype` for the two products; db sums it before that rounding.
+ * dY, Z, X and W must be 16-byte aligned with leading dimensions (and w_stride) multiples
+ * of 8, the outputs aligned to their elements.  Groups, errors and limits as in
+ * gemm_linear; dX's rows from offsets[groups] on are not written.
+ * The pages have no counterpart to it. */
+int gemm_linear_backward(gemm_handle_t h, const gemm_linear_grad_args* args, void* stream);
+
+/* ------------------------------------------------------------------ routing to experts
+ *
+ * The steps around the grouped products of a mixture-of-experts block: T tokens, E experts,
+ * k of them a token.  dtype is GEMM_F32, GEMM_BF16 or GEMM_F16; sums are held in fp32.
+ * k <= 32 and E <= 1024, else GEMM_ERR_UNSUPPORTED; T * k must stay below 2^31 - 1024. */
+
+/* For each token the k largest logits, in descending order; equal logits (and +0, -0) by
+ * the lower index, NaN before everything.  A logit of -inf is an expert that is not there:
+ * it is never picked, and a token with fewer than k others has picks of expert -1 and
+ * weight 0 (a token of -inf only goes nowhere).
+ *   weights[t][j] = exp(l[t][e_j]) / sum exp(l[t][i]), i over the token's picks
+ *   (renormalize != 0) or over all its experts; fp32 [T][k].
+ *   experts [T][k]: e_j or -1.
+ *   offsets [E+1]: the rows of expert e, sorted by expert and then by (t, j), are
+ *   offsets[e] .. offsets[e+1]-1 (the groups of gemm_linear).
+ *   slots [T][k]: the row of pick (t, j), or -1.  rows [T*k]: the pick t*k + j at each row,
+ *   -1 from offsets[E] on.
+ * The router's choice itself is not differentiated (moe_route_backward: the weights only).
+ * The pages have no counterpart to it. */
+int moe_route(gemm_handle_t h, int64_t T, int64_t E, int64_t k, const void* logits, int64_t ldl, int dtype,
+              int renormalize, float* weights, int32_t* experts, int32_t* slots, int32_t* rows, int32_t* offsets,
+              void* stream);
+
+/* dlogits[t][i] = p_i (g_i - sum_j p_j g_j) over the token's picks (renormalize != 0) or all
+ * its experts, g the gradient dweights [T][k] of the weights at the picked experts and 0
+ * elsewhere.  `experts` as moe_route left it; dlogits [T][E] of type dtype, overwritten.
+ * The pages have no counterpart to it. */
+int moe_route_backward(gemm_handle_t h, int64_t T, int64_t E, int64_t k, const float* dweights, const void* logits,
+                       int64_t ldl, int dtype, const int32_t* experts, int renormalize, void* dlogits, int64_t lddl,
+                       void* stream);
+
+/* xr[r] = x[rows[r] / k] for r < T*k, zeros where rows[r] < 0: the tokens' rows in the
+ * experts' order.  x [T][N], xr [T*k][N].  Its gradient is moe_combine without weights.
+ * The pages have no counterpart to it. */
+int moe_dispatch(gemm_handle_t h, int64_t T, int64_t N, int64_t k, const void* x, int64_t ldx, int dtype,
+                 const int32_t* rows, void* xr, int64_t ldxr, void* stream);
+
+/* out[t] = sum over j of weights[t][j] * y[slots[t][j]] + R[t], picks without a row (slot
+ * -1) left out.  y [rows_y][N]; weights fp32 [T][k] or NULL (ones); R [T][N] or NULL, may be
+ * out itself; out [T][N].  Summed in fp32 in the order of j, R last, and rounded once.
+ * The pages have no counterpart to it. */
+int moe_combine(gemm_handle_t h, int64_t T, int64_t N, int64_t k, const void* y, int64_t ldy, int64_t rows_y,
+                int dtype, const int32_t* slots, const float* weights, const void* R, int64_t ldr, void* out,
+                int64_t ldo, void* stream);
+
+/* The gradients of moe_combine: dy[slots[t][j]] = weights[t][j] * dout[t], zeros in the rows
+ * that hold no pick (rows[r] < 0), and dweights[t][j] = <dout[t], y[slots[t][j]]> (0 where
+ * there is no row).  y and dy [T*k][N], dout [T][N].
+ * The pages have no counterpart to it. */
+int moe_combine_backward(gemm_handle_t h, int64_t T, int64_t N, int64_t k, const void* dout, int64_t lddo,
+                         const void* y, int64_t ldy, int dtype, const int32_t* slots, const int32_t* rows,
+                         const float* weights, void* dy, int64_t lddy, float* dweights, void* stream);
+
 /* Synchronise `stream`, then read and clear the handle's device status word (and, in the
  * debug library, the kernels' bounds-check flags).  This is
  * the wait of "Learning to develop for GPU with GEMM as the example", section "Writing a
@@ -284,7 +433,7 @@ typedef enum {
                                    128x256 tile, 2 a pair of CTAs (cluster of two) per 256x256 tile.  Any
                                    other value (3 included) is GEMM_ERR_INVALID_ARG */
     GEMM_OPT_TEST_STALL = 6,    /* test hook for failure detection, 0 (default) or 1: the kernels with
-                                   bounded waits (tensor-core GEMMs and convolution, TMA skinny GEMM, persistent
+                                   bounded waits (tensor-core GEMMs, linear layers and convolution, TMA skinny GEMM, persistent
                                    fp32 GEMM) first wait on a
                                    barrier nothing arrives on; the wait runs out after the wait limit, the
                                    kernel drains its copies and MMAs, frees its tensor memory, returns,

@@ -13,6 +13,7 @@
 #include <new>
 #include <vector>
 
+#include "context.h"
 #include "internal.h"
 
 using namespace gemm_gb300;
@@ -69,78 +70,7 @@ bool beyond_kernel_limits(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t 
 
 }  // namespace gemm_gb300
 
-struct gemm_ctx {
-    int device = 0;
-    int num_sms = 0;
-    int* d_status = nullptr;  // device status word written by kernels with bounded waits
-    float* workspace = nullptr;
-    size_t workspace_bytes = 0;
-    unsigned long long* tc_counters = nullptr;  // last-wave split counters of the tensor-core GEMM
-    size_t tc_counters_bytes = 0;
-    unsigned tc_seq = 0;  // tag of the last split tensor-core launch
-    unsigned long long* f32_counters = nullptr;  // K-slice counters of the persistent fp32 GEMM
-    size_t f32_counters_bytes = 0;
-    unsigned f32_seq = 0;  // tag of the last split persistent fp32 launch
-    void* host_stage = nullptr;  // gemm_run_host(_batch) device copies of A, B and C
-    size_t host_stage_bytes = 0;
-    float* product = nullptr;  // fp32 product for the generalised epilogue of fp32 inputs
-    size_t product_bytes = 0;
-    int opt_f32_kernel = 0;
-    int opt_split_k = 0;
-    int opt_tc_chunk = 0;  // tensor-core accumulation chunk in 64-wide k-blocks (0 = default)
-    int opt_tc_pair = 0;   // tensor-core tile: 0 choose, 1 single CTA, 2 CTA pair
-    int opt_test_stall = 0;  // test hook: kernels with bounded waits let one wait run out
-    int opt_conv_stack = 0;  // tensor-core convolution: output positions stacked along N (0 = choose)
-    int opt_conv_split = 0;  // tensor-core convolution: 0 choose, 1 one CTA pair per tile, 2 two pairs
-    uint64_t wait_limit_ns = 2000000000ull;
-    int64_t launches = 0;  // kernels launched through this handle
-    // gemm_run_host pipeline: copy-in and copy-out streams and their events
-    cudaStream_t s_in = nullptr, s_out = nullptr;
-    static constexpr int kMaxChunks = 8;
-    cudaEvent_t ev_start = nullptr, ev_done = nullptr;
-    cudaEvent_t ev_a[kMaxChunks] = {}, ev_c[kMaxChunks] = {};
-};
-
 namespace {
-
-class DeviceGuard {
-  public:
-    explicit DeviceGuard(int dev) : ok_(false), prev_(-1)
-    {
-        if (cudaGetDevice(&prev_) != cudaSuccess) prev_ = -1;
-        ok_ = (prev_ == dev) || (cudaSetDevice(dev) == cudaSuccess);
-    }
-    ~DeviceGuard()
-    {
-        if (prev_ >= 0) cudaSetDevice(prev_);
-    }
-    bool ok() const { return ok_; }
-
-  private:
-    bool ok_;
-    int prev_;
-};
-
-int from_cuda(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA; }
-
-// Grow a device buffer to at least `bytes` (contents are not kept).
-int ensure_buffer(void** buf, size_t* have, size_t bytes)
-{
-    if (*have >= bytes && *buf) return GEMM_OK;
-    if (*buf) {
-        cudaFree(*buf);  // implicit device synchronisation: no kernel still uses it
-        *buf = nullptr;
-        *have = 0;
-    }
-    size_t want = bytes < 256 ? 256 : bytes;
-    if (cudaMalloc(buf, want) != cudaSuccess) {
-        *buf = nullptr;
-        (void)cudaGetLastError();  // an allocation failure is not sticky: keep it out of later launch checks
-        return GEMM_ERR_CUDA;
-    }
-    *have = want;
-    return GEMM_OK;
-}
 
 int check_common(gemm_handle_t h, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                  const void* B, int64_t ldb, const void* C, int64_t ldc, int dtype)
@@ -278,6 +208,10 @@ int gemm_destroy(gemm_handle_t h)
     if (h->f32_counters) cudaFree(h->f32_counters);
     if (h->product) cudaFree(h->product);
     if (h->host_stage) cudaFree(h->host_stage);
+    if (h->lin_partials) cudaFree(h->lin_partials);
+    if (h->lin_dz) cudaFree(h->lin_dz);
+    if (h->lin_sums) cudaFree(h->lin_sums);
+    if (h->lin_counters) cudaFree(h->lin_counters);
     delete h;
     return GEMM_OK;
 }
@@ -769,6 +703,9 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
     if (cudaMemcpy(&v, h->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
     if (v != 0) {
         if (cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) return GEMM_ERR_CUDA;
+        // a linear-layer kernel that gave up may have left arrivals uncounted
+        if (h->lin_counters && cudaMemset(h->lin_counters, 0, h->lin_counters_bytes) != cudaSuccess)
+            return GEMM_ERR_CUDA;
         glog("gemm_get_device_status: a bounded wait ran out (device code %d)", v);
         return GEMM_ERR_DEVICE_TIMEOUT;
     }
@@ -776,7 +713,8 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
     int bad = 0;
     for (auto take : {bounds_flag_take_ffma, bounds_flag_take_ffma_tma, bounds_flag_take_skinny,
                       bounds_flag_take_skinny_tma, bounds_flag_take_im2col, bounds_flag_take_conv_implicit,
-                      bounds_flag_take_conv_tc, bounds_flag_take_tc_gemm}) {
+                      bounds_flag_take_conv_tc, bounds_flag_take_tc_gemm, bounds_flag_take_linear_tc,
+                      bounds_flag_take_linear_act, bounds_flag_take_moe}) {
         const int r = take();
         if (r < 0) return GEMM_ERR_CUDA;
         bad |= r;

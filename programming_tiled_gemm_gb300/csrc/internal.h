@@ -65,6 +65,9 @@ int bounds_flag_take_im2col();
 int bounds_flag_take_conv_implicit();
 int bounds_flag_take_conv_tc();
 int bounds_flag_take_tc_gemm();
+int bounds_flag_take_linear_tc();
+int bounds_flag_take_linear_act();
+int bounds_flag_take_moe();
 #else
 #define GEMM_DEBUG_UNIT(name) \
     static __device__ __forceinline__ constexpr bool in_range(int64_t, int64_t) { return true; }

@@ -1,0 +1,300 @@
+// The elementwise half of a linear layer's gradient: dZ = dY act'(Z), rounded once to the
+// operands' 16-bit type for the two products that follow, and db = sum over the rows of dZ
+// (per group), summed in fp32 from the unrounded dZ in the same pass.
+//
+// Bound by memory: dY and Z are read and dZ written once, 16 bytes a thread.  A block takes
+// 256 columns x 128 rows (a warp a row, eight columns a lane), keeps its column sums in
+// registers, and leaves them in the workspace; the block that counts last for a group's
+// columns adds the row pieces in order.  Nothing waits, and the order is fixed.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "linear.h"
+
+namespace gemm_gb300 {
+
+GEMM_DEBUG_UNIT(linear_act)
+
+namespace {
+
+constexpr int THREADS = 256, WARPS = 8, COLS = 256, ROWS = 128;
+
+struct ActParams {
+    int M, N, G;
+    const int32_t* offsets;
+    const void* dY;
+    int64_t lddy;
+    const void* Z;
+    int64_t ldz;
+    void* dZ;  // null: not wanted (no activation)
+    int64_t lddz;
+    float* db;  // [G][Nw] or null
+    float* ws;  // [item][Nw]
+    unsigned* cnt;
+    int act, col_blocks;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack(uint32_t u)
+{
+    if (BF16) return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u));
+    return __half22float2(*reinterpret_cast<__half2*>(&u));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float a, float b)
+{
+    if (BF16) {
+        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&v);
+    }
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Eight 16-bit values of a row from column c on, of which those below `n` exist.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&v)[8])
+{
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (n >= 8) {
+        u = __ldg(reinterpret_cast<const uint4*>(p));
+    } else {
+        uint16_t t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : (uint16_t)0;
+        u = make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack<BF16>(w[i]);
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, int64_t at, int n, const float (&v)[8])
+{
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
+    const uint4 u = make_uint4(pack<BF16>(v[0], v[1]), pack<BF16>(v[2], v[3]), pack<BF16>(v[4], v[5]),
+                               pack<BF16>(v[6], v[7]));
+    if (n >= 8) {
+        *reinterpret_cast<uint4*>(p) = u;
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// dz[i] = dy[i] act'(z[i])
+__device__ __forceinline__ void act_grad(float (&dz)[8], const float (&z)[8], int act)
+{
+    switch (act) {
+    case GEMM_ACT_RELU:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dz[i] = z[i] > 0.f ? dz[i] : 0.f;
+        break;
+    case GEMM_ACT_GELU:  // Phi(z) + z phi(z)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            dz[i] *= 0.5f * (1.f + erff(z[i] * 0.70710678118654752f)) +
+                     z[i] * 0.39894228040143268f * __expf(-0.5f * z[i] * z[i]);
+        break;
+    case GEMM_ACT_GELU_TANH:  // s = 1 / (1 + e^-2u), u = c (z + a z^3): s + z s (1 - s) 2 u'
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float z2 = z[i] * z[i];
+            const float s = sigmoid(1.5957691216057308f * z[i] * (1.f + 0.044715f * z2));
+            dz[i] *= s + z[i] * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z2);
+        }
+        break;
+    case GEMM_ACT_SILU:
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float s = sigmoid(z[i]);
+            dz[i] *= s * (1.f + z[i] * (1.f - s));
+        }
+        break;
+    default: break;
+    }
+}
+
+template <bool BF16, bool GATED, bool BIAS>
+__global__ void __launch_bounds__(THREADS) linear_act_kernel(ActParams p)
+{
+    extern __shared__ int table[];  // off[G + 1], cum[G + 1] (BIAS)
+    __shared__ float sums[WARPS][COLS];
+    __shared__ int last;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int item = blockIdx.x / p.col_blocks, cblock = blockIdx.x % p.col_blocks;
+    const int col = cblock * COLS + lane * 8;
+    const int ncol = p.N - col;  // columns of this lane that exist (may be <= 0 or above 8)
+    const int Nw = GATED ? 2 * p.N : p.N;
+    int g = 0, first, rows, piece = 0, pieces = 1;
+    if (BIAS) {
+        int* off = table;
+        int* cum = table + p.G + 1;
+        group_table(p.offsets, p.G, p.M, ROWS, 1, 1, off, cum);
+        __syncthreads();
+        if (item >= cum[p.G]) return;
+        int hi = p.G - 1;  // the group whose pieces hold item item
+        while (g < hi) {
+            const int mid = (g + hi + 1) / 2;
+            if (cum[mid] <= item) g = mid;
+            else hi = mid - 1;
+        }
+        piece = item - cum[g];
+        pieces = cum[g + 1] - cum[g];
+        first = off[g] + piece * ROWS;
+        rows = min(ROWS, off[g + 1] - first);
+    } else {
+        first = item * ROWS;
+        rows = min(ROWS, p.M - first);
+    }
+    float s[8] = {}, su[8] = {};
+    if (ncol > 0) {
+#pragma unroll 2
+        for (int r = warp; r < rows; r += WARPS) {
+            const int64_t row = first + r;
+            if (!in_range(row, p.M)) continue;
+            float d[8], z[8];
+            load8<BF16>(p.dY, row * p.lddy + col, ncol, d);
+            if (GATED) {
+                float u[8], du[8];
+                load8<BF16>(p.Z, row * p.ldz + col, ncol, z);
+                load8<BF16>(p.Z, row * p.ldz + p.N + col, ncol, u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float q = sigmoid(z[i]);
+                    du[i] = d[i] * z[i] * q;
+                    d[i] = d[i] * u[i] * q * (1.f + z[i] * (1.f - q));
+                }
+                store8<BF16>(p.dZ, row * p.lddz + p.N + col, ncol, du);
+                if (BIAS)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) su[i] += du[i];
+            } else if (p.dZ) {
+                load8<BF16>(p.Z, row * p.ldz + col, ncol, z);
+                act_grad(d, z, p.act);
+            }
+            if (p.dZ) store8<BF16>(p.dZ, row * p.lddz + col, ncol, d);
+            if (BIAS)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] += d[i];
+        }
+    }
+    if (!BIAS) return;
+    // the warps' sums in order, one column a thread; then the pieces' sums in order
+    float* dst = pieces == 1 ? p.db + (int64_t)g * Nw : p.ws + (int64_t)item * Nw;
+    const int c = cblock * COLS + threadIdx.x;
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = h ? su[i] : s[i];
+        __syncthreads();
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) t += sums[w][threadIdx.x];
+        if (c < p.N) dst[h * p.N + c] = t;
+    }
+    if (pieces == 1) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        unsigned* cnt = p.cnt + (int64_t)g * p.col_blocks + cblock;
+        last = atomicAdd(cnt, 1u) == (unsigned)(pieces - 1);
+        if (last) *cnt = 0;  // ready for the next launch
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    // warp w adds pieces w, w + 8, ...; the warps' sums are added in order
+    const float* src = p.ws + (int64_t)(item - piece) * Nw;
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        float t[8] = {};
+#pragma unroll 4
+        for (int i = warp; i < pieces; i += WARPS)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int cc = cblock * COLS + 32 * j + lane;
+                if (cc < p.N) t[j] += __ldcg(src + (int64_t)i * Nw + h * p.N + cc);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[warp][32 * j + lane] = t[j];
+        __syncthreads();
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v += sums[w][threadIdx.x];
+        if (c < p.N) p.db[(int64_t)g * Nw + h * p.N + c] = v;
+    }
+}
+
+template <bool BF16, bool GATED>
+cudaError_t launch_typed(const ActParams& p, dim3 grid, cudaStream_t s)
+{
+    if (p.db)
+        linear_act_kernel<BF16, GATED, true><<<grid, THREADS, 2 * (p.G + 1) * sizeof(int), s>>>(p);
+    else
+        linear_act_kernel<BF16, GATED, false><<<grid, THREADS, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+int64_t items(const LinActArgs& a)
+{
+    const int64_t n = (a.M + ROWS - 1) / ROWS;
+    return a.db ? n + (a.G > 0 ? a.G : 1) : n;
+}
+
+}  // namespace
+
+size_t linear_act_ws_bytes(const LinActArgs& a)
+{
+    return a.db ? (size_t)items(a) * (size_t)(a.act == GEMM_ACT_SWIGLU ? 2 * a.N : a.N) * sizeof(float) : 0;
+}
+
+int64_t linear_act_counters(const LinActArgs& a)
+{
+    return a.db ? (int64_t)(a.G > 0 ? a.G : 1) * ((a.N + COLS - 1) / COLS) : 0;
+}
+
+int launch_linear_act(const LinActArgs& a, float* ws, unsigned* counters, cudaStream_t stream, int* launches)
+{
+    ActParams p = {};
+    p.M = (int)a.M;
+    p.N = (int)a.N;
+    p.G = a.G > 0 ? a.G : 1;
+    p.offsets = a.G > 0 ? a.offsets : nullptr;
+    p.dY = a.dY;
+    p.lddy = a.lddy;
+    p.Z = a.Z;
+    p.ldz = a.ldz;
+    p.dZ = a.dZ;
+    p.lddz = a.lddz;
+    p.db = a.db;
+    p.ws = ws;
+    p.cnt = counters;
+    p.act = a.act;
+    p.col_blocks = (int)((a.N + COLS - 1) / COLS);
+    const int64_t n = items(a);
+    if (n == 0 || a.N == 0) return GEMM_OK;
+    if (n * p.col_blocks > 0x7fffffffLL) return GEMM_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)(n * p.col_blocks));
+    const bool gated = a.act == GEMM_ACT_SWIGLU;
+    const cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true>(p, grid, stream) : launch_typed<true, false>(p, grid, stream))
+                                 : (gated ? launch_typed<false, true>(p, grid, stream) : launch_typed<false, false>(p, grid, stream));
+    if (e != cudaSuccess) return GEMM_ERR_CUDA;
+    *launches += 1;
+    return GEMM_OK;
+}
+
+}  // namespace gemm_gb300

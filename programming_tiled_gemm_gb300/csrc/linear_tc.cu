@@ -1,0 +1,1072 @@
+// Linear layers on the 5th-generation tensor cores: the product with bias, activation and
+// residual in its epilogue, for one weight matrix or for rows grouped by expert, and the
+// two products of its gradient.
+//
+// All three are D[t][f] = sum_k A[f][k] B[t][k] with the FEATURES f on the MMA's M side and
+// the ROWS t (tokens) on its N side: a CTA pair's tcgen05.mma is 256 features x w rows, and
+// w is any multiple of 16 up to 256, chosen per tile at run time.  So one kernel takes one
+// token (w = 16: the weights stream past, nothing else counts), ragged groups (a group of
+// 300 rows becomes two tiles of 160 and 140 rows instead of 512 padded ones) and large
+// products (256 x 256 tiles).  Putting the features on the TMEM lanes also makes the
+// epilogue's accesses contiguous: a warp holds 32 features of a row.
+//   * kLinFwd: A is W (MN-major in shared memory: W is K x N row-major), B is X (K-major);
+//   * kLinDx:  A is W read along N (K-major), B is dZ (K-major);
+//   * kLinDw:  A is dZ, B is X, both MN-major, reduced over the rows.
+// Gated (SwiGLU): W's gate columns f and up columns N + f are rows 0..63 and 64..127 of a
+// CTA's operand, so a tile holds both halves of 128 outputs; the two halves lie in
+// different TMEM lanes, and each pair of epilogue warps swaps half of its columns through
+// shared memory.
+//
+// Pipeline, as in the plain product's CTA-pair kernel: a producer warp per CTA (TMA, ring
+// of stages), one MMA thread a pair, eight epilogue warps a CTA.  The tensor core's fp32
+// accumulation rounds toward zero, so K is cut into chunks of `kc` k-blocks, each in a
+// fresh TMEM accumulator, added in fp32 round-to-nearest registers in order: 1024 of K for
+// fp32 results, as in the plain product, 2048 for 16-bit ones, whose own rounding is a
+// hundred times the sum's error (the epilogue then has twice the time).
+//
+// Work: tiles are walked round robin by the persistent pairs.  The tiles of the last,
+// partial wave (all tiles, when there are fewer than pairs) are cut along K into equal
+// lengths of k-blocks, one a pair: a pair's range covers parts of at most two tiles.  Every
+// part goes to the workspace in fp32; the CTA that counts last adds the parts of its tile in
+// K order and runs the epilogue.  Nothing waits for another CTA, and the order of the sum
+// does not depend on who is last.
+//
+// kLinDw over groups: a group's last k-block ends inside the next group's rows.  Those rows
+// are zeroed in shared memory, in both operands (zero times a neighbour's NaN would be NaN),
+// by a fixer warp before the MMAs may read the stage.
+//
+// Every wait is bounded; on expiry the status word is set and the CTA drains and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "linear.h"
+#include "ptx.h"
+
+namespace gemm_gb300 {
+
+GEMM_DEBUG_UNIT(linear_tc)
+
+namespace {
+
+constexpr int BK = 64;                // k per stage: one 128-byte swizzle row of 16-bit values
+constexpr int UMMA_K = 16;
+constexpr int CTA_F = 128;            // features (MMA rows) of one CTA
+constexpr int MAX_W = 256;            // rows (MMA columns) of a tile
+constexpr int EPI_WARPS = 8;
+constexpr int A_BYTES = CTA_F * BK * 2;  // 16 KiB a stage
+constexpr int BOX_BYTES = 64 * BK * 2;   // 64 x 64 box of an MN-major operand
+constexpr int MAX_STAGES = 12;
+constexpr int RASTER = 8;             // row tiles per raster group (2048 rows share W's columns in L2)
+constexpr int STG_BYTES = 2048;       // an epilogue warp's staging block: 32 rows x 32 features of 16 bits,
+                                      // or (gated) 16 columns of fp32 for the other warp
+constexpr int SMEM_MAX = 232448;      // 227 KiB
+
+// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; 4..11: epilogue.  The epilogue's warps
+// hold 128 sums each and take registers from the first four: 72 + 2 * 216 a thread of the
+// three warpgroups is the 3 * 168 the block is launched with (checked before the launch).
+constexpr int EPI_WARP0 = 4;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int LAUNCH_REGS = 168, LEAN_REGS = 72, EPI_REGS = 216;
+static_assert(LEAN_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "the epilogue's registers come from the block's own");
+
+struct LinParams {
+    int M;       // rows of X
+    int rows;    // extent of the row (t) side: M, or K for kLinDw
+    int F;       // output columns
+    int kb;      // k-blocks of a tile (kLinDw over groups: taken from the group's rows)
+    int G;
+    const int32_t* offsets;
+    int f_tiles;
+    int bx;      // rows of a K-major B box
+    int b_bytes, stages, kc;
+    int split_w;     // tile width the last wave's split is planned for (0: no split)
+    const void* bias;
+    int64_t bias_stride;
+    const void* R;
+    int64_t ldr;
+    void* Z;
+    int64_t ldz;
+    void* out;
+    int64_t ldo, out_stride;
+    int act, out_f32;
+    int vec_r, vec_z, vec_out;  // 16-bit R, Z and out with 16-byte aligned rows
+    uint32_t idesc;  // without N
+    float* ws;
+    unsigned* cnt;
+    int ws_cols;     // columns of a partial tile in the workspace
+    int* status;
+    uint64_t limit_ns;
+    int test_stall;
+};
+
+__host__ __device__ inline int tile_width(int rows)
+{
+    // equal tiles: 300 rows are 160 + 140, not 256 + 44
+    const int nt = (rows + MAX_W - 1) / MAX_W;
+    const int w = (rows + nt - 1) / nt;
+    return (w + 15) / 16 * 16;
+}
+
+// k-blocks a pair takes of the last wave's `rem` tiles of kb k-blocks each (kb: whole
+// tiles).  A slice costs its publication and its addition, about 2 us + 3 us a 256-wide
+// tile, against 0.3 us a k-block saved.
+__host__ __device__ inline int slice_len(int rem, int kb, int pairs, int w)
+{
+    if (rem <= 0 || w <= 0) return kb;
+    const int64_t all = (int64_t)rem * kb;
+    int len = (int)((all + pairs - 1) / pairs);
+    const int least = 2 + w / 16;
+    if (len < least) len = least;
+    return (kb - len < 4 + w / 16) ? kb : len;
+}
+
+struct Item {
+    int g, row0, valid, w, f0;  // group, first row, rows to store, tile width, first feature
+    int kb0, kb1;               // k-blocks
+    int red0, red_rows;         // kLinDw: first reduced row of the group, its rows
+    int part, c0, c1;           // slice: index among the last wave's tiles, its first and last pair; part -1: whole
+    int slot;                   // this slice's place in the workspace
+};
+
+// The work items of one pair, in the order every role of the kernel walks them.
+template <int MODE>
+class Walk {
+  public:
+    __device__ Walk(const LinParams& p, const int* off, const int* cum, int pair, int pairs)
+        : p_(p), off_(off), cum_(cum), pairs_(pairs), pair_(pair), t_(pair), g_(0)
+    {
+        const int total = cum[p.G];
+        const int rem = total % pairs;
+        len_ = slice_len(rem, p.kb, pairs, p.split_w);
+        whole_ = total;
+        lo_ = hi_ = start_ = 0;
+        if (len_ < p.kb) {
+            whole_ = total - rem;
+            const int64_t all = (int64_t)rem * p.kb;
+            start_ = (int64_t)pair * len_;
+            lo_ = min(start_, all);
+            hi_ = min(start_ + len_, all);
+        }
+    }
+
+    __device__ bool next(Item& it)
+    {
+        int tile;
+        it.part = -1;
+        if (t_ < whole_) {
+            tile = t_;
+            t_ += pairs_;
+            it.kb0 = 0, it.kb1 = p_.kb;
+        } else if (lo_ < hi_) {
+            const int j = (int)(lo_ / p_.kb);
+            it.kb0 = (int)(lo_ - (int64_t)j * p_.kb);
+            it.kb1 = (int)min((int64_t)p_.kb, it.kb0 + (hi_ - lo_));
+            if (it.kb1 - it.kb0 < p_.kb) {
+                it.part = j;
+                it.c0 = (int)(((int64_t)j * p_.kb) / len_);
+                it.c1 = (int)((((int64_t)j + 1) * p_.kb - 1) / len_);
+                it.slot = slot_of(pair_, j);
+            }
+            tile = whole_ + j;
+            lo_ += it.kb1 - it.kb0;
+        } else {
+            return false;
+        }
+        while (tile >= cum_[g_ + 1]) ++g_;
+        it.g = g_;
+        int rows = off_[g_ + 1] - off_[g_], first = off_[g_];
+        if (MODE == kLinDw) {
+            it.red0 = first;
+            it.red_rows = max(rows, 0);
+            if (p_.offsets) it.kb0 = 0, it.kb1 = (it.red_rows + BK - 1) / BK;
+            rows = p_.rows, first = 0;
+        }
+        const int local = tile - cum_[g_];
+        const int nt = (rows + MAX_W - 1) / MAX_W;
+        const int per = RASTER * p_.f_tiles;
+        const int rg = local / per;
+        const int m0 = rg * RASTER, m = min(nt - m0, RASTER);
+        const int r = local - rg * per;
+        it.w = tile_width(rows);
+        const int t0 = (m0 + r % m) * it.w;
+        it.row0 = first + t0;
+        it.valid = min(it.w, rows - t0);  // (may be <= 0 for the last of equal tiles)
+        it.f0 = r / m;                    // (in tiles; the caller scales it)
+        return true;
+    }
+
+    // Workspace slot of pair c's slice of the last wave's tile j: its first or its second part.
+    __device__ int slot_of(int c, int j) const { return 2 * c + ((int64_t)c * len_ / p_.kb == j ? 0 : 1); }
+
+  private:
+    const LinParams& p_;
+    const int* off_;
+    const int* cum_;
+    int pairs_, pair_, t_, g_, whole_, len_;
+    int64_t lo_, hi_, start_;
+};
+
+__device__ __forceinline__ void record_error(int* status, int code, volatile int* abort_flag)
+{
+    atomicCAS(status, 0, code);
+    *abort_flag = 1;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint16_t to_16(float v)
+{
+    if (BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    return __half_as_ushort(__float2half_rn(v));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float from_16(uint16_t v)
+{
+    if (BF16) return __bfloat162float(__ushort_as_bfloat16(v));
+    return __half2float(__ushort_as_half(v));
+}
+
+// z / (1 + e^-z): e^-z = inf gives -0 for large negative z
+__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act)
+{
+    switch (act) {
+    case GEMM_ACT_RELU:
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = v[i] > 0.f ? v[i] : (v[i] <= 0.f ? 0.f : v[i]);  // NaN stays
+        break;
+    case GEMM_ACT_GELU:
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+        break;
+    case GEMM_ACT_GELU_TANH:
+        // 0.5 (1 + tanh u) = 1 / (1 + e^-2u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float u2 = 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);
+            v[i] = __fdividef(v[i], 1.f + __expf(-u2));
+        }
+        break;
+    case GEMM_ACT_SILU:
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = silu(v[i]);
+        break;
+    default: break;
+    }
+}
+
+// The epilogue's 16-bit matrices as it reads and writes them: a warp holds 32 features (one
+// a lane) of N rows, and the rows lie `ld` apart.  With 16-byte aligned rows (`vec`) the
+// block goes through the warp's staging block as words of two rows, [row pair][feature]:
+// a lane then holds eight features of a row pair and makes one 16-byte access a row.  The
+// lanes of odd row pairs take their two halves in the other order, so that the 16-byte
+// accesses to shared memory meet no bank conflicts.
+struct Matrix16 {
+    uint16_t* base;  // row 0, feature 0 of the block
+    int64_t ld;
+    int n, nf;       // rows and features of the block that exist (nf may exceed 32)
+    bool vec;
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_16(float lo, float hi)
+{
+    if (BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// eight features of one row
+__device__ __forceinline__ void store_row8(const Matrix16& m, int row, int f, uint4 v)
+{
+    if (row >= m.n || f >= m.nf) return;
+    uint16_t* o = m.base + row * m.ld + f;
+    if (f + 8 <= m.nf) {
+        *reinterpret_cast<uint4*>(o) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (f + i < m.nf) o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+}
+
+__device__ __forceinline__ uint4 load_row8(const Matrix16& m, int row, int f)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row >= m.n || f >= m.nf) return v;
+    const uint16_t* o = m.base + row * m.ld + f;
+    if (f + 8 <= m.nf) return *reinterpret_cast<const uint4*>(o);
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (f + i < m.nf) w[i / 2] |= (uint32_t)o[i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool BF16, int N>
+__device__ __forceinline__ void store_block(const Matrix16& m, uint32_t* stg, int lane, const float (&v)[N])
+{
+    if (m.n <= 0 || m.nf <= 0) return;  // (uniform over the warp)
+    if (!m.vec) {
+        uint16_t* o = m.base + lane;
+        if (lane < m.nf)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < m.n) o[i * m.ld] = to_16<BF16>(v[i]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) stg[i * 32 + lane] = pack_16<BF16>(v[2 * i], v[2 * i + 1]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+        const int pr = i * 8 + lane / 4, f = lane % 4 * 8;
+        const uint4* src = reinterpret_cast<const uint4*>(stg + pr * 32 + f);
+        const uint4 x = src[pr & 1], y = src[(pr & 1) ^ 1];
+        const uint4 lo = (pr & 1) ? y : x, hi = (pr & 1) ? x : y;  // features f..f+3, f+4..f+7
+        store_row8(m, 2 * pr, f, make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
+                                            __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410)));
+        store_row8(m, 2 * pr + 1, f, make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
+                                                __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632)));
+    }
+    __syncwarp();
+}
+
+// The residual's block, loaded ahead of its use: rows 2 pr and 2 pr + 1 of each lane's
+// eight features.
+template <int N>
+struct Ahead {
+    uint4 r[N / 16][2];
+    __device__ __forceinline__ void load(const Matrix16& m, int lane)
+    {
+        if (!m.vec) return;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            const int pr = i * 8 + lane / 4, f = lane % 4 * 8;
+            r[i][0] = load_row8(m, 2 * pr, f);
+            r[i][1] = load_row8(m, 2 * pr + 1, f);
+        }
+    }
+};
+
+template <bool BF16, int N>
+__device__ __forceinline__ void add_block(const Matrix16& m, const Ahead<N>& a, uint32_t* stg, int lane, float (&v)[N])
+{
+    if (m.n <= 0 || m.nf <= 0) return;
+    if (!m.vec) {
+        const uint16_t* r = m.base + lane;
+        if (lane < m.nf)
+#pragma unroll
+            for (int b = 0; b < N; b += 16) {
+                uint16_t t[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (b + i < m.n) t[i] = r[(b + i) * m.ld];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (b + i < m.n) v[b + i] += from_16<BF16>(t[i]);
+            }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+        const int pr = i * 8 + lane / 4, f = lane % 4 * 8;
+        const uint4 e = a.r[i][0], o = a.r[i][1];
+        uint4* dst = reinterpret_cast<uint4*>(stg + pr * 32 + f);
+        const uint4 lo = make_uint4(__byte_perm(e.x, o.x, 0x5410), __byte_perm(e.x, o.x, 0x7632),
+                                    __byte_perm(e.y, o.y, 0x5410), __byte_perm(e.y, o.y, 0x7632));
+        const uint4 hi = make_uint4(__byte_perm(e.z, o.z, 0x5410), __byte_perm(e.z, o.z, 0x7632),
+                                    __byte_perm(e.w, o.w, 0x5410), __byte_perm(e.w, o.w, 0x7632));
+        dst[pr & 1] = (pr & 1) ? hi : lo;
+        dst[(pr & 1) ^ 1] = (pr & 1) ? lo : hi;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const uint32_t w = stg[i * 32 + lane];
+        v[2 * i] += from_16<BF16>((uint16_t)w);
+        v[2 * i + 1] += from_16<BF16>((uint16_t)(w >> 16));
+    }
+    __syncwarp();
+}
+
+// The same in fp32: a row's 32 features are 128 contiguous bytes as they are.
+template <int N>
+__device__ __forceinline__ void store_f32(const float* R, int64_t ldr, float* out, int64_t ldo, int n, bool on,
+                                          float (&v)[N])
+{
+    if (!on) return;
+    if (R) {
+#pragma unroll
+        for (int b = 0; b < N; b += 16) {
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (b + i < n) t[i] = R[(b + i) * ldr];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (b + i < n) v[b + i] += t[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < n) out[i * ldo] = v[i];
+}
+
+template <int MODE, bool GATED, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p)
+{
+    constexpr bool A_MN = MODE != kLinDx, B_MN = MODE == kLinDw;
+    constexpr int TILE_F = GATED ? CTA_F : 2 * CTA_F;  // output features of a tile
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+    uint8_t* smem_a = smem;
+    uint8_t* smem_b = smem + p.stages * A_BYTES;
+    uint8_t* after = smem_b + p.stages * p.b_bytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(after + EPI_WARPS * STG_BYTES);
+    uint64_t* full_bar = bars;                     // (used in the even CTA)
+    uint64_t* empty_bar = bars + MAX_STAGES;       // (both CTAs, multicast)
+    uint64_t* tail_bar = bars + 2 * MAX_STAGES;    // kLinDw: a stage the fixer passes on (each CTA's own)
+    uint64_t* peer_bar = bars + 3 * MAX_STAGES;    // kLinDw: the odd CTA's fixer is done (used in the even CTA)
+    uint64_t* tfull_bar = bars + 4 * MAX_STAGES;   // [2] (both CTAs, multicast)
+    uint64_t* tempty_bar = tfull_bar + 2;          // [2] (used in the even CTA)
+    uint64_t* drain_bar = tfull_bar + 4;           // (both CTAs, multicast)
+    uint64_t* never_bar = tfull_bar + 5;           // never completes (test hook)
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tfull_bar + 6);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_holder + 2);
+    int* off = reinterpret_cast<int*>(tmem_holder + 4);
+    int* cum = off + p.G + 1;
+
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const uint16_t pair_mask = 0x3;
+    const int pair = blockIdx.x / 2;
+    const int npairs = gridDim.x / 2;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(smem_u32(&full_bar[s]), 1);
+            mbar_init(smem_u32(&empty_bar[s]), 1);
+            mbar_init(smem_u32(&tail_bar[s]), 1);
+            mbar_init(smem_u32(&peer_bar[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&tfull_bar[a]), 1);
+            mbar_init(smem_u32(&tempty_bar[a]), 2 * EPI_WARPS);
+        }
+        mbar_init(smem_u32(drain_bar), 1);
+        mbar_init(smem_u32(never_bar), 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+        if (p.kb > 0) {
+            prefetch_tensormap(&tmA);
+            prefetch_tensormap(&tmB);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 2 * MAX_W);
+        tc_fence_before();
+    }
+    if (MODE == kLinDw)
+        group_table(p.offsets, p.G, p.M, 0, (p.rows + MAX_W - 1) / MAX_W * p.f_tiles, 0, off, cum);
+    else
+        group_table(p.offsets, p.G, p.M, MAX_W, p.f_tiles, 0, off, cum);
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    bool aborted = false;
+
+    if (warp < EPI_WARP0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LEAN_REGS));
+        if (warp == 0 || warp == 3) {
+            // ---------------------------------------------------------------- producers
+            // warp 0 loads A (and announces a stage's bytes), warp 3 loads B: one thread issuing
+            // all of a stage's copies was what the MMAs waited for
+            if (lane == 0) {
+                Walk<MODE> walk(p, off, cum, pair, npairs);
+                Item it;
+                int stage = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                const bool load_a = warp == 0;
+                const uint32_t a_base = smem_u32(smem_a), b_base = smem_u32(smem_b);
+                const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0), tail_own = mapa_shared(smem_u32(tail_bar), rank);
+                while (ok && walk.next(it)) {
+                    const int f0 = it.f0 * TILE_F;
+                    const int half = it.w / 2;
+                    const int nb = B_MN ? (half + 63) / 64 : (half + p.bx - 1) / p.bx;
+                    const uint32_t b_box = B_MN ? BOX_BYTES : p.bx * 128;
+                    const uint32_t bytes = A_BYTES + nb * b_box;
+                    const int b_row = it.row0 + (int)rank * half;
+                    // A's two boxes of 64 features (kLinDx: one of 128 rows of W)
+                    const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
+                    const int fa2 = GATED ? p.F + fa : fa + 64;
+                    for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                        if (!mbar_wait_cluster(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag)) {
+                            record_error(p.status, kDevTimeoutProducer, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        // a k-block that ends inside the next group's rows goes through the fixer
+                        const bool tail = MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK;
+                        // (the even CTA alone announces both CTAs' bytes: arrivals from the odd one,
+                        // released at cluster scope, took the kernel from 0.71 to 1.66 ms at 8192^3)
+                        const uint32_t bar = (tail ? tail_own : full0) + stage * 8;
+                        const int k = (MODE == kLinDw ? it.red0 : 0) + kb * BK;
+                        if (load_a) {
+                            if (tail) mbar_arrive_expect_tx(smem_u32(&tail_bar[stage]), bytes);
+                            else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
+                            const uint32_t dst = a_base + stage * A_BYTES;
+                            if (MODE == kLinFwd) {
+                                tma_load_3d_pair(dst, &tmA, bar, fa, k, it.g);
+                                tma_load_3d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k, it.g);
+                            } else if (MODE == kLinDx) {
+                                tma_load_3d_pair(dst, &tmA, bar, k, fa, it.g);
+                            } else {
+                                tma_load_2d_pair(dst, &tmA, bar, fa, k);
+                                tma_load_2d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k);
+                            }
+                        } else {
+                            const uint32_t dst = b_base + stage * p.b_bytes;
+                            if (B_MN) {
+                                tma_load_2d_pair(dst, &tmB, bar, b_row, k);
+                                if (nb > 1) tma_load_2d_pair(dst + BOX_BYTES, &tmB, bar, b_row + 64, k);
+                            } else {
+                                tma_load_2d_pair(dst, &tmB, bar, k, b_row);
+                                for (int i = 1; i < nb; ++i)
+                                    tma_load_2d_pair(dst + i * b_box, &tmB, bar, k, b_row + i * p.bx);
+                            }
+                        }
+                        if (++stage == p.stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+                if (!ok) aborted = true;
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------------------------------------------------------- MMA issuer (even CTA)
+            if (lane == 0 && rank == 0) {
+                Walk<MODE> walk(p, off, cum, pair, npairs);
+                Item it;
+                int stage = 0, buf = 0;
+                uint32_t phase = 0, buf_phase = 0;
+                bool ok = true;
+                // descriptors of stage 0; a stage or a step of 16 along K moves the start address
+                constexpr uint32_t A_STEP = A_MN ? UMMA_K * 128 : UMMA_K * 2, B_STEP = B_MN ? UMMA_K * 128 : UMMA_K * 2;
+                const uint64_t a_desc0 = smem_desc_sw128(smem_u32(smem_a), A_MN ? BOX_BYTES : 16, 1024);
+                const uint64_t b_desc0 = smem_desc_sw128(smem_u32(smem_b), B_MN ? BOX_BYTES : 16, 1024);
+                while (ok && walk.next(it)) {
+                    const uint32_t idesc = p.idesc | ((uint32_t)(it.w >> 3) << 17);
+                    for (int kb0 = it.kb0; kb0 < it.kb1 && ok; kb0 += p.kc) {
+                        if (!mbar_wait_cluster(smem_u32(&tempty_bar[buf]), buf_phase ^ 1, p.limit_ns, abort_flag)) {
+                            record_error(p.status, kDevTimeoutMma, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAX_W);
+                        const int kb1 = min(kb0 + p.kc, it.kb1);
+                        for (int kb = kb0; kb < kb1; ++kb) {
+                            if (!mbar_wait_cluster(smem_u32(&full_bar[stage]), phase, p.limit_ns, abort_flag)) {
+                                record_error(p.status, kDevTimeoutMma, abort_flag);
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint64_t a_desc = a_desc0 + (uint32_t)(stage * A_BYTES >> 4);
+                            const uint64_t b_desc = b_desc0 + (uint32_t)(stage * p.b_bytes >> 4);
+                            if (MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK) {
+                                const int steps = (it.red_rows - kb * BK + UMMA_K - 1) / UMMA_K;
+                                for (int k = 0; k < steps; ++k)
+                                    umma_f16_pair(d_tmem, a_desc + k * (A_STEP >> 4), b_desc + k * (B_STEP >> 4), idesc,
+                                                  (kb > kb0 || k > 0) ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < BK / UMMA_K; ++k)
+                                    umma_f16_pair(d_tmem, a_desc + k * (A_STEP >> 4), b_desc + k * (B_STEP >> 4), idesc,
+                                                  (kb > kb0 || k > 0) ? 1u : 0u);
+                            }
+                            umma_commit_mask(smem_u32(&empty_bar[stage]), pair_mask);
+                            if (++stage == p.stages) {
+                                stage = 0;
+                                phase ^= 1;
+                            }
+                        }
+                        if (!ok) break;
+                        umma_commit_mask(smem_u32(&tfull_bar[buf]), pair_mask);
+                        if (++buf == 2) {
+                            buf = 0;
+                            buf_phase ^= 1;
+                        }
+                    }
+                }
+                if (!ok) aborted = true;
+                umma_commit_mask(smem_u32(drain_bar), pair_mask);
+            }
+            if (lane == 0) {
+                if (!mbar_wait_cluster(smem_u32(drain_bar), 0, p.limit_ns, nullptr)) {
+                    record_error(p.status, kDevTimeoutDrain, abort_flag);
+                    aborted = true;
+                }
+            }
+            __syncwarp();
+        } else if (MODE == kLinDw && warp == 2) {
+            // ---------------------------------------------------------------- fixer (both CTAs)
+            Walk<MODE> walk(p, off, cum, pair, npairs);
+            Item it;
+            int stage = 0;
+            uint32_t used = 0;  // bit s: parity of stage s's next tail
+            bool ok = true;
+            while (ok && p.offsets && walk.next(it)) {
+                const int nk = it.kb1 - it.kb0;
+                if (nk == 0) continue;
+                const int r = it.red_rows - (it.kb1 - 1) * BK;  // rows of the last k-block
+                const int s = (stage + nk - 1) % p.stages;
+                stage = (stage + nk) % p.stages;
+                if (r >= BK) continue;
+                const uint32_t parity = (used >> s) & 1;
+                ok = mbar_wait_cluster(smem_u32(&tail_bar[s]), parity, p.limit_ns, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0) record_error(p.status, kDevTimeoutMma, abort_flag);
+                    aborted = true;
+                    break;
+                }
+                used ^= 1u << s;
+                // rows r .. up to the MMA's next multiple of 16, 128 bytes each, in every box
+                const int r1 = (r + UMMA_K - 1) / UMMA_K * UMMA_K;
+                const int nb = (it.w / 2 + 63) / 64;
+                const int chunks = (r1 - r) * 8;
+                for (int b = 0; b < 2 + nb; ++b) {
+                    uint8_t* box = b < 2 ? smem_a + s * A_BYTES + b * BOX_BYTES
+                                         : smem_b + s * p.b_bytes + (b - 2) * BOX_BYTES;
+                    for (int c = lane; c < chunks; c += 32)
+                        *reinterpret_cast<uint4*>(box + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (rank == 1) {
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&peer_bar[s]), 0));
+                    continue;
+                }
+                ok = mbar_wait_cluster(smem_u32(&peer_bar[s]), parity, p.limit_ns, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0) record_error(p.status, kDevTimeoutMma, abort_flag);
+                    aborted = true;
+                    break;
+                }
+                if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+        // ---------------------------------------------------------------- epilogue (both CTAs)
+        const int q = warp & 3;             // TMEM lane quarter
+        const int half = (warp - EPI_WARP0) >> 2;   // takes 32-column blocks half, half + 2, ...
+        const int e = threadIdx.x - 32 * EPI_WARP0;
+        uint32_t* stg = reinterpret_cast<uint32_t*>(after + (warp - EPI_WARP0) * STG_BYTES);
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        // After a wait has run out a warp goes on through its items without waiting or
+        // storing, so that the others' barriers are still met.
+        bool dead = false;
+        if (p.test_stall) {
+            bool ok = mbar_wait_cluster(smem_u32(never_bar), 0, p.limit_ns, nullptr);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok && lane == 0) record_error(p.status, kDevTimeoutEpilogue, abort_flag);
+            dead = true;
+        }
+        Walk<MODE> walk(p, off, cum, pair, npairs);
+        Item it;
+        float acc[4][32];
+        while (walk.next(it)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[j][i] = 0.f;
+            for (int kb0 = it.kb0; kb0 < it.kb1 && !dead; kb0 += p.kc) {
+                bool ok = mbar_wait_cluster(smem_u32(&tfull_bar[buf]), buf_phase, p.limit_ns, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0) record_error(p.status, kDevTimeoutEpilogue, abort_flag);
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t_addr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAX_W + half * 32);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if ((2 * j + half) * 32 < it.w) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(t_addr + j * 64, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[j][i] = __fadd_rn(acc[j][i], __uint_as_float(v[i]));
+                    }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+                if (++buf == 2) {
+                    buf = 0;
+                    buf_phase ^= 1;
+                }
+            }
+            if (it.part >= 0) {
+                // publish this slice; the CTA that counts last adds the tile's slices in K order
+                const int64_t zs = (int64_t)2 * p.ws_cols * CTA_F;  // floats of a slot (both CTAs)
+                float* base = p.ws + (int64_t)rank * p.ws_cols * CTA_F + q * 32 + lane;
+                if (!dead && in_range(it.slot, 2 * npairs)) {
+                    float* mine = base + it.slot * zs;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int cb = (2 * j + half) * 32;
+                        if (cb < it.w && in_range(cb + 31, p.ws_cols)) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) __stcg(mine + (cb + i) * CTA_F, acc[j][i]);
+                        }
+                    }
+                    __threadfence();
+                }
+                if (dead) *abort_flag = 1;
+                named_barrier(1, 32 * EPI_WARPS);
+                if (e == 0) {
+                    int last = 0;
+                    if (!*abort_flag) {
+                        unsigned* c = p.cnt + 2 * it.part + rank;
+                        last = atomicAdd(c, 1u) == (unsigned)(it.c1 - it.c0);
+                        if (last) *c = 0;  // ready for the next launch
+                    }
+                    __threadfence();
+                    *last_flag = last;
+                }
+                named_barrier(1, 32 * EPI_WARPS);
+                const int last = *last_flag;
+                // (read by every warp before the next item's first barrier lets thread 0 on)
+                if (!last) continue;
+                __threadfence();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int cb = (2 * j + half) * 32;
+                    if (cb < it.w) {
+                        // (every slice, this CTA's own included, is read back)
+                        for (int c = it.c0; c <= it.c1; ++c) {
+                            const float* src = base + walk.slot_of(c, it.part) * zs + cb * CTA_F;
+                            float v[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __ldcg(src + i * CTA_F);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) acc[j][i] = c == it.c0 ? v[i] : __fadd_rn(acc[j][i], v[i]);
+                        }
+                    }
+                }
+            }
+            // feature of lane 0, and the column of W it comes from
+            const int fw = it.f0 * TILE_F + (GATED ? 64 * (int)rank + 32 * (q & 1) : CTA_F * (int)rank + 32 * q);
+            const int nf = dead ? 0 : p.F - fw;
+            const int zw = GATED && q >= 2 ? p.F + fw : fw;
+            float bias = 0.f;
+            if (MODE == kLinFwd && p.bias && lane < nf)
+                bias = from_16<BF16>(static_cast<const uint16_t*>(p.bias)[it.g * p.bias_stride + zw + lane]);
+            const int64_t out0 = MODE == kLinDw ? it.g * p.out_stride : 0;
+            constexpr int OUT_N = GATED ? 16 : 32;       // rows a warp finishes of 32 (gated: the pair shares them)
+            const int own = GATED && q >= 2 ? 16 : 0;    // and the first of them
+            const bool residual = MODE == kLinFwd && p.R && !p.out_f32;
+            Matrix16 mr = {}, mo = {}, mz = {};
+            Ahead<OUT_N> ahead;
+            const auto block = [&](const void* base, int64_t ld, int col, int cb, bool vec) {
+                const int64_t row = it.row0 + cb;
+                const int n = it.valid - cb;
+                const bool in = n <= 0 || in_range(row + min(n, 32) - 1, p.rows);
+                return Matrix16{static_cast<uint16_t*>(const_cast<void*>(base)) + row * ld + col, ld, in ? n : 0, nf, vec};
+            };
+            if (residual) {
+                mr = block(p.R, p.ldr, fw, half * 32 + own, p.vec_r);
+                ahead.load(mr, lane);
+            }
+            // (the sums move down a block an iteration, so that one copy of the code below does)
+#pragma unroll 1
+            for (int cb = half * 32; cb < it.w; cb += 64) {
+                float(&v)[32] = acc[0];
+                if (MODE == kLinFwd) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += bias;
+                    if (p.Z) {
+                        mz = block(p.Z, p.ldz, zw, cb, p.vec_z);
+                        store_block<BF16>(mz, stg, lane, v);
+                    }
+                }
+                const auto finish = [&](auto& h) {
+                    if (MODE != kLinDx && p.out_f32) {
+                        const int64_t row = it.row0 + cb + own;
+                        const int n = it.valid - cb - own;
+                        if (n <= 0 || !in_range(row + min(n, OUT_N) - 1, p.rows)) return;
+                        store_f32(MODE == kLinFwd && p.R ? static_cast<const float*>(p.R) + row * p.ldr + fw + lane : nullptr,
+                                  p.ldr, static_cast<float*>(p.out) + out0 + row * p.ldo + fw + lane, p.ldo, n, lane < nf, h);
+                        return;
+                    }
+                    if (residual) {
+                        const Ahead<OUT_N> now = ahead;
+                        const Matrix16 m = mr;
+                        if (cb + 64 < it.w) {
+                            mr = block(p.R, p.ldr, fw, cb + 64 + own, p.vec_r);
+                            ahead.load(mr, lane);
+                        }
+                        add_block<BF16>(m, now, stg, lane, h);
+                    }
+                    mo = block(static_cast<const uint16_t*>(p.out) + out0, p.ldo, fw, cb + own, p.vec_out);
+                    store_block<BF16>(mo, stg, lane, h);
+                };
+                if constexpr (GATED) {
+                    // gate warps finish rows 0..15, up warps 16..31; each leaves the other's part in
+                    // its own staging block
+                    const bool up = q >= 2;
+                    float* mine = reinterpret_cast<float*>(stg) + lane;
+                    const float* other = reinterpret_cast<const float*>(
+                                             after + ((warp - EPI_WARP0) + (up ? -2 : 2)) * STG_BYTES) + lane;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) mine[i * 32] = up ? v[i] : v[16 + i];
+                    named_barrier(2 + (q & 1) + 2 * half, 64);
+                    float h[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float o = other[i * 32];
+                        h[i] = up ? silu(o) * v[16 + i] : silu(v[i]) * o;
+                    }
+                    named_barrier(2 + (q & 1) + 2 * half, 64);
+                    finish(h);
+                } else {
+                    if (MODE == kLinFwd) activate(v, p.act);
+                    finish(v);
+                }
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[j][i] = acc[j + 1][i];
+            }
+        }
+        if (dead) aborted = true;
+    }
+
+    if (__syncthreads_or(aborted ? 1 : 0)) grace_period(2000000ull);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 2 * MAX_W);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+// 16-bit tensor [d2][d1][d0] (d0 contiguous) with strides of s1 and s2 elements; 128-byte
+// swizzled boxes of 64 x box1.  rank 2 ignores d2.
+bool encode(CUtensorMap* map, int rank, const void* base, bool bf16, int64_t d0, int64_t d1, int64_t d2, int64_t s1,
+            int64_t s2, int box1)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box1, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct LinPlan {
+    int rows, F, kb, f_tiles, wmax, pairs;
+    int bx, b_bytes, stages, smem;
+    bool gated;
+    int split_w;  // 0: the last wave is not cut
+    int64_t tiles;  // an upper bound when the groups' rows are only known on the device
+};
+
+LinPlan plan(const LinArgs& a, int num_sms)
+{
+    LinPlan pl;
+    pl.gated = a.mode == kLinFwd && a.act == GEMM_ACT_SWIGLU;
+    pl.rows = (int)(a.mode == kLinDw ? a.K : a.M);
+    pl.F = (int)(a.mode == kLinFwd ? a.N : a.mode == kLinDx ? a.K : a.Nw);
+    const int64_t red = a.mode == kLinFwd ? a.K : a.mode == kLinDx ? a.Nw : a.M;
+    pl.kb = (int)((red + BK - 1) / BK);
+    const int tile_f = pl.gated ? CTA_F : 2 * CTA_F;
+    pl.f_tiles = (pl.F + tile_f - 1) / tile_f;
+    const int G = a.G > 0 ? a.G : 1;
+    const bool ragged = a.G > 0 && a.mode != kLinDw;  // the tiles' widths are known on the device only
+    pl.wmax = ragged ? (int)(a.M < MAX_W ? (a.M + 15) / 16 * 16 : MAX_W) : tile_width(pl.rows);
+    int64_t row_tiles = (pl.rows + MAX_W - 1) / MAX_W;
+    if (ragged) row_tiles += a.G < a.M ? a.G : a.M;
+    pl.tiles = row_tiles * pl.f_tiles * (a.mode == kLinDw ? G : 1);
+    // rows of a TMA box of the K-major B operand: a whole half tile where its height is
+    // known, else pieces of a typical group's half tile
+    int typical = pl.wmax / 2;
+    if (ragged) {
+        const int64_t mean = (a.M + a.G - 1) / a.G;
+        typical = mean >= 128 ? 64 : mean >= 32 ? 32 : 16;
+        if (typical > pl.wmax / 2) typical = pl.wmax / 2;
+    }
+    pl.bx = typical < 8 ? 8 : (typical + 7) / 8 * 8;
+    const int b_rows = (pl.wmax / 2 + pl.bx - 1) / pl.bx * pl.bx;
+    pl.b_bytes = a.mode == kLinDw ? (pl.wmax / 2 + 63) / 64 * BOX_BYTES : (b_rows * 128 + 1023) / 1024 * 1024;
+    const int fixed = 1024 + EPI_WARPS * STG_BYTES + (4 * MAX_STAGES + 6) * 8 + 16 + 2 * (G + 1) * 4 + 16;
+    pl.stages = (SMEM_MAX - fixed) / (A_BYTES + pl.b_bytes);
+    if (pl.stages > MAX_STAGES) pl.stages = MAX_STAGES;
+    pl.smem = fixed + pl.stages * (A_BYTES + pl.b_bytes);
+    // groups' dW tiles have lengths of their own and are not cut
+    pl.split_w = a.mode == kLinDw && a.G > 0 ? 0 : pl.wmax;
+    if (ragged && a.M > a.G) {
+        const int64_t mean = (a.M + a.G - 1) / a.G;
+        if (mean < pl.wmax) pl.split_w = (int)((mean + 15) / 16 * 16);
+    }
+    pl.pairs = num_sms / 2;
+    return pl;
+}
+
+// The kernel of one instantiation and the clusters of it that can be resident at once
+// (cached per process: every device a process drives is taken to be the same part).
+template <int MODE, bool GATED, bool BF16>
+int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p, int num_sms,
+                  cudaStream_t stream)
+{
+    static std::atomic<int> fit{0};
+    auto kern = linear_pair_kernel<MODE, GATED, BF16>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_MAX;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = fit.load();
+    if (clusters == 0) {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return GEMM_ERR_CUDA;
+        if (fa.numRegs < LAUNCH_REGS) return GEMM_ERR_UNSUPPORTED;  // the epilogue would wait for registers
+        if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
+            (void)cudaGetLastError();
+            return GEMM_ERR_CUDA;
+        }
+        fit.store(clusters);
+    }
+    if (clusters > num_sms / 2) clusters = num_sms / 2;
+    if (p.split_w == 0 && pl.tiles < clusters) clusters = (int)pl.tiles;
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.dynamicSmemBytes = pl.smem;
+    return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, p) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+template <bool BF16>
+int launch_typed(int mode, const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p,
+                 int num_sms, cudaStream_t s)
+{
+    if (mode == kLinDx) return launch_kernel<kLinDx, false, BF16>(pl, tmA, tmB, p, num_sms, s);
+    if (mode == kLinDw) return launch_kernel<kLinDw, false, BF16>(pl, tmA, tmB, p, num_sms, s);
+    if (pl.gated) return launch_kernel<kLinFwd, true, BF16>(pl, tmA, tmB, p, num_sms, s);
+    return launch_kernel<kLinFwd, false, BF16>(pl, tmA, tmB, p, num_sms, s);
+}
+
+}  // namespace
+
+size_t linear_partials_bytes(const LinArgs& a, int num_sms)
+{
+    const LinPlan pl = plan(a, num_sms);
+    if (pl.split_w == 0) return 0;
+    return (size_t)2 * pl.pairs * 2 * CTA_F * ((pl.wmax + 31) / 32 * 32) * sizeof(float);
+}
+
+int64_t linear_counters(int num_sms) { return num_sms; }  // two a tile of the last wave, fewer tiles than pairs
+
+int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* dev_status, uint64_t limit_ns, int kc,
+                  int test_stall, cudaStream_t stream, int* launches)
+{
+    const LinPlan pl = plan(a, num_sms);
+    if (pl.tiles <= 0) return GEMM_OK;
+    if (pl.tiles > 0x7fffffffLL || pl.stages < 2) return GEMM_ERR_UNSUPPORTED;
+    LinParams p = {};
+    p.M = (int)a.M;
+    p.rows = pl.rows;
+    p.F = pl.F;
+    p.kb = pl.kb;
+    p.G = a.G > 0 ? a.G : 1;
+    p.offsets = a.G > 0 ? a.offsets : nullptr;
+    p.f_tiles = pl.f_tiles;
+    p.bx = pl.bx;
+    p.b_bytes = pl.b_bytes;
+    p.stages = pl.stages;
+    p.kc = kc > 0 ? kc : (a.out_f32 ? 16 : 32);
+    p.split_w = ws.partials && ws.counters ? pl.split_w : 0;
+    p.bias = a.bias;
+    p.bias_stride = a.Nw;
+    p.R = a.R;
+    p.ldr = a.ldr;
+    p.Z = a.Z;
+    p.ldz = a.ldz;
+    p.out = a.out;
+    p.ldo = a.ldo;
+    p.out_stride = a.out_stride;
+    const auto vec = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld % 8 == 0; };
+    p.vec_r = vec(a.R, a.ldr);
+    p.vec_z = vec(a.Z, a.ldz);
+    p.vec_out = vec(a.out, a.ldo) && a.out_stride % 8 == 0;
+    p.act = a.act;
+    p.out_f32 = a.out_f32 ? 1 : 0;
+    p.ws = ws.partials;
+    p.cnt = ws.counters;
+    p.ws_cols = (pl.wmax + 31) / 32 * 32;
+    p.status = dev_status;
+    p.limit_ns = limit_ns;
+    p.test_stall = test_stall;
+    const bool a_mn = a.mode != kLinDx, b_mn = a.mode == kLinDw;
+    // kind::f16: fp32 accumulator, both operands of one type, MN-major bits, M = 256
+    p.idesc = (1u << 4) | ((a.bf16 ? 1u : 0u) << 7) | ((a.bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+              ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(2 * CTA_F >> 4) << 24);
+    CUtensorMap tmA = {}, tmB = {};
+    if (pl.kb > 0) {
+        bool ok;
+        if (a.mode == kLinDw)
+            ok = encode(&tmA, 2, a.dZ, a.bf16, a.Nw, a.M, 1, a.lddz, 0, 64) &&
+                 encode(&tmB, 2, a.X, a.bf16, a.K, a.M, 1, a.ldx, 0, 64);
+        else
+            ok = encode(&tmA, 3, a.W, a.bf16, a.Nw, a.K, p.G, a.ldw, p.G > 1 ? a.w_stride : a.K * a.ldw,
+                        a.mode == kLinFwd ? 64 : CTA_F) &&
+                 (a.mode == kLinFwd ? encode(&tmB, 2, a.X, a.bf16, a.K, a.M, 1, a.ldx, 0, pl.bx)
+                                    : encode(&tmB, 2, a.dZ, a.bf16, a.Nw, a.M, 1, a.lddz, 0, pl.bx));
+        if (!ok) return GEMM_ERR_CUDA;
+    }
+    const int rc = a.bf16 ? launch_typed<true>(a.mode, pl, tmA, tmB, p, num_sms, stream)
+                          : launch_typed<false>(a.mode, pl, tmA, tmB, p, num_sms, stream);
+    if (rc == GEMM_OK) *launches += 1;
+    return rc;
+}
+
+}  // namespace gemm_gb300

@@ -464,6 +464,23 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// 3-D tiled load for a CTA pair (coordinates innermost first); completes on a barrier
+// that may live in the peer CTA (cluster address).  Out-of-range boxes read zeros.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int c0,
+                                                 int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// Barrier over `count` threads of this CTA (whole warps), number `id` of the CTA's 16.
+__device__ __forceinline__ void named_barrier(uint32_t id, uint32_t count)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 
 // Count one arrival on a 64-bit counter whose upper half holds a launch tag: a count left
 // by another launch (or by one that stopped early) restarts at 1.  Returns the arrival
