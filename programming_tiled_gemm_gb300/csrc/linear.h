@@ -46,7 +46,7 @@ struct LinWorkspace {
 };
 
 // Workspace bytes of the K-sliced last wave, and counters (of 4 bytes).
-size_t linear_partials_bytes(const LinArgs& a, int num_sms);
+size_t linear_partials_bytes(const LinArgs& a, int num_sms, int kc);
 int64_t linear_counters(int num_sms);
 // Returns GEMM_OK or a negative gemm_status_t.
 int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* dev_status, uint64_t limit_ns, int kc,

@@ -45,7 +45,7 @@ int64_t product_counters(gemm_handle_t h) { return linear_counters(h->num_sms); 
 
 int run_product(gemm_handle_t h, const LinArgs& a, cudaStream_t s)
 {
-    const size_t need = linear_partials_bytes(a, h->num_sms);
+    const size_t need = linear_partials_bytes(a, h->num_sms, h->opt_tc_chunk);
     if (need > 0) {
         const int rc = ensure_buffer(reinterpret_cast<void**>(&h->lin_partials), &h->lin_partials_bytes, need);
         if (rc != GEMM_OK) return rc;

@@ -19,10 +19,12 @@
 //
 // Pipeline, as in the plain product's CTA-pair kernel: a producer warp per CTA (TMA, ring
 // of stages), one MMA thread a pair, eight epilogue warps a CTA.  The tensor core's fp32
-// accumulation rounds toward zero, so K is cut into chunks of `kc` k-blocks, each in a
-// fresh TMEM accumulator, added in fp32 round-to-nearest registers in order: 1024 of K for
-// fp32 results, as in the plain product, 2048 for 16-bit ones, whose own rounding is a
-// hundred times the sum's error (the epilogue then has twice the time).
+// accumulation rounds toward zero: 2^-24 of the sum lost per 16 of K.  For fp32 results, and
+// for more than 16384 of K, it is cut into chunks of `kc` k-blocks (16: 1024 of K, as in the
+// plain product), each in a fresh TMEM accumulator, added in fp32 round-to-nearest registers
+// in order (CHUNKED).  Otherwise one accumulator takes all of K: at 16384 that is 2^-14 of
+// the sum, an eighth of an fp16 result's own rounding and 1/64 of a bf16 result's, and the
+// epilogue, which takes its sums straight from TMEM, overlaps the whole next tile.
 //
 // Work: tiles are walked round robin by the persistent pairs.  The tiles of the last,
 // partial wave (all tiles, when there are fewer than pairs) are cut along K into equal
@@ -34,6 +36,10 @@
 // kLinDw over groups: a group's last k-block ends inside the next group's rows.  Those rows
 // are zeroed in shared memory, in both operands (zero times a neighbour's NaN would be NaN),
 // by a fixer warp before the MMAs may read the stage.
+//
+// Few rows: MMAs of 16 .. 128 columns into one accumulator wait for each other (175 cycles
+// each at 16 columns, ten times their own work), so the steps of 16 along K go round robin
+// to 256 / w (up to 4) accumulators, which the epilogue adds in order.
 //
 // Every wait is bounded; on expiry the status word is set and the CTA drains and returns.
 #include <cuda.h>
@@ -56,21 +62,23 @@ constexpr int BK = 64;                // k per stage: one 128-byte swizzle row o
 constexpr int UMMA_K = 16;
 constexpr int CTA_F = 128;            // features (MMA rows) of one CTA
 constexpr int MAX_W = 256;            // rows (MMA columns) of a tile
+constexpr int MAX_W_CHUNKED = 128;    // and with chunks, whose sums an epilogue thread holds: 64 of them
 constexpr int EPI_WARPS = 8;
 constexpr int A_BYTES = CTA_F * BK * 2;  // 16 KiB a stage
 constexpr int BOX_BYTES = 64 * BK * 2;   // 64 x 64 box of an MN-major operand
 constexpr int MAX_STAGES = 12;
+constexpr int MAX_KB_WHOLE = 256;     // k-blocks one accumulator takes for a 16-bit result
 constexpr int RASTER = 8;             // row tiles per raster group (2048 rows share W's columns in L2)
 constexpr int STG_BYTES = 2048;       // an epilogue warp's staging block: 32 rows x 32 features of 16 bits,
                                       // or (gated) 16 columns of fp32 for the other warp
 constexpr int SMEM_MAX = 232448;      // 227 KiB
 
-// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; 4..11: epilogue.  The epilogue's warps
-// hold 128 sums each and take registers from the first four: 72 + 2 * 216 a thread of the
-// three warpgroups is the 3 * 168 the block is launched with (checked before the launch).
+// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; 4..11: epilogue, which takes
+// registers from the first four: 104 + 2 * 200 a thread of the three warpgroups is within
+// the 3 * 168 the block is launched with (checked before the launch).
 constexpr int EPI_WARP0 = 4;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-constexpr int LAUNCH_REGS = 168, LEAN_REGS = 72, EPI_REGS = 216;
+constexpr int LAUNCH_REGS = 168, LEAN_REGS = 104, EPI_REGS = 200;
 static_assert(LEAN_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "the epilogue's registers come from the block's own");
 
 struct LinParams {
@@ -83,6 +91,7 @@ struct LinParams {
     int f_tiles;
     int bx;      // rows of a K-major B box
     int b_bytes, stages, kc;
+    int wcap;        // rows of a tile at most (a multiple of 16)
     int split_w;     // tile width the last wave's split is planned for (0: no split)
     const void* bias;
     int64_t bias_stride;
@@ -103,25 +112,36 @@ struct LinParams {
     int test_stall;
 };
 
-__host__ __device__ inline int tile_width(int rows)
+// Accumulators a tile's MMAs take turns on (kLinDw's last k-block may have fewer steps
+// than accumulators, and its tiles are wide).
+__host__ __device__ constexpr int accumulators(int mode, int w)
 {
-    // equal tiles: 300 rows are 160 + 140, not 256 + 44
-    const int nt = (rows + MAX_W - 1) / MAX_W;
-    const int w = (rows + nt - 1) / nt;
-    return (w + 15) / 16 * 16;
+    return mode == kLinDw ? 1 : w <= MAX_W / 4 ? 4 : w <= MAX_W / 2 ? 2 : 1;
 }
 
+// The width of `rows` rows' tiles of at most `wcap` (a multiple of 16): equal ones, so that
+// 300 rows are 160 + 140, not 256 + 44.
+__host__ __device__ inline int tile_width(int rows, int wcap)
+{
+    const unsigned nt = (unsigned)(rows + wcap - 1) / (unsigned)wcap;
+    const unsigned w = nt ? ((unsigned)rows + nt - 1) / nt : 16;
+    return (int)((w + 15) / 16 * 16);
+}
+
+// Estimated cycles: a k-block of a tile of w rows (its MMAs, or the 16 KiB of A that an SM
+// loads for it), and what cutting a tile along K costs (its slices' publication, the
+// addition and their latencies).
+__host__ __device__ inline int kb_cycles(int w) { return w < 150 ? 300 : 2 * w; }
+__host__ __device__ inline int split_cycles(int w) { return 4000 + 40 * w; }
+
 // k-blocks a pair takes of the last wave's `rem` tiles of kb k-blocks each (kb: whole
-// tiles).  A slice costs its publication and its addition, about 2 us + 3 us a 256-wide
-// tile, against 0.3 us a k-block saved.
+// tiles), where that is worth its cost.
 __host__ __device__ inline int slice_len(int rem, int kb, int pairs, int w)
 {
     if (rem <= 0 || w <= 0) return kb;
-    const int64_t all = (int64_t)rem * kb;
-    int len = (int)((all + pairs - 1) / pairs);
-    const int least = 2 + w / 16;
-    if (len < least) len = least;
-    return (kb - len < 4 + w / 16) ? kb : len;
+    int len = (int)(((uint32_t)rem * (uint32_t)kb + pairs - 1) / (uint32_t)pairs);
+    if (len < 2) len = 2;
+    return (int64_t)(kb - len) * kb_cycles(w) <= split_cycles(w) ? kb : len;
 }
 
 struct Item {
@@ -129,10 +149,12 @@ struct Item {
     int kb0, kb1;               // k-blocks
     int red0, red_rows;         // kLinDw: first reduced row of the group, its rows
     int part, c0, c1;           // slice: index among the last wave's tiles, its first and last pair; part -1: whole
-    int slot;                   // this slice's place in the workspace
+    bool second;                // slice: the first pair's part is the second of its range
 };
 
-// The work items of one pair, in the order every role of the kernel walks them.
+// The work items of one pair, in the order every role of the kernel walks them.  (All in 32
+// bits: the last wave's k-blocks are fewer than pairs * 2^25, and a 64-bit division takes
+// hundreds of cycles.)
 template <int MODE>
 class Walk {
   public:
@@ -143,13 +165,12 @@ class Walk {
         const int rem = total % pairs;
         len_ = slice_len(rem, p.kb, pairs, p.split_w);
         whole_ = total;
-        lo_ = hi_ = start_ = 0;
+        lo_ = hi_ = 0;
         if (len_ < p.kb) {
             whole_ = total - rem;
-            const int64_t all = (int64_t)rem * p.kb;
-            start_ = (int64_t)pair * len_;
-            lo_ = min(start_, all);
-            hi_ = min(start_ + len_, all);
+            const uint32_t all = (uint32_t)rem * p.kb, start = (uint32_t)pair * len_;
+            lo_ = min(start, all);
+            hi_ = min(start + len_, all);
         }
     }
 
@@ -162,16 +183,17 @@ class Walk {
             t_ += pairs_;
             it.kb0 = 0, it.kb1 = p_.kb;
         } else if (lo_ < hi_) {
-            const int j = (int)(lo_ / p_.kb);
-            it.kb0 = (int)(lo_ - (int64_t)j * p_.kb);
-            it.kb1 = (int)min((int64_t)p_.kb, it.kb0 + (hi_ - lo_));
+            const uint32_t j = lo_ / p_.kb, tile_lo = j * p_.kb;
+            it.kb0 = (int)(lo_ - tile_lo);
+            it.kb1 = (int)min((uint32_t)p_.kb, it.kb0 + (hi_ - lo_));
             if (it.kb1 - it.kb0 < p_.kb) {
-                it.part = j;
-                it.c0 = (int)(((int64_t)j * p_.kb) / len_);
-                it.c1 = (int)((((int64_t)j + 1) * p_.kb - 1) / len_);
-                it.slot = slot_of(pair_, j);
+                it.part = (int)j;
+                it.c0 = (int)(tile_lo / len_);
+                it.c1 = (int)((tile_lo + p_.kb - 1) / len_);
+                // a tile's first pair may have begun in the tile before: this is its second part
+                it.second = (uint32_t)it.c0 * len_ < tile_lo;
             }
-            tile = whole_ + j;
+            tile = whole_ + (int)j;
             lo_ += it.kb1 - it.kb0;
         } else {
             return false;
@@ -185,29 +207,30 @@ class Walk {
             if (p_.offsets) it.kb0 = 0, it.kb1 = (it.red_rows + BK - 1) / BK;
             rows = p_.rows, first = 0;
         }
-        const int local = tile - cum_[g_];
-        const int nt = (rows + MAX_W - 1) / MAX_W;
-        const int per = RASTER * p_.f_tiles;
-        const int rg = local / per;
-        const int m0 = rg * RASTER, m = min(nt - m0, RASTER);
-        const int r = local - rg * per;
-        it.w = tile_width(rows);
-        const int t0 = (m0 + r % m) * it.w;
+        const uint32_t local = tile - cum_[g_];
+        const uint32_t nt = (uint32_t)(rows + p_.wcap - 1) / p_.wcap;
+        const uint32_t per = RASTER * p_.f_tiles;
+        const uint32_t rg = local / per;
+        const uint32_t m0 = rg * RASTER, m = min(nt - m0, (uint32_t)RASTER);
+        const uint32_t r = local - rg * per, ft = r / m;
+        it.w = tile_width(rows, p_.wcap);
+        const int t0 = (int)(m0 + r - ft * m) * it.w;
         it.row0 = first + t0;
-        it.valid = min(it.w, rows - t0);  // (may be <= 0 for the last of equal tiles)
-        it.f0 = r / m;                    // (in tiles; the caller scales it)
+        it.valid = min(it.w, rows - t0);
+        it.f0 = (int)ft;  // (in tiles; the caller scales it)
         return true;
     }
 
-    // Workspace slot of pair c's slice of the last wave's tile j: its first or its second part.
-    __device__ int slot_of(int c, int j) const { return 2 * c + ((int64_t)c * len_ / p_.kb == j ? 0 : 1); }
+    // Workspace slot of pair c's slice of the item's tile.
+    __device__ static int slot_of(int c, const Item& it) { return 2 * c + (c == it.c0 && it.second ? 1 : 0); }
+    __device__ int slot(const Item& it) const { return slot_of(pair_, it); }
 
   private:
     const LinParams& p_;
     const int* off_;
     const int* cum_;
     int pairs_, pair_, t_, g_, whole_, len_;
-    int64_t lo_, hi_, start_;
+    uint32_t lo_, hi_;
 };
 
 __device__ __forceinline__ void record_error(int* status, int code, volatile int* abort_flag)
@@ -423,7 +446,7 @@ __device__ __forceinline__ void store_f32(const float* R, int64_t ldr, float* ou
         if (i < n) out[i * ldo] = v[i];
 }
 
-template <int MODE, bool GATED, bool BF16>
+template <int MODE, bool GATED, bool BF16, bool CHUNKED>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p)
 {
@@ -481,10 +504,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         tmem_alloc_pair(smem_u32(tmem_holder), 2 * MAX_W);
         tc_fence_before();
     }
+    grid_dependency_wait();  // what follows reads what the kernel before this one wrote
+    grid_dependents_launch();
     if (MODE == kLinDw)
-        group_table(p.offsets, p.G, p.M, 0, (p.rows + MAX_W - 1) / MAX_W * p.f_tiles, 0, off, cum);
+        group_table(p.offsets, p.G, p.M, 0, (p.rows + p.wcap - 1) / p.wcap * p.f_tiles, 0, off, cum);
     else
-        group_table(p.offsets, p.G, p.M, MAX_W, p.f_tiles, 0, off, cum);
+        group_table(p.offsets, p.G, p.M, p.wcap, p.f_tiles, 0, off, cum);
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
@@ -517,7 +542,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
                     const int fa2 = GATED ? p.F + fa : fa + 64;
                     for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                        if (!mbar_wait_cluster(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag)) {
+                        if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag)) {
                             record_error(p.status, kDevTimeoutProducer, abort_flag);
                             ok = false;
                             break;
@@ -563,7 +588,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             __syncwarp();
         } else if (warp == 1) {
             // ---------------------------------------------------------------- MMA issuer (even CTA)
-            if (lane == 0 && rank == 0) {
+            // (the whole warp walks, one elected lane issues: the descriptors then stay in uniform
+            // registers; a loop in one lane took 610 cycles a k-block, more than its MMAs)
+            if (rank == 0) {
                 Walk<MODE> walk(p, off, cum, pair, npairs);
                 Item it;
                 int stage = 0, buf = 0;
@@ -575,17 +602,21 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 const uint64_t b_desc0 = smem_desc_sw128(smem_u32(smem_b), B_MN ? BOX_BYTES : 16, 1024);
                 while (ok && walk.next(it)) {
                     const uint32_t idesc = p.idesc | ((uint32_t)(it.w >> 3) << 17);
-                    for (int kb0 = it.kb0; kb0 < it.kb1 && ok; kb0 += p.kc) {
-                        if (!mbar_wait_cluster(smem_u32(&tempty_bar[buf]), buf_phase ^ 1, p.limit_ns, abort_flag)) {
+                    const int turns = accumulators(MODE, it.w);
+                    const uint32_t turn_cols = MAX_W / turns;
+                    const int kc = CHUNKED ? p.kc : it.kb1 - it.kb0;
+                    for (int kb0 = it.kb0; kb0 < it.kb1 && ok; kb0 += kc) {
+                        if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&tempty_bar[buf]), buf_phase ^ 1, p.limit_ns,
+                                                                       abort_flag))) {
                             record_error(p.status, kDevTimeoutMma, abort_flag);
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAX_W);
-                        const int kb1 = min(kb0 + p.kc, it.kb1);
+                        const int kb1 = min(kb0 + kc, it.kb1);
                         for (int kb = kb0; kb < kb1; ++kb) {
-                            if (!mbar_wait_cluster(smem_u32(&full_bar[stage]), phase, p.limit_ns, abort_flag)) {
+                            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, abort_flag))) {
                                 record_error(p.status, kDevTimeoutMma, abort_flag);
                                 ok = false;
                                 break;
@@ -593,25 +624,25 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                             tc_fence_after();
                             const uint64_t a_desc = a_desc0 + (uint32_t)(stage * A_BYTES >> 4);
                             const uint64_t b_desc = b_desc0 + (uint32_t)(stage * p.b_bytes >> 4);
-                            if (MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK) {
-                                const int steps = (it.red_rows - kb * BK + UMMA_K - 1) / UMMA_K;
-                                for (int k = 0; k < steps; ++k)
-                                    umma_f16_pair(d_tmem, a_desc + k * (A_STEP >> 4), b_desc + k * (B_STEP >> 4), idesc,
-                                                  (kb > kb0 || k > 0) ? 1u : 0u);
-                            } else {
+                            const bool tail = MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK;
+                            const int steps = tail ? (it.red_rows - kb * BK + UMMA_K - 1) / UMMA_K : BK / UMMA_K;
+                            if (elect_one()) {
 #pragma unroll
                                 for (int k = 0; k < BK / UMMA_K; ++k)
-                                    umma_f16_pair(d_tmem, a_desc + k * (A_STEP >> 4), b_desc + k * (B_STEP >> 4), idesc,
-                                                  (kb > kb0 || k > 0) ? 1u : 0u);
+                                    if (MODE != kLinDw || k < steps)
+                                        umma_f16_pair(d_tmem + (k & (turns - 1)) * turn_cols, a_desc + k * (A_STEP >> 4),
+                                                      b_desc + k * (B_STEP >> 4), idesc, (kb > kb0 || k >= turns) ? 1u : 0u);
+                                umma_commit_mask(smem_u32(&empty_bar[stage]), pair_mask);
                             }
-                            umma_commit_mask(smem_u32(&empty_bar[stage]), pair_mask);
+                            __syncwarp();
                             if (++stage == p.stages) {
                                 stage = 0;
                                 phase ^= 1;
                             }
                         }
                         if (!ok) break;
-                        umma_commit_mask(smem_u32(&tfull_bar[buf]), pair_mask);
+                        if (elect_one()) umma_commit_mask(smem_u32(&tfull_bar[buf]), pair_mask);
+                        __syncwarp();
                         if (++buf == 2) {
                             buf = 0;
                             buf_phase ^= 1;
@@ -619,13 +650,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     }
                 }
                 if (!ok) aborted = true;
-                umma_commit_mask(smem_u32(drain_bar), pair_mask);
+                if (elect_one()) umma_commit_mask(smem_u32(drain_bar), pair_mask);
+                __syncwarp();
             }
-            if (lane == 0) {
-                if (!mbar_wait_cluster(smem_u32(drain_bar), 0, p.limit_ns, nullptr)) {
-                    record_error(p.status, kDevTimeoutDrain, abort_flag);
-                    aborted = true;
-                }
+            if (!mbar_wait_cluster(smem_u32(drain_bar), 0, p.limit_ns, nullptr)) {
+                record_error(p.status, kDevTimeoutDrain, abort_flag);
+                aborted = true;
             }
             __syncwarp();
         } else if (MODE == kLinDw && warp == 2) {
@@ -643,7 +673,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 stage = (stage + nk) % p.stages;
                 if (r >= BK) continue;
                 const uint32_t parity = (used >> s) & 1;
-                ok = mbar_wait_cluster(smem_u32(&tail_bar[s]), parity, p.limit_ns, abort_flag);
+                ok = mbar_wait(smem_u32(&tail_bar[s]), parity, p.limit_ns, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     if (lane == 0) record_error(p.status, kDevTimeoutMma, abort_flag);
@@ -696,33 +726,34 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             if (!ok && lane == 0) record_error(p.status, kDevTimeoutEpilogue, abort_flag);
             dead = true;
         }
+        const int64_t slot_floats = (int64_t)2 * p.ws_cols * CTA_F;  // a slice of the workspace (both CTAs)
+        float* const slices = p.ws + (int64_t)rank * p.ws_cols * CTA_F + q * 32 + lane;
         Walk<MODE> walk(p, off, cum, pair, npairs);
         Item it;
-        float acc[4][32];
+        float acc[CHUNKED ? 2 : 1][32];  // one chunk: blocks come straight from tensor memory
         while (walk.next(it)) {
+            const int turns = accumulators(MODE, it.w);
+            // columns cb .. cb + 31 of the finished accumulator, its turns added in order
+            const auto block_sum = [&](int cb, float(&v)[32]) {
+                const uint32_t t_addr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAX_W + cb);
+                for (int r = 0; r < turns; ++r) {
+                    uint32_t u[32];
+                    tmem_ld_32x32b_x32(t_addr + r * (MAX_W / turns), u);
+                    tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[j][i] = 0.f;
-            for (int kb0 = it.kb0; kb0 < it.kb1 && !dead; kb0 += p.kc) {
-                bool ok = mbar_wait_cluster(smem_u32(&tfull_bar[buf]), buf_phase, p.limit_ns, abort_flag);
+                    for (int i = 0; i < 32; ++i) v[i] = __fadd_rn(v[i], __uint_as_float(u[i]));
+                }
+            };
+            const auto wait_full = [&] {
+                bool ok = dead ? false : mbar_wait(smem_u32(&tfull_bar[buf]), buf_phase, p.limit_ns, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
+                if (!ok && !dead) {
                     if (lane == 0) record_error(p.status, kDevTimeoutEpilogue, abort_flag);
                     dead = true;
-                    break;
                 }
                 tc_fence_after();
-                const uint32_t t_addr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAX_W + half * 32);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if ((2 * j + half) * 32 < it.w) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(t_addr + j * 64, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[j][i] = __fadd_rn(acc[j][i], __uint_as_float(v[i]));
-                    }
+            };
+            const auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
@@ -730,20 +761,48 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     buf = 0;
                     buf_phase ^= 1;
                 }
+            };
+            const bool any = it.kb0 < it.kb1;  // (a group without rows: zeros)
+            if constexpr (CHUNKED) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[j][i] = 0.f;
+                for (int kb0 = it.kb0; kb0 < it.kb1 && !dead; kb0 += p.kc) {
+                    wait_full();
+                    if (dead) break;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if ((2 * j + half) * 32 < it.w) block_sum((2 * j + half) * 32, acc[j]);
+                    release();
+                }
+            } else if (any) {
+                wait_full();
             }
             if (it.part >= 0) {
                 // publish this slice; the CTA that counts last adds the tile's slices in K order
-                const int64_t zs = (int64_t)2 * p.ws_cols * CTA_F;  // floats of a slot (both CTAs)
-                float* base = p.ws + (int64_t)rank * p.ws_cols * CTA_F + q * 32 + lane;
-                if (!dead && in_range(it.slot, 2 * npairs)) {
-                    float* mine = base + it.slot * zs;
+                if (!dead && in_range(walk.slot(it), 2 * npairs)) {
+                    float* mine = slices + walk.slot(it) * slot_floats;
+                    const auto publish = [&](int cb, const float(&v)[32]) {
+                        if (!in_range(min(cb + 32, it.w) - 1, p.ws_cols)) return;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int cb = (2 * j + half) * 32;
-                        if (cb < it.w && in_range(cb + 31, p.ws_cols)) {
+                        for (int i = 0; i < 16; ++i) __stcg(mine + (cb + i) * CTA_F, v[i]);
+                        if (cb + 16 < it.w)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) __stcg(mine + (cb + i) * CTA_F, acc[j][i]);
+                            for (int i = 16; i < 32; ++i) __stcg(mine + (cb + i) * CTA_F, v[i]);
+                    };
+                    if constexpr (CHUNKED) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if ((2 * j + half) * 32 < it.w) publish((2 * j + half) * 32, acc[j]);
+                    } else {
+#pragma unroll 1
+                        for (int cb = half * 32; cb < it.w; cb += 64) {
+                            float v[32] = {};
+                            block_sum(cb, v);
+                            publish(cb, v);
                         }
+                        release();
                     }
                     __threadfence();
                 }
@@ -764,21 +823,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 // (read by every warp before the next item's first barrier lets thread 0 on)
                 if (!last) continue;
                 __threadfence();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int cb = (2 * j + half) * 32;
-                    if (cb < it.w) {
-                        // (every slice, this CTA's own included, is read back)
-                        for (int c = it.c0; c <= it.c1; ++c) {
-                            const float* src = base + walk.slot_of(c, it.part) * zs + cb * CTA_F;
-                            float v[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __ldcg(src + i * CTA_F);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[j][i] = c == it.c0 ? v[i] : __fadd_rn(acc[j][i], v[i]);
-                        }
-                    }
-                }
             }
             // feature of lane 0, and the column of W it comes from
             const int fw = it.f0 * TILE_F + (GATED ? 64 * (int)rank + 32 * (q & 1) : CTA_F * (int)rank + 32 * q);
@@ -803,10 +847,42 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 mr = block(p.R, p.ldr, fw, half * 32 + own, p.vec_r);
                 ahead.load(mr, lane);
             }
-            // (the sums move down a block an iteration, so that one copy of the code below does)
+            // (chunked: the sums move down a block an iteration, so that one copy of the code does)
 #pragma unroll 1
             for (int cb = half * 32; cb < it.w; cb += 64) {
                 float(&v)[32] = acc[0];
+                if (!CHUNKED) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    if (any && it.part < 0 && !dead) {
+                        block_sum(cb, v);
+                        if (cb + 64 >= it.w) release();
+                    }
+                }
+                if (it.part >= 0) {
+                    // every slice, this CTA's own included, is read back, 8 columns of four slices
+                    // at a time so that their latencies overlap, and added in K order
+#pragma unroll
+                    for (int h = 0; h < 32; h += 8) {
+                        if (cb + h >= it.w) break;
+                        for (int c = it.c0; c <= it.c1; c += 4) {
+                            float t[4][8];
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+                                if (c + s <= it.c1) {
+                                    const float* src = slices + walk.slot_of(c + s, it) * slot_floats + (cb + h) * CTA_F;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) t[s][i] = __ldcg(src + i * CTA_F);
+                                }
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+                                if (c + s <= it.c1)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        v[h + i] = c + s == it.c0 ? t[s][i] : __fadd_rn(v[h + i], t[s][i]);
+                        }
+                    }
+                }
                 if (MODE == kLinFwd) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] += bias;
@@ -858,11 +934,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if (MODE == kLinFwd) activate(v, p.act);
                     finish(v);
                 }
+                if constexpr (CHUNKED) {
 #pragma unroll
-                for (int j = 0; j < 3; ++j)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[j][i] = acc[j + 1][i];
+                    for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i];
+                }
             }
+            // (a warp without a block of its own lets go of the accumulator all the same)
+            if (!CHUNKED && any && it.part < 0 && !dead && half * 32 >= it.w) release();
         }
         if (dead) aborted = true;
     }
@@ -897,14 +975,33 @@ bool encode(CUtensorMap* map, int rank, const void* base, bool bf16, int64_t d0,
 }
 
 struct LinPlan {
-    int rows, F, kb, f_tiles, wmax, pairs;
+    int rows, F, kb, f_tiles, wcap, wmax, pairs;
     int bx, b_bytes, stages, smem;
-    bool gated;
+    bool gated, ragged;
     int split_w;  // 0: the last wave is not cut
     int64_t tiles;  // an upper bound when the groups' rows are only known on the device
 };
 
-LinPlan plan(const LinArgs& a, int num_sms)
+// The tile width for `rows` rows: the multiple of 16 whose tiles take least by the estimates
+// above, waves of tiles and a last wave's slices counted (4096 x 4096 outputs: 304 tiles of
+// 224 rows are four whole waves of 76 pairs, 256 tiles of 256 rows are 3.4).
+int choose_width(int rows, int f_tiles, int kb, int pairs, int cap, bool split)
+{
+    int best = 16;
+    double least = 0;
+    for (int c = 16; c <= cap; c += 16) {
+        const int w = tile_width(rows, c);
+        const int64_t tiles = (int64_t)((rows + w - 1) / w) * f_tiles;
+        const int rem = (int)(tiles % pairs);
+        const int len = split ? slice_len(rem, kb, pairs, w) : kb;
+        double t = (double)(tiles / pairs) * kb * kb_cycles(w) + 1500 + 30 * w;
+        if (rem > 0) t += (double)len * kb_cycles(w) + (len < kb ? split_cycles(w) : 0);
+        if (c == 16 || t < least) least = t, best = w;
+    }
+    return best;
+}
+
+LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
 {
     LinPlan pl;
     pl.gated = a.mode == kLinFwd && a.act == GEMM_ACT_SWIGLU;
@@ -915,9 +1012,13 @@ LinPlan plan(const LinArgs& a, int num_sms)
     const int tile_f = pl.gated ? CTA_F : 2 * CTA_F;
     pl.f_tiles = (pl.F + tile_f - 1) / tile_f;
     const int G = a.G > 0 ? a.G : 1;
-    const bool ragged = a.G > 0 && a.mode != kLinDw;  // the tiles' widths are known on the device only
-    pl.wmax = ragged ? (int)(a.M < MAX_W ? (a.M + 15) / 16 * 16 : MAX_W) : tile_width(pl.rows);
-    int64_t row_tiles = (pl.rows + MAX_W - 1) / MAX_W;
+    const bool ragged = pl.ragged = a.G > 0 && a.mode != kLinDw;  // the tiles' widths are known on the device only
+    const int cap = chunked ? MAX_W_CHUNKED : MAX_W;
+    pl.pairs = num_sms / 2;
+    pl.wcap = ragged ? cap : choose_width(pl.rows, pl.f_tiles * (a.mode == kLinDw ? G : 1), pl.kb, pl.pairs, cap,
+                                          a.mode != kLinDw || a.G == 0);
+    pl.wmax = ragged ? (int)(a.M < cap ? (a.M + 15) / 16 * 16 : cap) : pl.wcap;
+    int64_t row_tiles = (pl.rows + pl.wcap - 1) / pl.wcap;
     if (ragged) row_tiles += a.G < a.M ? a.G : a.M;
     pl.tiles = row_tiles * pl.f_tiles * (a.mode == kLinDw ? G : 1);
     // rows of a TMA box of the K-major B operand: a whole half tile where its height is
@@ -941,18 +1042,17 @@ LinPlan plan(const LinArgs& a, int num_sms)
         const int64_t mean = (a.M + a.G - 1) / a.G;
         if (mean < pl.wmax) pl.split_w = (int)((mean + 15) / 16 * 16);
     }
-    pl.pairs = num_sms / 2;
     return pl;
 }
 
 // The kernel of one instantiation and the clusters of it that can be resident at once
 // (cached per process: every device a process drives is taken to be the same part).
-template <int MODE, bool GATED, bool BF16>
+template <int MODE, bool GATED, bool BF16, bool CHUNKED>
 int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p, int num_sms,
                   cudaStream_t stream)
 {
     static std::atomic<int> fit{0};
-    auto kern = linear_pair_kernel<MODE, GATED, BF16>;
+    auto kern = linear_pair_kernel<MODE, GATED, BF16, CHUNKED>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess)
         return GEMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -960,11 +1060,14 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.dynamicSmemBytes = SMEM_MAX;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    // set-up (barriers, tensor memory, descriptors) overlaps the end of the kernel before
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int clusters = fit.load();
@@ -979,29 +1082,42 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
         fit.store(clusters);
     }
     if (clusters > num_sms / 2) clusters = num_sms / 2;
-    if (p.split_w == 0 && pl.tiles < clusters) clusters = (int)pl.tiles;
+    // pairs with nothing to do are not launched (where the host knows the tiles)
+    if (pl.tiles < clusters) {
+        const int len = slice_len((int)pl.tiles, pl.kb, clusters, p.split_w);
+        if (p.split_w == 0 || (!pl.ragged && len >= pl.kb)) clusters = (int)pl.tiles;
+    }
     cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.numAttrs = 2;
     cfg.dynamicSmemBytes = pl.smem;
     return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, p) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-template <bool BF16>
+template <bool BF16, bool CHUNKED>
 int launch_typed(int mode, const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p,
                  int num_sms, cudaStream_t s)
 {
-    if (mode == kLinDx) return launch_kernel<kLinDx, false, BF16>(pl, tmA, tmB, p, num_sms, s);
-    if (mode == kLinDw) return launch_kernel<kLinDw, false, BF16>(pl, tmA, tmB, p, num_sms, s);
-    if (pl.gated) return launch_kernel<kLinFwd, true, BF16>(pl, tmA, tmB, p, num_sms, s);
-    return launch_kernel<kLinFwd, false, BF16>(pl, tmA, tmB, p, num_sms, s);
+    if (mode == kLinDx) return launch_kernel<kLinDx, false, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
+    if (mode == kLinDw) return launch_kernel<kLinDw, false, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
+    if (pl.gated) return launch_kernel<kLinFwd, true, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
+    return launch_kernel<kLinFwd, false, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
 }
 
 }  // namespace
 
-size_t linear_partials_bytes(const LinArgs& a, int num_sms)
+namespace {
+bool is_chunked(const LinArgs& a, int kc)
 {
-    const LinPlan pl = plan(a, num_sms);
+    const int64_t red = a.mode == kLinFwd ? a.K : a.mode == kLinDx ? a.Nw : a.M;
+    return a.out_f32 || kc > 0 || red > (int64_t)MAX_KB_WHOLE * BK;
+}
+}  // namespace
+
+size_t linear_partials_bytes(const LinArgs& a, int num_sms, int kc)
+{
+    const LinPlan pl = plan(a, num_sms, is_chunked(a, kc));
     if (pl.split_w == 0) return 0;
-    return (size_t)2 * pl.pairs * 2 * CTA_F * ((pl.wmax + 31) / 32 * 32) * sizeof(float);
+    return (size_t)2 * pl.pairs * 2 * CTA_F * pl.wmax * sizeof(float);
 }
 
 int64_t linear_counters(int num_sms) { return num_sms; }  // two a tile of the last wave, fewer tiles than pairs
@@ -1009,7 +1125,8 @@ int64_t linear_counters(int num_sms) { return num_sms; }  // two a tile of the l
 int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* dev_status, uint64_t limit_ns, int kc,
                   int test_stall, cudaStream_t stream, int* launches)
 {
-    const LinPlan pl = plan(a, num_sms);
+    const bool chunked = is_chunked(a, kc);
+    const LinPlan pl = plan(a, num_sms, chunked);
     if (pl.tiles <= 0) return GEMM_OK;
     if (pl.tiles > 0x7fffffffLL || pl.stages < 2) return GEMM_ERR_UNSUPPORTED;
     LinParams p = {};
@@ -1020,10 +1137,11 @@ int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* de
     p.G = a.G > 0 ? a.G : 1;
     p.offsets = a.G > 0 ? a.offsets : nullptr;
     p.f_tiles = pl.f_tiles;
+    p.wcap = pl.wcap;
     p.bx = pl.bx;
     p.b_bytes = pl.b_bytes;
     p.stages = pl.stages;
-    p.kc = kc > 0 ? kc : (a.out_f32 ? 16 : 32);
+    p.kc = kc > 0 ? kc : 16;
     p.split_w = ws.partials && ws.counters ? pl.split_w : 0;
     p.bias = a.bias;
     p.bias_stride = a.Nw;
@@ -1042,7 +1160,7 @@ int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* de
     p.out_f32 = a.out_f32 ? 1 : 0;
     p.ws = ws.partials;
     p.cnt = ws.counters;
-    p.ws_cols = (pl.wmax + 31) / 32 * 32;
+    p.ws_cols = pl.wmax;
     p.status = dev_status;
     p.limit_ns = limit_ns;
     p.test_stall = test_stall;
@@ -1063,8 +1181,9 @@ int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* de
                                     : encode(&tmB, 2, a.dZ, a.bf16, a.Nw, a.M, 1, a.lddz, 0, pl.bx));
         if (!ok) return GEMM_ERR_CUDA;
     }
-    const int rc = a.bf16 ? launch_typed<true>(a.mode, pl, tmA, tmB, p, num_sms, stream)
-                          : launch_typed<false>(a.mode, pl, tmA, tmB, p, num_sms, stream);
+    const auto launch = a.bf16 ? (chunked ? launch_typed<true, true> : launch_typed<true, false>)
+                               : (chunked ? launch_typed<false, true> : launch_typed<false, false>);
+    const int rc = launch(a.mode, pl, tmA, tmB, p, num_sms, stream);
     if (rc == GEMM_OK) *launches += 1;
     return rc;
 }

@@ -476,6 +476,23 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// Programmatic dependent launch: wait until the kernels this one depends on have finished
+// and their writes are visible; let the kernels that depend on this one start their set-up.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(p)::"memory");
+    return p != 0;
+}
+
 // Barrier over `count` threads of this CTA (whole warps), number `id` of the CTA's 16.
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t count)
 {
