@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -261,22 +262,15 @@ def _row_major_2d(t, name):
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None else None
+    return t.data_ptr() if t is not None else 0
 
 
-def _ints(t, name, shape, device):
-    """A contiguous int32 tensor of that shape."""
-    import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError("%s must be a contiguous int32 tensor of shape %s on %s" % (name, tuple(shape), device))
-    return t.data_ptr()
-
-
-def _floats(t, name, shape, device):
-    import torch
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError("%s must be a contiguous float32 tensor of shape %s on %s" % (name, tuple(shape), device))
-    return t.data_ptr()
+# The argument structures packed into a buffer of the handle's (a ctypes structure of twenty
+# fields takes several microseconds to build), and entry points that take their addresses.
+_LINEAR = struct.Struct("@qqqPqPqqPPqPqPqqPiii")
+_LINEAR_GRAD = struct.Struct("@qqqPqPqPqqPqPqPqqPqPiii")
+_raw = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
+_linear_raw, _linear_backward_raw = _raw(("gemm_linear", _lib)), _raw(("gemm_linear_backward", _lib))
 
 
 class Gemm:
@@ -285,6 +279,9 @@ class Gemm:
     def __init__(self, device: int = 0):
         self.device = int(device)
         self.handle = gemm_create(self.device)
+        self._args = ctypes.create_string_buffer(max(_LINEAR.size, _LINEAR_GRAD.size) + 8)
+        self._args_at = ctypes.addressof(self._args)
+        self._dev = None
 
     def close(self):
         if self.handle:
@@ -469,44 +466,53 @@ class Gemm:
     def _new(self, shape, dtype, stream):
         """An output of the call on `stream` (None: the current one)."""
         import torch
-        dev = torch.device("cuda", self.device)
+        if self._dev is None:
+            self._dev = torch.device("cuda", self.device)
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev)):
-            return torch.empty(shape, dtype=dtype, device=dev)
+            return torch.empty(shape, dtype=dtype, device=self._dev)
+        with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=self._dev)):
+            return torch.empty(shape, dtype=dtype, device=self._dev)
 
     def _stream(self, stream):
         if stream is not None:
             return int(stream)
         import torch
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device)
 
-    def _mat(self, t, name, shape, dtype):
+    def _mat(self, t, name, rows, cols, dtype):
         """Leading dimension of a row-major matrix of that shape and type on this device."""
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if tuple(t.shape) != shape:
-            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-        if t.device.type != "cuda" or t.device.index != self.device:
+        if t.shape != (rows, cols):
+            raise ValueError("%s must have shape %s, got %s" % (name, (rows, cols), tuple(t.shape)))
+        if t.get_device() != self.device:
             raise ValueError("%s must be on cuda:%d, got %s" % (name, self.device, t.device))
-        return _row_major_2d(t, name)
+        ld, step = t.stride()
+        if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+            raise ValueError("%s must be row-major (unit column stride), got strides %s" % (name, (ld, step)))
+        return ld if ld > cols else (cols or 1)
+
+    def _flat(self, t, name, shape, dtype):
+        """Address of a contiguous tensor of that shape and type on this device."""
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device:
+            raise ValueError("%s must be a contiguous %s tensor of shape %s on cuda:%d" % (name, dtype, shape, self.device))
+        return t.data_ptr()
 
     def _weights(self, w, K, dtype, offsets):
         """(groups, ldw, w_stride, columns) of w: [K, Nw], or [G, K, Nw] with offsets [G + 1]."""
-        dims = 2 if offsets is None else 3
-        if w.dim() != dims or w.shape[-2] != K:
-            raise ValueError("w must be %s with K = %d, got %s" % ("[K, N]" if dims == 2 else "[G, K, N]", K,
-                                                                  tuple(w.shape)))
-        if dims == 2:
-            return 0, self._mat(w, "w", tuple(w.shape), dtype), 0, w.shape[1]
-        G = w.shape[0]
-        if G == 0:
-            raise ValueError("w has no group")
-        ld = self._mat(w[0], "w", tuple(w.shape[1:]), dtype)
-        if G > 1 and w.stride(0) < 0:
-            raise ValueError("w's group stride must not be negative")
-        _ints(offsets, "offsets", (G + 1,), w.device)
-        return G, ld, w.stride(0), w.shape[2]
+        shape = w.shape
+        if offsets is None:
+            if len(shape) != 2 or shape[0] != K:
+                raise ValueError("w must be [K, N] with K = %d, got %s" % (K, tuple(shape)))
+            return 0, self._mat(w, "w", K, shape[1], dtype), 0, shape[1]
+        if len(shape) != 3 or shape[1] != K or shape[0] == 0:
+            raise ValueError("w must be [G, K, N] with K = %d, got %s" % (K, tuple(shape)))
+        G, _, Nw = shape
+        ld = self._mat(w[0], "w", K, Nw, dtype)
+        stride = w.stride(0)
+        import torch
+        self._flat(offsets, "offsets", (G + 1,), torch.int32)
+        return G, ld, stride, Nw
 
     def _linear(self, x, w, offsets, bias, act, residual, out, out_dtype, save_preact, stream):
         code = ACTIVATIONS[act]
@@ -514,25 +520,29 @@ class Gemm:
             raise ValueError("x must be [M, K]")
         M, K = x.shape
         dt = x.dtype
-        ldx = self._mat(x, "x", (M, K), dt)
+        dcode = _dtype_code(x)
+        ldx = self._mat(x, "x", M, K, dt)
         G, ldw, w_stride, Nw = self._weights(w, K, dt, offsets)
-        gated = code == GEMM_ACT_SWIGLU
-        if gated and Nw % 2:
-            raise ValueError("swiglu needs an even number of columns of w (gate, then up)")
-        N = Nw // 2 if gated else Nw
-        if bias is not None:
-            if bias.dtype != dt or tuple(bias.shape) != ((G, Nw) if G else (Nw,)) or not bias.is_contiguous() or \
-                    bias.device != x.device:
-                raise ValueError("bias must be contiguous %s %s on %s" % (dt, (G, Nw) if G else (Nw,), x.device))
+        if code == GEMM_ACT_SWIGLU:
+            if Nw % 2:
+                raise ValueError("swiglu needs an even number of columns of w (gate, then up)")
+            N = Nw // 2
+        else:
+            N = Nw
+        at_bias = self._flat(bias, "bias", (G, Nw) if G else (Nw,), dt) if bias is not None else 0
         if out is None:
             out = self._new((M, N), out_dtype or (residual.dtype if residual is not None else dt), stream)
-        ldy = self._mat(out, "out", (M, N), out.dtype)
-        ldr = self._mat(residual, "residual", (M, N), out.dtype) if residual is not None else 0
+            ldy = N
+        else:
+            ldy = self._mat(out, "out", M, N, out.dtype)
+        ycode = dcode if out.dtype is dt else _dtype_code(out)
+        ldr = at_r = 0
+        if residual is not None:
+            ldr, at_r = self._mat(residual, "residual", M, N, out.dtype), residual.data_ptr()
         z = self._new((M, Nw), dt, stream) if save_preact else None
-        a = LinearArgs(M, K, N, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride, _ptr(bias), _ptr(residual), ldr,
-                       _ptr(z), max(Nw, 1), out.data_ptr(), ldy, G, _ptr(offsets), _dtype_code(x), _dtype_code(out),
-                       code)
-        rc = _lib.gemm_linear(self.handle, a, self._stream(stream))
+        _LINEAR.pack_into(self._args, 0, M, K, N, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride, at_bias, at_r, ldr,
+                          _ptr(z), Nw, out.data_ptr(), ldy, G, _ptr(offsets), dcode, ycode, code)
+        rc = _linear_raw(self.handle, self._args_at, self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "gemm_linear")
         return (out, z) if save_preact else out
@@ -555,31 +565,34 @@ class Gemm:
         return self._linear(x, w, offsets, bias, act, residual, out, out_dtype, save_preact, stream)
 
     def _linear_backward(self, dy, x, w, offsets, z, act, bias, need_dx, need_dw, dw_dtype, stream):
+        import torch
         code = ACTIVATIONS[act]
         if x.dim() != 2:
             raise ValueError("x must be [M, K]")
         M, K = x.shape
         dt = x.dtype
-        ldx = self._mat(x, "x", (M, K), dt)
+        dcode = _dtype_code(x)
+        ldx = self._mat(x, "x", M, K, dt)
         G, ldw, w_stride, Nw = self._weights(w, K, dt, offsets)
-        gated = code == GEMM_ACT_SWIGLU
-        if gated and Nw % 2:
-            raise ValueError("swiglu needs an even number of columns of w (gate, then up)")
-        N = Nw // 2 if gated else Nw
-        lddy = self._mat(dy, "dy", (M, N), dt)
-        if code == GEMM_ACT_NONE:
-            z = None
-        elif z is None:
-            raise ValueError("act %r needs z, the activation's input" % act)
-        ldz = self._mat(z, "z", (M, Nw), dt) if z is not None else 0
-        import torch
+        if code == GEMM_ACT_SWIGLU:
+            if Nw % 2:
+                raise ValueError("swiglu needs an even number of columns of w (gate, then up)")
+            N = Nw // 2
+        else:
+            N = Nw
+        lddy = self._mat(dy, "dy", M, N, dt)
+        ldz = at_z = 0
+        if code != GEMM_ACT_NONE:
+            if z is None:
+                raise ValueError("act %r needs z, the activation's input" % act)
+            ldz, at_z = self._mat(z, "z", M, Nw, dt), z.data_ptr()
         dx = self._new((M, K), dt, stream) if need_dx else None
-        dw = self._new(tuple(w.shape), dw_dtype or dt, stream) if need_dw else None
+        dw = self._new(w.shape, dw_dtype or dt, stream) if need_dw else None
         db = self._new((G, Nw) if G else (Nw,), torch.float32, stream) if bias else None
-        a = LinearGradArgs(M, K, N, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride, _ptr(z), ldz,
-                           _ptr(dx), max(K, 1), _ptr(dw), max(Nw, 1), K * Nw, _ptr(db), G, _ptr(offsets),
-                           _dtype_code(x), _dtype_code(dw) if need_dw else _dtype_code(x), code)
-        rc = _lib.gemm_linear_backward(self.handle, a, self._stream(stream))
+        _LINEAR_GRAD.pack_into(self._args, 0, M, K, N, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, w_stride,
+                               at_z, ldz, _ptr(dx), K, _ptr(dw), Nw, K * Nw, _ptr(db), G, _ptr(offsets), dcode,
+                               _dtype_code(dw) if need_dw else dcode, code)
+        rc = _linear_backward_raw(self.handle, self._args_at, self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "gemm_linear_backward")
         return dx, dw, db
@@ -606,34 +619,39 @@ class Gemm:
             raise ValueError("logits must be [T, E]")
         T, E = logits.shape
         k = int(k)
-        ld = self._mat(logits, "logits", (T, E), logits.dtype)
+        dcode = _dtype_code(logits)
+        ld = self._mat(logits, "logits", T, E, logits.dtype)
         if not 1 <= k <= E:
             raise ValueError("k must be between 1 and the number of experts")
         weights = self._new((T, k), torch.float32, stream)
         # one allocation for the whole numbers: experts, slots, rows, offsets
         n = T * k
         ints = self._new((3 * n + E + 1,), torch.int32, stream)
-        r = Routing(weights, ints[:n].view(T, k), ints[n:2 * n].view(T, k), ints[2 * n:3 * n], ints[3 * n:])
+        experts, slots, rows, offsets = ints.split_with_sizes((n, n, n, E + 1))
         at = ints.data_ptr()
-        rc = _lib.moe_route(self.handle, T, E, k, logits.data_ptr(), ld, _dtype_code(logits), 1 if renormalize else 0,
+        rc = _lib.moe_route(self.handle, T, E, k, logits.data_ptr(), ld, dcode, 1 if renormalize else 0,
                             weights.data_ptr(), at, at + 4 * n, at + 8 * n, at + 12 * n, self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "moe_route")
-        return r
+        return Routing(weights, experts.view(T, k), slots.view(T, k), rows, offsets)
 
     def moe_route_backward(self, dweights, logits, experts, renormalize=True, out=None, stream=None):
         """The gradient of the logits for the gradient dweights [T, k] of Routing.weights."""
+        import torch
         if logits.dim() != 2 or experts.dim() != 2:
             raise ValueError("logits must be [T, E] and experts [T, k]")
         T, E = logits.shape
         k = experts.shape[1]
-        ld = self._mat(logits, "logits", (T, E), logits.dtype)
+        dt = logits.dtype
+        dcode = _dtype_code(logits)
+        ld = self._mat(logits, "logits", T, E, dt)
         if out is None:
-            out = self._new((T, E), logits.dtype, stream)
-        rc = _lib.moe_route_backward(self.handle, T, E, k, _floats(dweights, "dweights", (T, k), logits.device),
-                                     logits.data_ptr(), ld, _dtype_code(logits),
-                                     _ints(experts, "experts", (T, k), logits.device), 1 if renormalize else 0,
-                                     out.data_ptr(), self._mat(out, "out", (T, E), logits.dtype), self._stream(stream))
+            out, ldo = self._new((T, E), dt, stream), E
+        else:
+            ldo = self._mat(out, "out", T, E, dt)
+        rc = _lib.moe_route_backward(self.handle, T, E, k, self._flat(dweights, "dweights", (T, k), torch.float32),
+                                     logits.data_ptr(), ld, dcode, self._flat(experts, "experts", (T, k), torch.int32),
+                                     1 if renormalize else 0, out.data_ptr(), ldo, self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "moe_route_backward")
         return out
@@ -641,35 +659,46 @@ class Gemm:
     def moe_dispatch(self, x, rows, k, out=None, stream=None):
         """x [T, N] in the experts' order: [T * k, N], zeros where rows is -1.  Its gradient is
         moe_combine of the rows' gradients without weights."""
+        import torch
         if x.dim() != 2:
             raise ValueError("x must be [T, N]")
         T, N = x.shape
         k = int(k)
-        ldx = self._mat(x, "x", (T, N), x.dtype)
+        dt = x.dtype
+        dcode = _dtype_code(x)
+        ldx = self._mat(x, "x", T, N, dt)
+        at_rows = self._flat(rows, "rows", (T * k,), torch.int32)
         if out is None:
-            out = self._new((T * k, N), x.dtype, stream)
-        rc = _lib.moe_dispatch(self.handle, T, N, k, x.data_ptr(), ldx, _dtype_code(x),
-                               _ints(rows, "rows", (T * k,), x.device), out.data_ptr(),
-                               self._mat(out, "out", (T * k, N), x.dtype), self._stream(stream))
+            out, ldo = self._new((T * k, N), dt, stream), N
+        else:
+            ldo = self._mat(out, "out", T * k, N, dt)
+        rc = _lib.moe_dispatch(self.handle, T, N, k, x.data_ptr(), ldx, dcode, at_rows, out.data_ptr(), ldo,
+                               self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "moe_dispatch")
         return out
 
     def moe_combine(self, y, slots, weights=None, residual=None, out=None, stream=None):
         """sum over j of weights[t, j] * y[slots[t, j]] + residual[t]: [T, N].  weights None: ones."""
+        import torch
         if y.dim() != 2 or slots.dim() != 2:
             raise ValueError("y must be [rows, N] and slots [T, k]")
         T, k = slots.shape
         R, N = y.shape
-        ldy = self._mat(y, "y", (R, N), y.dtype)
+        dt = y.dtype
+        dcode = _dtype_code(y)
+        ldy = self._mat(y, "y", R, N, dt)
         if out is None:
-            out = self._new((T, N), y.dtype, stream)
-        ldo = self._mat(out, "out", (T, N), y.dtype)
-        ldr = self._mat(residual, "residual", (T, N), y.dtype) if residual is not None else 0
-        rc = _lib.moe_combine(self.handle, T, N, k, y.data_ptr(), ldy, R, _dtype_code(y),
-                              _ints(slots, "slots", (T, k), y.device),
-                              _floats(weights, "weights", (T, k), y.device) if weights is not None else None,
-                              _ptr(residual), ldr, out.data_ptr(), ldo, self._stream(stream))
+            out, ldo = self._new((T, N), dt, stream), N
+        else:
+            ldo = self._mat(out, "out", T, N, dt)
+        at_w = self._flat(weights, "weights", (T, k), torch.float32) if weights is not None else 0
+        ldr = at_r = 0
+        if residual is not None:
+            ldr, at_r = self._mat(residual, "residual", T, N, dt), residual.data_ptr()
+        rc = _lib.moe_combine(self.handle, T, N, k, y.data_ptr(), ldy, R, dcode,
+                              self._flat(slots, "slots", (T, k), torch.int32), at_w, at_r, ldr, out.data_ptr(), ldo,
+                              self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "moe_combine")
         return out
@@ -681,15 +710,17 @@ class Gemm:
             raise ValueError("dout must be [T, N] and slots [T, k]")
         T, N = dout.shape
         k = slots.shape[1]
-        lddo = self._mat(dout, "dout", (T, N), dout.dtype)
-        ldy = self._mat(y, "y", (T * k, N), dout.dtype)
-        dev = dout.device
-        dy = self._new((T * k, N), dout.dtype, stream)
+        dt = dout.dtype
+        dcode = _dtype_code(dout)
+        lddo = self._mat(dout, "dout", T, N, dt)
+        ldy = self._mat(y, "y", T * k, N, dt)
+        at_slots = self._flat(slots, "slots", (T, k), torch.int32)
+        at_rows = self._flat(rows, "rows", (T * k,), torch.int32)
+        at_w = self._flat(weights, "weights", (T, k), torch.float32)
+        dy = self._new((T * k, N), dt, stream)
         dweights = self._new((T, k), torch.float32, stream)
-        rc = _lib.moe_combine_backward(self.handle, T, N, k, dout.data_ptr(), lddo, y.data_ptr(), ldy,
-                                       _dtype_code(dout), _ints(slots, "slots", (T, k), dev),
-                                       _ints(rows, "rows", (T * k,), dev), _floats(weights, "weights", (T, k), dev),
-                                       dy.data_ptr(), max(N, 1), dweights.data_ptr(), self._stream(stream))
+        rc = _lib.moe_combine_backward(self.handle, T, N, k, dout.data_ptr(), lddo, y.data_ptr(), ldy, dcode, at_slots,
+                                       at_rows, at_w, dy.data_ptr(), N, dweights.data_ptr(), self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "moe_combine_backward")
         return dy, dweights

@@ -27,11 +27,10 @@
 // epilogue, which takes its sums straight from TMEM, overlaps the whole next tile.
 //
 // Work: tiles are walked round robin by the persistent pairs.  The tiles of the last,
-// partial wave (all tiles, when there are fewer than pairs) are cut along K into equal
-// lengths of k-blocks, one a pair: a pair's range covers parts of at most two tiles.  Every
-// part goes to the workspace in fp32; the CTA that counts last adds the parts of its tile in
-// K order and runs the epilogue.  Nothing waits for another CTA, and the order of the sum
-// does not depend on who is last.
+// partial wave (all tiles, when there are fewer than pairs) may be cut along K into slices,
+// one a pair.  Every slice goes to the workspace in fp32; the CTA that counts last adds the
+// slices of its tile in K order and runs the epilogue.  Nothing waits for another CTA, and
+// the order of the sum does not depend on who is last.
 //
 // kLinDw over groups: a group's last k-block ends inside the next group's rows.  Those rows
 // are zeroed in shared memory, in both operands (zero times a neighbour's NaN would be NaN),
@@ -74,11 +73,11 @@ constexpr int STG_BYTES = 2048;       // an epilogue warp's staging block: 32 ro
 constexpr int SMEM_MAX = 232448;      // 227 KiB
 
 // Warps 0..3: producer of A, MMA issuer, fixer, producer of B; 4..11: epilogue, which takes
-// registers from the first four: 104 + 2 * 200 a thread of the three warpgroups is within
+// registers from the first four: 80 + 2 * 208 a thread of the three warpgroups is within
 // the 3 * 168 the block is launched with (checked before the launch).
 constexpr int EPI_WARP0 = 4;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-constexpr int LAUNCH_REGS = 168, LEAN_REGS = 104, EPI_REGS = 200;
+constexpr int LAUNCH_REGS = 168, LEAN_REGS = 80, EPI_REGS = 208;
 static_assert(LEAN_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "the epilogue's registers come from the block's own");
 
 struct LinParams {
@@ -128,49 +127,49 @@ __host__ __device__ inline int tile_width(int rows, int wcap)
     return (int)((w + 15) / 16 * 16);
 }
 
-// Estimated cycles: a k-block of a tile of w rows (its MMAs, or the 16 KiB of A that an SM
-// loads for it), and what cutting a tile along K costs (its slices' publication, the
-// addition and their latencies).
-__host__ __device__ inline int kb_cycles(int w) { return w < 150 ? 300 : 2 * w; }
-__host__ __device__ inline int split_cycles(int w) { return 4000 + 40 * w; }
+// Estimated cycles, from measurements: a k-block of a tile of w rows (its MMAs, or the issue
+// of its copies), and what cutting a tile into S slices along K costs (their publication,
+// the addition and its latencies: 3.6 us for 9 slices of 16 rows, 6.6 us for 2 of 64, 20 us
+// for 2 of 256).
+__host__ __device__ inline int kb_cycles(int w) { return w < 212 ? 425 : 2 * w; }
+__host__ __device__ inline int split_cycles(int S, int w) { return S > 1 ? 4900 + w * (78 + 24 * S) : 0; }
 
-// k-blocks a pair takes of the last wave's `rem` tiles of kb k-blocks each (kb: whole
-// tiles), where that is worth its cost.
-__host__ __device__ inline int slice_len(int rem, int kb, int pairs, int w)
+// K slices of each of the last wave's `rem` tiles of kb k-blocks (1: whole): at most one
+// slice a pair, about as many as balance their addition with the k-blocks saved, and none
+// that costs more than it saves.
+__host__ __device__ inline int slices(int rem, int kb, int pairs, int w)
 {
-    if (rem <= 0 || w <= 0) return kb;
-    int len = (int)(((uint32_t)rem * (uint32_t)kb + pairs - 1) / (uint32_t)pairs);
-    if (len < 2) len = 2;
-    return (int64_t)(kb - len) * kb_cycles(w) <= split_cycles(w) ? kb : len;
+    if (rem <= 0 || w <= 0) return 1;
+    int S = pairs / rem;
+    const int balanced = (int)sqrtf((float)kb * kb_cycles(w) / (24.f * w));
+    if (S > balanced) S = balanced;
+    if (S > kb / 2) S = kb / 2;
+    if (S < 2 || (kb - (kb + S - 1) / S) * (int64_t)kb_cycles(w) <= split_cycles(S, w)) return 1;
+    return S;
 }
 
 struct Item {
     int g, row0, valid, w, f0;  // group, first row, rows to store, tile width, first feature
     int kb0, kb1;               // k-blocks
     int red0, red_rows;         // kLinDw: first reduced row of the group, its rows
-    int part, c0, c1;           // slice: index among the last wave's tiles, its first and last pair; part -1: whole
-    bool second;                // slice: the first pair's part is the second of its range
+    int part, slot0;            // slice: index among the last wave's tiles (-1: whole), the first slice's place
 };
 
 // The work items of one pair, in the order every role of the kernel walks them.  (All in 32
-// bits: the last wave's k-blocks are fewer than pairs * 2^25, and a 64-bit division takes
-// hundreds of cycles.)
+// bits: a 64-bit division takes hundreds of cycles.)
 template <int MODE>
 class Walk {
   public:
     __device__ Walk(const LinParams& p, const int* off, const int* cum, int pair, int pairs)
-        : p_(p), off_(off), cum_(cum), pairs_(pairs), pair_(pair), t_(pair), g_(0)
+        : p_(p), off_(off), cum_(cum), pairs_(pairs), t_(pair), g_(0), tail_(-1)
     {
         const int total = cum[p.G];
         const int rem = total % pairs;
-        len_ = slice_len(rem, p.kb, pairs, p.split_w);
         whole_ = total;
-        lo_ = hi_ = 0;
-        if (len_ < p.kb) {
+        S_ = slices(rem, p.kb, pairs, p.split_w);
+        if (S_ > 1) {
             whole_ = total - rem;
-            const uint32_t all = (uint32_t)rem * p.kb, start = (uint32_t)pair * len_;
-            lo_ = min(start, all);
-            hi_ = min(start + len_, all);
+            if (pair < rem * S_) tail_ = pair;
         }
     }
 
@@ -182,19 +181,15 @@ class Walk {
             tile = t_;
             t_ += pairs_;
             it.kb0 = 0, it.kb1 = p_.kb;
-        } else if (lo_ < hi_) {
-            const uint32_t j = lo_ / p_.kb, tile_lo = j * p_.kb;
-            it.kb0 = (int)(lo_ - tile_lo);
-            it.kb1 = (int)min((uint32_t)p_.kb, it.kb0 + (hi_ - lo_));
-            if (it.kb1 - it.kb0 < p_.kb) {
-                it.part = (int)j;
-                it.c0 = (int)(tile_lo / len_);
-                it.c1 = (int)((tile_lo + p_.kb - 1) / len_);
-                // a tile's first pair may have begun in the tile before: this is its second part
-                it.second = (uint32_t)it.c0 * len_ < tile_lo;
-            }
+        } else if (tail_ >= 0) {
+            const unsigned j = (unsigned)tail_ / (unsigned)S_, sl = tail_ - j * S_;
+            it.part = (int)j;
+            it.slot0 = (int)j * S_;
+            it.kb0 = (int)(sl * (unsigned)p_.kb / (unsigned)S_);
+            it.kb1 = (int)((sl + 1) * (unsigned)p_.kb / (unsigned)S_);
             tile = whole_ + (int)j;
-            lo_ += it.kb1 - it.kb0;
+            slot_ = tail_;
+            tail_ = -1;
         } else {
             return false;
         }
@@ -221,16 +216,14 @@ class Walk {
         return true;
     }
 
-    // Workspace slot of pair c's slice of the item's tile.
-    __device__ static int slot_of(int c, const Item& it) { return 2 * c + (c == it.c0 && it.second ? 1 : 0); }
-    __device__ int slot(const Item& it) const { return slot_of(pair_, it); }
+    __device__ int slices_of_tile() const { return S_; }
+    __device__ int slot() const { return slot_; }  // this slice's place in the workspace
 
   private:
     const LinParams& p_;
     const int* off_;
     const int* cum_;
-    int pairs_, pair_, t_, g_, whole_, len_;
-    uint32_t lo_, hi_;
+    int pairs_, t_, g_, whole_, S_, tail_, slot_ = 0;
 };
 
 __device__ __forceinline__ void record_error(int* status, int code, volatile int* abort_flag)
@@ -266,7 +259,10 @@ __device__ __forceinline__ void activate(float (&v)[N], int act)
         break;
     case GEMM_ACT_GELU:
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+        for (int i = 0; i < N; ++i) {
+            v[i] = 0.5f * v[i] * (1.f + erff(v[i] * 0.70710678118654752f));
+            if (i % 4 == 3) asm volatile("" ::: "memory");  // (not all at once: registers)
+        }
         break;
     case GEMM_ACT_GELU_TANH:
         // 0.5 (1 + tanh u) = 1 / (1 + e^-2u)
@@ -365,7 +361,7 @@ __device__ __forceinline__ void store_block(const Matrix16& m, uint32_t* stg, in
     __syncwarp();
 }
 
-// The residual's block, loaded ahead of its use: rows 2 pr and 2 pr + 1 of each lane's
+// The residual's block as it is loaded, ahead of its use: rows 2 pr and 2 pr + 1 of each lane's
 // eight features.
 template <int N>
 struct Ahead {
@@ -522,7 +518,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             // ---------------------------------------------------------------- producers
             // warp 0 loads A (and announces a stage's bytes), warp 3 loads B: one thread issuing
             // all of a stage's copies was what the MMAs waited for
-            if (lane == 0) {
+            // (whole warps walk and one elected lane issues, as the MMA warp)
+            {
                 Walk<MODE> walk(p, off, cum, pair, npairs);
                 Item it;
                 int stage = 0;
@@ -542,7 +539,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
                     const int fa2 = GATED ? p.F + fa : fa + 64;
                     for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                        if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag)) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
                             record_error(p.status, kDevTimeoutProducer, abort_flag);
                             ok = false;
                             break;
@@ -553,30 +550,33 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                         // released at cluster scope, took the kernel from 0.71 to 1.66 ms at 8192^3)
                         const uint32_t bar = (tail ? tail_own : full0) + stage * 8;
                         const int k = (MODE == kLinDw ? it.red0 : 0) + kb * BK;
-                        if (load_a) {
-                            if (tail) mbar_arrive_expect_tx(smem_u32(&tail_bar[stage]), bytes);
-                            else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
-                            const uint32_t dst = a_base + stage * A_BYTES;
-                            if (MODE == kLinFwd) {
-                                tma_load_3d_pair(dst, &tmA, bar, fa, k, it.g);
-                                tma_load_3d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k, it.g);
-                            } else if (MODE == kLinDx) {
-                                tma_load_3d_pair(dst, &tmA, bar, k, fa, it.g);
+                        if (elect_one()) {
+                            if (load_a) {
+                                if (tail) mbar_arrive_expect_tx(smem_u32(&tail_bar[stage]), bytes);
+                                else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
+                                const uint32_t dst = a_base + stage * A_BYTES;
+                                if (MODE == kLinFwd) {
+                                    tma_load_3d_pair(dst, &tmA, bar, fa, k, it.g);
+                                    tma_load_3d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k, it.g);
+                                } else if (MODE == kLinDx) {
+                                    tma_load_3d_pair(dst, &tmA, bar, k, fa, it.g);
+                                } else {
+                                    tma_load_2d_pair(dst, &tmA, bar, fa, k);
+                                    tma_load_2d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k);
+                                }
                             } else {
-                                tma_load_2d_pair(dst, &tmA, bar, fa, k);
-                                tma_load_2d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k);
-                            }
-                        } else {
-                            const uint32_t dst = b_base + stage * p.b_bytes;
-                            if (B_MN) {
-                                tma_load_2d_pair(dst, &tmB, bar, b_row, k);
-                                if (nb > 1) tma_load_2d_pair(dst + BOX_BYTES, &tmB, bar, b_row + 64, k);
-                            } else {
-                                tma_load_2d_pair(dst, &tmB, bar, k, b_row);
-                                for (int i = 1; i < nb; ++i)
-                                    tma_load_2d_pair(dst + i * b_box, &tmB, bar, k, b_row + i * p.bx);
+                                const uint32_t dst = b_base + stage * p.b_bytes;
+                                if (B_MN) {
+                                    tma_load_2d_pair(dst, &tmB, bar, b_row, k);
+                                    if (nb > 1) tma_load_2d_pair(dst + BOX_BYTES, &tmB, bar, b_row + 64, k);
+                                } else {
+                                    tma_load_2d_pair(dst, &tmB, bar, k, b_row);
+                                    for (int i = 1; i < nb; ++i)
+                                        tma_load_2d_pair(dst + i * b_box, &tmB, bar, k, b_row + i * p.bx);
+                                }
                             }
                         }
+                        __syncwarp();
                         if (++stage == p.stages) {
                             stage = 0;
                             phase ^= 1;
@@ -712,7 +712,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3;             // TMEM lane quarter
-        const int half = (warp - EPI_WARP0) >> 2;   // takes 32-column blocks half, half + 2, ...
+        const int half = (warp - EPI_WARP0) >> 2;   // takes column blocks half, half + 2, ...
         const int e = threadIdx.x - 32 * EPI_WARP0;
         uint32_t* stg = reinterpret_cast<uint32_t*>(after + (warp - EPI_WARP0) * STG_BYTES);
         int buf = 0;
@@ -727,12 +727,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             dead = true;
         }
         const int64_t slot_floats = (int64_t)2 * p.ws_cols * CTA_F;  // a slice of the workspace (both CTAs)
-        float* const slices = p.ws + (int64_t)rank * p.ws_cols * CTA_F + q * 32 + lane;
+        float* const parts = p.ws + (int64_t)rank * p.ws_cols * CTA_F + q * 32 + lane;
         Walk<MODE> walk(p, off, cum, pair, npairs);
         Item it;
         float acc[CHUNKED ? 2 : 1][32];  // one chunk: blocks come straight from tensor memory
         while (walk.next(it)) {
             const int turns = accumulators(MODE, it.w);
+            // columns of a warp's block: up to 32 rows are shared by both halves of the warps
+            const int bw = it.w <= 16 ? 8 : it.w <= 32 ? 16 : 32, cb0 = half * bw;
             // columns cb .. cb + 31 of the finished accumulator, its turns added in order
             const auto block_sum = [&](int cb, float(&v)[32]) {
                 const uint32_t t_addr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAX_W + cb);
@@ -773,7 +775,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if (dead) break;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if ((2 * j + half) * 32 < it.w) block_sum((2 * j + half) * 32, acc[j]);
+                        if (cb0 + 2 * j * bw < it.w) block_sum(cb0 + 2 * j * bw, acc[j]);
                     release();
                 }
             } else if (any) {
@@ -781,23 +783,24 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             }
             if (it.part >= 0) {
                 // publish this slice; the CTA that counts last adds the tile's slices in K order
-                if (!dead && in_range(walk.slot(it), 2 * npairs)) {
-                    float* mine = slices + walk.slot(it) * slot_floats;
+                if (!dead && in_range(walk.slot(), npairs)) {
+                    float* mine = parts + walk.slot() * slot_floats;
                     const auto publish = [&](int cb, const float(&v)[32]) {
-                        if (!in_range(min(cb + 32, it.w) - 1, p.ws_cols)) return;
+                        const int n = min(bw, it.w - cb);
+                        if (!in_range(cb + n - 1, p.ws_cols)) return;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) __stcg(mine + (cb + i) * CTA_F, v[i]);
-                        if (cb + 16 < it.w)
+                        for (int i = 0; i < 32; i += 8)
+                            if (i < n)
 #pragma unroll
-                            for (int i = 16; i < 32; ++i) __stcg(mine + (cb + i) * CTA_F, v[i]);
+                                for (int k = 0; k < 8; ++k) __stcg(mine + (cb + i + k) * CTA_F, v[i + k]);
                     };
                     if constexpr (CHUNKED) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            if ((2 * j + half) * 32 < it.w) publish((2 * j + half) * 32, acc[j]);
+                            if (cb0 + 2 * j * bw < it.w) publish(cb0 + 2 * j * bw, acc[j]);
                     } else {
 #pragma unroll 1
-                        for (int cb = half * 32; cb < it.w; cb += 64) {
+                        for (int cb = cb0; cb < it.w; cb += 2 * bw) {
                             float v[32] = {};
                             block_sum(cb, v);
                             publish(cb, v);
@@ -812,7 +815,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     int last = 0;
                     if (!*abort_flag) {
                         unsigned* c = p.cnt + 2 * it.part + rank;
-                        last = atomicAdd(c, 1u) == (unsigned)(it.c1 - it.c0);
+                        last = atomicAdd(c, 1u) == (unsigned)(walk.slices_of_tile() - 1);
                         if (last) *c = 0;  // ready for the next launch
                     }
                     __threadfence();
@@ -837,79 +840,74 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             const bool residual = MODE == kLinFwd && p.R && !p.out_f32;
             Matrix16 mr = {}, mo = {}, mz = {};
             Ahead<OUT_N> ahead;
-            const auto block = [&](const void* base, int64_t ld, int col, int cb, bool vec) {
+            const auto block = [&](const void* base, int64_t ld, int col, int cb, int cb_end, bool vec) {
                 const int64_t row = it.row0 + cb;
-                const int n = it.valid - cb;
+                const int n = min(it.valid, cb_end) - cb;
                 const bool in = n <= 0 || in_range(row + min(n, 32) - 1, p.rows);
                 return Matrix16{static_cast<uint16_t*>(const_cast<void*>(base)) + row * ld + col, ld, in ? n : 0, nf, vec};
             };
-            if (residual) {
-                mr = block(p.R, p.ldr, fw, half * 32 + own, p.vec_r);
-                ahead.load(mr, lane);
-            }
             // (chunked: the sums move down a block an iteration, so that one copy of the code does)
 #pragma unroll 1
-            for (int cb = half * 32; cb < it.w; cb += 64) {
+            for (int cb = cb0; cb < it.w; cb += 2 * bw) {
                 float(&v)[32] = acc[0];
+                // the residual's loads run while the sums are fetched and activated (a slice's
+                // addition needs the registers: after it)
+                if (residual) mr = block(p.R, p.ldr, fw, cb + own, cb + bw, p.vec_r);
+                if (residual && it.part < 0) ahead.load(mr, lane);
                 if (!CHUNKED) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     if (any && it.part < 0 && !dead) {
                         block_sum(cb, v);
-                        if (cb + 64 >= it.w) release();
+                        if (cb + 2 * bw >= it.w) release();
                     }
                 }
                 if (it.part >= 0) {
-                    // every slice, this CTA's own included, is read back, 8 columns of four slices
+                    // every slice, this CTA's own included, is read back, COLS columns of DEEP slices
                     // at a time so that their latencies overlap, and added in K order
+                    constexpr int DEEP = CHUNKED ? 4 : 6, COLS = 8;
+                    const int S = walk.slices_of_tile();
 #pragma unroll
-                    for (int h = 0; h < 32; h += 8) {
-                        if (cb + h >= it.w) break;
-                        for (int c = it.c0; c <= it.c1; c += 4) {
-                            float t[4][8];
+                    for (int h = 0; h < 32; h += COLS) {
+                        if (h >= bw || cb + h >= it.w) break;
+                        for (int c = 0; c < S; c += DEEP) {
+                            float t[DEEP][COLS];
 #pragma unroll
-                            for (int s = 0; s < 4; ++s)
-                                if (c + s <= it.c1) {
-                                    const float* src = slices + walk.slot_of(c + s, it) * slot_floats + (cb + h) * CTA_F;
+                            for (int s = 0; s < DEEP; ++s)
+                                if (c + s < S) {
+                                    const float* src = parts + (it.slot0 + c + s) * slot_floats + (cb + h) * CTA_F;
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) t[s][i] = __ldcg(src + i * CTA_F);
+                                    for (int i = 0; i < COLS; ++i) t[s][i] = __ldcg(src + i * CTA_F);
                                 }
 #pragma unroll
-                            for (int s = 0; s < 4; ++s)
-                                if (c + s <= it.c1)
+                            for (int s = 0; s < DEEP; ++s)
+                                if (c + s < S)
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        v[h + i] = c + s == it.c0 ? t[s][i] : __fadd_rn(v[h + i], t[s][i]);
+                                    for (int i = 0; i < COLS; ++i)
+                                        v[h + i] = c + s == 0 ? t[s][i] : __fadd_rn(v[h + i], t[s][i]);
                         }
                     }
+                    if (residual) ahead.load(mr, lane);
                 }
                 if (MODE == kLinFwd) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] += bias;
                     if (p.Z) {
-                        mz = block(p.Z, p.ldz, zw, cb, p.vec_z);
+                        mz = block(p.Z, p.ldz, zw, cb, cb + bw, p.vec_z);
                         store_block<BF16>(mz, stg, lane, v);
                     }
                 }
                 const auto finish = [&](auto& h) {
-                    if (MODE != kLinDx && p.out_f32) {
+                    if (CHUNKED && MODE != kLinDx && p.out_f32) {
                         const int64_t row = it.row0 + cb + own;
-                        const int n = it.valid - cb - own;
+                        const int n = min(it.valid, cb + bw) - cb - own;
                         if (n <= 0 || !in_range(row + min(n, OUT_N) - 1, p.rows)) return;
                         store_f32(MODE == kLinFwd && p.R ? static_cast<const float*>(p.R) + row * p.ldr + fw + lane : nullptr,
                                   p.ldr, static_cast<float*>(p.out) + out0 + row * p.ldo + fw + lane, p.ldo, n, lane < nf, h);
                         return;
                     }
-                    if (residual) {
-                        const Ahead<OUT_N> now = ahead;
-                        const Matrix16 m = mr;
-                        if (cb + 64 < it.w) {
-                            mr = block(p.R, p.ldr, fw, cb + 64 + own, p.vec_r);
-                            ahead.load(mr, lane);
-                        }
-                        add_block<BF16>(m, now, stg, lane, h);
-                    }
-                    mo = block(static_cast<const uint16_t*>(p.out) + out0, p.ldo, fw, cb + own, p.vec_out);
+                    if (residual) add_block<BF16>(mr, ahead, stg, lane, h);
+                    mo = block(static_cast<const uint16_t*>(p.out) + out0, p.ldo, fw, cb + own, cb + bw, p.vec_out);
                     store_block<BF16>(mo, stg, lane, h);
                 };
                 if constexpr (GATED) {
@@ -940,7 +938,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 }
             }
             // (a warp without a block of its own lets go of the accumulator all the same)
-            if (!CHUNKED && any && it.part < 0 && !dead && half * 32 >= it.w) release();
+            if (!CHUNKED && any && it.part < 0 && !dead && cb0 >= it.w) release();
         }
         if (dead) aborted = true;
     }
@@ -993,9 +991,9 @@ int choose_width(int rows, int f_tiles, int kb, int pairs, int cap, bool split)
         const int w = tile_width(rows, c);
         const int64_t tiles = (int64_t)((rows + w - 1) / w) * f_tiles;
         const int rem = (int)(tiles % pairs);
-        const int len = split ? slice_len(rem, kb, pairs, w) : kb;
-        double t = (double)(tiles / pairs) * kb * kb_cycles(w) + 1500 + 30 * w;
-        if (rem > 0) t += (double)len * kb_cycles(w) + (len < kb ? split_cycles(w) : 0);
+        const int S = split ? slices(rem, kb, pairs, w) : 1;
+        double t = (double)(tiles / pairs) * kb * kb_cycles(w) + 25 * w;  // (and the last epilogue)
+        if (rem > 0) t += (double)((kb + S - 1) / S) * kb_cycles(w) + split_cycles(S, w);
         if (c == 16 || t < least) least = t, best = w;
     }
     return best;
@@ -1015,8 +1013,10 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
     const bool ragged = pl.ragged = a.G > 0 && a.mode != kLinDw;  // the tiles' widths are known on the device only
     const int cap = chunked ? MAX_W_CHUNKED : MAX_W;
     pl.pairs = num_sms / 2;
-    pl.wcap = ragged ? cap : choose_width(pl.rows, pl.f_tiles * (a.mode == kLinDw ? G : 1), pl.kb, pl.pairs, cap,
-                                          a.mode != kLinDw || a.G == 0);
+    pl.wcap = ragged ? cap
+              : a.mode == kLinDw && a.G > 0
+                  ? choose_width(pl.rows, pl.f_tiles * G, (pl.kb + G - 1) / G, pl.pairs, cap, false)
+                  : choose_width(pl.rows, pl.f_tiles, pl.kb, pl.pairs, cap, true);
     pl.wmax = ragged ? (int)(a.M < cap ? (a.M + 15) / 16 * 16 : cap) : pl.wcap;
     int64_t row_tiles = (pl.rows + pl.wcap - 1) / pl.wcap;
     if (ragged) row_tiles += a.G < a.M ? a.G : a.M;
@@ -1084,8 +1084,8 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
     if (clusters > num_sms / 2) clusters = num_sms / 2;
     // pairs with nothing to do are not launched (where the host knows the tiles)
     if (pl.tiles < clusters) {
-        const int len = slice_len((int)pl.tiles, pl.kb, clusters, p.split_w);
-        if (p.split_w == 0 || (!pl.ragged && len >= pl.kb)) clusters = (int)pl.tiles;
+        if (p.split_w == 0) clusters = (int)pl.tiles;
+        else if (!pl.ragged) clusters = (int)pl.tiles * slices((int)pl.tiles, pl.kb, clusters, p.split_w);
     }
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     cfg.numAttrs = 2;
@@ -1117,7 +1117,7 @@ size_t linear_partials_bytes(const LinArgs& a, int num_sms, int kc)
 {
     const LinPlan pl = plan(a, num_sms, is_chunked(a, kc));
     if (pl.split_w == 0) return 0;
-    return (size_t)2 * pl.pairs * 2 * CTA_F * pl.wmax * sizeof(float);
+    return (size_t)pl.pairs * 2 * CTA_F * pl.wmax * sizeof(float);
 }
 
 int64_t linear_counters(int num_sms) { return num_sms; }  // two a tile of the last wave, fewer tiles than pairs
