@@ -624,16 +624,15 @@ class Gemm:
         if not 1 <= k <= E:
             raise ValueError("k must be between 1 and the number of experts")
         weights = self._new((T, k), torch.float32, stream)
-        # one allocation for the whole numbers: experts, slots, rows, offsets
-        n = T * k
-        ints = self._new((3 * n + E + 1,), torch.int32, stream)
-        experts, slots, rows, offsets = ints.split_with_sizes((n, n, n, E + 1))
-        at = ints.data_ptr()
+        i32 = torch.int32
+        r = Routing(weights, self._new((T, k), i32, stream), self._new((T, k), i32, stream),
+                    self._new((T * k,), i32, stream), self._new((E + 1,), i32, stream))
         rc = _lib.moe_route(self.handle, T, E, k, logits.data_ptr(), ld, dcode, 1 if renormalize else 0,
-                            weights.data_ptr(), at, at + 4 * n, at + 8 * n, at + 12 * n, self._stream(stream))
+                            weights.data_ptr(), r.experts.data_ptr(), r.slots.data_ptr(), r.rows.data_ptr(),
+                            r.offsets.data_ptr(), self._stream(stream))
         if rc != GEMM_OK:
             raise GemmError(rc, "moe_route")
-        return Routing(weights, experts.view(T, k), slots.view(T, k), rows, offsets)
+        return r
 
     def moe_route_backward(self, dweights, logits, experts, renormalize=True, out=None, stream=None):
         """The gradient of the logits for the gradient dweights [T, k] of Routing.weights."""

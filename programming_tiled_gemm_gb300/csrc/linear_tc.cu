@@ -119,19 +119,22 @@ __host__ __device__ constexpr int accumulators(int mode, int w)
 }
 
 // The width of `rows` rows' tiles of at most `wcap` (a multiple of 16): equal ones, so that
-// 300 rows are 160 + 140, not 256 + 44.
-__host__ __device__ inline int tile_width(int rows, int wcap)
+// 300 rows are 160 + 140, not 256 + 44.  (kLinDw: wcap itself.  Its rows lie along a line of
+// X, and copies from the middle of 128-byte lines took twice the time: 1.17 ms instead of
+// 0.67 at 8192^3 with 176 rows.)
+__host__ __device__ inline int tile_width(int mode, int rows, int wcap)
 {
+    if (mode == kLinDw) return wcap;
     const unsigned nt = (unsigned)(rows + wcap - 1) / (unsigned)wcap;
     const unsigned w = nt ? ((unsigned)rows + nt - 1) / nt : 16;
     return (int)((w + 15) / 16 * 16);
 }
 
-// Estimated cycles, from measurements: a k-block of a tile of w rows (its MMAs, or the issue
-// of its copies), and what cutting a tile into S slices along K costs (their publication,
+// Estimated cycles, from measurements: a k-block of a tile of w rows (its MMAs and loads, or
+// their issue), and what cutting a tile into S slices along K costs (their publication,
 // the addition and its latencies: 3.6 us for 9 slices of 16 rows, 6.6 us for 2 of 64, 20 us
 // for 2 of 256).
-__host__ __device__ inline int kb_cycles(int w) { return w < 212 ? 425 : 2 * w; }
+__host__ __device__ inline int kb_cycles(int w) { return w < 165 ? 355 : 67 + w * 7 / 4; }
 __host__ __device__ inline int split_cycles(int S, int w) { return S > 1 ? 4900 + w * (78 + 24 * S) : 0; }
 
 // K slices of each of the last wave's `rem` tiles of kb k-blocks (1: whole): at most one
@@ -208,7 +211,7 @@ class Walk {
         const uint32_t rg = local / per;
         const uint32_t m0 = rg * RASTER, m = min(nt - m0, (uint32_t)RASTER);
         const uint32_t r = local - rg * per, ft = r / m;
-        it.w = tile_width(rows, p_.wcap);
+        it.w = tile_width(MODE, rows, p_.wcap);
         const int t0 = (int)(m0 + r - ft * m) * it.w;
         it.row0 = first + t0;
         it.valid = min(it.w, rows - t0);
@@ -846,6 +849,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 const bool in = n <= 0 || in_range(row + min(n, 32) - 1, p.rows);
                 return Matrix16{static_cast<uint16_t*>(const_cast<void*>(base)) + row * ld + col, ld, in ? n : 0, nf, vec};
             };
+            const bool fetch = !CHUNKED && any && it.part < 0 && !dead;
             // (chunked: the sums move down a block an iteration, so that one copy of the code does)
 #pragma unroll 1
             for (int cb = cb0; cb < it.w; cb += 2 * bw) {
@@ -857,7 +861,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 if (!CHUNKED) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                    if (any && it.part < 0 && !dead) {
+                    if (fetch) {
                         block_sum(cb, v);
                         if (cb + 2 * bw >= it.w) release();
                     }
@@ -938,7 +942,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 }
             }
             // (a warp without a block of its own lets go of the accumulator all the same)
-            if (!CHUNKED && any && it.part < 0 && !dead && cb0 >= it.w) release();
+            if (fetch && cb0 >= it.w) release();
         }
         if (dead) aborted = true;
     }
@@ -983,18 +987,20 @@ struct LinPlan {
 // The tile width for `rows` rows: the multiple of 16 whose tiles take least by the estimates
 // above, waves of tiles and a last wave's slices counted (4096 x 4096 outputs: 304 tiles of
 // 224 rows are four whole waves of 76 pairs, 256 tiles of 256 rows are 3.4).
-int choose_width(int rows, int f_tiles, int kb, int pairs, int cap, bool split)
+int choose_width(int mode, int rows, int f_tiles, int kb, int pairs, int cap, bool split)
 {
+    if (mode == kLinDw && rows <= 128) return rows < 16 ? 16 : (rows + 15) / 16 * 16;  // one tile
     int best = 16;
     double least = 0;
-    for (int c = 16; c <= cap; c += 16) {
-        const int w = tile_width(rows, c);
+    const int step = mode == kLinDw ? 128 : 16;
+    for (int c = step; c <= cap; c += step) {
+        const int w = tile_width(mode, rows, c);
         const int64_t tiles = (int64_t)((rows + w - 1) / w) * f_tiles;
         const int rem = (int)(tiles % pairs);
         const int S = split ? slices(rem, kb, pairs, w) : 1;
         double t = (double)(tiles / pairs) * kb * kb_cycles(w) + 25 * w;  // (and the last epilogue)
         if (rem > 0) t += (double)((kb + S - 1) / S) * kb_cycles(w) + split_cycles(S, w);
-        if (c == 16 || t < least) least = t, best = w;
+        if (c == step || t < least) least = t, best = w;
     }
     return best;
 }
@@ -1015,8 +1021,8 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
     pl.pairs = num_sms / 2;
     pl.wcap = ragged ? cap
               : a.mode == kLinDw && a.G > 0
-                  ? choose_width(pl.rows, pl.f_tiles * G, (pl.kb + G - 1) / G, pl.pairs, cap, false)
-                  : choose_width(pl.rows, pl.f_tiles, pl.kb, pl.pairs, cap, true);
+                  ? choose_width(a.mode, pl.rows, pl.f_tiles * G, (pl.kb + G - 1) / G, pl.pairs, cap, false)
+                    : choose_width(a.mode, pl.rows, pl.f_tiles, pl.kb, pl.pairs, cap, true);
     pl.wmax = ragged ? (int)(a.M < cap ? (a.M + 15) / 16 * 16 : cap) : pl.wcap;
     int64_t row_tiles = (pl.rows + pl.wcap - 1) / pl.wcap;
     if (ragged) row_tiles += a.G < a.M ? a.G : a.M;

@@ -86,8 +86,9 @@ __global__ void __launch_bounds__(R_THREADS) route_kernel(RouteParams p)
     const int E = p.E, k = p.k;
     for (int i = threadIdx.x; i < R_WARPS * E; i += R_THREADS) wc[i] = 0;
     __syncthreads();
-    const int per = R_TOKENS / R_WARPS;
-    const int t0 = blockIdx.x * R_TOKENS + warp * per, t1 = min(t0 + per, p.T);
+    // (a single block spreads its tokens over all its warps)
+    const int per = p.nblk == 1 ? (p.T + R_WARPS - 1) / R_WARPS : R_TOKENS / R_WARPS;
+    const int t0 = min(blockIdx.x * R_TOKENS + warp * per, p.T), t1 = min(t0 + per, p.T);
     uint16_t* mine = wc + warp * E;
     for (int t = t0; t < t1; ++t) {
         const typename D::T* l = static_cast<const typename D::T*>(p.logits) + (int64_t)t * p.ld;
