@@ -90,6 +90,7 @@ struct LinParams {
     int f_tiles;
     int bx;      // rows of a K-major B box
     int b_bytes, stages, kc;
+    unsigned per_inv;  // 2^32 / (RASTER * f_tiles), rounded down
     int wcap;        // rows of a tile at most (a multiple of 16)
     int split_w;     // tile width the last wave's split is planned for (0: no split)
     const void* bias;
@@ -125,8 +126,9 @@ __host__ __device__ constexpr int accumulators(int mode, int w)
 __host__ __device__ inline int tile_width(int mode, int rows, int wcap)
 {
     if (mode == kLinDw) return wcap;
+    if (rows <= wcap) return (rows + 15) / 16 * 16;
     const unsigned nt = (unsigned)(rows + wcap - 1) / (unsigned)wcap;
-    const unsigned w = nt ? ((unsigned)rows + nt - 1) / nt : 16;
+    const unsigned w = ((unsigned)rows + nt - 1) / nt;
     return (int)((w + 15) / 16 * 16);
 }
 
@@ -196,22 +198,30 @@ class Walk {
         } else {
             return false;
         }
-        while (tile >= cum_[g_ + 1]) ++g_;
+        if (tile >= end_ || w_ == 0) {
+            // the next group with this tile: its rows, tiles and their width
+            while (tile >= cum_[g_ + 1]) ++g_;
+            begin_ = cum_[g_], end_ = cum_[g_ + 1];
+            first_ = off_[g_], rows_ = off_[g_ + 1] - first_;
+            const int n = MODE == kLinDw ? p_.rows : rows_;
+            nt_ = (unsigned)(n + p_.wcap - 1) / (unsigned)p_.wcap;
+            w_ = tile_width(MODE, n, p_.wcap);
+        }
         it.g = g_;
-        int rows = off_[g_ + 1] - off_[g_], first = off_[g_];
+        it.w = w_;
+        int rows = rows_, first = first_;
         if (MODE == kLinDw) {
             it.red0 = first;
-            it.red_rows = max(rows, 0);
-            if (p_.offsets) it.kb0 = 0, it.kb1 = (it.red_rows + BK - 1) / BK;
+            it.red_rows = rows;
+            if (p_.offsets) it.kb0 = 0, it.kb1 = (rows + BK - 1) / BK;
             rows = p_.rows, first = 0;
         }
-        const uint32_t local = tile - cum_[g_];
-        const uint32_t nt = (uint32_t)(rows + p_.wcap - 1) / p_.wcap;
-        const uint32_t per = RASTER * p_.f_tiles;
-        const uint32_t rg = local / per;
-        const uint32_t m0 = rg * RASTER, m = min(nt - m0, (uint32_t)RASTER);
-        const uint32_t r = local - rg * per, ft = r / m;
-        it.w = tile_width(MODE, rows, p_.wcap);
+        // raster: groups of RASTER row tiles, the rows fastest (division by a launch constant)
+        const unsigned local = tile - begin_, per = RASTER * p_.f_tiles;
+        unsigned rg = __umulhi(local, p_.per_inv);
+        if (local - rg * per >= per) ++rg;
+        const unsigned m0 = rg * RASTER, r = local - rg * per, m = min(nt_ - m0, (unsigned)RASTER);
+        const unsigned ft = m == RASTER ? r / RASTER : r / m;
         const int t0 = (int)(m0 + r - ft * m) * it.w;
         it.row0 = first + t0;
         it.valid = min(it.w, rows - t0);
@@ -227,6 +237,8 @@ class Walk {
     const int* off_;
     const int* cum_;
     int pairs_, t_, g_, whole_, S_, tail_, slot_ = 0;
+    int begin_ = 0, end_ = 0, first_ = 0, rows_ = 0, w_ = 0;  // the current group
+    unsigned nt_ = 0;
 };
 
 __device__ __forceinline__ void record_error(int* status, int code, volatile int* abort_flag)
@@ -1143,6 +1155,7 @@ int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* de
     p.G = a.G > 0 ? a.G : 1;
     p.offsets = a.G > 0 ? a.offsets : nullptr;
     p.f_tiles = pl.f_tiles;
+    p.per_inv = (unsigned)((1ull << 32) / (unsigned)(RASTER * pl.f_tiles));
     p.wcap = pl.wcap;
     p.bx = pl.bx;
     p.b_bytes = pl.b_bytes;
