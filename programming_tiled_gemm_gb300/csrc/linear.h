@@ -67,9 +67,8 @@ struct LinActArgs {
     int G;
     const int32_t* offsets;
 };
-size_t linear_act_ws_bytes(const LinActArgs& a);
-int64_t linear_act_counters(const LinActArgs& a);  // of 4 bytes; every launch leaves them zero
-int launch_linear_act(const LinActArgs& a, float* ws, unsigned* counters, cudaStream_t stream, int* launches);
+size_t linear_act_ws_bytes(const LinActArgs& a, int num_sms);
+int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t stream, int* launches);
 
 // First unit of every group when each group's rows are cut into pieces of `unit` rows (at
 // least `least` of them) and every piece counts `per` units: cum[g] for g = 0 .. G, and the

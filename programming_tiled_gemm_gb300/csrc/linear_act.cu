@@ -3,13 +3,16 @@
 // (per group), summed in fp32 from the unrounded dZ in the same pass.
 //
 // Bound by memory: dY and Z are read and dZ written once, 16 bytes a thread.  A block takes
-// 256 columns x 128 rows (a warp a row, eight columns a lane), keeps its column sums in
-// registers, and leaves them in the workspace; the block that counts last for a group's
-// columns adds the row pieces in order.  Nothing waits, and the order is fixed.
+// 256 columns (a warp a row, eight columns a lane) of a piece of 8 .. 128 rows, as many as
+// make about eight blocks an SM, keeps its column sums in registers and leaves them in the
+// workspace; a second, small launch adds a group's pieces in order.  (Adding them in the
+// block that counts last took 10 us more at 4096 x 4096: one block reads what 32 warps of
+// many blocks can.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "linear.h"
+#include "ptx.h"
 
 namespace gemm_gb300 {
 
@@ -17,7 +20,7 @@ GEMM_DEBUG_UNIT(linear_act)
 
 namespace {
 
-constexpr int THREADS = 256, WARPS = 8, COLS = 256, ROWS = 128;
+constexpr int THREADS = 256, WARPS = 8, COLS = 256;
 
 struct ActParams {
     int M, N, G;
@@ -30,8 +33,8 @@ struct ActParams {
     int64_t lddz;
     float* db;  // [G][Nw] or null
     float* ws;  // [item][Nw]
-    unsigned* cnt;
     int act, col_blocks;
+    int piece;  // rows of a piece
 };
 
 template <bool BF16>
@@ -59,7 +62,7 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
     uint4 u = make_uint4(0, 0, 0, 0);
     if (n >= 8) {
-        u = __ldg(reinterpret_cast<const uint4*>(p));
+        u = __ldcs(reinterpret_cast<const uint4*>(p));  // (read once: out of L2 before dZ)
     } else {
         uint16_t t[8];
 #pragma unroll
@@ -130,18 +133,18 @@ __global__ void __launch_bounds__(THREADS) linear_act_kernel(ActParams p)
 {
     extern __shared__ int table[];  // off[G + 1], cum[G + 1] (BIAS)
     __shared__ float sums[WARPS][COLS];
-    __shared__ int last;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int item = blockIdx.x / p.col_blocks, cblock = blockIdx.x % p.col_blocks;
     const int col = cblock * COLS + lane * 8;
     const int ncol = p.N - col;  // columns of this lane that exist (may be <= 0 or above 8)
     const int Nw = GATED ? 2 * p.N : p.N;
-    int g = 0, first, rows, piece = 0, pieces = 1;
+    int g = 0, first, rows;
     if (BIAS) {
         int* off = table;
         int* cum = table + p.G + 1;
-        group_table(p.offsets, p.G, p.M, ROWS, 1, 1, off, cum);
+        group_table(p.offsets, p.G, p.M, p.piece, 1, 1, off, cum);
         __syncthreads();
+        grid_dependents_launch();
         if (item >= cum[p.G]) return;
         int hi = p.G - 1;  // the group whose pieces hold item item
         while (g < hi) {
@@ -149,17 +152,15 @@ __global__ void __launch_bounds__(THREADS) linear_act_kernel(ActParams p)
             if (cum[mid] <= item) g = mid;
             else hi = mid - 1;
         }
-        piece = item - cum[g];
-        pieces = cum[g + 1] - cum[g];
-        first = off[g] + piece * ROWS;
-        rows = min(ROWS, off[g + 1] - first);
+        first = off[g] + (item - cum[g]) * p.piece;
+        rows = min(p.piece, off[g + 1] - first);
     } else {
-        first = item * ROWS;
-        rows = min(ROWS, p.M - first);
+        first = item * p.piece;
+        rows = min(p.piece, p.M - first);
     }
     float s[8] = {}, su[8] = {};
     if (ncol > 0) {
-#pragma unroll 2
+#pragma unroll 4
         for (int r = warp; r < rows; r += WARPS) {
             const int64_t row = first + r;
             if (!in_range(row, p.M)) continue;
@@ -190,8 +191,8 @@ __global__ void __launch_bounds__(THREADS) linear_act_kernel(ActParams p)
         }
     }
     if (!BIAS) return;
-    // the warps' sums in order, one column a thread; then the pieces' sums in order
-    float* dst = pieces == 1 ? p.db + (int64_t)g * Nw : p.ws + (int64_t)item * Nw;
+    // the warps' sums in order, one column a thread
+    float* dst = p.ws + (int64_t)item * Nw;
     const int c = cblock * COLS + threadIdx.x;
 #pragma unroll
     for (int h = 0; h < (GATED ? 2 : 1); ++h) {
@@ -204,38 +205,36 @@ __global__ void __launch_bounds__(THREADS) linear_act_kernel(ActParams p)
         for (int w = 0; w < WARPS; ++w) t += sums[w][threadIdx.x];
         if (c < p.N) dst[h * p.N + c] = t;
     }
-    if (pieces == 1) return;
-    __threadfence();
+}
+
+constexpr int SUM_WARPS = 32;
+
+// db of 32 columns of a group: warp w adds pieces w, w + 32, ...; the warps' sums are added
+// in order.  The groups' first pieces come from the same table as above.
+__global__ void __launch_bounds__(32 * SUM_WARPS) linear_db_kernel(ActParams p, int Nw)
+{
+    extern __shared__ int table[];
+    __shared__ float sums[SUM_WARPS][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int blocks = (Nw + 31) / 32, g = blockIdx.x / blocks, c = blockIdx.x % blocks * 32 + lane;
+    int* cum = table + p.G + 1;
+    group_table(p.offsets, p.G, p.M, p.piece, 1, 1, table, cum);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        unsigned* cnt = p.cnt + (int64_t)g * p.col_blocks + cblock;
-        last = atomicAdd(cnt, 1u) == (unsigned)(pieces - 1);
-        if (last) *cnt = 0;  // ready for the next launch
-        __threadfence();
-    }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    // warp w adds pieces w, w + 8, ...; the warps' sums are added in order
-    const float* src = p.ws + (int64_t)(item - piece) * Nw;
-#pragma unroll
-    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-        float t[8] = {};
+    grid_dependency_wait();
+    const float* src = p.ws + (int64_t)cum[g] * Nw + c;
+    const int pieces = cum[g + 1] - cum[g];
+    float t = 0.f;
+    if (c < Nw) {
 #pragma unroll 4
-        for (int i = warp; i < pieces; i += WARPS)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int cc = cblock * COLS + 32 * j + lane;
-                if (cc < p.N) t[j] += __ldcg(src + (int64_t)i * Nw + h * p.N + cc);
-            }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sums[warp][32 * j + lane] = t[j];
-        __syncthreads();
+        for (int i = warp; i < pieces; i += SUM_WARPS) t += __ldcg(src + (int64_t)i * Nw);
+    }
+    sums[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0 && c < Nw) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) v += sums[w][threadIdx.x];
-        if (c < p.N) p.db[(int64_t)g * Nw + h * p.N + c] = v;
+        for (int w = 0; w < SUM_WARPS; ++w) v += sums[w][lane];
+        p.db[(int64_t)g * Nw + c] = v;
     }
 }
 
@@ -249,25 +248,28 @@ cudaError_t launch_typed(const ActParams& p, dim3 grid, cudaStream_t s)
     return cudaGetLastError();
 }
 
-int64_t items(const LinActArgs& a)
+int piece_rows(const LinActArgs& a, int num_sms)
 {
-    const int64_t n = (a.M + ROWS - 1) / ROWS;
+    const int64_t col_blocks = (a.N + COLS - 1) / COLS;
+    const int64_t r = a.M * col_blocks / (8 * (int64_t)num_sms) / WARPS * WARPS;
+    return (int)(r < WARPS ? WARPS : r > 128 ? 128 : r);
+}
+
+int64_t items(const LinActArgs& a, int num_sms)
+{
+    const int piece = piece_rows(a, num_sms);
+    const int64_t n = (a.M + piece - 1) / piece;
     return a.db ? n + (a.G > 0 ? a.G : 1) : n;
 }
 
 }  // namespace
 
-size_t linear_act_ws_bytes(const LinActArgs& a)
+size_t linear_act_ws_bytes(const LinActArgs& a, int num_sms)
 {
-    return a.db ? (size_t)items(a) * (size_t)(a.act == GEMM_ACT_SWIGLU ? 2 * a.N : a.N) * sizeof(float) : 0;
+    return a.db ? (size_t)items(a, num_sms) * (size_t)(a.act == GEMM_ACT_SWIGLU ? 2 * a.N : a.N) * sizeof(float) : 0;
 }
 
-int64_t linear_act_counters(const LinActArgs& a)
-{
-    return a.db ? (int64_t)(a.G > 0 ? a.G : 1) * ((a.N + COLS - 1) / COLS) : 0;
-}
-
-int launch_linear_act(const LinActArgs& a, float* ws, unsigned* counters, cudaStream_t stream, int* launches)
+int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t stream, int* launches)
 {
     ActParams p = {};
     p.M = (int)a.M;
@@ -282,10 +284,10 @@ int launch_linear_act(const LinActArgs& a, float* ws, unsigned* counters, cudaSt
     p.lddz = a.lddz;
     p.db = a.db;
     p.ws = ws;
-    p.cnt = counters;
     p.act = a.act;
     p.col_blocks = (int)((a.N + COLS - 1) / COLS);
-    const int64_t n = items(a);
+    const int64_t n = items(a, num_sms);
+    p.piece = piece_rows(a, num_sms);
     if (n == 0 || a.N == 0) return GEMM_OK;
     if (n * p.col_blocks > 0x7fffffffLL) return GEMM_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)(n * p.col_blocks));
@@ -294,6 +296,15 @@ int launch_linear_act(const LinActArgs& a, float* ws, unsigned* counters, cudaSt
                                  : (gated ? launch_typed<false, true>(p, grid, stream) : launch_typed<false, false>(p, grid, stream));
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
+    if (a.db) {
+        const int Nw = (int)(gated ? 2 * a.N : a.N);
+        const int64_t blocks = (int64_t)p.G * ((Nw + 31) / 32);
+        if (blocks > 0x7fffffffLL) return GEMM_ERR_UNSUPPORTED;
+        if (launch_dependent(linear_db_kernel, dim3((unsigned)blocks), dim3(32 * SUM_WARPS), 2 * (p.G + 1) * sizeof(int), stream,
+                             p, Nw) != cudaSuccess)
+            return GEMM_ERR_CUDA;
+        *launches += 1;
+    }
     return GEMM_OK;
 }
 

@@ -40,7 +40,7 @@ int counters(gemm_handle_t h, int64_t n, cudaStream_t s)
     return from_cuda(cudaMemsetAsync(h->lin_counters, 0, h->lin_counters_bytes, s));
 }
 
-// The counters of the products, then those of the column sums and of the router.
+// The counters of the products, then that of the router.
 int64_t product_counters(gemm_handle_t h) { return linear_counters(h->num_sms); }
 
 int run_product(gemm_handle_t h, const LinArgs& a, cudaStream_t s)
@@ -168,14 +168,11 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
             e.lddz = lddz;
         }
         if (a->db) {
-            rc = ensure_buffer(&h->lin_sums, &h->lin_sums_bytes, linear_act_ws_bytes(e));
+            rc = ensure_buffer(&h->lin_sums, &h->lin_sums_bytes, linear_act_ws_bytes(e, h->num_sms));
             if (rc != GEMM_OK) return rc;
         }
-        const int64_t first = product_counters(h);
-        rc = counters(h, first + linear_act_counters(e), s);
-        if (rc != GEMM_OK) return rc;
         int n = 0;
-        rc = launch_linear_act(e, static_cast<float*>(h->lin_sums), h->lin_counters + first, s, &n);
+        rc = launch_linear_act(e, static_cast<float*>(h->lin_sums), h->num_sms, s, &n);
         h->launches += n;
         if (rc != GEMM_OK) return rc;
     }

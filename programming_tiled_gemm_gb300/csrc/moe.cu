@@ -43,13 +43,16 @@ struct F16 {
 
 // ------------------------------------------------------------------ router
 
-constexpr int R_WARPS = 16, R_THREADS = 32 * R_WARPS;
-constexpr int R_TOKENS = 128;  // a block's tokens, eight a warp
+constexpr int R_EACH = 4;  // tokens of a warp
+// Warps of a block for C logits a lane (by the registers they take), and its tokens.
+__host__ __device__ constexpr int route_warps(int C) { return C <= 8 ? 32 : 16; }
+__host__ __device__ constexpr int route_tokens(int C) { return R_EACH * route_warps(C); }
 
 struct RouteParams {
     const void* logits;
     int64_t ld;
     int T, E, k, renorm, nblk;
+    int tokens;  // of a block
     float* weights;
     int* experts;
     int* slots;
@@ -68,6 +71,9 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+// The value of a key (a NaN for any NaN's).
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -77,8 +83,9 @@ __device__ __forceinline__ float warp_sum(float v)
 
 // C logits a lane: expert 32 c + lane
 template <typename D, int C>
-__global__ void __launch_bounds__(R_THREADS) route_kernel(RouteParams p)
+__global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams p)
 {
+    constexpr int R_WARPS = route_warps(C), R_THREADS = 32 * R_WARPS;
     // [R_WARPS][E]: a warp's picks per expert, then the places its first picks take in the block
     extern __shared__ uint16_t wc[];
     __shared__ int last, scan[R_WARPS];
@@ -87,44 +94,87 @@ __global__ void __launch_bounds__(R_THREADS) route_kernel(RouteParams p)
     for (int i = threadIdx.x; i < R_WARPS * E; i += R_THREADS) wc[i] = 0;
     __syncthreads();
     // (a single block spreads its tokens over all its warps)
-    const int per = p.nblk == 1 ? (p.T + R_WARPS - 1) / R_WARPS : R_TOKENS / R_WARPS;
-    const int t0 = min(blockIdx.x * R_TOKENS + warp * per, p.T), t1 = min(t0 + per, p.T);
+    const int per = p.nblk == 1 ? (p.T + R_WARPS - 1) / R_WARPS : R_EACH;
+    const int t0 = min(blockIdx.x * p.tokens + warp * per, p.T), n_own = min(per, p.T - t0);
     uint16_t* mine = wc + warp * E;
-    for (int t = t0; t < t1; ++t) {
+    const auto fetch = [&](int t, float(&v)[C]) {
         const typename D::T* l = static_cast<const typename D::T*>(p.logits) + (int64_t)t * p.ld;
-        float v[C];
-        uint32_t key[C];
-        float rest = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = 32 * c + lane;
             v[c] = e < E ? D::get(l[e]) : -INFINITY;
+        }
+    };
+    int picks[R_EACH], ranks[R_EACH];  // lane j: the j-th pick of each token
+    float next[C];
+    if (n_own > 0) fetch(t0, next);
+#pragma unroll
+    for (int q = 0; q < R_EACH; ++q) {
+        if (q >= n_own) break;
+        const int t = t0 + q;
+        float v[C];
+        uint32_t key[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            v[c] = next[c];
             key[c] = order_key(v[c]);
         }
-        int pick = -1;        // lane j: the j-th pick, its logit
+        if (q + 1 < n_own) fetch(t + 1, next);  // travels while this token is sorted out
+        int pick = -1;
         float val = 0.f, top = 0.f;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = 0;
-            int at = 0;
+        if constexpr (C <= 8) {
+            // each lane sorts its keys once (equal ones stay in order); a round then looks at
+            // the lanes' heads only: half the instructions of searching all keys again
+            uint32_t order = 0x76543210u;  // the keys' c, a nibble each
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (key[c] > best) best = key[c], at = c;
-            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-            if (m == 0) break;  // no expert is left
-            const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (unsigned)(32 * at + lane) : 0xffffffffu);
-            float x = 0.f;
+            for (int i = C - 1; i > 0; --i)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (32 * c + lane == e) {
-                    x = v[c];
-                    key[c] = 0;
+                for (int c = 0; c < i; ++c) {
+                    const bool swap = key[c + 1] > key[c];
+                    const uint32_t lo = key[c], hi = key[c + 1];
+                    key[c] = swap ? hi : lo;
+                    key[c + 1] = swap ? lo : hi;
+                    const uint32_t d = ((order >> (4 * c)) ^ (order >> (4 * c + 4))) & 15u;
+                    order ^= swap ? (d << (4 * c)) | (d << (4 * c + 4)) : 0u;
                 }
-            x = __shfl_sync(0xffffffffu, x, e & 31);
-            if (j == 0) top = x;
-            if (lane == j) pick = e, val = x;
+            for (int j = 0; j < k; ++j) {
+                const uint32_t m = __reduce_max_sync(0xffffffffu, key[0]);
+                if (m == 0) break;  // no expert is left
+                const uint32_t who = __ballot_sync(0xffffffffu, key[0] == m);
+                const int own = (int)(order & 15u) * 32 + lane;
+                const int e = (who & (who - 1)) ? (int)__reduce_min_sync(0xffffffffu, key[0] == m ? (unsigned)own : 0xffffffffu)
+                                                : __shfl_sync(0xffffffffu, own, __ffs(who) - 1);
+                if (own == e) {
+#pragma unroll
+                    for (int c = 0; c + 1 < C; ++c) key[c] = key[c + 1];
+                    key[C - 1] = 0;
+                    order >>= 4;
+                }
+                const float x = key_value(m);
+                if (j == 0) top = x;
+                if (lane == j) pick = e, val = x;
+            }
+        } else {
+            for (int j = 0; j < k; ++j) {
+                uint32_t best = 0;
+                int at = 0;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (key[c] > best) best = key[c], at = c;
+                const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+                if (m == 0) break;
+                const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (unsigned)(32 * at + lane) : 0xffffffffu);
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (32 * c + lane == e) key[c] = 0;
+                const float x = key_value(m);
+                if (j == 0) top = x;
+                if (lane == j) pick = e, val = x;
+            }
         }
         const bool have = pick >= 0;
         const float ex = have ? expf(val - top) : 0.f;
+        float rest = 0.f;
         if (p.renorm) {
             rest = ex;
         } else {
@@ -134,14 +184,13 @@ __global__ void __launch_bounds__(R_THREADS) route_kernel(RouteParams p)
         }
         rest = warp_sum(rest);
         // rank among the warp's earlier picks of the same expert (a token's picks differ)
-        int rank = 0;
-        if (have) rank = mine[pick]++;
+        ranks[q] = have ? mine[pick]++ : 0;
+        picks[q] = pick;
         __syncwarp();
         if (lane < k) {
             const int64_t i = (int64_t)t * k + lane;
             p.weights[i] = have ? ex / rest : 0.f;
             p.experts[i] = pick;
-            p.slots[i] = rank;
         }
     }
     __syncthreads();
@@ -158,11 +207,10 @@ __global__ void __launch_bounds__(R_THREADS) route_kernel(RouteParams p)
         counts[e] = s;
     }
     __syncthreads();
-    for (int i = lane; i < (t1 - t0) * k; i += 32) {
-        const int64_t a = (int64_t)t0 * k + i;
-        const int e = p.experts[a];
-        if (e >= 0) p.slots[a] += mine[e];
-    }
+#pragma unroll
+    for (int q = 0; q < R_EACH; ++q)
+        if (q < n_own && lane < k)
+            p.slots[(int64_t)(t0 + q) * k + lane] = picks[q] >= 0 ? ranks[q] + mine[picks[q]] : 0;
     // the last block: each block's first place per expert
     if (p.nblk > 1) {
         __threadfence();
@@ -176,22 +224,33 @@ __global__ void __launch_bounds__(R_THREADS) route_kernel(RouteParams p)
         if (!last) return;
         __threadfence();
     }
-    // experts in chunks of R_THREADS / S, S threads an expert, each a stretch of blocks
-    int S = 1;
-    while (S < 16 && 2 * S * E <= R_THREADS && 2 * S <= p.nblk) S *= 2;
-    const int width = R_THREADS / S;
+    // chunks of `width` experts, neighbours in neighbouring threads; R_THREADS / width threads
+    // an expert, each a stretch of the blocks
+    __shared__ int sums[R_THREADS];
+    int width = 32;
+    while (width < E && width < R_THREADS) width *= 2;
+    const int S = R_THREADS / width, part = threadIdx.x / width, col = threadIdx.x % width;
+    const int b0 = (int)((unsigned)p.nblk * part / S), b1 = (int)((unsigned)p.nblk * (part + 1) / S);
     int before = 0;  // rows of the earlier chunks' experts
     for (int e0 = 0; e0 < E; e0 += width) {
-        // thread: stretch `part` of expert e; the S threads of an expert are neighbours
-        const int e = e0 + (int)threadIdx.x / S, part = threadIdx.x % S;
-        const int b0 = (int)((int64_t)p.nblk * part / S), b1 = (int)((int64_t)p.nblk * (part + 1) / S);
+        const int e = e0 + col;
         int n = 0;
         if (e < E) {
-#pragma unroll 8
+#pragma unroll 16
             for (int b = b0; b < b1; ++b) n += __ldcg(p.base + (int64_t)b * E + e);
         }
-        // exclusive scan over the block's threads, in the order (expert, stretch)
-        int s = n;
+        sums[threadIdx.x] = n;
+        __syncthreads();
+        // the stretches' sums before each, and the experts' totals
+        int total = 0;
+        if (part == 0)
+            for (int q = 0; q < S; ++q) {
+                const int t = sums[q * width + col];
+                sums[q * width + col] = total;
+                total += t;
+            }
+        // exclusive scan of the totals
+        int s = total;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int u = __shfl_up_sync(0xffffffffu, s, d);
@@ -205,14 +264,25 @@ __global__ void __launch_bounds__(R_THREADS) route_kernel(RouteParams p)
             if (w < warp) low += scan[w];
             all += scan[w];
         }
-        int at = before + low + s - n;
+        if (part == 0) {
+            const int first = before + low + s - total;
+            if (e < E) p.offsets[e] = first;
+            for (int q = 0; q < S; ++q) sums[q * width + col] += first;
+        }
+        __syncthreads();
+        int at = sums[threadIdx.x];
         if (e < E) {
-            if (part == 0) p.offsets[e] = at;
-            for (int b = b0; b < b1; ++b) {
-                int* q = p.base + (int64_t)b * E + e;
-                const int m = __ldcg(q);
-                *q = at;
-                at += m;
+            for (int b = b0; b < b1; b += 16) {
+                // (sixteen loads before their stores: one latency)
+                int m[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) m[i] = b + i < b1 ? __ldcg(p.base + (int64_t)(b + i) * E + e) : 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (b + i < b1) {
+                        p.base[(int64_t)(b + i) * E + e] = at;
+                        at += m[i];
+                    }
             }
         }
         before += all;
@@ -241,7 +311,7 @@ __global__ void route_place_kernel(RouteParams p)
     const int e = p.experts[i];
     int slot = -1;
     if (e >= 0) {
-        slot = p.base[(i / p.k / R_TOKENS) * p.E + e] + p.slots[i];
+        slot = p.base[(i / p.k / p.tokens) * p.E + e] + p.slots[i];
         if (in_range(slot, n)) p.rows[slot] = (int)i;
     }
     p.slots[i] = slot;
@@ -325,6 +395,13 @@ struct Vec {
         if constexpr (V * sizeof(v[0]) == 16) *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(v);
         else *q = v[0];
     }
+    // written once, not read soon: out of L2 first
+    __device__ __forceinline__ void store_once(void* base, int64_t i) const
+    {
+        typename D::T* q = static_cast<typename D::T*>(base) + i;
+        if constexpr (V * sizeof(v[0]) == 16) __stcs(reinterpret_cast<uint4*>(q), *reinterpret_cast<const uint4*>(v));
+        else *q = v[0];
+    }
     __device__ __forceinline__ void zero()
     {
 #pragma unroll
@@ -340,11 +417,20 @@ __global__ void dispatch_kernel(DispatchArgs a)
     const int at = a.rows[r];
     const int64_t t = at >= 0 ? at / a.k : -1;
     if (t >= a.T) return;  // (no row of x)
-    for (int c = threadIdx.x * V; c < a.N; c += blockDim.x * V) {
-        Vec<D, V> v;
-        if (t >= 0) v.load(a.x, t * a.ldx + c);
-        else v.zero();
-        v.store(a.xr, r * a.ldxr + c);
+    // four accesses in flight a thread; x's row is read again for the token's other experts,
+    // the copies are not
+    const int step = blockDim.x * V;
+    for (int c = threadIdx.x * V; c < a.N; c += 4 * step) {
+        Vec<D, V> v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i * step < a.N) {
+                if (t >= 0) v[i].load(a.x, t * a.ldx + c + i * step);
+                else v[i].zero();
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i * step < a.N) v[i].store_once(a.xr, r * a.ldxr + c + i * step);
     }
 }
 
@@ -441,9 +527,9 @@ __global__ void combine_grad_kernel(CombineGradArgs a)
     }
 }
 
-int row_threads(int64_t N, int V)
+int row_threads(int64_t N, int V, int each = 1)
 {
-    const int64_t n = (N + V - 1) / V;
+    const int64_t n = (N + (int64_t)V * each - 1) / ((int64_t)V * each);
     return n >= 256 ? 256 : (int)((n + 31) / 32 * 32);
 }
 
@@ -452,7 +538,7 @@ bool aligned(const void* p, int64_t ld, int es) { return (reinterpret_cast<uintp
 template <typename D, int C>
 cudaError_t launch_route_c(const RouteParams& p, cudaStream_t s)
 {
-    route_kernel<D, C><<<p.nblk, R_THREADS, R_WARPS * p.E * sizeof(uint16_t), s>>>(p);
+    route_kernel<D, C><<<p.nblk, 32 * route_warps(C), route_warps(C) * p.E * sizeof(uint16_t), s>>>(p);
     return cudaGetLastError();
 }
 
@@ -477,9 +563,14 @@ cudaError_t by_type(int dtype, F f)
 
 }  // namespace
 
+namespace {
+int block_tokens(int64_t E) { return E <= 256 ? route_tokens(8) : route_tokens(16); }
+}  // namespace
+
 size_t moe_route_ws_bytes(const RouteArgs& a)
 {
-    return (size_t)((a.T + R_TOKENS - 1) / R_TOKENS) * a.E * sizeof(int);
+    const int n = block_tokens(a.E);
+    return (size_t)((a.T + n - 1) / n) * a.E * sizeof(int);
 }
 
 int launch_moe_route(const RouteArgs& a, int* ws, unsigned* counter, cudaStream_t s, int* launches)
@@ -491,7 +582,8 @@ int launch_moe_route(const RouteArgs& a, int* ws, unsigned* counter, cudaStream_
     p.E = (int)a.E;
     p.k = a.k;
     p.renorm = a.renormalize;
-    p.nblk = (int)((a.T + R_TOKENS - 1) / R_TOKENS);
+    p.tokens = block_tokens(a.E);
+    p.nblk = (int)((a.T + p.tokens - 1) / p.tokens);
     p.weights = a.weights;
     p.experts = a.experts;
     p.slots = a.slots;
@@ -534,8 +626,8 @@ int launch_rows(const Args& a, int dtype, bool vec, int64_t blocks, cudaStream_t
     const cudaError_t e = by_type(dtype, [&](auto d) {
         using D = decltype(d);
         constexpr int V = 16 / sizeof(typename D::T);
-        if (vec) Launch<D, V>::run(a, (unsigned)blocks, row_threads(a.N, V), s);
-        else Launch<D, 1>::run(a, (unsigned)blocks, row_threads(a.N, 1), s);
+        if (vec) Launch<D, V>::run(a, (unsigned)blocks, row_threads(a.N, V, Launch<D, V>::EACH), s);
+        else Launch<D, 1>::run(a, (unsigned)blocks, row_threads(a.N, 1, Launch<D, 1>::EACH), s);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
@@ -545,14 +637,17 @@ int launch_rows(const Args& a, int dtype, bool vec, int64_t blocks, cudaStream_t
 
 template <typename D, int V>
 struct Dispatch {
+    static constexpr int EACH = 4;  // accesses a thread has in flight
     static void run(const DispatchArgs& a, unsigned b, int t, cudaStream_t s) { dispatch_kernel<D, V><<<b, t, 0, s>>>(a); }
 };
 template <typename D, int V>
 struct Combine {
+    static constexpr int EACH = 1;
     static void run(const CombineArgs& a, unsigned b, int t, cudaStream_t s) { combine_kernel<D, V><<<b, t, 0, s>>>(a); }
 };
 template <typename D, int V>
 struct CombineGrad {
+    static constexpr int EACH = 1;
     static void run(const CombineGradArgs& a, unsigned b, int t, cudaStream_t s)
     {
         combine_grad_kernel<D, V><<<b, t, 0, s>>>(a);
