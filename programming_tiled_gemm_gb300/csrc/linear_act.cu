@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(THREADS) linear_act_kernel(ActParams p)
     }
 }
 
-constexpr int SUM_WARPS = 32;
+constexpr int SUM_WARPS = 8;
 
-// db of 32 columns of a group: warp w adds pieces w, w + 32, ...; the warps' sums are added
+// db of 32 columns of a group: warp w adds pieces w, w + 8, ...; the warps' sums are added
 // in order.  The groups' first pieces come from the same table as above.
 __global__ void __launch_bounds__(32 * SUM_WARPS) linear_db_kernel(ActParams p, int Nw)
 {
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) linear_db_kernel(ActParams p, 
     const int pieces = cum[g + 1] - cum[g];
     float t = 0.f;
     if (c < Nw) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = warp; i < pieces; i += SUM_WARPS) t += __ldcg(src + (int64_t)i * Nw);
     }
     sums[warp][lane] = t;

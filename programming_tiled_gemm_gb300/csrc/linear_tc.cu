@@ -62,7 +62,6 @@ constexpr int UMMA_K = 16;
 constexpr int CTA_F = 128;            // features (MMA rows) of one CTA
 constexpr int MAX_W = 256;            // rows (MMA columns) of a tile
 constexpr int MAX_W_CHUNKED = 128;    // and with chunks, whose sums an epilogue thread holds: 64 of them
-constexpr int EPI_WARPS = 8;
 constexpr int A_BYTES = CTA_F * BK * 2;  // 16 KiB a stage
 constexpr int BOX_BYTES = 64 * BK * 2;   // 64 x 64 box of an MN-major operand
 constexpr int MAX_STAGES = 12;
@@ -72,13 +71,24 @@ constexpr int STG_BYTES = 2048;       // an epilogue warp's staging block: 32 ro
                                       // or (gated) 16 columns of fp32 for the other warp
 constexpr int SMEM_MAX = 232448;      // 227 KiB
 
-// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; 4..11: epilogue, which takes
-// registers from the first four: 80 + 2 * 208 a thread of the three warpgroups is within
-// the 3 * 168 the block is launched with (checked before the launch).
+// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; then the epilogue's, which
+// take registers from the first four.  dW's plain epilogue runs on 16 warps: with 8 it took
+// longer than the MMAs of a tile reduced over 500 rows.
 constexpr int EPI_WARP0 = 4;
-constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-constexpr int LAUNCH_REGS = 168, LEAN_REGS = 80, EPI_REGS = 208;
-static_assert(LEAN_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "the epilogue's registers come from the block's own");
+struct Roles {
+    int epi_warps, launch_regs, lean_regs, epi_regs;
+    __host__ __device__ constexpr int threads() const { return 32 * (EPI_WARP0 + epi_warps); }
+};
+__host__ __device__ constexpr Roles roles(int mode, bool chunked)
+{
+    return mode == kLinDw && !chunked ? Roles{16, 96, 64, 104} : Roles{8, 168, 80, 208};
+}
+// (setmaxnreg draws on the registers the block is launched with; checked before the launch)
+constexpr bool balanced(Roles r)
+{
+    return 4 * r.lean_regs + r.epi_warps * r.epi_regs <= (EPI_WARP0 + r.epi_warps) * r.launch_regs;
+}
+static_assert(balanced(roles(kLinFwd, true)) && balanced(roles(kLinDw, false)), "registers beyond the block's own");
 
 struct LinParams {
     int M;       // rows of X
@@ -303,9 +313,10 @@ __device__ __forceinline__ void activate(float (&v)[N], int act)
 // accesses to shared memory meet no bank conflicts.
 struct Matrix16 {
     uint16_t* base;  // row 0, feature 0 of the block
-    int64_t ld;
+    int ld;
     int n, nf;       // rows and features of the block that exist (nf may exceed 32)
     bool vec;
+    __device__ __forceinline__ uint16_t* at(int row, int f) const { return base + (int64_t)row * ld + f; }
 };
 
 template <bool BF16>
@@ -323,7 +334,7 @@ __device__ __forceinline__ uint32_t pack_16(float lo, float hi)
 __device__ __forceinline__ void store_row8(const Matrix16& m, int row, int f, uint4 v)
 {
     if (row >= m.n || f >= m.nf) return;
-    uint16_t* o = m.base + row * m.ld + f;
+    uint16_t* o = m.at(row, f);
     if (f + 8 <= m.nf) {
         *reinterpret_cast<uint4*>(o) = v;
         return;
@@ -338,7 +349,7 @@ __device__ __forceinline__ uint4 load_row8(const Matrix16& m, int row, int f)
 {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (row >= m.n || f >= m.nf) return v;
-    const uint16_t* o = m.base + row * m.ld + f;
+    const uint16_t* o = m.at(row, f);
     if (f + 8 <= m.nf) return *reinterpret_cast<const uint4*>(o);
     uint32_t w[4] = {};
 #pragma unroll
@@ -356,22 +367,32 @@ __device__ __forceinline__ void store_block(const Matrix16& m, uint32_t* stg, in
         if (lane < m.nf)
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (i < m.n) o[i * m.ld] = to_16<BF16>(v[i]);
+                if (i < m.n) o[(int64_t)i * m.ld] = to_16<BF16>(v[i]);
         return;
     }
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) stg[i * 32 + lane] = pack_16<BF16>(v[2 * i], v[2 * i + 1]);
     __syncwarp();
+    // features f .. f+7 of row pairs pr, pr + 8
+    const int pr = lane / 4, f = lane % 4 * 8, odd = pr & 1;
+    const uint4* src = reinterpret_cast<const uint4*>(stg + pr * 32 + f);
+    const bool whole = m.n >= N && m.nf >= 32;  // (uniform over the warp)
+    uint16_t* o = m.at(2 * pr, f);
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
-        const int pr = i * 8 + lane / 4, f = lane % 4 * 8;
-        const uint4* src = reinterpret_cast<const uint4*>(stg + pr * 32 + f);
-        const uint4 x = src[pr & 1], y = src[(pr & 1) ^ 1];
-        const uint4 lo = (pr & 1) ? y : x, hi = (pr & 1) ? x : y;  // features f..f+3, f+4..f+7
-        store_row8(m, 2 * pr, f, make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
-                                            __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410)));
-        store_row8(m, 2 * pr + 1, f, make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
-                                                __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632)));
+        const uint4 x = src[i * 64 + odd], y = src[i * 64 + (odd ^ 1)];
+        const uint4 lo = odd ? y : x, hi = odd ? x : y;  // features f..f+3, f+4..f+7
+        const uint4 even = make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
+                                      __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
+        const uint4 next = make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
+                                      __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
+        if (whole) {
+            *reinterpret_cast<uint4*>(o + (int64_t)(16 * i) * m.ld) = even;
+            *reinterpret_cast<uint4*>(o + (int64_t)(16 * i + 1) * m.ld) = next;
+        } else {
+            store_row8(m, 2 * pr + 16 * i, f, even);
+            store_row8(m, 2 * pr + 16 * i + 1, f, next);
+        }
     }
     __syncwarp();
 }
@@ -384,11 +405,17 @@ struct Ahead {
     __device__ __forceinline__ void load(const Matrix16& m, int lane)
     {
         if (!m.vec) return;
+        const int row = lane / 4 * 2, f = lane % 4 * 8;
+        if (m.n >= N && m.nf >= 32) {
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i) {
-            const int pr = i * 8 + lane / 4, f = lane % 4 * 8;
-            r[i][0] = load_row8(m, 2 * pr, f);
-            r[i][1] = load_row8(m, 2 * pr + 1, f);
+            for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) r[i][k] = *reinterpret_cast<const uint4*>(m.at(row + 16 * i + k, f));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) r[i][k] = load_row8(m, row + 16 * i + k, f);
         }
     }
 };
@@ -405,7 +432,7 @@ __device__ __forceinline__ void add_block(const Matrix16& m, const Ahead<N>& a, 
                 uint16_t t[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (b + i < m.n) t[i] = r[(b + i) * m.ld];
+                    if (b + i < m.n) t[i] = r[(int64_t)(b + i) * m.ld];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (b + i < m.n) v[b + i] += from_16<BF16>(t[i]);
@@ -458,9 +485,11 @@ __device__ __forceinline__ void store_f32(const float* R, int64_t ldr, float* ou
 }
 
 template <int MODE, bool GATED, bool BF16, bool CHUNKED>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(roles(MODE, CHUNKED).threads(), 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p)
 {
+    constexpr Roles ROLES = roles(MODE, CHUNKED);
+    constexpr int EPI_WARPS = ROLES.epi_warps, EPI_GROUPS = EPI_WARPS / 4;  // a group covers the TMEM lanes
     constexpr bool A_MN = MODE != kLinDx, B_MN = MODE == kLinDw;
     constexpr int TILE_F = GATED ? CTA_F : 2 * CTA_F;  // output features of a tile
     extern __shared__ uint8_t smem_raw[];
@@ -528,7 +557,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     bool aborted = false;
 
     if (warp < EPI_WARP0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LEAN_REGS));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLES.lean_regs));
         if (warp == 0 || warp == 3) {
             // ---------------------------------------------------------------- producers
             // warp 0 loads A (and announces a stage's bytes), warp 3 loads B: one thread issuing
@@ -610,6 +639,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 Item it;
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, buf_phase = 0;
+                uint32_t tails = 0;  // bit s: parity of stage s's next tail
                 bool ok = true;
                 // descriptors of stage 0; a stage or a step of 16 along K moves the start address
                 constexpr uint32_t A_STEP = A_MN ? UMMA_K * 128 : UMMA_K * 2, B_STEP = B_MN ? UMMA_K * 128 : UMMA_K * 2;
@@ -635,6 +665,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                                 record_error(p.status, kDevTimeoutMma, abort_flag);
                                 ok = false;
                                 break;
+                            }
+                            if (MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK) {
+                                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&peer_bar[stage]), (tails >> stage) & 1,
+                                                                               p.limit_ns, abort_flag))) {
+                                    record_error(p.status, kDevTimeoutMma, abort_flag);
+                                    ok = false;
+                                    break;
+                                }
+                                tails ^= 1u << stage;
                             }
                             tc_fence_after();
                             const uint64_t a_desc = a_desc0 + (uint32_t)(stage * A_BYTES >> 4);
@@ -708,26 +747,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
-                if (rank == 1) {
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&peer_bar[s]), 0));
-                    continue;
+                // (the MMA warp waits for both CTAs' fixers, so that they need not for each other)
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(smem_u32(&full_bar[s]));
+                    else mbar_arrive_cluster(mapa_shared(smem_u32(&peer_bar[s]), 0));
                 }
-                ok = mbar_wait_cluster(smem_u32(&peer_bar[s]), parity, p.limit_ns, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) {
-                    if (lane == 0) record_error(p.status, kDevTimeoutMma, abort_flag);
-                    aborted = true;
-                    break;
-                }
-                if (lane == 0) mbar_arrive(smem_u32(&full_bar[s]));
             }
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROLES.epi_regs));
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3;             // TMEM lane quarter
-        const int half = (warp - EPI_WARP0) >> 2;   // takes column blocks half, half + 2, ...
+        const int half = (warp - EPI_WARP0) >> 2;   // takes column blocks half, half + EPI_GROUPS, ...
         const int e = threadIdx.x - 32 * EPI_WARP0;
         uint32_t* stg = reinterpret_cast<uint32_t*>(after + (warp - EPI_WARP0) * STG_BYTES);
         int buf = 0;
@@ -748,11 +780,20 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         float acc[CHUNKED ? 2 : 1][32];  // one chunk: blocks come straight from tensor memory
         while (walk.next(it)) {
             const int turns = accumulators(MODE, it.w);
-            // columns of a warp's block: up to 32 rows are shared by both halves of the warps
-            const int bw = it.w <= 16 ? 8 : it.w <= 32 ? 16 : 32, cb0 = half * bw;
+            // columns of a warp's block: few rows are shared by all the groups
+            const int bw = it.w <= 8 * EPI_GROUPS ? 8 : it.w <= 16 * EPI_GROUPS ? 16 : 32, cb0 = half * bw;
+            const int cb_step = EPI_GROUPS * bw;
             // columns cb .. cb + 31 of the finished accumulator, its turns added in order
             const auto block_sum = [&](int cb, float(&v)[32]) {
                 const uint32_t t_addr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAX_W + cb);
+                if (!CHUNKED && turns == 1) {
+                    uint32_t u[32];
+                    tmem_ld_32x32b_x32(t_addr, u);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                    return;
+                }
                 for (int r = 0; r < turns; ++r) {
                     uint32_t u[32];
                     tmem_ld_32x32b_x32(t_addr + r * (MAX_W / turns), u);
@@ -773,7 +814,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             const auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+                // (a cluster-scope release would wait for this tile's stores: 2000 cycles a tile)
+                if (lane == 0) mbar_arrive_cluster_light(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
                 if (++buf == 2) {
                     buf = 0;
                     buf_phase ^= 1;
@@ -790,7 +832,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if (dead) break;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if (cb0 + 2 * j * bw < it.w) block_sum(cb0 + 2 * j * bw, acc[j]);
+                        if (cb0 + j * cb_step < it.w) block_sum(cb0 + j * cb_step, acc[j]);
                     release();
                 }
             } else if (any) {
@@ -812,10 +854,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if constexpr (CHUNKED) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            if (cb0 + 2 * j * bw < it.w) publish(cb0 + 2 * j * bw, acc[j]);
+                            if (cb0 + j * cb_step < it.w) publish(cb0 + j * cb_step, acc[j]);
                     } else {
 #pragma unroll 1
-                        for (int cb = cb0; cb < it.w; cb += 2 * bw) {
+                        for (int cb = cb0; cb < it.w; cb += cb_step) {
                             float v[32] = {};
                             block_sum(cb, v);
                             publish(cb, v);
@@ -859,12 +901,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 const int64_t row = it.row0 + cb;
                 const int n = min(it.valid, cb_end) - cb;
                 const bool in = n <= 0 || in_range(row + min(n, 32) - 1, p.rows);
-                return Matrix16{static_cast<uint16_t*>(const_cast<void*>(base)) + row * ld + col, ld, in ? n : 0, nf, vec};
+                return Matrix16{static_cast<uint16_t*>(const_cast<void*>(base)) + row * ld + col, (int)ld, in ? n : 0, nf, vec};
             };
             const bool fetch = !CHUNKED && any && it.part < 0 && !dead;
             // (chunked: the sums move down a block an iteration, so that one copy of the code does)
 #pragma unroll 1
-            for (int cb = cb0; cb < it.w; cb += 2 * bw) {
+            for (int cb = cb0; cb < it.w; cb += cb_step) {
                 float(&v)[32] = acc[0];
                 // the residual's loads run while the sums are fetched and activated (a slice's
                 // addition needs the registers: after it)
@@ -875,13 +917,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
                     if (fetch) {
                         block_sum(cb, v);
-                        if (cb + 2 * bw >= it.w) release();
+                        if (cb + cb_step >= it.w) release();
                     }
                 }
                 if (it.part >= 0) {
                     // every slice, this CTA's own included, is read back, COLS columns of DEEP slices
                     // at a time so that their latencies overlap, and added in K order
-                    constexpr int DEEP = CHUNKED ? 4 : 6, COLS = 8;
+                    constexpr int DEEP = CHUNKED ? 4 : EPI_WARPS > 8 ? 2 : 6, COLS = 8;
                     const int S = walk.slices_of_tile();
 #pragma unroll
                     for (int h = 0; h < 32; h += COLS) {
@@ -906,8 +948,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if (residual) ahead.load(mr, lane);
                 }
                 if (MODE == kLinFwd) {
+                    if (p.bias)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += bias;
+                        for (int i = 0; i < 32; ++i) v[i] += bias;
                     if (p.Z) {
                         mz = block(p.Z, p.ldz, zw, cb, cb + bw, p.vec_z);
                         store_block<BF16>(mz, stg, lane, v);
@@ -1050,7 +1093,7 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
     pl.bx = typical < 8 ? 8 : (typical + 7) / 8 * 8;
     const int b_rows = (pl.wmax / 2 + pl.bx - 1) / pl.bx * pl.bx;
     pl.b_bytes = a.mode == kLinDw ? (pl.wmax / 2 + 63) / 64 * BOX_BYTES : (b_rows * 128 + 1023) / 1024 * 1024;
-    const int fixed = 1024 + EPI_WARPS * STG_BYTES + (4 * MAX_STAGES + 6) * 8 + 16 + 2 * (G + 1) * 4 + 16;
+    const int fixed = 1024 + roles(a.mode, chunked).epi_warps * STG_BYTES + (4 * MAX_STAGES + 6) * 8 + 16 + 2 * (G + 1) * 4 + 16;
     pl.stages = (SMEM_MAX - fixed) / (A_BYTES + pl.b_bytes);
     if (pl.stages > MAX_STAGES) pl.stages = MAX_STAGES;
     pl.smem = fixed + pl.stages * (A_BYTES + pl.b_bytes);
@@ -1070,12 +1113,13 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
                   cudaStream_t stream)
 {
     static std::atomic<int> fit{0};
+    constexpr Roles ROLES = roles(MODE, CHUNKED);
     auto kern = linear_pair_kernel<MODE, GATED, BF16, CHUNKED>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess)
         return GEMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.blockDim = dim3(ROLES.threads(), 1, 1);
     cfg.dynamicSmemBytes = SMEM_MAX;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1092,7 +1136,7 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
     if (clusters == 0) {
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return GEMM_ERR_CUDA;
-        if (fa.numRegs < LAUNCH_REGS) return GEMM_ERR_UNSUPPORTED;  // the epilogue would wait for registers
+        if (fa.numRegs < ROLES.launch_regs) return GEMM_ERR_UNSUPPORTED;  // the epilogue would wait for registers
         if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
             (void)cudaGetLastError();
             return GEMM_ERR_CUDA;

@@ -476,6 +476,14 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// Arrive on a barrier of this cluster (cluster address) without ordering earlier global
+// stores before it, as the cluster-scope form does by waiting for them: for arrivals that
+// hand over tensor memory already read (tcgen05.wait::ld), not data in memory.
+__device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Programmatic dependent launch: wait until the kernels this one depends on have finished
 // and their writes are visible; let the kernels that depend on this one start their set-up.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
