@@ -2,10 +2,10 @@
 // operands' 16-bit type for the two products that follow, and db = sum over the rows of dZ
 // (per group), summed in fp32 from the unrounded dZ in the same pass.
 //
-// Bound by memory: dY and Z are read and dZ written once, 16 bytes a thread.  A block takes
-// 256 columns (a warp a row, eight columns a lane) of a piece of 8 .. 128 rows, as many as
-// make about eight blocks an SM, keeps its column sums in registers and leaves them in the
-// workspace; a second, small launch adds a group's pieces in order.  (Adding them in the
+// Bound by memory: dY and Z are read and dZ written once, 16 bytes a thread.  Resident blocks
+// walk pieces of 256 columns (a warp a row, eight columns a lane) x 8 .. 32 rows with four
+// rows' loads in flight a warp, keep a piece's column sums in registers and leave them in
+// the workspace; a second, small launch adds a group's pieces in order.  (Adding them in the
 // block that counts last took 10 us more at 4096 x 4096: one block reads what 32 warps of
 // many blocks can.)
 #include <cuda_bf16.h>
@@ -34,7 +34,7 @@ struct ActParams {
     float* db;  // [G][Nw] or null
     float* ws;  // [item][Nw]
     int act, col_blocks;
-    int piece;  // rows of a piece
+    int piece, items;  // rows of a piece; pieces (an upper bound over groups)
 };
 
 template <bool BF16>
@@ -55,20 +55,21 @@ __device__ __forceinline__ uint32_t pack(float a, float b)
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Eight 16-bit values of a row from column c on, of which those below `n` exist.
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&v)[8])
+// Eight 16-bit values of a row from element `at` on, of which the first `n` exist; as they
+// are in memory, and in fp32.
+__device__ __forceinline__ uint4 load8(const void* base, int64_t at, int n)
 {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (n >= 8) {
-        u = __ldcs(reinterpret_cast<const uint4*>(p));  // (read once: out of L2 before dZ)
-    } else {
-        uint16_t t[8];
+    if (n >= 8) return __ldcs(reinterpret_cast<const uint4*>(p));  // (read once: out of L2 before dZ)
+    uint32_t t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : (uint16_t)0;
-        u = make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
-    }
+    for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : 0u;
+    return make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen(uint4 u, float (&v)[8])
+{
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -129,81 +130,95 @@ __device__ __forceinline__ void act_grad(float (&dz)[8], const float (&z)[8], in
 }
 
 template <bool BF16, bool GATED, bool BIAS>
-__global__ void __launch_bounds__(THREADS) linear_act_kernel(ActParams p)
+__global__ void __launch_bounds__(THREADS, 3) linear_act_kernel(ActParams p)
 {
     extern __shared__ int table[];  // off[G + 1], cum[G + 1] (BIAS)
-    __shared__ float sums[WARPS][COLS];
+    // a lane's eight columns lie in nine words, so that neither side meets bank conflicts
+    __shared__ float sums[WARPS][32 * 9];
+    constexpr int DEEP = GATED ? 2 : 4;  // rows of a warp whose loads are in flight together
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int item = blockIdx.x / p.col_blocks, cblock = blockIdx.x % p.col_blocks;
-    const int col = cblock * COLS + lane * 8;
-    const int ncol = p.N - col;  // columns of this lane that exist (may be <= 0 or above 8)
     const int Nw = GATED ? 2 * p.N : p.N;
-    int g = 0, first, rows;
+    int* off = table;
+    int* cum = table + p.G + 1;
+    int items = p.items;
     if (BIAS) {
-        int* off = table;
-        int* cum = table + p.G + 1;
         group_table(p.offsets, p.G, p.M, p.piece, 1, 1, off, cum);
         __syncthreads();
         grid_dependents_launch();
-        if (item >= cum[p.G]) return;
-        int hi = p.G - 1;  // the group whose pieces hold item item
-        while (g < hi) {
-            const int mid = (g + hi + 1) / 2;
-            if (cum[mid] <= item) g = mid;
-            else hi = mid - 1;
-        }
-        first = off[g] + (item - cum[g]) * p.piece;
-        rows = min(p.piece, off[g + 1] - first);
-    } else {
-        first = item * p.piece;
-        rows = min(p.piece, p.M - first);
+        items = cum[p.G];
     }
-    float s[8] = {}, su[8] = {};
-    if (ncol > 0) {
-#pragma unroll 4
-        for (int r = warp; r < rows; r += WARPS) {
-            const int64_t row = first + r;
-            if (!in_range(row, p.M)) continue;
-            float d[8], z[8];
-            load8<BF16>(p.dY, row * p.lddy + col, ncol, d);
-            if (GATED) {
-                float u[8], du[8];
-                load8<BF16>(p.Z, row * p.ldz + col, ncol, z);
-                load8<BF16>(p.Z, row * p.ldz + p.N + col, ncol, u);
+    int g = 0;
+    for (int w = blockIdx.x; w < items * p.col_blocks; w += gridDim.x) {
+        const int item = w / p.col_blocks, cblock = w % p.col_blocks;
+        const int col = cblock * COLS + lane * 8;
+        const int ncol = p.N - col;  // columns of this lane that exist (may be <= 0 or above 8)
+        int first, rows;
+        if (BIAS) {
+            while (cum[g + 1] <= item) ++g;  // (a block's items ascend)
+            first = off[g] + (item - cum[g]) * p.piece;
+            rows = min(p.piece, off[g + 1] - first);
+        } else {
+            first = item * p.piece;
+            rows = min(p.piece, p.M - first);
+        }
+        if (!in_range(first, p.M + 1) || !in_range(first + rows, p.M + 1)) rows = 0;
+        float s[8] = {}, su[8] = {};
+        for (int r0 = warp; ncol > 0 && r0 < rows; r0 += DEEP * WARPS) {
+            uint4 dy[DEEP], zg[DEEP], zu[DEEP];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float q = sigmoid(z[i]);
-                    du[i] = d[i] * z[i] * q;
-                    d[i] = d[i] * u[i] * q * (1.f + z[i] * (1.f - q));
+            for (int i = 0; i < DEEP; ++i) {
+                const int64_t row = first + r0 + i * WARPS;
+                if (r0 + i * WARPS < rows) {
+                    dy[i] = load8(p.dY, row * p.lddy + col, ncol);
+                    if (p.dZ) zg[i] = load8(p.Z, row * p.ldz + col, ncol);
+                    if (GATED) zu[i] = load8(p.Z, row * p.ldz + p.N + col, ncol);
                 }
-                store8<BF16>(p.dZ, row * p.lddz + p.N + col, ncol, du);
+            }
+#pragma unroll
+            for (int i = 0; i < DEEP; ++i) {
+                if (r0 + i * WARPS >= rows) break;
+                const int64_t row = first + r0 + i * WARPS;
+                float d[8], z[8];
+                widen<BF16>(dy[i], d);
+                if (GATED) {
+                    float u[8], du[8];
+                    widen<BF16>(zg[i], z);
+                    widen<BF16>(zu[i], u);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float q = sigmoid(z[k]);
+                        du[k] = d[k] * z[k] * q;
+                        d[k] = d[k] * u[k] * q * (1.f + z[k] * (1.f - q));
+                    }
+                    store8<BF16>(p.dZ, row * p.lddz + p.N + col, ncol, du);
+                    if (BIAS)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) su[k] += du[k];
+                } else if (p.dZ) {
+                    widen<BF16>(zg[i], z);
+                    act_grad(d, z, p.act);
+                }
+                if (p.dZ) store8<BF16>(p.dZ, row * p.lddz + col, ncol, d);
                 if (BIAS)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) su[i] += du[i];
-            } else if (p.dZ) {
-                load8<BF16>(p.Z, row * p.ldz + col, ncol, z);
-                act_grad(d, z, p.act);
+                    for (int k = 0; k < 8; ++k) s[k] += d[k];
             }
-            if (p.dZ) store8<BF16>(p.dZ, row * p.lddz + col, ncol, d);
-            if (BIAS)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] += d[i];
         }
-    }
-    if (!BIAS) return;
-    // the warps' sums in order, one column a thread
-    float* dst = p.ws + (int64_t)item * Nw;
-    const int c = cblock * COLS + threadIdx.x;
+        if (!BIAS) continue;
+        // the warps' sums in order, one column a thread
+        float* dst = p.ws + (int64_t)item * Nw;
+        const int c = cblock * COLS + threadIdx.x;
 #pragma unroll
-    for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-        __syncthreads();
+        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sums[warp][lane * 8 + i] = h ? su[i] : s[i];
-        __syncthreads();
-        float t = 0.f;
+            for (int i = 0; i < 8; ++i) sums[warp][lane * 9 + i] = h ? su[i] : s[i];
+            __syncthreads();
+            float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) t += sums[w][threadIdx.x];
-        if (c < p.N) dst[h * p.N + c] = t;
+            for (int q = 0; q < WARPS; ++q) t += sums[q][threadIdx.x / 8 * 9 + threadIdx.x % 8];
+            if (c < p.N) dst[h * p.N + c] = t;
+        }
     }
 }
 
@@ -251,8 +266,8 @@ cudaError_t launch_typed(const ActParams& p, dim3 grid, cudaStream_t s)
 int piece_rows(const LinActArgs& a, int num_sms)
 {
     const int64_t col_blocks = (a.N + COLS - 1) / COLS;
-    const int64_t r = a.M * col_blocks / (8 * (int64_t)num_sms) / WARPS * WARPS;
-    return (int)(r < WARPS ? WARPS : r > 128 ? 128 : r);
+    const int64_t r = a.M * col_blocks / (3 * (int64_t)num_sms) / WARPS * WARPS;
+    return (int)(r < WARPS ? WARPS : r > 32 ? 32 : r);
 }
 
 int64_t items(const LinActArgs& a, int num_sms)
@@ -288,9 +303,11 @@ int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t 
     p.col_blocks = (int)((a.N + COLS - 1) / COLS);
     const int64_t n = items(a, num_sms);
     p.piece = piece_rows(a, num_sms);
+    p.items = (int)n;
     if (n == 0 || a.N == 0) return GEMM_OK;
     if (n * p.col_blocks > 0x7fffffffLL) return GEMM_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)(n * p.col_blocks));
+    const int64_t resident = 3 * (int64_t)num_sms;  // blocks walk the pieces
+    const dim3 grid((unsigned)(n * p.col_blocks < resident ? n * p.col_blocks : resident));
     const bool gated = a.act == GEMM_ACT_SWIGLU;
     const cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true>(p, grid, stream) : launch_typed<true, false>(p, grid, stream))
                                  : (gated ? launch_typed<false, true>(p, grid, stream) : launch_typed<false, false>(p, grid, stream));
