@@ -343,7 +343,8 @@ int gemm_linear_backward(gemm_handle_t h, const gemm_linear_grad_args* args, voi
  *
  * The steps around the grouped products of a mixture-of-experts block: T tokens, E experts,
  * k of them a token.  dtype is GEMM_F32, GEMM_BF16 or GEMM_F16; sums are held in fp32.
- * k <= 32 and E <= 1024, else GEMM_ERR_UNSUPPORTED; T * k must stay below 2^31 - 1024. */
+ * k <= 32, E <= 1024 and N <= 2^30, else GEMM_ERR_UNSUPPORTED; T * k must stay below
+ * 2^31 - 1024. */
 
 /* For each token the k largest logits, in descending order; equal logits (and +0, -0) by
  * the lower index, NaN before everything.  A logit of -inf is an expert that is not there:

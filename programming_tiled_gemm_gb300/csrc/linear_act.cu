@@ -305,7 +305,7 @@ int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t 
     p.piece = piece_rows(a, num_sms);
     p.items = (int)n;
     if (n == 0 || a.N == 0) return GEMM_OK;
-    if (n * p.col_blocks > 0x7fffffffLL) return GEMM_ERR_UNSUPPORTED;
+    if (n * p.col_blocks > 0x7fff0000LL) return GEMM_ERR_UNSUPPORTED;  // (room for a stride beyond)
     const int64_t resident = 3 * (int64_t)num_sms;  // blocks walk the pieces
     const dim3 grid((unsigned)(n * p.col_blocks < resident ? n * p.col_blocks : resident));
     const bool gated = a.act == GEMM_ACT_SWIGLU;

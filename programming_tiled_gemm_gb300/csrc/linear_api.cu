@@ -264,7 +264,7 @@ int check_exchange(gemm_handle_t h, int64_t T, int64_t N, int64_t k, int dtype)
     if (!h || N < 0 || !known_dtype(dtype)) return GEMM_ERR_INVALID_ARG;
     const int rc = check_routing(T, k);
     if (rc != GEMM_OK) return rc;
-    return N > kLim32 ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+    return N > (1 << 30) ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
 }
 
 int dispatch_impl(gemm_handle_t h, int64_t T, int64_t N, int64_t k, const void* x, int64_t ldx, int dtype,

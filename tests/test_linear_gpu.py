@@ -156,6 +156,81 @@ def test_strides_and_alignment(lib, act):
     assert lib.device_status() == 0
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 1, 1), (33, 13, 21), (300, 67, 259)])
+def test_odd_sizes_in_padded_rows(lib, M, K, N):
+    """K and N that are no multiples of anything: only the rows' starts are aligned."""
+    gen = gen_of(M, K, N, 2)
+
+    def padded(rows, cols, scale=1.0):
+        t = torch.full((rows, (cols + 7) // 8 * 8), math.nan, device="cuda", dtype=torch.float16)
+        t[:, :cols] = randn(gen, rows, cols, scale=scale)
+        return t[:, :cols]
+
+    x, w, z, dy = padded(M, K), padded(K, N, K ** -0.5), padded(M, N), padded(M, N)
+    b, r = randn(gen, N, dtype=torch.float16), randn(gen, M, N, dtype=torch.float16)
+    y, zk = lib.linear(x, w, bias=b, act="silu", residual=r, save_preact=True)
+    check_forward(y, zk, x, w, b, "silu", r)
+    dx, dw, db = lib.linear_backward(dy, x, w, z=z, act="silu", bias=True)
+    check_grads(dx, dw, db, dy, x, w, z, "silu")
+    assert lib.device_status() == 0
+
+
+def test_offsets_past_32_bits(lib):
+    """Results and weights of more than 2^31 elements: the last rows and the last group."""
+    gen = gen_of(10)
+    M, K, N = 270_000, 64, 8192
+    x, w = randn(gen, M, K, dtype=torch.bfloat16), randn(gen, K, N, dtype=torch.bfloat16, scale=K ** -0.5)
+    y, z = lib.linear(x, w, act="silu", save_preact=True)
+    assert y.numel() > 2 ** 31
+    check_forward(y[-300:], z[-300:], x[-300:], w, None, "silu", None)
+    dx, _, _ = lib.linear_backward(y, x, w, z=z, act="silu", need_dw=False)
+    check_grads(dx[-300:], None, None, y[-300:], x[-300:], w, z[-300:], "silu")
+    del y, z, dx
+    G, K, N = 36, 8192, 8192
+    counts = [1] * (G - 1) + [70]
+    x, dy = randn(gen, sum(counts), K, dtype=torch.bfloat16), randn(gen, sum(counts), N, dtype=torch.bfloat16)
+    w = torch.zeros(G, K, N, device="cuda", dtype=torch.bfloat16)
+    w[-1] = randn(gen, K, N, dtype=torch.bfloat16, scale=K ** -0.5)
+    assert w.numel() > 2 ** 31
+    y = lib.grouped_linear(x, w, offsets_of(counts))
+    check_forward(y[-70:], None, x[-70:], w[-1], None, "none", None)
+    dx, dw, _ = lib.grouped_linear_backward(dy, x, w, offsets_of(counts))
+    check_grads(dx[-70:], dw[-1], None, dy[-70:], x[-70:], w[-1], y[-70:], "none")
+    check_grads(dx[:1], dw[0], None, dy[:1], x[:1], w[0], y[:1], "none")
+    assert lib.device_status() == 0
+
+
+def test_long_reductions(lib):
+    """Beyond 16384 of K the sum is cut into chunks for 16-bit results too."""
+    gen = gen_of(11)
+    for M, K, N in ((24, 20000, 264), (200, 16384, 72), (130, 16392, 72)):
+        x, w = randn(gen, M, K, dtype=torch.float16), randn(gen, K, N, dtype=torch.float16, scale=K ** -0.5)
+        y, z = lib.linear(x, w, act="gelu", save_preact=True)
+        check_forward_any(y, z, x, w, "gelu")
+
+
+def check_forward_any(y, z_out, x, w, act):
+    """check_forward for a sum in one accumulator: 2^-23 of S lost at most every 16 of K."""
+    z = x.double() @ w.double()
+    zt = (x.shape[1] / 16 + 4) * 2.0 ** -23 * (x.double().abs() @ w.double().abs())
+    assert_within(z_out, z, zt + UNIT[z_out.dtype] * (z.abs() + zt) + 2.0 ** -25)
+    ref, tol = act64(z, act), 1.13 * zt + 2.0 ** -19 * (1 + z.abs())
+    assert_within(y, ref, tol + UNIT[y.dtype] * (ref.abs() + tol) + 2.0 ** -25)
+
+
+def test_groups_without_rows(lib):
+    """All offsets zero: nothing is written but the gradients' zeros."""
+    gen = gen_of(12)
+    x, w = randn(gen, 20, 64, dtype=torch.bfloat16), randn(gen, 3, 64, 32, dtype=torch.bfloat16)
+    off = torch.zeros(4, device="cuda", dtype=torch.int32)
+    out = torch.full((20, 32), 2.0, device="cuda", dtype=torch.bfloat16)
+    lib.grouped_linear(x, w, off, out=out)
+    assert (out == 2).all()
+    _, dw, db = lib.grouped_linear_backward(out, x, w, off, bias=True)
+    assert (dw == 0).all() and (db == 0).all()
+    assert lib.device_status() == 0
+
+
 def test_empty_sizes(lib):
     x, w = torch.zeros(0, 64, device="cuda", dtype=torch.bfloat16), torch.ones(64, 32, device="cuda", dtype=torch.bfloat16)
     assert lib.linear(x, w).shape == (0, 32)
@@ -264,6 +339,8 @@ def check_grads(dx, dw, db, dy, x, w, z, act):
     aw, ax = w.double().abs(), x.double().abs()
     tol = zt @ aw.t() + sum_tol(w.shape[1], dz.abs() @ aw.t())
     assert_within(dx, rx, tol + u * (rx.abs() + tol) + 2.0 ** -25)
+    if dw is None:
+        return
     tol = ax.t() @ zt + sum_tol(M, ax.t() @ dz.abs())
     assert_within(dw, rw, tol + UNIT[dw.dtype] * (rw.abs() + tol) + 2.0 ** -25)
     if db is not None:

@@ -250,6 +250,25 @@ def test_exchange_strides_and_in_place(lib):
         assert torch.isnan(X[shift:].view(T, N + pad)[:, N:]).all()
 
 
+def test_exchange_past_32_bits(lib):
+    """More than 2^31 elements on the experts' side: the last rows."""
+    T, N, k = 140_000, 8192, 2
+    x = torch.zeros(T, N, device="cuda", dtype=torch.bfloat16)
+    x[-2:] = torch.randn(2, N, generator=gen_of(6), device="cuda")
+    rows = torch.arange(T * k, device="cuda", dtype=torch.int32)  # each pick at its own place
+    slots = rows.view(T, k)
+    xr = lib.moe_dispatch(x, rows, k)
+    assert xr.numel() > 2 ** 31 and torch.equal(xr[-4:], x[-2:].repeat_interleave(2, 0)) and (xr[:4] == 0).all()
+    w = torch.ones(T, k, device="cuda")
+    out = lib.moe_combine(xr, slots, w)
+    assert torch.equal(out[-2:], (2 * x[-2:].float()).bfloat16())
+    dy, dw = lib.moe_combine_backward(x, xr, slots, rows, w)
+    assert torch.equal(dy[-4:], xr[-4:])
+    ref = (x[-2:].double() ** 2).sum(1, keepdim=True).expand(2, k)
+    assert ((dw[-2:].double() - ref).abs() <= (N + 8) * 2.0 ** -24 * ref).all()
+    assert lib.device_status() == 0
+
+
 def test_empty_and_refusals(g, lib):
     e = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
     i32 = dict(dtype=torch.int32)
