@@ -17,8 +17,8 @@
 // different TMEM lanes, and each pair of epilogue warps swaps half of its columns through
 // shared memory.
 //
-// Pipeline, as in the plain product's CTA-pair kernel: a producer warp per CTA (TMA, ring
-// of stages), one MMA thread a pair, eight epilogue warps a CTA.  The tensor core's fp32
+// Pipeline, as in the plain product's CTA-pair kernel: TMA producers, a ring of stages, one
+// warp a pair that issues MMAs, eight epilogue warps a CTA.  The tensor core's fp32
 // accumulation rounds toward zero: 2^-24 of the sum lost per 16 of K.  For fp32 results, and
 // for more than 16384 of K, it is cut into chunks of `kc` k-blocks (16: 1024 of K, as in the
 // plain product), each in a fresh TMEM accumulator, added in fp32 round-to-nearest registers
@@ -35,10 +35,6 @@
 // kLinDw over groups: a group's last k-block ends inside the next group's rows.  Those rows
 // are zeroed in shared memory, in both operands (zero times a neighbour's NaN would be NaN),
 // by a fixer warp before the MMAs may read the stage.
-//
-// Few rows: MMAs of 16 .. 128 columns into one accumulator wait for each other (175 cycles
-// each at 16 columns, ten times their own work), so the steps of 16 along K go round robin
-// to 256 / w (up to 4) accumulators, which the epilogue adds in order.
 //
 // Every wait is bounded; on expiry the status word is set and the CTA drains and returns.
 #include <cuda.h>
@@ -71,24 +67,14 @@ constexpr int STG_BYTES = 2048;       // an epilogue warp's staging block: 32 ro
                                       // or (gated) 16 columns of fp32 for the other warp
 constexpr int SMEM_MAX = 232448;      // 227 KiB
 
-// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; then the epilogue's, which
-// take registers from the first four.  dW's plain epilogue runs on 16 warps: with 8 it took
-// longer than the MMAs of a tile reduced over 500 rows.
-constexpr int EPI_WARP0 = 4;
-struct Roles {
-    int epi_warps, launch_regs, lean_regs, epi_regs;
-    __host__ __device__ constexpr int threads() const { return 32 * (EPI_WARP0 + epi_warps); }
-};
-__host__ __device__ constexpr Roles roles(int mode, bool chunked)
-{
-    return mode == kLinDw && !chunked ? Roles{16, 96, 64, 104} : Roles{8, 168, 80, 208};
-}
-// (setmaxnreg draws on the registers the block is launched with; checked before the launch)
-constexpr bool balanced(Roles r)
-{
-    return 4 * r.lean_regs + r.epi_warps * r.epi_regs <= (EPI_WARP0 + r.epi_warps) * r.launch_regs;
-}
-static_assert(balanced(roles(kLinFwd, true)) && balanced(roles(kLinDw, false)), "registers beyond the block's own");
+// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; 4..11: epilogue, which takes
+// registers from the first four: 80 + 2 * 208 a thread of the three warpgroups are within
+// the 3 * 168 the block is launched with (checked before the launch).
+constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
+constexpr int EPI_GROUPS = EPI_WARPS / 4;  // four warps cover the TMEM lanes
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int LAUNCH_REGS = 168, LEAN_REGS = 80, EPI_REGS = 208;
+static_assert(LEAN_REGS + 2 * EPI_REGS <= 3 * LAUNCH_REGS, "the epilogue's registers come from the block's own");
 
 struct LinParams {
     int M;       // rows of X
@@ -122,13 +108,6 @@ struct LinParams {
     int test_stall;
 };
 
-// Accumulators a tile's MMAs take turns on (kLinDw's last k-block may have fewer steps
-// than accumulators, and its tiles are wide).
-__host__ __device__ constexpr int accumulators(int mode, int w)
-{
-    return mode == kLinDw ? 1 : w <= MAX_W / 4 ? 4 : w <= MAX_W / 2 ? 2 : 1;
-}
-
 // The width of `rows` rows' tiles of at most `wcap` (a multiple of 16): equal ones, so that
 // 300 rows are 160 + 140, not 256 + 44.  (kLinDw: wcap itself.  Its rows lie along a line of
 // X, and copies from the middle of 128-byte lines took twice the time: 1.17 ms instead of
@@ -142,25 +121,31 @@ __host__ __device__ inline int tile_width(int mode, int rows, int wcap)
     return (int)((w + 15) / 16 * 16);
 }
 
-// Estimated cycles, from measurements: a k-block of a tile of w rows (its MMAs and loads, or
-// their issue), and what cutting a tile into S slices along K costs (their publication,
-// the addition and its latencies: 3.6 us for 9 slices of 16 rows, 6.6 us for 2 of 64, 20 us
-// for 2 of 256).
+// Estimated cycles, fitted to measurements: a k-block of a tile of w rows (its MMAs and loads,
+// or their issue: 0.18 us up to 160 rows, 0.26 us for 256), and what cutting a tile into S
+// slices along K costs: their publication, the count and the addition, six slices' loads at a
+// time (2.5 us for 2 to 6 slices of 16 rows, 4.4 us of 64, 12.8 us of 256).
+constexpr int SUM_DEEP = 6;
 __host__ __device__ inline int kb_cycles(int w) { return w < 165 ? 355 : 67 + w * 7 / 4; }
-__host__ __device__ inline int split_cycles(int S, int w) { return S > 1 ? 4900 + w * (78 + 24 * S) : 0; }
+__host__ __device__ inline int split_cycles(int S, int w)
+{
+    return S < 2 ? 0 : 3500 + w * (74 + 5 * S + 60 * ((S - 1) / SUM_DEEP));
+}
 
-// K slices of each of the last wave's `rem` tiles of kb k-blocks (1: whole): at most one
-// slice a pair, about as many as balance their addition with the k-blocks saved, and none
-// that costs more than it saves.
+// K slices of each of the last wave's `rem` tiles of kb k-blocks (1: whole), at most one a
+// pair: one or two rounds of additions, where that costs less than it saves.
 __host__ __device__ inline int slices(int rem, int kb, int pairs, int w)
 {
     if (rem <= 0 || w <= 0) return 1;
-    int S = pairs / rem;
-    const int balanced = (int)sqrtf((float)kb * kb_cycles(w) / (24.f * w));
-    if (S > balanced) S = balanced;
-    if (S > kb / 2) S = kb / 2;
-    if (S < 2 || (kb - (kb + S - 1) / S) * (int64_t)kb_cycles(w) <= split_cycles(S, w)) return 1;
-    return S;
+    int best = 1;
+    int64_t least = (int64_t)kb * kb_cycles(w);
+    for (int round = 1; round <= 2; ++round) {
+        const int S = min(min(pairs / rem, kb / 2), round * SUM_DEEP);
+        if (S < 2) break;
+        const int64_t t = (int64_t)((kb + S - 1) / S) * kb_cycles(w) + split_cycles(S, w);
+        if (t < least) least = t, best = S;
+    }
+    return best;
 }
 
 struct Item {
@@ -485,11 +470,9 @@ __device__ __forceinline__ void store_f32(const float* R, int64_t ldr, float* ou
 }
 
 template <int MODE, bool GATED, bool BF16, bool CHUNKED>
-__global__ void __launch_bounds__(roles(MODE, CHUNKED).threads(), 1)
+__global__ void __launch_bounds__(THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p)
 {
-    constexpr Roles ROLES = roles(MODE, CHUNKED);
-    constexpr int EPI_WARPS = ROLES.epi_warps, EPI_GROUPS = EPI_WARPS / 4;  // a group covers the TMEM lanes
     constexpr bool A_MN = MODE != kLinDx, B_MN = MODE == kLinDw;
     constexpr int TILE_F = GATED ? CTA_F : 2 * CTA_F;  // output features of a tile
     extern __shared__ uint8_t smem_raw[];
@@ -557,78 +540,76 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     bool aborted = false;
 
     if (warp < EPI_WARP0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLES.lean_regs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LEAN_REGS));
         if (warp == 0 || warp == 3) {
             // ---------------------------------------------------------------- producers
             // warp 0 loads A (and announces a stage's bytes), warp 3 loads B: one thread issuing
             // all of a stage's copies was what the MMAs waited for
             // (whole warps walk and one elected lane issues, as the MMA warp)
-            {
-                Walk<MODE> walk(p, off, cum, pair, npairs);
-                Item it;
-                int stage = 0;
-                uint32_t phase = 0;
-                bool ok = true;
-                const bool load_a = warp == 0;
-                const uint32_t a_base = smem_u32(smem_a), b_base = smem_u32(smem_b);
-                const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0), tail_own = mapa_shared(smem_u32(tail_bar), rank);
-                while (ok && walk.next(it)) {
-                    const int f0 = it.f0 * TILE_F;
-                    const int half = it.w / 2;
-                    const int nb = B_MN ? (half + 63) / 64 : (half + p.bx - 1) / p.bx;
-                    const uint32_t b_box = B_MN ? BOX_BYTES : p.bx * 128;
-                    const uint32_t bytes = A_BYTES + nb * b_box;
-                    const int b_row = it.row0 + (int)rank * half;
-                    // A's two boxes of 64 features (kLinDx: one of 128 rows of W)
-                    const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
-                    const int fa2 = GATED ? p.F + fa : fa + 64;
-                    for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
-                            record_error(p.status, kDevTimeoutProducer, abort_flag);
-                            ok = false;
-                            break;
-                        }
-                        // a k-block that ends inside the next group's rows goes through the fixer
-                        const bool tail = MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK;
-                        // (the even CTA alone announces both CTAs' bytes: arrivals from the odd one,
-                        // released at cluster scope, took the kernel from 0.71 to 1.66 ms at 8192^3)
-                        const uint32_t bar = (tail ? tail_own : full0) + stage * 8;
-                        const int k = (MODE == kLinDw ? it.red0 : 0) + kb * BK;
-                        if (elect_one()) {
-                            if (load_a) {
-                                if (tail) mbar_arrive_expect_tx(smem_u32(&tail_bar[stage]), bytes);
-                                else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
-                                const uint32_t dst = a_base + stage * A_BYTES;
-                                if (MODE == kLinFwd) {
-                                    tma_load_3d_pair(dst, &tmA, bar, fa, k, it.g);
-                                    tma_load_3d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k, it.g);
-                                } else if (MODE == kLinDx) {
-                                    tma_load_3d_pair(dst, &tmA, bar, k, fa, it.g);
-                                } else {
-                                    tma_load_2d_pair(dst, &tmA, bar, fa, k);
-                                    tma_load_2d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k);
-                                }
+            Walk<MODE> walk(p, off, cum, pair, npairs);
+            Item it;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const bool load_a = warp == 0;
+            const uint32_t a_base = smem_u32(smem_a), b_base = smem_u32(smem_b);
+            const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0), tail_own = mapa_shared(smem_u32(tail_bar), rank);
+            while (ok && walk.next(it)) {
+                const int f0 = it.f0 * TILE_F;
+                const int half = it.w / 2;
+                const int nb = B_MN ? (half + 63) / 64 : (half + p.bx - 1) / p.bx;
+                const uint32_t b_box = B_MN ? BOX_BYTES : p.bx * 128;
+                const uint32_t bytes = A_BYTES + nb * b_box;
+                const int b_row = it.row0 + (int)rank * half;
+                // A's two boxes of 64 features (kLinDx: one of 128 rows of W)
+                const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
+                const int fa2 = GATED ? p.F + fa : fa + 64;
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
+                        record_error(p.status, kDevTimeoutProducer, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    // a k-block that ends inside the next group's rows goes through the fixer
+                    const bool tail = MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK;
+                    // (the even CTA alone announces both CTAs' bytes: arrivals from the odd one,
+                    // released at cluster scope, took the kernel from 0.71 to 1.66 ms at 8192^3)
+                    const uint32_t bar = (tail ? tail_own : full0) + stage * 8;
+                    const int k = (MODE == kLinDw ? it.red0 : 0) + kb * BK;
+                    if (elect_one()) {
+                        if (load_a) {
+                            if (tail) mbar_arrive_expect_tx(smem_u32(&tail_bar[stage]), bytes);
+                            else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
+                            const uint32_t dst = a_base + stage * A_BYTES;
+                            if (MODE == kLinFwd) {
+                                tma_load_3d_pair(dst, &tmA, bar, fa, k, it.g);
+                                tma_load_3d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k, it.g);
+                            } else if (MODE == kLinDx) {
+                                tma_load_3d_pair(dst, &tmA, bar, k, fa, it.g);
                             } else {
-                                const uint32_t dst = b_base + stage * p.b_bytes;
-                                if (B_MN) {
-                                    tma_load_2d_pair(dst, &tmB, bar, b_row, k);
-                                    if (nb > 1) tma_load_2d_pair(dst + BOX_BYTES, &tmB, bar, b_row + 64, k);
-                                } else {
-                                    tma_load_2d_pair(dst, &tmB, bar, k, b_row);
-                                    for (int i = 1; i < nb; ++i)
-                                        tma_load_2d_pair(dst + i * b_box, &tmB, bar, k, b_row + i * p.bx);
-                                }
+                                tma_load_2d_pair(dst, &tmA, bar, fa, k);
+                                tma_load_2d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k);
+                            }
+                        } else {
+                            const uint32_t dst = b_base + stage * p.b_bytes;
+                            if (B_MN) {
+                                tma_load_2d_pair(dst, &tmB, bar, b_row, k);
+                                if (nb > 1) tma_load_2d_pair(dst + BOX_BYTES, &tmB, bar, b_row + 64, k);
+                            } else {
+                                tma_load_2d_pair(dst, &tmB, bar, k, b_row);
+                                for (int i = 1; i < nb; ++i)
+                                    tma_load_2d_pair(dst + i * b_box, &tmB, bar, k, b_row + i * p.bx);
                             }
                         }
-                        __syncwarp();
-                        if (++stage == p.stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                    }
+                    __syncwarp();
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1;
                     }
                 }
-                if (!ok) aborted = true;
             }
+            if (!ok) aborted = true;
             __syncwarp();
         } else if (warp == 1) {
             // ---------------------------------------------------------------- MMA issuer (even CTA)
@@ -647,8 +628,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 const uint64_t b_desc0 = smem_desc_sw128(smem_u32(smem_b), B_MN ? BOX_BYTES : 16, 1024);
                 while (ok && walk.next(it)) {
                     const uint32_t idesc = p.idesc | ((uint32_t)(it.w >> 3) << 17);
-                    const int turns = accumulators(MODE, it.w);
-                    const uint32_t turn_cols = MAX_W / turns;
                     const int kc = CHUNKED ? p.kc : it.kb1 - it.kb0;
                     for (int kb0 = it.kb0; kb0 < it.kb1 && ok; kb0 += kc) {
                         if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&tempty_bar[buf]), buf_phase ^ 1, p.limit_ns,
@@ -684,8 +663,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 #pragma unroll
                                 for (int k = 0; k < BK / UMMA_K; ++k)
                                     if (MODE != kLinDw || k < steps)
-                                        umma_f16_pair(d_tmem + (k & (turns - 1)) * turn_cols, a_desc + k * (A_STEP >> 4),
-                                                      b_desc + k * (B_STEP >> 4), idesc, (kb > kb0 || k >= turns) ? 1u : 0u);
+                                        umma_f16_pair(d_tmem, a_desc + k * (A_STEP >> 4), b_desc + k * (B_STEP >> 4), idesc,
+                                                      (kb > kb0 || k > 0) ? 1u : 0u);
                                 umma_commit_mask(smem_u32(&empty_bar[stage]), pair_mask);
                             }
                             __syncwarp();
@@ -756,10 +735,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(ROLES.epi_regs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
         // ---------------------------------------------------------------- epilogue (both CTAs)
         const int q = warp & 3;             // TMEM lane quarter
-        const int half = (warp - EPI_WARP0) >> 2;   // takes column blocks half, half + EPI_GROUPS, ...
+        const int group = (warp - EPI_WARP0) / 4;   // takes column blocks group, group + 2, ...
         const int e = threadIdx.x - 32 * EPI_WARP0;
         uint32_t* stg = reinterpret_cast<uint32_t*>(after + (warp - EPI_WARP0) * STG_BYTES);
         int buf = 0;
@@ -779,28 +758,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         Item it;
         float acc[CHUNKED ? 2 : 1][32];  // one chunk: blocks come straight from tensor memory
         while (walk.next(it)) {
-            const int turns = accumulators(MODE, it.w);
-            // columns of a warp's block: few rows are shared by all the groups
-            const int bw = it.w <= 8 * EPI_GROUPS ? 8 : it.w <= 16 * EPI_GROUPS ? 16 : 32, cb0 = half * bw;
-            const int cb_step = EPI_GROUPS * bw;
-            // columns cb .. cb + 31 of the finished accumulator, its turns added in order
-            const auto block_sum = [&](int cb, float(&v)[32]) {
-                const uint32_t t_addr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAX_W + cb);
-                if (!CHUNKED && turns == 1) {
-                    uint32_t u[32];
-                    tmem_ld_32x32b_x32(t_addr, u);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                    return;
-                }
-                for (int r = 0; r < turns; ++r) {
-                    uint32_t u[32];
-                    tmem_ld_32x32b_x32(t_addr + r * (MAX_W / turns), u);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __fadd_rn(v[i], __uint_as_float(u[i]));
-                }
+            // columns of a warp's block: up to 32 rows are shared by both groups
+            const int bw = it.w <= 16 ? 8 : it.w <= 32 ? 16 : 32, cb0 = group * bw, cb_step = EPI_GROUPS * bw;
+            // columns cb .. cb + 31 of the finished accumulator
+            const auto fetch_block = [&](int cb, uint32_t(&u)[32]) {
+                tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAX_W + cb), u);
+                tmem_ld_wait();
             };
             const auto wait_full = [&] {
                 bool ok = dead ? false : mbar_wait(smem_u32(&tfull_bar[buf]), buf_phase, p.limit_ns, abort_flag);
@@ -832,7 +795,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if (dead) break;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if (cb0 + j * cb_step < it.w) block_sum(cb0 + j * cb_step, acc[j]);
+                        if (cb0 + j * cb_step < it.w) {
+                            uint32_t u[32];
+                            fetch_block(cb0 + j * cb_step, u);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) acc[j][i] = __fadd_rn(acc[j][i], __uint_as_float(u[i]));
+                        }
                     release();
                 }
             } else if (any) {
@@ -858,8 +826,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     } else {
 #pragma unroll 1
                         for (int cb = cb0; cb < it.w; cb += cb_step) {
-                            float v[32] = {};
-                            block_sum(cb, v);
+                            uint32_t u[32];
+                            fetch_block(cb, u);
+                            float v[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
                             publish(cb, v);
                         }
                         release();
@@ -912,18 +883,20 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 // addition needs the registers: after it)
                 if (residual) mr = block(p.R, p.ldr, fw, cb + own, cb + bw, p.vec_r);
                 if (residual && it.part < 0) ahead.load(mr, lane);
-                if (!CHUNKED) {
+                if (fetch) {
+                    uint32_t u[32];
+                    fetch_block(cb, u);
+                    if (cb + cb_step >= it.w) release();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                } else if (!CHUNKED) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                    if (fetch) {
-                        block_sum(cb, v);
-                        if (cb + cb_step >= it.w) release();
-                    }
                 }
                 if (it.part >= 0) {
                     // every slice, this CTA's own included, is read back, COLS columns of DEEP slices
                     // at a time so that their latencies overlap, and added in K order
-                    constexpr int DEEP = CHUNKED ? 4 : EPI_WARPS > 8 ? 2 : 6, COLS = 8;
+                    constexpr int DEEP = CHUNKED ? 4 : SUM_DEEP, COLS = 8;
                     const int S = walk.slices_of_tile();
 #pragma unroll
                     for (int h = 0; h < 32; h += COLS) {
@@ -975,17 +948,17 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     const bool up = q >= 2;
                     float* mine = reinterpret_cast<float*>(stg) + lane;
                     const float* other = reinterpret_cast<const float*>(
-                                             after + ((warp - EPI_WARP0) + (up ? -2 : 2)) * STG_BYTES) + lane;
+                                             after + (warp - EPI_WARP0 + (up ? -2 : 2)) * STG_BYTES) + lane;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) mine[i * 32] = up ? v[i] : v[16 + i];
-                    named_barrier(2 + (q & 1) + 2 * half, 64);
+                    named_barrier(2 + (q & 1) + 2 * group, 64);
                     float h[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float o = other[i * 32];
                         h[i] = up ? silu(o) * v[16 + i] : silu(v[i]) * o;
                     }
-                    named_barrier(2 + (q & 1) + 2 * half, 64);
+                    named_barrier(2 + (q & 1) + 2 * group, 64);
                     finish(h);
                 } else {
                     if (MODE == kLinFwd) activate(v, p.act);
@@ -1093,7 +1066,7 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
     pl.bx = typical < 8 ? 8 : (typical + 7) / 8 * 8;
     const int b_rows = (pl.wmax / 2 + pl.bx - 1) / pl.bx * pl.bx;
     pl.b_bytes = a.mode == kLinDw ? (pl.wmax / 2 + 63) / 64 * BOX_BYTES : (b_rows * 128 + 1023) / 1024 * 1024;
-    const int fixed = 1024 + roles(a.mode, chunked).epi_warps * STG_BYTES + (4 * MAX_STAGES + 6) * 8 + 16 + 2 * (G + 1) * 4 + 16;
+    const int fixed = 1024 + EPI_WARPS * STG_BYTES + (4 * MAX_STAGES + 6) * 8 + 16 + 2 * (G + 1) * 4 + 16;
     pl.stages = (SMEM_MAX - fixed) / (A_BYTES + pl.b_bytes);
     if (pl.stages > MAX_STAGES) pl.stages = MAX_STAGES;
     pl.smem = fixed + pl.stages * (A_BYTES + pl.b_bytes);
@@ -1113,13 +1086,12 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
                   cudaStream_t stream)
 {
     static std::atomic<int> fit{0};
-    constexpr Roles ROLES = roles(MODE, CHUNKED);
     auto kern = linear_pair_kernel<MODE, GATED, BF16, CHUNKED>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess)
         return GEMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(ROLES.threads(), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.dynamicSmemBytes = SMEM_MAX;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1136,7 +1108,7 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
     if (clusters == 0) {
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return GEMM_ERR_CUDA;
-        if (fa.numRegs < ROLES.launch_regs) return GEMM_ERR_UNSUPPORTED;  // the epilogue would wait for registers
+        if (fa.numRegs < LAUNCH_REGS) return GEMM_ERR_UNSUPPORTED;  // the epilogue would wait for registers
         if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) {
             (void)cudaGetLastError();
             return GEMM_ERR_CUDA;
