@@ -57,7 +57,7 @@ constexpr int BK = 64;                // k per stage: one 128-byte swizzle row o
 constexpr int UMMA_K = 16;
 constexpr int CTA_F = 128;            // features (MMA rows) of one CTA
 constexpr int MAX_W = 256;            // rows (MMA columns) of a tile
-constexpr int MAX_W_CHUNKED = 128;    // and with chunks, whose sums an epilogue thread holds: 64 of them
+constexpr int NARROW_W = 128;         // and with chunks, whose sums an epilogue thread holds: 64 of them
 constexpr int A_BYTES = CTA_F * BK * 2;  // 16 KiB a stage
 constexpr int BOX_BYTES = 64 * BK * 2;   // 64 x 64 box of an MN-major operand
 constexpr int MAX_STAGES = 12;
@@ -122,11 +122,11 @@ __host__ __device__ inline int tile_width(int mode, int rows, int wcap)
 }
 
 // Estimated cycles, fitted to measurements: a k-block of a tile of w rows (its MMAs and loads,
-// or their issue: 0.18 us up to 160 rows, 0.26 us for 256), and what cutting a tile into S
+// or their issue: 0.14 us up to 64 rows, 0.2 us for 160, 0.26 us for 256), and what cutting a tile into S
 // slices along K costs: their publication, the count and the addition, six slices' loads at a
 // time (2.5 us for 2 to 6 slices of 16 rows, 4.4 us of 64, 12.8 us of 256).
 constexpr int SUM_DEEP = 6;
-__host__ __device__ inline int kb_cycles(int w) { return w < 165 ? 355 : 67 + w * 7 / 4; }
+__host__ __device__ inline int kb_cycles(int w) { return w <= 64 ? 270 : w <= 178 ? 380 : 67 + w * 7 / 4; }
 __host__ __device__ inline int split_cycles(int S, int w)
 {
     return S < 2 ? 0 : 3500 + w * (74 + 5 * S + 60 * ((S - 1) / SUM_DEEP));
@@ -469,7 +469,8 @@ __device__ __forceinline__ void store_f32(const float* R, int64_t ldr, float* ou
         if (i < n) out[i * ldo] = v[i];
 }
 
-template <int MODE, bool GATED, bool BF16, bool CHUNKED>
+// KPS: k-blocks of a stage, which are waited for and committed together.
+template <int MODE, bool GATED, bool BF16, bool CHUNKED, int KPS>
 __global__ void __launch_bounds__(THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, LinParams p)
 {
@@ -479,8 +480,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     uint8_t* smem_a = smem;
-    uint8_t* smem_b = smem + p.stages * A_BYTES;
-    uint8_t* after = smem_b + p.stages * p.b_bytes;
+    uint8_t* smem_b = smem + p.stages * KPS * A_BYTES;
+    uint8_t* after = smem_b + p.stages * KPS * p.b_bytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(after + EPI_WARPS * STG_BYTES);
     uint64_t* full_bar = bars;                     // (used in the even CTA)
     uint64_t* empty_bar = bars + MAX_STAGES;       // (both CTAs, multicast)
@@ -564,7 +565,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 // A's two boxes of 64 features (kLinDx: one of 128 rows of W)
                 const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
                 const int fa2 = GATED ? p.F + fa : fa + 64;
-                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                for (int kb = it.kb0; kb < it.kb1; kb += KPS) {
                     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
                         record_error(p.status, kDevTimeoutProducer, abort_flag);
                         ok = false;
@@ -575,30 +576,34 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     // (the even CTA alone announces both CTAs' bytes: arrivals from the odd one,
                     // released at cluster scope, took the kernel from 0.71 to 1.66 ms at 8192^3)
                     const uint32_t bar = (tail ? tail_own : full0) + stage * 8;
-                    const int k = (MODE == kLinDw ? it.red0 : 0) + kb * BK;
+                    const int n = KPS == 1 ? 1 : min(KPS, it.kb1 - kb);
                     if (elect_one()) {
                         if (load_a) {
                             if (tail) mbar_arrive_expect_tx(smem_u32(&tail_bar[stage]), bytes);
-                            else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
-                            const uint32_t dst = a_base + stage * A_BYTES;
-                            if (MODE == kLinFwd) {
-                                tma_load_3d_pair(dst, &tmA, bar, fa, k, it.g);
-                                tma_load_3d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k, it.g);
-                            } else if (MODE == kLinDx) {
-                                tma_load_3d_pair(dst, &tmA, bar, k, fa, it.g);
-                            } else {
-                                tma_load_2d_pair(dst, &tmA, bar, fa, k);
-                                tma_load_2d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k);
-                            }
-                        } else {
-                            const uint32_t dst = b_base + stage * p.b_bytes;
-                            if (B_MN) {
+                            else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * n * bytes);
+                        }
+#pragma unroll
+                        for (int i = 0; i < KPS; ++i) {
+                            if (i >= n) break;
+                            const int k = (MODE == kLinDw ? it.red0 : 0) + (kb + i) * BK;
+                            const uint32_t dst = (load_a ? a_base : b_base) + (stage * KPS + i) * (load_a ? A_BYTES : p.b_bytes);
+                            if (load_a) {
+                                if (MODE == kLinFwd) {
+                                    tma_load_3d_pair(dst, &tmA, bar, fa, k, it.g);
+                                    tma_load_3d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k, it.g);
+                                } else if (MODE == kLinDx) {
+                                    tma_load_3d_pair(dst, &tmA, bar, k, fa, it.g);
+                                } else {
+                                    tma_load_2d_pair(dst, &tmA, bar, fa, k);
+                                    tma_load_2d_pair(dst + BOX_BYTES, &tmA, bar, fa2, k);
+                                }
+                            } else if (B_MN) {
                                 tma_load_2d_pair(dst, &tmB, bar, b_row, k);
                                 if (nb > 1) tma_load_2d_pair(dst + BOX_BYTES, &tmB, bar, b_row + 64, k);
                             } else {
                                 tma_load_2d_pair(dst, &tmB, bar, k, b_row);
-                                for (int i = 1; i < nb; ++i)
-                                    tma_load_2d_pair(dst + i * b_box, &tmB, bar, k, b_row + i * p.bx);
+                                for (int j = 1; j < nb; ++j)
+                                    tma_load_2d_pair(dst + j * b_box, &tmB, bar, k, b_row + j * p.bx);
                             }
                         }
                     }
@@ -639,7 +644,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                         tc_fence_after();
                         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAX_W);
                         const int kb1 = min(kb0 + kc, it.kb1);
-                        for (int kb = kb0; kb < kb1; ++kb) {
+                        for (int kb = kb0; kb < kb1; kb += KPS) {
                             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, abort_flag))) {
                                 record_error(p.status, kDevTimeoutMma, abort_flag);
                                 ok = false;
@@ -655,16 +660,22 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                                 tails ^= 1u << stage;
                             }
                             tc_fence_after();
-                            const uint64_t a_desc = a_desc0 + (uint32_t)(stage * A_BYTES >> 4);
-                            const uint64_t b_desc = b_desc0 + (uint32_t)(stage * p.b_bytes >> 4);
                             const bool tail = MODE == kLinDw && p.offsets && it.red_rows - kb * BK < BK;
                             const int steps = tail ? (it.red_rows - kb * BK + UMMA_K - 1) / UMMA_K : BK / UMMA_K;
+                            const int n = KPS == 1 ? 1 : min(KPS, kb1 - kb);
                             if (elect_one()) {
 #pragma unroll
-                                for (int k = 0; k < BK / UMMA_K; ++k)
-                                    if (MODE != kLinDw || k < steps)
-                                        umma_f16_pair(d_tmem, a_desc + k * (A_STEP >> 4), b_desc + k * (B_STEP >> 4), idesc,
-                                                      (kb > kb0 || k > 0) ? 1u : 0u);
+                                for (int i = 0; i < KPS; ++i) {
+                                    if (i >= n) break;
+                                    const int at = stage * KPS + i;
+                                    const uint64_t a_desc = a_desc0 + (uint32_t)(at * A_BYTES >> 4);
+                                    const uint64_t b_desc = b_desc0 + (uint32_t)(at * p.b_bytes >> 4);
+#pragma unroll
+                                    for (int k = 0; k < BK / UMMA_K; ++k)
+                                        if (MODE != kLinDw || k < steps)
+                                            umma_f16_pair(d_tmem, a_desc + k * (A_STEP >> 4), b_desc + k * (B_STEP >> 4),
+                                                          idesc, (kb + i > kb0 || k > 0) ? 1u : 0u);
+                                }
                                 umma_commit_mask(smem_u32(&empty_bar[stage]), pair_mask);
                             }
                             __syncwarp();
@@ -1006,7 +1017,7 @@ bool encode(CUtensorMap* map, int rank, const void* base, bool bf16, int64_t d0,
 
 struct LinPlan {
     int rows, F, kb, f_tiles, wcap, wmax, pairs;
-    int bx, b_bytes, stages, smem;
+    int bx, b_bytes, kps, stages, smem;
     bool gated, ragged;
     int split_w;  // 0: the last wave is not cut
     int64_t tiles;  // an upper bound when the groups' rows are only known on the device
@@ -1045,7 +1056,8 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
     pl.f_tiles = (pl.F + tile_f - 1) / tile_f;
     const int G = a.G > 0 ? a.G : 1;
     const bool ragged = pl.ragged = a.G > 0 && a.mode != kLinDw;  // the tiles' widths are known on the device only
-    const int cap = chunked ? MAX_W_CHUNKED : MAX_W;
+    // (groups of few rows on average: narrow tiles, which stream the weights faster)
+    const int cap = chunked || (ragged && a.M <= 64 * (int64_t)G) ? NARROW_W : MAX_W;
     pl.pairs = num_sms / 2;
     pl.wcap = ragged ? cap
               : a.mode == kLinDw && a.G > 0
@@ -1067,9 +1079,14 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
     const int b_rows = (pl.wmax / 2 + pl.bx - 1) / pl.bx * pl.bx;
     pl.b_bytes = a.mode == kLinDw ? (pl.wmax / 2 + 63) / 64 * BOX_BYTES : (b_rows * 128 + 1023) / 1024 * 1024;
     const int fixed = 1024 + EPI_WARPS * STG_BYTES + (4 * MAX_STAGES + 6) * 8 + 16 + 2 * (G + 1) * 4 + 16;
-    pl.stages = (SMEM_MAX - fixed) / (A_BYTES + pl.b_bytes);
+    // Narrow tiles: two k-blocks a stage, so that waiting for it and committing it, some 300
+    // cycles, take less than its copies and MMAs (per k-block 295 cycles instead of 400 at 16
+    // rows, 404 instead of 430 at 160; at 192 it would be 594 instead of 400: three stages).
+    // dW's fixer counts stages by k-block.
+    pl.kps = a.mode != kLinDw && pl.wmax <= 160 ? 2 : 1;
+    pl.stages = (SMEM_MAX - fixed) / (pl.kps * (A_BYTES + pl.b_bytes));
     if (pl.stages > MAX_STAGES) pl.stages = MAX_STAGES;
-    pl.smem = fixed + pl.stages * (A_BYTES + pl.b_bytes);
+    pl.smem = fixed + pl.stages * pl.kps * (A_BYTES + pl.b_bytes);
     // groups' dW tiles have lengths of their own and are not cut
     pl.split_w = a.mode == kLinDw && a.G > 0 ? 0 : pl.wmax;
     if (ragged && a.M > a.G) {
@@ -1081,12 +1098,12 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
 
 // The kernel of one instantiation and the clusters of it that can be resident at once
 // (cached per process: every device a process drives is taken to be the same part).
-template <int MODE, bool GATED, bool BF16, bool CHUNKED>
+template <int MODE, bool GATED, bool BF16, bool CHUNKED, int KPS>
 int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p, int num_sms,
                   cudaStream_t stream)
 {
     static std::atomic<int> fit{0};
-    auto kern = linear_pair_kernel<MODE, GATED, BF16, CHUNKED>;
+    auto kern = linear_pair_kernel<MODE, GATED, BF16, CHUNKED, KPS>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess)
         return GEMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -1131,15 +1148,19 @@ template <bool BF16, bool CHUNKED>
 int launch_typed(int mode, const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p,
                  int num_sms, cudaStream_t s)
 {
-    if (mode == kLinDx) return launch_kernel<kLinDx, false, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
-    if (mode == kLinDw) return launch_kernel<kLinDw, false, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
-    if (pl.gated) return launch_kernel<kLinFwd, true, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
-    return launch_kernel<kLinFwd, false, BF16, CHUNKED>(pl, tmA, tmB, p, num_sms, s);
+    if (mode == kLinDw) return launch_kernel<kLinDw, false, BF16, CHUNKED, 1>(pl, tmA, tmB, p, num_sms, s);
+    if constexpr (!CHUNKED) {  // (chunked tiles are narrow)
+        if (pl.kps == 1) {
+            if (mode == kLinDx) return launch_kernel<kLinDx, false, BF16, false, 1>(pl, tmA, tmB, p, num_sms, s);
+            if (pl.gated) return launch_kernel<kLinFwd, true, BF16, false, 1>(pl, tmA, tmB, p, num_sms, s);
+            return launch_kernel<kLinFwd, false, BF16, false, 1>(pl, tmA, tmB, p, num_sms, s);
+        }
+    }
+    if (mode == kLinDx) return launch_kernel<kLinDx, false, BF16, CHUNKED, 2>(pl, tmA, tmB, p, num_sms, s);
+    if (pl.gated) return launch_kernel<kLinFwd, true, BF16, CHUNKED, 2>(pl, tmA, tmB, p, num_sms, s);
+    return launch_kernel<kLinFwd, false, BF16, CHUNKED, 2>(pl, tmA, tmB, p, num_sms, s);
 }
 
-}  // namespace
-
-namespace {
 bool is_chunked(const LinArgs& a, int kc)
 {
     const int64_t red = a.mode == kLinFwd ? a.K : a.mode == kLinDx ? a.Nw : a.M;
@@ -1176,7 +1197,7 @@ int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* de
     p.bx = pl.bx;
     p.b_bytes = pl.b_bytes;
     p.stages = pl.stages;
-    p.kc = kc > 0 ? kc : 16;
+    p.kc = kc > 0 ? (kc + 1) / 2 * 2 : 16;  // (chunks end on whole stages)
     p.split_w = ws.partials && ws.counters ? pl.split_w : 0;
     p.bias = a.bias;
     p.bias_stride = a.Nw;
