@@ -240,18 +240,18 @@ gemm_status_string = status_string
 
 # ------------------------------------------------------- tensor conveniences (torch)
 
-_DTYPES = None
+_DTYPES = {}
 
 
 def _dtype_code(t):
-    global _DTYPES
-    import torch
-    if _DTYPES is None:
-        _DTYPES = {torch.float32: GEMM_F32, torch.bfloat16: GEMM_BF16, torch.float16: GEMM_F16}
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise TypeError("unsupported input dtype %s" % t.dtype) from None
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        import torch
+        _DTYPES.update({torch.float32: GEMM_F32, torch.bfloat16: GEMM_BF16, torch.float16: GEMM_F16})
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise TypeError("unsupported input dtype %s" % t.dtype)
+    return code
 
 
 def _row_major_2d(t, name):

