@@ -426,7 +426,8 @@ typedef enum {
     GEMM_OPT_WAIT_LIMIT_US = 3, /* 0 default (2 s), else the bounded-wait limit of device waits in microseconds */
     GEMM_OPT_TC_CHUNK = 4,      /* 0 default (16), else the tensor-core accumulation chunk in 64-wide k-blocks
                                    (1..4096): the tensor core's fp32 accumulator is restarted every chunk and
-                                   chunk sums are added in fp32 round-to-nearest */
+                                   chunk sums are added in fp32 round-to-nearest (linear layers: rounded up to
+                                   an even number) */
     GEMM_OPT_TC_PAIR = 5,       /* tensor-core tiles: 0 choose (default: pairs when M > 128; for M <= 128 with
                                    128x256 tiles that fill under half the SMs, K split into 2 to 16 slices,
                                    one CTA each, on a cluster per tile that adds the fp32 partial tiles in
@@ -434,9 +435,9 @@ typedef enum {
                                    128x256 tile, 2 a pair of CTAs (cluster of two) per 256x256 tile.  Any
                                    other value (3 included) is GEMM_ERR_INVALID_ARG */
     GEMM_OPT_TEST_STALL = 6,    /* test hook for failure detection, 0 (default) or 1: the kernels with
-                                   bounded waits (tensor-core GEMMs, linear layers and convolution, TMA skinny GEMM, persistent
-                                   fp32 GEMM) first wait on a
-                                   barrier nothing arrives on; the wait runs out after the wait limit, the
+                                   bounded waits (tensor-core GEMMs, linear layers and convolution, TMA
+                                   skinny GEMM, persistent fp32 GEMM) first wait on a barrier nothing
+                                   arrives on; the wait runs out after the wait limit, the
                                    kernel drains its copies and MMAs, frees its tensor memory, returns,
                                    and gemm_get_device_status reports GEMM_ERR_DEVICE_TIMEOUT.  C is not
                                    written.  No fault, trap or unbounded wait is involved. */

@@ -40,9 +40,7 @@ struct LinArgs {
 // Buffers the handle keeps for the linear kernels.
 struct LinWorkspace {
     float* partials = nullptr;    // K slices of the last wave's tiles
-    size_t partials_bytes = 0;
     unsigned* counters = nullptr;  // arrivals; every launch leaves them zero
-    size_t counters_bytes = 0;
 };
 
 // Workspace bytes of the K-sliced last wave, and counters (of 4 bytes).
@@ -72,9 +70,10 @@ int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t 
 
 // First unit of every group when each group's rows are cut into pieces of `unit` rows (at
 // least `least` of them) and every piece counts `per` units: cum[g] for g = 0 .. G, and the
-// rows' clamped bounds in off[0 .. G].  unit = 0: `per` units a group whatever its rows.  Every thread of the block calls it; `cum` and `off` are shared memory, read
-// after the caller's next block barrier.  Offsets are clamped to [0, M] and to their running
-// maximum, so that wrong ones give wrong results but no access outside the operands.
+// rows' clamped bounds in off[0 .. G].  unit = 0: `per` units a group whatever its rows.
+// Every thread of the block calls it; `cum` and `off` are shared memory, read after the
+// caller's next block barrier.  Offsets are clamped to [0, M] and to their running maximum,
+// so that wrong ones give wrong results but no access outside the operands.
 __device__ __forceinline__ int group_units(int rows, int unit, int per, int least)
 {
     if (unit == 0) return per;

@@ -7,7 +7,7 @@
 // rows' loads in flight a warp, keep a piece's column sums in registers and leave them in
 // the workspace; a second, small launch adds a group's pieces in order.  (Adding them in the
 // block that counts last took 10 us more at 4096 x 4096: one block reads what many can.)
-// 4096 x 4096 bf16: relu 15 us (6.7 TB/s), gelu_tanh 20 us (its arithmetic: 57 % of the
+// 4096 x 4096 bf16: relu 15 us (6.7 TB/s), gelu_tanh 19 us (its arithmetic: over half the
 // issue slots), swiglu 26 us (168 MB); with db 5 us more.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -79,12 +79,9 @@ __device__ __forceinline__ void widen(uint4 u, float (&v)[8])
     }
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store8(void* base, int64_t at, int n, const float (&v)[8])
+__device__ __forceinline__ void store8(void* base, int64_t at, int n, uint4 u)
 {
     uint16_t* p = static_cast<uint16_t*>(base) + at;
-    const uint4 u = make_uint4(pack<BF16>(v[0], v[1]), pack<BF16>(v[2], v[3]), pack<BF16>(v[4], v[5]),
-                               pack<BF16>(v[6], v[7]));
     if (n >= 8) {
         *reinterpret_cast<uint4*>(p) = u;
     } else {
@@ -93,6 +90,13 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int n, const floa
         for (int i = 0; i < 8; ++i)
             if (i < n) p[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* base, int64_t at, int n, const float (&v)[8])
+{
+    store8(base, at, n, make_uint4(pack<BF16>(v[0], v[1]), pack<BF16>(v[2], v[3]), pack<BF16>(v[4], v[5]),
+                                   pack<BF16>(v[6], v[7])));
 }
 
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
@@ -111,12 +115,12 @@ __device__ __forceinline__ void act_grad(float (&dz)[8], const float (&z)[8], in
             dz[i] *= 0.5f * (1.f + erff(z[i] * 0.70710678118654752f)) +
                      z[i] * 0.39894228040143268f * __expf(-0.5f * z[i] * z[i]);
         break;
-    case GEMM_ACT_GELU_TANH:  // s = 1 / (1 + e^-2u), u = c (z + a z^3): s + z s (1 - s) 2 u'
+    case GEMM_ACT_GELU_TANH:  // s = 1 / (1 + e^-2u), 2 u = z (c + c a z^2): s + z s (1 - s) 2 u'
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float z2 = z[i] * z[i];
-            const float s = sigmoid(1.5957691216057308f * z[i] * (1.f + 0.044715f * z2));
-            dz[i] *= s + z[i] * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z2);
+            const float z2 = fminf(z[i] * z[i], 1e4f);  // (saturated long before; 0 times infinity is NaN)
+            const float s = sigmoid(z[i] * (1.5957691216057308f + 0.07135481627260025f * z2));
+            dz[i] *= s + z[i] * s * ((1.f - s) * (1.5957691216057308f + 0.2140644488178007f * z2));
         }
         break;
     case GEMM_ACT_SILU:
@@ -128,6 +132,15 @@ __device__ __forceinline__ void act_grad(float (&dz)[8], const float (&z)[8], in
         break;
     default: break;
     }
+}
+
+// silu(z) u: the gate's gradient d u silu'(z) and the up half's d silu(z), q = sigmoid(z).
+// (q's zero first: the other factors may overflow)
+__device__ __forceinline__ void gated_grad(float d, float z, float u, float& dg, float& du)
+{
+    const float q = sigmoid(z), zq = z * q;
+    du = d * zq;
+    dg = d * (u * (q + zq * (1.f - q)));
 }
 
 template <bool BF16, bool GATED, bool BIAS>
@@ -179,30 +192,34 @@ __global__ void __launch_bounds__(THREADS, 3) linear_act_kernel(ActParams p)
             for (int i = 0; i < DEEP; ++i) {
                 if (r0 + i * WARPS >= rows) break;
                 const int64_t row = first + r0 + i * WARPS;
-                float d[8], z[8];
-                widen<BF16>(dy[i], d);
-                if (GATED) {
-                    float u[8], du[8];
-                    widen<BF16>(zg[i], z);
-                    widen<BF16>(zu[i], u);
+                if constexpr (GATED) {
+                    // (two columns at a time, into the words they came from: registers)
+                    uint32_t wd[4] = {dy[i].x, dy[i].y, dy[i].z, dy[i].w}, wu[4] = {zu[i].x, zu[i].y, zu[i].z, zu[i].w};
+                    const uint32_t wz[4] = {zg[i].x, zg[i].y, zg[i].z, zg[i].w};
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float q = sigmoid(z[k]);
-                        du[k] = d[k] * z[k] * q;
-                        d[k] = d[k] * u[k] * q * (1.f + z[k] * (1.f - q));
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 d = unpack<BF16>(wd[k]), z = unpack<BF16>(wz[k]), u = unpack<BF16>(wu[k]);
+                        float2 dg, du;
+                        gated_grad(d.x, z.x, u.x, dg.x, du.x);
+                        gated_grad(d.y, z.y, u.y, dg.y, du.y);
+                        if (BIAS) s[2 * k] += dg.x, s[2 * k + 1] += dg.y, su[2 * k] += du.x, su[2 * k + 1] += du.y;
+                        wd[k] = pack<BF16>(dg.x, dg.y);
+                        wu[k] = pack<BF16>(du.x, du.y);
                     }
-                    store8<BF16>(p.dZ, row * p.lddz + p.N + col, ncol, du);
+                    store8(p.dZ, row * p.lddz + col, ncol, make_uint4(wd[0], wd[1], wd[2], wd[3]));
+                    store8(p.dZ, row * p.lddz + p.N + col, ncol, make_uint4(wu[0], wu[1], wu[2], wu[3]));
+                } else {
+                    float d[8], z[8];
+                    widen<BF16>(dy[i], d);
+                    if (p.dZ) {
+                        widen<BF16>(zg[i], z);
+                        act_grad(d, z, p.act);
+                        store8<BF16>(p.dZ, row * p.lddz + col, ncol, d);
+                    }
                     if (BIAS)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) su[k] += du[k];
-                } else if (p.dZ) {
-                    widen<BF16>(zg[i], z);
-                    act_grad(d, z, p.act);
+                        for (int k = 0; k < 8; ++k) s[k] += d[k];
                 }
-                if (p.dZ) store8<BF16>(p.dZ, row * p.lddz + col, ncol, d);
-                if (BIAS)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) s[k] += d[k];
             }
         }
         if (!BIAS) continue;

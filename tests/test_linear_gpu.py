@@ -386,6 +386,41 @@ def test_grouped_backward(lib, kind, act):
     assert lib.device_status() == 0
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+def test_activations_saturate(lib, act, dt):
+    """Far from zero act(z) is z or 0 and act'(z) is 1 or 0: from |z| = 128 on the sigmoid and the
+    normal distribution are 0 or 1 in fp32 exactly.  So is the result but for the roundings of
+    two products in fp32 (2^-22 of it) and, forward, of the result (u); no step may overflow."""
+    dtype = DTYPES[dt]
+    size = [128.0, 1024.0, 2.0 ** 15]
+    if dtype == torch.bfloat16:
+        size += [2.0 ** 40, 2.0 ** 62, 2.0 ** 65, 2.0 ** 100, 2.0 ** 124]
+    v = torch.tensor(size + [-a for a in size] + ([-1.5 * 2.0 ** 127] if dtype == torch.bfloat16 else []))
+    v = v.to(dtype).cuda()
+    M = v.numel()
+    on = torch.where(v > 0, 1.0, 0.0).double()
+    # forward: z is the one value of its row
+    x = torch.zeros(M, 8, dtype=dtype, device="cuda")
+    x[:, 0], x[:, 1] = v, 1.0
+    w = torch.zeros(8, 16 if act == "swiglu" else 8, dtype=dtype, device="cuda")
+    w[0, :8] = 1.0
+    w[1, 8:] = 0.5
+    y = lib.linear(x, w, act=act)
+    ref = (on * v.double() * (0.5 if act == "swiglu" else 1.0))[:, None].expand(M, 8)
+    assert_within(y, ref, (UNIT[dtype] + 2.0 ** -22) * ref.abs() + 2.0 ** -25)
+    # backward: each row a group of its own, whose db is the row of dZ
+    z = x.double() @ w.double()
+    dy = torch.full((M, 8), 4.0, dtype=dtype, device="cuda")
+    off = torch.arange(M + 1, dtype=torch.int32, device="cuda")
+    _, _, db = lib.grouped_linear_backward(dy, x, w.expand(M, *w.shape).contiguous(), off, z=z.to(dtype), act=act,
+                                           bias=True, need_dx=False, need_dw=False)
+    ref = 4.0 * on[:, None].expand(M, 8)
+    if act == "swiglu":
+        ref = torch.cat([0.5 * ref, ref * v.double()[:, None]], dim=1)
+    assert_within(db, ref, 2.0 ** -22 * ref.abs() + 2.0 ** -25)
+
+
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "swiglu"])
 def test_gradients_against_differences(lib, act):
     """<dX, V> and <dW, V> against central differences of <dY, Y> along V.
