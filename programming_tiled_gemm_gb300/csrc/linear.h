@@ -35,6 +35,10 @@ struct LinArgs {
     bool out_f32;         // output (and R) in fp32 instead of that type
     int G;                // groups, or 0: one group of all rows
     const int32_t* offsets;  // device, [G + 1]: rows of group g are [offsets[g], offsets[g+1])
+    // kLinDx, or null: db [G][Nw] is added up here from the pieces' sums (launch_linear_act)
+    float* db;
+    const float* db_ws;
+    int db_piece;
 };
 
 // Buffers the handle keeps for the linear kernels.
@@ -66,7 +70,12 @@ struct LinActArgs {
     const int32_t* offsets;
 };
 size_t linear_act_ws_bytes(const LinActArgs& a, int num_sms);
-int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t stream, int* launches);
+int linear_act_piece(const LinActArgs& a, int num_sms);  // rows of a piece
+// `leave_sums`: the pieces' sums stay in `ws` for the dX product to add
+int launch_linear_act(const LinActArgs& a, float* ws, bool leave_sums, int num_sms, cudaStream_t stream,
+                      int* launches);
+// Whether the dX product `a` has the time to add db's pieces of `piece` rows.
+bool linear_adds_db(const LinArgs& a, int piece, int num_sms, int kc);
 
 // First unit of every group when each group's rows are cut into pieces of `unit` rows (at
 // least `least` of them) and every piece counts `per` units: cum[g] for g = 0 .. G, and the

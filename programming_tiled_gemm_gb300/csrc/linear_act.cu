@@ -5,8 +5,10 @@
 // Bound by memory: dY and Z are read and dZ written once, 16 bytes a thread.  Resident blocks
 // walk pieces of 256 columns (a warp a row, eight columns a lane) x 8 .. 32 rows with four
 // rows' loads in flight a warp, keep a piece's column sums in registers and leave them in
-// the workspace; a second, small launch adds a group's pieces in order.  (Adding them in the
-// block that counts last took 10 us more at 4096 x 4096: one block reads what many can.)
+// the workspace.  A group's pieces are added in order by a warp of the dX product that has
+// nothing else to do, or, where dX is not wanted or too short for it, by a second, small
+// launch: the same sums in the same order.  (Adding them in the block that counts last took 10
+// us more at 4096 x 4096: one block reads what many can.)
 // 4096 x 4096 bf16: relu 15 us (6.7 TB/s), gelu_tanh 19 us (its arithmetic: over half the
 // issue slots), swiglu 26 us (168 MB); with db 5 us more.
 #include <cuda_bf16.h>
@@ -302,7 +304,10 @@ size_t linear_act_ws_bytes(const LinActArgs& a, int num_sms)
     return a.db ? (size_t)items(a, num_sms) * (size_t)(a.act == GEMM_ACT_SWIGLU ? 2 * a.N : a.N) * sizeof(float) : 0;
 }
 
-int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t stream, int* launches)
+int linear_act_piece(const LinActArgs& a, int num_sms) { return piece_rows(a, num_sms); }
+
+int launch_linear_act(const LinActArgs& a, float* ws, bool leave_sums, int num_sms, cudaStream_t stream,
+                      int* launches)
 {
     ActParams p = {};
     p.M = (int)a.M;
@@ -331,7 +336,7 @@ int launch_linear_act(const LinActArgs& a, float* ws, int num_sms, cudaStream_t 
                                  : (gated ? launch_typed<false, true>(p, grid, stream) : launch_typed<false, false>(p, grid, stream));
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
-    if (a.db) {
+    if (a.db && !leave_sums) {
         const int Nw = (int)(gated ? 2 * a.N : a.N);
         const int64_t blocks = (int64_t)p.G * ((Nw + 31) / 32);
         if (blocks > 0x7fffffffLL) return GEMM_ERR_UNSUPPORTED;

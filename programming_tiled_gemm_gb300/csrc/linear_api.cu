@@ -149,7 +149,15 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
     int64_t lddz = a->lddy;
     if (M == 0 && a->db && Nw > 0 && cudaMemsetAsync(a->db, 0, (size_t)G * Nw * sizeof(float), s) != cudaSuccess)
         return GEMM_ERR_CUDA;
-    const bool products = (a->dX && K > 0) || (a->dW && K > 0);
+    const bool dx = a->dX && M > 0 && K > 0, products = dx || (a->dW && K > 0);
+    LinArgs l = {};
+    l.mode = kLinDx;
+    l.M = M, l.K = K, l.N = N, l.Nw = Nw;
+    l.X = a->X, l.ldx = a->ldx;
+    l.W = a->W, l.ldw = a->ldw, l.w_stride = a->w_stride;
+    l.bf16 = a->dtype == GEMM_BF16;
+    l.G = (int)a->groups;
+    l.offsets = a->offsets;
     if (M > 0 && N > 0 && ((act && products) || a->db)) {
         LinActArgs e = {};
         e.M = M, e.N = N;
@@ -172,25 +180,25 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
             if (rc != GEMM_OK) return rc;
         }
         int n = 0;
-        rc = launch_linear_act(e, static_cast<float*>(h->lin_sums), h->num_sms, s, &n);
+        if (a->db && dx) {
+            l.db_piece = linear_act_piece(e, h->num_sms);
+            if (linear_adds_db(l, l.db_piece, h->num_sms, h->opt_tc_chunk)) {
+                l.db = a->db;
+                l.db_ws = static_cast<float*>(h->lin_sums);
+            }
+        }
+        rc = launch_linear_act(e, static_cast<float*>(h->lin_sums), l.db != nullptr, h->num_sms, s, &n);
         h->launches += n;
         if (rc != GEMM_OK) return rc;
     }
-    LinArgs l = {};
-    l.M = M, l.K = K, l.N = N, l.Nw = Nw;
-    l.X = a->X, l.ldx = a->ldx;
-    l.W = a->W, l.ldw = a->ldw, l.w_stride = a->w_stride;
     l.dZ = dZ, l.lddz = lddz;
-    l.bf16 = a->dtype == GEMM_BF16;
-    l.G = (int)a->groups;
-    l.offsets = a->offsets;
-    if (a->dX && M > 0 && K > 0) {
-        l.mode = kLinDx;
+    if (dx) {
         l.out = a->dX, l.ldo = a->lddx;
         if ((rc = run_product(h, l, s)) != GEMM_OK) return rc;
     }
     if (a->dW && K > 0 && Nw > 0) {
         l.mode = kLinDw;
+        l.db = nullptr;
         l.out = a->dW, l.ldo = a->lddw, l.out_stride = a->dw_stride;
         l.out_f32 = a->dw_dtype == GEMM_F32;
         if ((rc = run_product(h, l, s)) != GEMM_OK) return rc;

@@ -76,7 +76,7 @@ constexpr int STG_BYTES = 2048;       // an epilogue warp's staging block: 32 ro
                                       // or (gated) 16 columns of fp32 for the other warp
 constexpr int SMEM_MAX = 232448;      // 227 KiB
 
-// Warps 0..3: producer of A, MMA issuer, fixer, producer of B; 4..11: epilogue, which takes
+// Warps 0..3: producer of A, MMA issuer, fixer (kLinDw; db's sums in kLinDx), producer of B; 4..11: epilogue, which takes
 // registers from the first four: 80 + 2 * 208 a thread of the three warpgroups are within
 // the 3 * 168 the block is launched with (checked before the launch).
 constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
@@ -115,6 +115,9 @@ struct LinParams {
     int* status;
     uint64_t limit_ns;
     int test_stall;
+    float* db;       // kLinDx: [G][db_cols], the sums of the pieces of db_piece rows in db_ws, or null
+    const float* db_ws;
+    int db_piece, db_cols;
 };
 
 // The width of `rows` rows' tiles of at most `wcap` (a multiple of 16): equal ones, so that
@@ -478,6 +481,39 @@ __device__ __forceinline__ void store_f32(const float* R, int64_t ldr, float* ou
         if (i < n) out[i * ldo] = v[i];
 }
 
+// db, by one warp of every CTA: 32 columns of a group at a time.  Pieces i, i + 8, ... have a
+// sum each and these are added in order, as linear_db_kernel's eight warps do; sixteen
+// loads in flight.
+__device__ __forceinline__ void add_db(const LinParams& p, const int* off, int lane)
+{
+    constexpr int SUMS = 8, FLY = 16;
+    const int blocks = (p.db_cols + 31) / 32;
+    int g = -1, first = 0, n = 0;  // a group, its first piece and its pieces
+    for (int item = blockIdx.x; item < p.G * blocks; item += gridDim.x) {
+        const int at = item / blocks, c = (item - at * blocks) * 32 + lane;
+        for (; g < at; ++g) {
+            first += n;
+            n = group_units(off[g + 2] - off[g + 1], p.db_piece, 1, 1);
+        }
+        if (c >= p.db_cols) continue;
+        const float* src = p.db_ws + (int64_t)first * p.db_cols + c;
+        float t[SUMS] = {};
+        for (int i = 0; i < n; i += FLY) {
+            float u[FLY];
+#pragma unroll
+            for (int j = 0; j < FLY; ++j)
+                if (i + j < n) u[j] = __ldcg(src + (int64_t)(i + j) * p.db_cols);
+#pragma unroll
+            for (int j = 0; j < FLY; ++j)
+                if (i + j < n) t[j % SUMS] += u[j];
+        }
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < SUMS; ++j) v += t[j];
+        p.db[(int64_t)at * p.db_cols + c] = v;
+    }
+}
+
 // KPS: k-blocks of a stage, which are waited for and committed together.
 template <int MODE, bool GATED, bool BF16, bool CHUNKED, int KPS>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -752,6 +788,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     else mbar_arrive_cluster(mapa_shared(smem_u32(&peer_bar[s]), 0));
                 }
             }
+            __syncwarp();
+        } else if (MODE == kLinDx && warp == 2) {
+            if (p.db) add_db(p, off, lane);
             __syncwarp();
         }
     } else {
@@ -1177,6 +1216,19 @@ bool is_chunked(const LinArgs& a, int kc)
 }
 }  // namespace
 
+// One warp a CTA has some 1500 cycles a round of loads; a launch of its own takes 8000 (4 us).
+bool linear_adds_db(const LinArgs& a, int piece, int num_sms, int kc)
+{
+    const LinPlan pl = plan(a, num_sms, is_chunked(a, kc));
+    const int64_t G = a.G > 0 ? a.G : 1, items = G * ((a.Nw + 31) / 32);
+    const int64_t ctas = 2 * (pl.tiles < pl.pairs ? pl.tiles : (int64_t)pl.pairs);
+    if (ctas < 1 || items > (1 << 30)) return false;
+    const int64_t pieces = a.M / G / piece + 1;  // of a group, on average
+    const double sums = 1500. * (double)((items + ctas - 1) / ctas) * (double)((pieces + 15) / 16);
+    const double tiles = (double)((pl.tiles + pl.pairs - 1) / pl.pairs) * pl.kb * kb_cycles(pl.wmax);
+    return sums <= tiles + 8000.;
+}
+
 size_t linear_partials_bytes(const LinArgs& a, int num_sms, int kc)
 {
     const LinPlan pl = plan(a, num_sms, is_chunked(a, kc));
@@ -1229,6 +1281,10 @@ int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* de
     p.status = dev_status;
     p.limit_ns = limit_ns;
     p.test_stall = test_stall;
+    p.db = a.db;
+    p.db_ws = a.db_ws;
+    p.db_piece = a.db_piece;
+    p.db_cols = (int)a.Nw;
     const bool a_mn = a.mode != kLinDx, b_mn = a.mode == kLinDw;
     // kind::f16: fp32 accumulator, both operands of one type, MN-major bits, M = 256
     p.idesc = (1u << 4) | ((a.bf16 ? 1u : 0u) << 7) | ((a.bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |

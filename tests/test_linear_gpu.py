@@ -421,6 +421,37 @@ def test_activations_saturate(lib, act, dt):
     assert_within(db, ref, 2.0 ** -22 * ref.abs() + 2.0 ** -25)
 
 
+@pytest.mark.parametrize("M,K,N,counts", [(1, 64, 72, None), (333, 200, 264, None), (2100, 1032, 1000, None),
+                                          (5000, 8, 4104, None), (700, 136, 40, [0, 300, 1, 0, 390, 0, 9]),
+                                          (90, 520, 264, [3] * 30)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_bias_gradient_with_and_without_dx(lib, M, K, N, counts, act):
+    """db does not depend on whether dX is wanted, to the bit, and is the sum of dZ's rows: n fp32
+    additions at most for n rows, and dZ's own error (swiglu: 2^-19 (1 + |z|) of |dY u|)."""
+    gen, dtype = gen_of(M, K, N), torch.bfloat16
+    G, Nw = len(counts) if counts else 1, 2 * N if act == "swiglu" else N
+    dy, x = randn(gen, M, N, dtype=dtype), randn(gen, M, K, dtype=dtype)
+    w = randn(gen, *((G, K, Nw) if counts else (K, Nw)), dtype=dtype, scale=K ** -0.5)
+    z = randn(gen, M, Nw, dtype=dtype) if act != "none" else None
+    off = torch.tensor([0] + counts).cumsum(0).int().cuda() if counts else None
+    got = []
+    for need in (True, False):
+        if counts:
+            got.append(lib.grouped_linear_backward(dy, x, w, off, z=z, act=act, bias=True, need_dx=need)[2])
+        else:
+            got.append(lib.linear_backward(dy, x, w, z=z, act=act, bias=True, need_dx=need)[2])
+    assert torch.equal(*got)
+    dz, own = dy.double(), 0
+    if act == "swiglu":
+        a, u = z.double().chunk(2, dim=1)
+        s = torch.sigmoid(a)
+        dz, own = (torch.cat([dz * u * (s + a * s * (1 - s)), dz * a * s], dim=1),
+                   2.0 ** -19 * torch.cat([(1 + a.abs()) * (dz * u).abs(), (1 + a.abs()) * dz.abs()], dim=1))
+    size = dz.abs() * M * 2.0 ** -24 + own
+    parts = lambda t: torch.stack([r.sum(0) for r in t.split(counts)]) if counts else t.sum(0)
+    assert_within(got[0], parts(dz), parts(size) + 2.0 ** -25)
+
+
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "swiglu"])
 def test_gradients_against_differences(lib, act):
     """<dX, V> and <dW, V> against central differences of <dY, Y> along V.
