@@ -10,7 +10,7 @@
 // warps' counts, and the block that counts last adds the blocks' counts; a second kernel
 // writes the places.  One block (up to 128 tokens) does all of it in one launch.  Bound by
 // latency and by the picks' integer instructions, not by its few MB: 16 tokens to 4 of 64
-// experts 6 us, 16384 to 8 of 128 22 us (11 us of it the picks, 7 us the last block's sums)
+// experts 5.3 us, 16384 to 8 of 128 21 us (11 us of it the picks, 7 us the last block's sums)
 // and 4 us for the places.
 //
 // Exchange: bound by memory; 16 bytes a thread, a block a row (dispatch) or a token
@@ -95,13 +95,15 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
     constexpr int R_WARPS = route_warps(C), R_THREADS = 32 * R_WARPS;
     // [R_WARPS][E]: a warp's picks per expert, then the places its first picks take in the block
     extern __shared__ uint16_t wc[];
+    int* own_counts = reinterpret_cast<int*>(wc + R_WARPS * p.E);  // [E]: a single block's counts, then first places
     __shared__ int last, scan[R_WARPS];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int E = p.E, k = p.k;
+    const bool one = p.nblk == 1;
     for (int i = threadIdx.x; i < R_WARPS * E; i += R_THREADS) wc[i] = 0;
     __syncthreads();
     // (a single block spreads its tokens over all its warps)
-    const int per = p.nblk == 1 ? (p.T + R_WARPS - 1) / R_WARPS : R_EACH;
+    const int per = one ? (p.T + R_WARPS - 1) / R_WARPS : R_EACH;
     const int t0 = min(blockIdx.x * p.tokens + warp * per, p.T), n_own = min(per, p.T - t0);
     uint16_t* mine = wc + warp * E;
     const auto fetch = [&](int t, float(&v)[C]) {
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
     }
     __syncthreads();
     // a block's count per expert, and each warp's first place in it
-    int* counts = p.base + (int64_t)blockIdx.x * E;
+    int* counts = one ? own_counts : p.base + (int64_t)blockIdx.x * E;
     for (int e = threadIdx.x; e < E; e += R_THREADS) {
         int s = 0;
 #pragma unroll
@@ -214,12 +216,12 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
         counts[e] = s;
     }
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < R_EACH; ++q)
-        if (q < n_own && lane < k)
-            p.slots[(int64_t)(t0 + q) * k + lane] = picks[q] >= 0 ? ranks[q] + mine[picks[q]] : 0;
     // the last block: each block's first place per expert
-    if (p.nblk > 1) {
+    if (!one) {
+#pragma unroll
+        for (int q = 0; q < R_EACH; ++q)
+            if (q < n_own && lane < k)
+                p.slots[(int64_t)(t0 + q) * k + lane] = picks[q] >= 0 ? ranks[q] + mine[picks[q]] : 0;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -242,7 +244,9 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
     for (int e0 = 0; e0 < E; e0 += width) {
         const int e = e0 + col;
         int n = 0;
-        if (e < E) {
+        if (e < E && one) {
+            if (part == 0) n = own_counts[e];
+        } else if (e < E) {
 #pragma unroll 16
             for (int b = b0; b < b1; ++b) n += __ldcg(p.base + (int64_t)b * E + e);
         }
@@ -278,7 +282,9 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
         }
         __syncthreads();
         int at = sums[threadIdx.x];
-        if (e < E) {
+        if (e < E && one) {
+            if (part == 0) own_counts[e] = at;
+        } else if (e < E) {
             for (int b = b0; b < b1; b += 16) {
                 // (sixteen loads before their stores: one latency)
                 int m[16];
@@ -296,19 +302,20 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
         __syncthreads();
     }
     if (threadIdx.x == 0) p.offsets[E] = before;
-    if (p.nblk > 1) return;
-    __syncthreads();
-    const int n = p.T * k;
-    for (int i = threadIdx.x; i < n; i += R_THREADS) {
-        const int e = p.experts[i];
-        int slot = -1;
-        if (e >= 0) {
-            slot = p.base[e] + p.slots[i];
-            p.rows[slot] = i;
+    if (!one) return;
+    // (nothing of a single block's places goes through memory: that took 1.1 us of its 6.5)
+#pragma unroll
+    for (int q = 0; q < R_EACH; ++q)
+        if (q < n_own && lane < k) {
+            const int i = (t0 + q) * k + lane;
+            int slot = -1;
+            if (picks[q] >= 0) {
+                slot = own_counts[picks[q]] + mine[picks[q]] + ranks[q];
+                p.rows[slot] = i;
+            }
+            p.slots[i] = slot;
         }
-        p.slots[i] = slot;
-        if (i >= before) p.rows[i] = -1;
-    }
+    for (int i = before + (int)threadIdx.x; i < p.T * k; i += R_THREADS) p.rows[i] = -1;
 }
 
 __global__ void route_place_kernel(RouteParams p)
@@ -553,7 +560,8 @@ bool aligned(const void* p, int64_t ld, int es) { return (reinterpret_cast<uintp
 template <typename D, int C>
 cudaError_t launch_route_c(const RouteParams& p, cudaStream_t s)
 {
-    route_kernel<D, C><<<p.nblk, 32 * route_warps(C), route_warps(C) * p.E * sizeof(uint16_t), s>>>(p);
+    const size_t smem = route_warps(C) * p.E * sizeof(uint16_t) + (p.nblk == 1 ? p.E * sizeof(int) : 0);
+    route_kernel<D, C><<<p.nblk, 32 * route_warps(C), smem, s>>>(p);
     return cudaGetLastError();
 }
 
