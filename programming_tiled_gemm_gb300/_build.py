@@ -23,7 +23,7 @@ LIB = os.path.join(LIBDIR, "libgemm_gb300.so")
 LIB_DEBUG = os.path.join(LIBDIR, "libgemm_gb300_debug.so")
 
 SOURCES = ["api.cu", "ffma.cu", "ffma_tma.cu", "skinny.cu", "skinny_tma.cu", "im2col.cu", "conv_implicit.cu", "conv_tc.cu", "tc_gemm.cu",
-           "skinny_noalloc.cu", "linear_tc.cu", "linear_act.cu", "moe.cu", "linear_api.cu"]
+           "skinny_noalloc.cu", "linear_tc.cu", "linear_act.cu", "linear_few.cu", "moe.cu", "linear_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xcompiler", "-Wall"]

@@ -714,7 +714,7 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
     for (auto take : {bounds_flag_take_ffma, bounds_flag_take_ffma_tma, bounds_flag_take_skinny,
                       bounds_flag_take_skinny_tma, bounds_flag_take_im2col, bounds_flag_take_conv_implicit,
                       bounds_flag_take_conv_tc, bounds_flag_take_tc_gemm, bounds_flag_take_linear_tc,
-                      bounds_flag_take_linear_act, bounds_flag_take_moe}) {
+                      bounds_flag_take_linear_act, bounds_flag_take_linear_few, bounds_flag_take_moe}) {
         const int r = take();
         if (r < 0) return GEMM_ERR_CUDA;
         bad |= r;

@@ -67,6 +67,7 @@ int bounds_flag_take_conv_tc();
 int bounds_flag_take_tc_gemm();
 int bounds_flag_take_linear_tc();
 int bounds_flag_take_linear_act();
+int bounds_flag_take_linear_few();
 int bounds_flag_take_moe();
 #else
 #define GEMM_DEBUG_UNIT(name) \

@@ -41,6 +41,11 @@ struct LinArgs {
     int db_piece;
 };
 
+// Forward products of a few rows without groups stream W through a kernel of their own.
+constexpr int kFewRows = 8;
+bool linear_is_few(const LinArgs& a);
+int launch_linear_few(const LinArgs& a, int num_sms, cudaStream_t stream, int* launches);
+
 // Buffers the handle keeps for the linear kernels.
 struct LinWorkspace {
     float* partials = nullptr;    // K slices of the last wave's tiles

@@ -115,6 +115,12 @@ int linear_impl(gemm_handle_t h, const gemm_linear_args* a, void* stream)
     l.offsets = a->offsets;
     glog("gemm_linear %s %lldx%lldx%lld, %lld groups, activation %d: tensor-core linear kernel", dtype_name(a->dtype),
          (long long)M, (long long)N, (long long)K, (long long)a->groups, a->act);
+    if (linear_is_few(l)) {
+        int n = 0;
+        rc = launch_linear_few(l, h->num_sms, reinterpret_cast<cudaStream_t>(stream), &n);
+        h->launches += n;
+        return rc;
+    }
     return run_product(h, l, reinterpret_cast<cudaStream_t>(stream));
 }
 
