@@ -42,7 +42,6 @@ struct LinArgs {
 };
 
 // Forward products of a few rows without groups stream W through a kernel of their own.
-constexpr int kFewRows = 8;
 bool linear_is_few(const LinArgs& a);
 int launch_linear_few(const LinArgs& a, int num_sms, cudaStream_t stream, int* launches);
 

@@ -113,9 +113,10 @@ int linear_impl(gemm_handle_t h, const gemm_linear_args* a, void* stream)
     l.out_f32 = a->y_dtype == GEMM_F32;
     l.G = (int)a->groups;
     l.offsets = a->offsets;
-    glog("gemm_linear %s %lldx%lldx%lld, %lld groups, activation %d: tensor-core linear kernel", dtype_name(a->dtype),
-         (long long)M, (long long)N, (long long)K, (long long)a->groups, a->act);
-    if (linear_is_few(l)) {
+    const bool few = linear_is_few(l);
+    glog("gemm_linear %s %lldx%lldx%lld, %lld groups, activation %d: %s kernel", dtype_name(a->dtype), (long long)M,
+         (long long)N, (long long)K, (long long)a->groups, a->act, few ? "few-row linear" : "tensor-core linear");
+    if (few) {
         int n = 0;
         rc = launch_linear_few(l, h->num_sms, reinterpret_cast<cudaStream_t>(stream), &n);
         h->launches += n;

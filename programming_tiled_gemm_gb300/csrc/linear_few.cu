@@ -1,12 +1,16 @@
 // Linear layers of a few rows (tokens): act(X W + b) + R for up to 8 rows, W streamed once.
 //
 // Bound by W's bytes, and for small W by latency: the tensor-core kernel's set-up, first
-// loads and drain cost 5 us whatever its size.  Here a thread loads 16 bytes (eight columns) of
-// eight rows of W at a time (four for more than four rows of X), all in flight, and adds their
-// products with the rows of X in fp32 (packed FMAs, two columns each).  A warp covers 64
-// columns x 32 (16) of K.  A CTA holds 64
-// columns (gated: 32 of the gate and the 32 of the up half that belong to them); a cluster of
-// up to 8 CTAs shares K and adds its sums through distributed shared memory, in order.
+// loads and drain cost 5 us whatever its size.  Here a thread copies 16 bytes (eight columns) of
+// eight rows of W a stage into slots of its own in shared memory, three stages ahead, and
+// multiplies them with the rows of X in fp32 (packed FMAs, two columns each); no block barrier
+// until the end.  A warp covers 64 columns x 32 of K.  A CTA holds 64 columns (gated: 32 of
+// the gate and the 32 of the up half that belong to them); a cluster of up to 8 CTAs shares K
+// and adds its sums through distributed shared memory, in order.
+// Measured (bf16, one row): 2048 x 64 2.5 us, 2048 x 2048 4.0 (tensor-core kernel 8.4 and 9.6),
+// 4096 x 4096 7.4 (12.7), 8192 x 8192 23.3, 5.8 TB/s (27.3).  Dropped: loads kept in registers
+// instead of the ring (4096 x 4096 12.8, and 100 us for 4 rows of 8192 x 28672); three CTAs of two
+// stages an SM (8192 x 28672 75 instead of 77, 4096 x 4096 8.3 instead of 7.4).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,13 +25,18 @@ GEMM_DEBUG_UNIT(linear_few)
 namespace {
 
 constexpr int WARPS = 8, THREADS = 32 * WARPS;
+constexpr int MAX_ROWS = 8;
 constexpr int COLS = 64;    // columns of W a CTA
 constexpr int MAX_CLUSTER = 8;
 
-// By the registers they take: rows of W a thread has in flight, and CTAs an SM.
-constexpr int deep(int rows) { return rows <= 4 ? 8 : 4; }
-constexpr int resident(int rows) { return rows <= 2 ? 3 : 2; }
-constexpr int batch(int rows) { return 4 * deep(rows); }  // of K, a warp
+constexpr int DEEP = 8;          // rows of W of a thread in a stage
+constexpr int BATCH = 4 * DEEP;  // of K, a warp and stage
+constexpr int STAGES = 3;
+constexpr int RESIDENT = 2;      // CTAs an SM, by their shared memory
+
+// A warp's stage: [row][lane] 16 bytes of W, then [row of X][4] 16 bytes.
+constexpr int stage_bytes(int rows) { return DEEP * 512 + rows * 64; }
+constexpr int smem_bytes(int rows) { return WARPS * STAGES * stage_bytes(rows); }
 
 struct FewParams {
     int M, K, N, Nw;
@@ -45,23 +54,11 @@ struct FewParams {
     int act, out_f32, cluster;
 };
 
-// The first n of eight 16-bit values, zeros for the others.
-__device__ __forceinline__ uint4 first_of_8(const uint16_t* p, int n)
+// 16 bytes to shared memory, of which the first n (of 16-bit values, 0 .. 8) are read and the
+// others zero.
+__device__ __forceinline__ void copy_8(uint32_t dst, const uint16_t* src, int n)
 {
-    uint32_t t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : 0u;
-    return make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
-}
-
-// read once: not kept in L1
-__device__ __forceinline__ uint4 load_once(const uint16_t* p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(2 * n) : "memory");
 }
 
 template <bool BF16>
@@ -72,10 +69,10 @@ __device__ __forceinline__ float2 two(uint32_t u)
 }
 
 template <int MT, bool GATED, bool BF16>
-__global__ void __launch_bounds__(THREADS, resident(MT)) linear_few_kernel(FewParams p)
+__global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams p)
 {
-    constexpr int OUT = GATED ? COLS / 2 : COLS, DEEP = deep(MT), BATCH = batch(MT);
-    __shared__ float red[WARPS][MT * COLS];
+    constexpr int OUT = GATED ? COLS / 2 : COLS;
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float part[MT * COLS];
     grid_dependency_wait();
     grid_dependents_launch();
@@ -84,52 +81,67 @@ __global__ void __launch_bounds__(THREADS, resident(MT)) linear_few_kernel(FewPa
     // eight columns of W: of the 64, or of the gate's 32, then the up half's
     const int cl = lane % 8, kr = lane / 8;
     const int first = out0 + (GATED ? cl % 4 : cl) * 8;
-    const int ncol = p.N - first;
-    const uint16_t* W = p.W + first + (GATED && cl >= 4 ? p.N : 0);
+    const int ncol = max(0, min(8, p.N - first));
+    const uint16_t* W = p.W + (ncol > 0 ? first + (GATED && cl >= 4 ? p.N : 0) : 0);
     float2 acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][i] = make_float2(0.f, 0.f);
-    const int batches = (p.K + BATCH - 1) / BATCH;
-    for (int b = rank * WARPS + warp; b < batches; b += C * WARPS) {
-        const int k0 = b * BATCH + kr * DEEP;
-        uint4 w[DEEP];
-        uint32_t x[MT][DEEP / 2];
+    const int batches = (p.K + BATCH - 1) / BATCH, step = C * WARPS;
+    uint8_t* mine = ring + warp * STAGES * stage_bytes(MT);
+    // every lane copies what it multiplies itself of W; lane (kr, m) row m's eight values of X
+    const auto fetch = [&](int b, int s) {
+        if (b < batches) {
+            const uint32_t at = smem_u32(mine + s * stage_bytes(MT));
+            const int k0 = b * BATCH + kr * DEEP;
 #pragma unroll
-        for (int u = 0; u < DEEP; ++u) {
-            w[u] = make_uint4(0, 0, 0, 0);
-            if (k0 + u < p.K) {
-                const uint16_t* row = W + (int64_t)(k0 + u) * p.ldw;
-                if (ncol >= 8) w[u] = load_once(row);
-                else if (ncol > 0) w[u] = first_of_8(row, ncol);
+            for (int u = 0; u < DEEP; ++u) {
+                const bool in = k0 + u < p.K;
+                copy_8(at + u * 512 + lane * 16, W + (in ? (int64_t)(k0 + u) * p.ldw : 0), in ? ncol : 0);
+            }
+            if (cl < MT) {
+                const int n = cl < p.M ? max(0, min(8, p.K - k0)) : 0;
+                copy_8(at + DEEP * 512 + (cl * 4 + kr) * 16, p.X + (n > 0 ? cl * p.ldx + k0 : 0), n);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int next = rank * WARPS + warp;  // the batch to fetch
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s, next += step) fetch(next, s);
+    int s = 0;
+    for (int b = rank * WARPS + warp; b < batches; b += step) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        __syncwarp();
+        const uint4* w = reinterpret_cast<const uint4*>(mine + s * stage_bytes(MT)) + lane;
+        const uint4* xs = reinterpret_cast<const uint4*>(mine + s * stage_bytes(MT) + DEEP * 512) + kr;
+        uint32_t x[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (m < p.M && k0 < p.K) {
-                const uint16_t* row = p.X + m * p.ldx + k0;
-                if (k0 + DEEP > p.K) v = first_of_8(row, p.K - k0);
-                else if (DEEP == 8) v = *reinterpret_cast<const uint4*>(row);
-                else *reinterpret_cast<uint2*>(&v) = *reinterpret_cast<const uint2*>(row);
-            }
-            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < DEEP / 2; ++i) x[m][i] = words[i];
+            const uint4 v = xs[m * 4];
+            x[m][0] = v.x, x[m][1] = v.y, x[m][2] = v.z, x[m][3] = v.w;
         }
 #pragma unroll
         for (int u = 0; u < DEEP; ++u) {
-            const float2 wf[4] = {two<BF16>(w[u].x), two<BF16>(w[u].y), two<BF16>(w[u].z), two<BF16>(w[u].w)};
+            const uint4 v = w[u * 32];
+            const float2 wf[4] = {two<BF16>(v.x), two<BF16>(v.y), two<BF16>(v.z), two<BF16>(v.w)};
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const float2 pair = two<BF16>(x[m][u / 2]);
-                const float v = u % 2 ? pair.y : pair.x;
+                const float f = u % 2 ? pair.y : pair.x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][i] = __ffma2_rn(make_float2(v, v), wf[i], acc[m][i]);
+                for (int i = 0; i < 4; ++i) acc[m][i] = __ffma2_rn(make_float2(f, f), wf[i], acc[m][i]);
             }
         }
+        __syncwarp();
+        fetch(next, s);
+        next += step;
+        if (++s == STAGES) s = 0;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the ring is free
+    float(*red)[MT * COLS] = reinterpret_cast<float(*)[MT * COLS]>(ring);
     // the warp's four parts of K, then the warps' and the cluster's sums in order
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -198,6 +210,10 @@ cudaError_t launch_typed(const FewParams& p, int blocks, cudaStream_t s)
     cfg.gridDim = dim3(blocks * p.cluster, 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.stream = s;
+    cfg.dynamicSmemBytes = smem_bytes(MT);
+    const cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<MT, GATED, BF16>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(MT));
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.cluster;
@@ -221,7 +237,15 @@ cudaError_t launch_rows(const FewParams& p, int rows, int blocks, cudaStream_t s
 
 }  // namespace
 
-bool linear_is_few(const LinArgs& a) { return a.mode == kLinFwd && a.G == 0 && a.M <= kFewRows; }
+// One row costs W's bytes alone; more are bound by the FMAs in time, and large W are then as fast
+// or faster on the tensor cores.  us here and there: 1 row 4096 x 28672 40 and 42, 8192 x 28672
+// 77 and 75; 4 rows 8192 x 8192 25 and 27, 4096 x 16384 gated 55 and 47; 8 rows 4096 x 4096 11.8
+// and 12.7, 8192 x 8192 35 and 27.
+bool linear_is_few(const LinArgs& a)
+{
+    if (a.mode != kLinFwd || a.G != 0) return false;
+    return a.M <= MAX_ROWS && a.K * a.Nw <= (int64_t)1 << (a.M <= 2 ? 27 : a.M <= 4 ? 26 : 24);
+}
 
 int launch_linear_few(const LinArgs& a, int num_sms, cudaStream_t stream, int* launches)
 {
@@ -236,11 +260,13 @@ int launch_linear_few(const LinArgs& a, int num_sms, cudaStream_t stream, int* l
     p.out = a.out, p.ldo = a.ldo;
     p.act = a.act, p.out_f32 = a.out_f32 ? 1 : 0;
     const int out = gated ? COLS / 2 : COLS, rows = p.M == 1 ? 1 : p.M == 2 ? 2 : p.M <= 4 ? 4 : 8;
-    const int blocks = (p.N + out - 1) / out, batches = (p.K + batch(rows) - 1) / batch(rows);
+    const int blocks = (p.N + out - 1) / out, batches = (p.K + BATCH - 1) / BATCH;
     // K is shared by as many CTAs as fit at once and have a batch for each of their warps
-    int c = num_sms * resident(rows) / blocks;
-    if (c > (batches + WARPS - 1) / WARPS) c = (batches + WARPS - 1) / WARPS;
-    p.cluster = c < 1 ? 1 : c > MAX_CLUSTER ? MAX_CLUSTER : c;
+    // (clusters of 7 left GPCs half empty: 12.8 instead of 10.1 us at 4096 x 4096)
+    p.cluster = 1;
+    while (p.cluster < MAX_CLUSTER && 2 * p.cluster * blocks <= RESIDENT * num_sms &&
+           2 * p.cluster * WARPS <= batches + WARPS - 1)
+        p.cluster *= 2;
     const cudaError_t e = a.bf16 ? (gated ? launch_rows<true, true>(p, rows, blocks, stream)
                                           : launch_rows<false, true>(p, rows, blocks, stream))
                                  : (gated ? launch_rows<true, false>(p, rows, blocks, stream)

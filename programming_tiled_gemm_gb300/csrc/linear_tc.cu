@@ -4,8 +4,8 @@
 //
 // All three are D[t][f] = sum_k A[f][k] B[t][k] with the FEATURES f on the MMA's M side and
 // the ROWS t (tokens) on its N side: a CTA pair's tcgen05.mma is 256 features x w rows, and
-// w is any multiple of 16 up to 256, chosen per tile at run time.  So one kernel takes one
-// token (w = 16: the weights stream past, nothing else counts), ragged groups (a group of
+// w is any multiple of 16 up to 256, chosen per tile at run time.  So one kernel takes a few
+// tokens (w = 16: the weights stream past, nothing else counts), ragged groups (a group of
 // 300 rows becomes two tiles of 160 and 140 rows instead of 512 padded ones) and large
 // products (256 x 256 tiles).  Putting the features on the TMEM lanes also makes the
 // epilogue's accesses contiguous: a warp holds 32 features of a row.
@@ -40,9 +40,9 @@
 //   8192^3, bias, gelu_tanh and residual: 575 us in a burst, 1912 TFLOP/s, tensor pipe busy;
 //     664 us (1656 TFLOP/s) back to back under the power limit
 //   4096^3: dX 74 us, dW 81 us, with the full epilogue 81 us (tensor pipe 90, 88, 81 % active)
-//   1 x 8192 x 8192: 27 us, 4.9 TB/s; 1 x 8192 x 28672: 73 us, 6.5 TB/s (HBM)
-//   1 x 2048 x 2048: 8.4 us, latency: 5 us of launch, set-up, first loads and drain, then
-//     0.14 us a k-block or 2.5 us for a cut
+//   16 x 8192 x 8192: 27 us, 4.9 TB/s; 16 x 8192 x 28672: 75 us, 6.3 TB/s (HBM)
+//   16 x 2048 x 2048: 8.4 us, latency: 5 us of launch, set-up, first loads and drain, then
+//     0.14 us a k-block or 2.5 us for a cut.  (Fewer rows: linear_few.cu)
 //   16384 rows over 32 experts, 2048 x 4096 swiglu, loads of 7 to 1610 rows: 188 us; 256-row
 //     tiles at 515 cycles a k-block, narrower ones bound by their loads
 // Every wait is bounded; on expiry the status word is set and the CTA drains and returns.

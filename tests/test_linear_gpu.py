@@ -123,6 +123,32 @@ def test_forward(lib, M, K, N, act, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+def test_few_rows(lib, M, dt):
+    """One to nine rows over sizes on both sides of the kernels' rule: K below and above a warp's
+    and a cluster's share, ends inside eight columns, padded rows, fp32 and 16-bit results."""
+    dtype = DTYPES[dt]
+    for K, N, act in ((1, 1, "none"), (7, 9, "relu"), (31, 65, "silu"), (33, 64, "gelu"), (257, 130, "none"),
+                      (300, 8, "swiglu"), (1000, 40, "swiglu"), (2048, 31, "gelu_tanh"), (4099, 77, "none"),
+                      (520, 8200, "silu"), (9000, 72, "swiglu"), (5000, 4104, "none")):
+        gen = gen_of(M, K, N)
+        Nw = 2 * N if act == "swiglu" else N
+        pad = lambda n: (n + 7) // 8 * 8
+        # what lies between the rows is NaN: it must not count
+        x = torch.full((M, pad(K) + 8), float("nan"), dtype=dtype, device="cuda")[:, :K]
+        w = torch.full((K, pad(Nw) + 8), float("nan"), dtype=dtype, device="cuda")[:, :Nw]
+        x.copy_(randn(gen, M, K))
+        w.copy_(randn(gen, K, Nw, scale=K ** -0.5))
+        b = randn(gen, Nw, dtype=dtype)
+        for out_dtype in (dtype, torch.float32):
+            r = randn(gen, M, N + 3, dtype=out_dtype)[:, 1:N + 1]
+            out = torch.full((M + 1, N + 2), 7.0, dtype=out_dtype, device="cuda")
+            y, z = lib.linear(x, w, bias=b, act=act, residual=r, out=out[:M, :N], save_preact=True)
+            check_forward(y, z, x, w, b, act, r)
+            assert (out[M] == 7).all() and (out[:, N:] == 7).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("M,K,N", [(1, 512, 256), (77, 1000, 136), (260, 4096, 264), (700, 640, 1032)])
 def test_forward_is_exact_on_integers(lib, M, K, N, dt):
     """Products of integers in [-4, 4] add without rounding."""
