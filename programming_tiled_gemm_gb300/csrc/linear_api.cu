@@ -239,13 +239,13 @@ int route_impl(gemm_handle_t h, int64_t T, int64_t E, int64_t k, const void* log
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (T == 0) return from_cuda(cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, s));
     RouteArgs a = {logits, ldl, T, E, (int)k, dtype, renormalize != 0, weights, experts, slots, rows, offsets};
-    rc = ensure_buffer(&h->lin_sums, &h->lin_sums_bytes, moe_route_ws_bytes(a));
+    rc = ensure_buffer(&h->lin_sums, &h->lin_sums_bytes, moe_route_ws_bytes(a, h->num_sms));
     if (rc != GEMM_OK) return rc;
     const int64_t first = product_counters(h);
     rc = counters(h, first + 1, s);
     if (rc != GEMM_OK) return rc;
     int n = 0;
-    rc = launch_moe_route(a, static_cast<int*>(h->lin_sums), h->lin_counters + first, s, &n);
+    rc = launch_moe_route(a, static_cast<int*>(h->lin_sums), h->lin_counters + first, h->num_sms, s, &n);
     h->launches += n;
     return rc;
 }

@@ -50,10 +50,9 @@ struct F16 {
 
 // ------------------------------------------------------------------ router
 
-constexpr int R_EACH = 4;  // tokens of a warp
-// Warps of a block for C logits a lane (by the registers they take), and its tokens.
+constexpr int R_EACH = 4;  // tokens of a warp at most
+// Warps of a block for C logits a lane (by the registers they take).
 __host__ __device__ constexpr int route_warps(int C) { return C <= 8 ? 32 : 16; }
-__host__ __device__ constexpr int route_tokens(int C) { return R_EACH * route_warps(C); }
 
 struct RouteParams {
     const void* logits;
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
     for (int i = threadIdx.x; i < R_WARPS * E; i += R_THREADS) wc[i] = 0;
     __syncthreads();
     // (a single block spreads its tokens over all its warps)
-    const int per = one ? (p.T + R_WARPS - 1) / R_WARPS : R_EACH;
+    const int per = one ? (p.T + R_WARPS - 1) / R_WARPS : p.tokens / R_WARPS;
     const int t0 = min(blockIdx.x * p.tokens + warp * per, p.T), n_own = min(per, p.T - t0);
     uint16_t* mine = wc + warp * E;
     const auto fetch = [&](int t, float(&v)[C]) {
@@ -587,16 +586,24 @@ cudaError_t by_type(int dtype, F f)
 }  // namespace
 
 namespace {
-int block_tokens(int64_t E) { return E <= 256 ? route_tokens(8) : route_tokens(16); }
+// Up to four tokens a warp one block does it all; else a warp takes as few tokens as fill the SMs (4096 x
+// 256 to eight: 128 blocks of a token a warp 20 us, 32 blocks of four 31 us).
+int block_tokens(int64_t T, int64_t E, int num_sms)
+{
+    const int warps = route_warps(E <= 256 ? 8 : 16);
+    if (T <= warps * R_EACH) return warps * R_EACH;
+    const int64_t each = (T + (int64_t)num_sms * warps - 1) / ((int64_t)num_sms * warps);
+    return warps * (int)(each < R_EACH ? each : R_EACH);
+}
 }  // namespace
 
-size_t moe_route_ws_bytes(const RouteArgs& a)
+size_t moe_route_ws_bytes(const RouteArgs& a, int num_sms)
 {
-    const int n = block_tokens(a.E);
+    const int n = block_tokens(a.T, a.E, num_sms);
     return (size_t)((a.T + n - 1) / n) * a.E * sizeof(int);
 }
 
-int launch_moe_route(const RouteArgs& a, int* ws, unsigned* counter, cudaStream_t s, int* launches)
+int launch_moe_route(const RouteArgs& a, int* ws, unsigned* counter, int num_sms, cudaStream_t s, int* launches)
 {
     RouteParams p = {};
     p.logits = a.logits;
@@ -605,7 +612,7 @@ int launch_moe_route(const RouteArgs& a, int* ws, unsigned* counter, cudaStream_
     p.E = (int)a.E;
     p.k = a.k;
     p.renorm = a.renormalize;
-    p.tokens = block_tokens(a.E);
+    p.tokens = block_tokens(a.T, a.E, num_sms);
     p.nblk = (int)((a.T + p.tokens - 1) / p.tokens);
     p.weights = a.weights;
     p.experts = a.experts;

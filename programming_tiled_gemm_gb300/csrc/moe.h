@@ -18,9 +18,9 @@ struct RouteArgs {
     int* rows;       // [T k]: the assignment t k + j at each place, -1 past the last
     int* offsets;    // [E + 1]
 };
-size_t moe_route_ws_bytes(const RouteArgs& a);
+size_t moe_route_ws_bytes(const RouteArgs& a, int num_sms);
 // `counter` is zero before and after every launch.  Returns a gemm_status_t.
-int launch_moe_route(const RouteArgs& a, int* ws, unsigned* counter, cudaStream_t s, int* launches);
+int launch_moe_route(const RouteArgs& a, int* ws, unsigned* counter, int num_sms, cudaStream_t s, int* launches);
 
 struct RouteGradArgs {
     const float* dweights;  // [T][k]
