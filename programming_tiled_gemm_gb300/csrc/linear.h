@@ -2,6 +2,8 @@
 // grouped by expert, their gradients, and the routing kernels around them (not installed).
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace gemm_gb300 {
@@ -54,6 +56,19 @@ struct LinWorkspace {
 // Workspace bytes of the K-sliced last wave, and counters (of 4 bytes).
 size_t linear_partials_bytes(const LinArgs& a, int num_sms, int kc);
 int64_t linear_counters(int num_sms);
+// Lets `kern` have `bytes` of shared memory on the current device: asked for once a device (`done`
+// has a bit for each), as it takes 0.4 us of a call.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+    return e;
+}
+
 // Returns GEMM_OK or a negative gemm_status_t.
 int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* dev_status, uint64_t limit_ns, int kc,
                   int test_stall, cudaStream_t stream, int* launches);

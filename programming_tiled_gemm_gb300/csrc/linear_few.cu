@@ -211,8 +211,8 @@ cudaError_t launch_typed(const FewParams& p, int blocks, cudaStream_t s)
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.stream = s;
     cfg.dynamicSmemBytes = smem_bytes(MT);
-    const cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<MT, GATED, BF16>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(MT));
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(linear_few_kernel<MT, GATED, BF16>, smem_bytes(MT), allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

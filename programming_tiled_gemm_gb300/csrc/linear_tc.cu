@@ -41,7 +41,7 @@
 //     664 us (1656 TFLOP/s) back to back under the power limit
 //   4096^3: dX 74 us, dW 81 us, with the full epilogue 81 us (tensor pipe 90, 88, 81 % active)
 //   16 x 8192 x 8192: 27 us, 4.9 TB/s; 16 x 8192 x 28672: 75 us, 6.3 TB/s (HBM)
-//   16 x 2048 x 2048: 8.4 us, latency: 5 us of launch, set-up, first loads and drain, then
+//   16 x 2048 x 2048: 9.6 us, latency: 5 us of launch, set-up, first loads and drain, then
 //     0.14 us a k-block or 2.5 us for a cut.  (Fewer rows: linear_few.cu)
 //   16384 rows over 32 experts, 2048 x 4096 swiglu, loads of 7 to 1610 rows: 188 us; 256-row
 //     tiles at 515 cycles a k-block, narrower ones bound by their loads
@@ -1105,8 +1105,8 @@ int launch_kernel(const LinPlan& pl, const CUtensorMap& tmA, const CUtensorMap& 
 {
     static std::atomic<int> fit{0};
     auto kern = linear_pair_kernel<MODE, GATED, BF16, CHUNKED, KPS>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX) != cudaSuccess)
-        return GEMM_ERR_CUDA;
+    static std::atomic<uint64_t> allowed{0};
+    if (allow_smem(kern, SMEM_MAX, allowed) != cudaSuccess) return GEMM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
