@@ -253,9 +253,15 @@ int conv4d_forward_tc(gemm_handle_t h, const void* x, int64_t C_in, const int64_
  * Operands are bf16 or fp16 (GEMM_F32 is GEMM_ERR_UNSUPPORTED: these run on the tensor
  * cores only).  Products of 16-bit values accumulate in fp32 as in gemm_run; bias,
  * activation and residual are applied in fp32 and the result is rounded once.  Results
- * are deterministic.  Calls on one handle share its workspace: calls on different streams
- * must not overlap in time.  Once a call of the largest sizes has grown the workspace,
- * calls allocate nothing and can be captured in a CUDA graph. */
+ * are deterministic.
+ *
+ * Workspace and CUDA graphs, of the calls here and of moe_route below: calls on one handle
+ * share its workspace, so calls on different streams (and replays of graphs) must not overlap
+ * in time.  It grows to the largest call so far: a call that needs no more allocates nothing
+ * and can be captured in a CUDA graph; one that needs more is GEMM_ERR_CUDA under capture
+ * (nothing is launched, the capture goes on).  Graphs stay valid whatever is called later:
+ * once a call was captured, a buffer that is outgrown is kept for them.  gemm_destroy frees
+ * all of it, nothing else does. */
 
 typedef enum {
     GEMM_ACT_NONE = 0,
@@ -344,7 +350,8 @@ int gemm_linear_backward(gemm_handle_t h, const gemm_linear_grad_args* args, voi
  * The steps around the grouped products of a mixture-of-experts block: T tokens, E experts,
  * k of them a token.  dtype is GEMM_F32, GEMM_BF16 or GEMM_F16; sums are held in fp32.
  * k <= 32, E <= 1024 and N <= 2^30, else GEMM_ERR_UNSUPPORTED; T * k must stay below
- * 2^31 - 1024. */
+ * 2^31 - 1024.  moe_route uses the handle's workspace, as the linear layers do and under the
+ * same rules; the others here use none. */
 
 /* For each token the k largest logits, in descending order; equal logits (and +0, -0) by
  * the lower index, NaN before everything.  A logit of -inf is an expert that is not there:

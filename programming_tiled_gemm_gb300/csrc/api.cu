@@ -15,6 +15,7 @@
 
 #include "context.h"
 #include "internal.h"
+#include "linear.h"
 
 using namespace gemm_gb300;
 
@@ -179,9 +180,13 @@ static int gemm_create_impl(gemm_handle_t* out, int device)
     if (!h) return GEMM_ERR_CUDA;
     h->device = device;
     h->num_sms = sms;
-    if (cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess ||
-        cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) {
+    // (cudaMemset runs on the legacy stream: done before any other stream may use the words)
+    const size_t counters = (size_t)(linear_counters(sms) + 1) * sizeof(unsigned);
+    if (cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess || cudaMalloc(&h->lin_counters, counters) != cudaSuccess ||
+        cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess || cudaMemset(h->lin_counters, 0, counters) != cudaSuccess ||
+        cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
         if (h->d_status) cudaFree(h->d_status);
+        if (h->lin_counters) cudaFree(h->lin_counters);
         delete h;
         return GEMM_ERR_CUDA;
     }
@@ -211,6 +216,12 @@ int gemm_destroy(gemm_handle_t h)
     if (h->lin_partials) cudaFree(h->lin_partials);
     if (h->lin_dz) cudaFree(h->lin_dz);
     if (h->lin_sums) cudaFree(h->lin_sums);
+    if (h->route_counts) cudaFree(h->route_counts);
+    while (gemm_ctx::KeptBuffer* k = h->kept) {
+        h->kept = k->next;
+        cudaFree(k->p);
+        delete k;
+    }
     if (h->lin_counters) cudaFree(h->lin_counters);
     delete h;
     return GEMM_OK;
@@ -704,7 +715,7 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
     if (v != 0) {
         if (cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) return GEMM_ERR_CUDA;
         // a linear-layer kernel that gave up may have left arrivals uncounted
-        if (h->lin_counters && cudaMemset(h->lin_counters, 0, h->lin_counters_bytes) != cudaSuccess)
+        if (cudaMemset(h->lin_counters, 0, (size_t)(linear_counters(h->num_sms) + 1) * sizeof(unsigned)) != cudaSuccess)
             return GEMM_ERR_CUDA;
         glog("gemm_get_device_status: a bounded wait ran out (device code %d)", v);
         return GEMM_ERR_DEVICE_TIMEOUT;

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstddef>
+#include <new>
 
 #include "internal.h"
 
@@ -30,16 +31,25 @@ struct gemm_ctx {
     int opt_conv_stack = 0;  // tensor-core convolution: output positions stacked along N (0 = choose)
     int opt_conv_split = 0;  // tensor-core convolution: 0 choose, 1 one CTA pair per tile, 2 two pairs
     uint64_t wait_limit_ns = 2000000000ull;
-    // linear layers and routing: partial tiles of K slices, dZ, pieces of column sums or the
-    // router's counts, and arrival counters (zero between launches)
+    // linear layers and routing: partial tiles of K slices, dZ, pieces of column sums, the
+    // router's counts per block; these grow by grow_buffer below
     float* lin_partials = nullptr;
     size_t lin_partials_bytes = 0;
     void* lin_dz = nullptr;
     size_t lin_dz_bytes = 0;
     void* lin_sums = nullptr;
     size_t lin_sums_bytes = 0;
+    void* route_counts = nullptr;
+    size_t route_counts_bytes = 0;
+    // arrival counters, zero between launches: linear_counters(num_sms) of the products, then
+    // the router's.  Made with the handle, so that they never move
     unsigned* lin_counters = nullptr;
-    size_t lin_counters_bytes = 0;
+    bool captured = false;    // a graph holds addresses of the buffers that grow
+    struct KeptBuffer {
+        void* p;
+        KeptBuffer* next;
+    };
+    KeptBuffer* kept = nullptr;  // outgrown buffers that a graph may hold
     int64_t launches = 0;  // kernels launched through this handle
     // gemm_run_host pipeline: copy-in and copy-out streams and their events
     cudaStream_t s_in = nullptr, s_out = nullptr;
@@ -88,6 +98,36 @@ inline int ensure_buffer(void** buf, size_t* have, size_t bytes)
     }
     *have = want;
     return GEMM_OK;
+}
+
+// The same for a buffer whose address calls captured in CUDA graphs may hold.  Under capture
+// the buffer must be large enough: the call is refused, with the capture and the buffer as they
+// were.  Once any call was captured, an outgrown buffer is kept until the handle is destroyed:
+// the graph's replays go on using it.
+inline int grow_buffer(gemm_ctx* h, void** buf, size_t* have, size_t bytes, cudaStream_t s)
+{
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+        (void)cudaGetLastError();  // (the legacy stream, while another one captures: its launch will say so)
+        st = cudaStreamCaptureStatusNone;
+    }
+    const bool capturing = st != cudaStreamCaptureStatusNone;
+    const bool enough = *buf && *have >= bytes;
+    if (capturing && !enough) {
+        glog("a captured call needs %zu bytes of workspace, %zu are there: run one such call before the capture", bytes,
+             *have);
+        return GEMM_ERR_CUDA;
+    }
+    if (capturing) h->captured = true;
+    if (enough) return GEMM_OK;
+    if (*buf && h->captured) {
+        gemm_ctx::KeptBuffer* k = new (std::nothrow) gemm_ctx::KeptBuffer{*buf, h->kept};
+        if (!k) return GEMM_ERR_CUDA;
+        h->kept = k;
+        *buf = nullptr;
+        *have = 0;
+    }
+    return ensure_buffer(buf, have, bytes);
 }
 
 const char* dtype_name(int d);

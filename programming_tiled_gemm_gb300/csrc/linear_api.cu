@@ -30,36 +30,23 @@ bool bad_rows16(const void* p, int64_t rows, int64_t cols, int64_t ld)
     return rows > 0 && cols > 0 && (misaligned(p, 16) || ld % 8 != 0);
 }
 
-// The counters' buffer: zeroed when it grows, and left zero by every launch.
-int counters(gemm_handle_t h, int64_t n, cudaStream_t s)
+// Grows the workspace to what the product needs, which *need tells run_product.
+int reserve_product(gemm_handle_t h, const LinArgs& a, cudaStream_t s, size_t* need)
 {
-    const size_t bytes = (size_t)n * sizeof(unsigned);
-    if (h->lin_counters && h->lin_counters_bytes >= bytes) return GEMM_OK;
-    const int rc = ensure_buffer(reinterpret_cast<void**>(&h->lin_counters), &h->lin_counters_bytes, bytes);
-    if (rc != GEMM_OK) return rc;
-    return from_cuda(cudaMemsetAsync(h->lin_counters, 0, h->lin_counters_bytes, s));
+    *need = linear_partials_bytes(a, h->num_sms, h->opt_tc_chunk);
+    return *need == 0 ? GEMM_OK : grow_buffer(h, reinterpret_cast<void**>(&h->lin_partials), &h->lin_partials_bytes, *need, s);
 }
 
-// The counters of the products, then that of the router.
-int64_t product_counters(gemm_handle_t h) { return linear_counters(h->num_sms); }
-
-int run_product(gemm_handle_t h, const LinArgs& a, cudaStream_t s)
+int run_product(gemm_handle_t h, const LinArgs& a, size_t need, cudaStream_t s)
 {
-    const size_t need = linear_partials_bytes(a, h->num_sms, h->opt_tc_chunk);
-    if (need > 0) {
-        const int rc = ensure_buffer(reinterpret_cast<void**>(&h->lin_partials), &h->lin_partials_bytes, need);
-        if (rc != GEMM_OK) return rc;
-    }
-    const int rc = counters(h, product_counters(h), s);
-    if (rc != GEMM_OK) return rc;
     LinWorkspace ws;
     ws.partials = need > 0 ? h->lin_partials : nullptr;
     ws.counters = h->lin_counters;
     int n = 0;
-    const int rc2 = launch_linear(a, ws, h->num_sms, h->d_status, h->wait_limit_ns, h->opt_tc_chunk, h->opt_test_stall,
-                                  s, &n);
+    const int rc = launch_linear(a, ws, h->num_sms, h->d_status, h->wait_limit_ns, h->opt_tc_chunk, h->opt_test_stall,
+                                 s, &n);
     h->launches += n;
-    return rc2;
+    return rc;
 }
 
 // What gemm_linear and gemm_linear_backward check alike.
@@ -122,7 +109,10 @@ int linear_impl(gemm_handle_t h, const gemm_linear_args* a, void* stream)
         h->launches += n;
         return rc;
     }
-    return run_product(h, l, reinterpret_cast<cudaStream_t>(stream));
+    size_t need = 0;
+    rc = reserve_product(h, l, reinterpret_cast<cudaStream_t>(stream), &need);
+    if (rc != GEMM_OK) return rc;
+    return run_product(h, l, need, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* stream)
@@ -154,9 +144,7 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
     // dZ and db in one pass over dY and Z
     const void* dZ = a->dY;
     int64_t lddz = a->lddy;
-    if (M == 0 && a->db && Nw > 0 && cudaMemsetAsync(a->db, 0, (size_t)G * Nw * sizeof(float), s) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    const bool dx = a->dX && M > 0 && K > 0, products = dx || (a->dW && K > 0);
+    const bool dx = a->dX && M > 0 && K > 0, dw = a->dW && K > 0 && Nw > 0, products = dx || dw;
     LinArgs l = {};
     l.mode = kLinDx;
     l.M = M, l.K = K, l.N = N, l.Nw = Nw;
@@ -165,6 +153,16 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
     l.bf16 = a->dtype == GEMM_BF16;
     l.G = (int)a->groups;
     l.offsets = a->offsets;
+    LinArgs w = l;
+    w.mode = kLinDw;
+    w.out = a->dW, w.ldo = a->lddw, w.out_stride = a->dw_stride;
+    w.out_f32 = a->dw_dtype == GEMM_F32;
+    // the products' workspace first: a call whose workspace cannot grow launches nothing
+    size_t need_dx = 0, need_dw = 0;
+    if (dx && (rc = reserve_product(h, l, s, &need_dx)) != GEMM_OK) return rc;
+    if (dw && (rc = reserve_product(h, w, s, &need_dw)) != GEMM_OK) return rc;
+    if (M == 0 && a->db && Nw > 0 && cudaMemsetAsync(a->db, 0, (size_t)G * Nw * sizeof(float), s) != cudaSuccess)
+        return GEMM_ERR_CUDA;
     if (M > 0 && N > 0 && ((act && products) || a->db)) {
         LinActArgs e = {};
         e.M = M, e.N = N;
@@ -177,13 +175,13 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
         e.offsets = a->offsets;
         if (act) {
             lddz = (Nw + 7) / 8 * 8;
-            rc = ensure_buffer(&h->lin_dz, &h->lin_dz_bytes, (size_t)M * lddz * 2);
+            rc = grow_buffer(h, &h->lin_dz, &h->lin_dz_bytes, (size_t)M * lddz * 2, s);
             if (rc != GEMM_OK) return rc;
             dZ = e.dZ = h->lin_dz;
             e.lddz = lddz;
         }
         if (a->db) {
-            rc = ensure_buffer(&h->lin_sums, &h->lin_sums_bytes, linear_act_ws_bytes(e, h->num_sms));
+            rc = grow_buffer(h, &h->lin_sums, &h->lin_sums_bytes, linear_act_ws_bytes(e, h->num_sms), s);
             if (rc != GEMM_OK) return rc;
         }
         int n = 0;
@@ -198,19 +196,12 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
         h->launches += n;
         if (rc != GEMM_OK) return rc;
     }
-    l.dZ = dZ, l.lddz = lddz;
+    l.dZ = w.dZ = dZ, l.lddz = w.lddz = lddz;
     if (dx) {
         l.out = a->dX, l.ldo = a->lddx;
-        if ((rc = run_product(h, l, s)) != GEMM_OK) return rc;
+        if ((rc = run_product(h, l, need_dx, s)) != GEMM_OK) return rc;
     }
-    if (a->dW && K > 0 && Nw > 0) {
-        l.mode = kLinDw;
-        l.db = nullptr;
-        l.out = a->dW, l.ldo = a->lddw, l.out_stride = a->dw_stride;
-        l.out_f32 = a->dw_dtype == GEMM_F32;
-        if ((rc = run_product(h, l, s)) != GEMM_OK) return rc;
-    }
-    return GEMM_OK;
+    return dw ? run_product(h, w, need_dw, s) : GEMM_OK;
 }
 
 bool known_dtype(int d) { return d == GEMM_F32 || is_16(d); }
@@ -239,13 +230,11 @@ int route_impl(gemm_handle_t h, int64_t T, int64_t E, int64_t k, const void* log
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (T == 0) return from_cuda(cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, s));
     RouteArgs a = {logits, ldl, T, E, (int)k, dtype, renormalize != 0, weights, experts, slots, rows, offsets};
-    rc = ensure_buffer(&h->lin_sums, &h->lin_sums_bytes, moe_route_ws_bytes(a, h->num_sms));
-    if (rc != GEMM_OK) return rc;
-    const int64_t first = product_counters(h);
-    rc = counters(h, first + 1, s);
+    rc = grow_buffer(h, &h->route_counts, &h->route_counts_bytes, moe_route_ws_bytes(a, h->num_sms), s);
     if (rc != GEMM_OK) return rc;
     int n = 0;
-    rc = launch_moe_route(a, static_cast<int*>(h->lin_sums), h->lin_counters + first, h->num_sms, s, &n);
+    rc = launch_moe_route(a, static_cast<int*>(h->route_counts), h->lin_counters + linear_counters(h->num_sms), h->num_sms,
+                          s, &n);
     h->launches += n;
     return rc;
 }
