@@ -453,6 +453,9 @@ typedef enum {
                                    with its K split over two CTA pairs per tile, fills between half and all
                                    of the SMs in one wave; else 2 when in[3] is even and 2*C_out <= 256;
                                    else 1), or 1, 2, 4 */
+    GEMM_OPT_TEST_STALL_PAIR = 9, /* test hook beside GEMM_OPT_TEST_STALL, linear layers only: 0 (default) every
+                                   pair of CTAs stalls, else (1..1024) the pair of that number alone, while
+                                   the others finish */
     GEMM_OPT_CONV_SPLIT = 8     /* tensor-core convolution: K split over CTA pairs, 0 choose (default: two
                                    pairs per tile when the tiles would fill at most a quarter of the SMs),
                                    1 one pair per tile, 2 two pairs per tile (GEMM_ERR_UNSUPPORTED from the

@@ -259,6 +259,10 @@ static int gemm_set_option_impl(gemm_handle_t h, int option, int64_t value)
         if (value < 0 || value > 1) return GEMM_ERR_INVALID_ARG;
         h->opt_test_stall = (int)value;
         return GEMM_OK;
+    case GEMM_OPT_TEST_STALL_PAIR:
+        if (value < 0 || value > 1024) return GEMM_ERR_INVALID_ARG;
+        h->opt_test_stall_pair = (int)value;
+        return GEMM_OK;
     case GEMM_OPT_WAIT_LIMIT_US:
         if (value < 0 || value > 60000000) return GEMM_ERR_INVALID_ARG;
         h->wait_limit_ns = value == 0 ? 2000000000ull : (uint64_t)value * 1000ull;
@@ -714,9 +718,6 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
     if (cudaMemcpy(&v, h->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
     if (v != 0) {
         if (cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) return GEMM_ERR_CUDA;
-        // a linear-layer kernel that gave up may have left arrivals uncounted
-        if (cudaMemset(h->lin_counters, 0, (size_t)(linear_counters(h->num_sms) + 1) * sizeof(unsigned)) != cudaSuccess)
-            return GEMM_ERR_CUDA;
         glog("gemm_get_device_status: a bounded wait ran out (device code %d)", v);
         return GEMM_ERR_DEVICE_TIMEOUT;
     }

@@ -28,6 +28,7 @@ struct gemm_ctx {
     int opt_tc_chunk = 0;  // tensor-core accumulation chunk in 64-wide k-blocks (0 = default)
     int opt_tc_pair = 0;   // tensor-core tile: 0 choose, 1 single CTA, 2 CTA pair
     int opt_test_stall = 0;  // test hook: kernels with bounded waits let one wait run out
+    int opt_test_stall_pair = 0;  // and of the linear layers' only this CTA pair (from 1; 0: all)
     int opt_conv_stack = 0;  // tensor-core convolution: output positions stacked along N (0 = choose)
     int opt_conv_split = 0;  // tensor-core convolution: 0 choose, 1 one CTA pair per tile, 2 two pairs
     uint64_t wait_limit_ns = 2000000000ull;
@@ -41,7 +42,7 @@ struct gemm_ctx {
     size_t lin_sums_bytes = 0;
     void* route_counts = nullptr;
     size_t route_counts_bytes = 0;
-    // arrival counters, zero between launches: linear_counters(num_sms) of the products, then
+    // arrival counters, zero after every launch: linear_counters(num_sms) of the products, then
     // the router's.  Made with the handle, so that they never move
     unsigned* lin_counters = nullptr;
     bool captured = false;    // a graph holds addresses of the buffers that grow

@@ -50,7 +50,7 @@ int launch_linear_few(const LinArgs& a, int num_sms, cudaStream_t stream, int* l
 // Buffers the handle keeps for the linear kernels.
 struct LinWorkspace {
     float* partials = nullptr;    // K slices of the last wave's tiles
-    unsigned* counters = nullptr;  // arrivals; every launch leaves them zero
+    unsigned* counters = nullptr;  // arrivals; every launch leaves them zero, one that gave up as well
 };
 
 // Workspace bytes of the K-sliced last wave, and counters (of 4 bytes).

@@ -43,8 +43,8 @@ int run_product(gemm_handle_t h, const LinArgs& a, size_t need, cudaStream_t s)
     ws.partials = need > 0 ? h->lin_partials : nullptr;
     ws.counters = h->lin_counters;
     int n = 0;
-    const int rc = launch_linear(a, ws, h->num_sms, h->d_status, h->wait_limit_ns, h->opt_tc_chunk, h->opt_test_stall,
-                                 s, &n);
+    const int stall = !h->opt_test_stall ? 0 : h->opt_test_stall_pair > 0 ? h->opt_test_stall_pair : -1;
+    const int rc = launch_linear(a, ws, h->num_sms, h->d_status, h->wait_limit_ns, h->opt_tc_chunk, stall, s, &n);
     h->launches += n;
     return rc;
 }

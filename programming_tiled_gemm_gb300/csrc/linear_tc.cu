@@ -30,7 +30,8 @@
 // partial wave (all tiles, when there are fewer than pairs) may be cut along K into slices,
 // one a pair.  Every slice goes to the workspace in fp32; the CTA that counts last adds the
 // slices of its tile in K order and runs the epilogue.  Nothing waits for another CTA, and
-// the order of the sum does not depend on who is last.
+// the order of the sum does not depend on who is last.  A CTA that gave up on a wait is counted
+// too, so that every launch leaves the counters zero.
 //
 // kLinDw over groups: a group's last k-block ends inside the next group's rows.  Those rows
 // are zeroed in shared memory, in both operands (zero times a neighbour's NaN would be NaN),
@@ -76,6 +77,7 @@ constexpr int RASTER = 8;             // row tiles per raster group (2048 rows s
 constexpr int STG_BYTES = 2048;       // an epilogue warp's staging block: 32 rows x 32 features of 16 bits,
                                       // or (gated) 16 columns of fp32 for the other warp
 constexpr int SMEM_MAX = 232448;      // 227 KiB
+constexpr unsigned SLICE_MISSING = 1u << 16;  // in the count of a tile's slices: one that gave up
 
 // Warps 0..3: producer of A, MMA issuer, fixer (kLinDw; db's sums in kLinDx), producer of B; 4..11: epilogue, which takes
 // registers from the first four: 80 + 2 * 208 a thread of the three warpgroups are within
@@ -115,7 +117,7 @@ struct LinParams {
     int ws_cols;     // columns of a partial tile in the workspace
     int* status;
     uint64_t limit_ns;
-    int test_stall;
+    int test_stall;  // test hook: pair n - 1 first waits on a barrier nothing arrives on (-1: every pair)
     float* db;       // kLinDx: [G][db_cols], the sums of the pieces of db_piece rows in db_ws, or null
     const float* db_ws;
     int db_piece, db_cols;
@@ -758,7 +760,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         // After a wait has run out a warp goes on through its items without waiting or
         // storing, so that the others' barriers are still met.
         bool dead = false;
-        if (p.test_stall) {
+        if (p.test_stall < 0 || p.test_stall == pair + 1) {
             bool ok = mbar_wait_cluster(smem_u32(never_bar), 0, p.limit_ns, nullptr);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok && lane == 0) record_error(p.status, kDevTimeoutEpilogue, abort_flag);
@@ -852,11 +854,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 if (dead) *abort_flag = 1;
                 named_barrier(1, 32 * EPI_WARPS);
                 if (e == 0) {
-                    int last = 0;
-                    if (!*abort_flag) {
-                        unsigned* c = p.cnt + 2 * it.part + rank;
-                        last = atomicAdd(c, 1u) == (unsigned)(walk.slices_of_tile() - 1);
-                        if (last) *c = 0;  // ready for the next launch
+                    // A CTA that gave up is counted as well (it comes here all the same), with
+                    // SLICE_MISSING: so the count always gets to the last and back to zero, and a tile
+                    // that lacks a slice is finished by nobody
+                    unsigned* c = p.cnt + 2 * it.part + rank;
+                    const unsigned mine = *abort_flag ? 1u + SLICE_MISSING : 1u, now = atomicAdd(c, mine) + mine;
+                    int last = now % SLICE_MISSING == (unsigned)walk.slices_of_tile();
+                    if (last) {
+                        *c = 0;  // ready for the next launch
+                        last = now < SLICE_MISSING;
                     }
                     __threadfence();
                     *last_flag = last;
