@@ -713,11 +713,16 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
     if (!h) return GEMM_ERR_INVALID_ARG;
     DeviceGuard g(h->device);
     if (!g.ok()) return GEMM_ERR_CUDA;
-    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GEMM_ERR_CUDA;
+    // read and cleared on the caller's stream: the legacy stream's copy would wait for others' work, and
+    // its memset, which does not wait for itself, could clear what a later call on `stream` reports
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int v = 0;
-    if (cudaMemcpy(&v, h->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return GEMM_ERR_CUDA;
+    if (cudaMemcpyAsync(&v, h->d_status, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return GEMM_ERR_CUDA;
     if (v != 0) {
-        if (cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) return GEMM_ERR_CUDA;
+        if (cudaMemsetAsync(h->d_status, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+            return GEMM_ERR_CUDA;
         glog("gemm_get_device_status: a bounded wait ran out (device code %d)", v);
         return GEMM_ERR_DEVICE_TIMEOUT;
     }

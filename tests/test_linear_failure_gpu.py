@@ -108,3 +108,19 @@ def test_a_tile_with_a_slice_missing_is_not_written(g, lib):
 def test_stall_hook_refuses_other_values(g, lib):
     for v in (-1, 1025):
         assert g.gemm_set_option(lib.handle, g.GEMM_OPT_TEST_STALL_PAIR, v) == g.GEMM_ERR_INVALID_ARG
+
+
+def test_status_waits_for_its_own_stream_only(g, lib):
+    """The status is read and cleared in the order of the stream it is asked for: not behind work of
+    the default stream, where it would also not be ordered before what that stream's caller runs next."""
+    x, w = randn(31, 24, 4096), randn(32, 4096, 512)
+    stream = torch.cuda.Stream()  # (does not wait for the default stream)
+    torch.cuda.synchronize()
+    stalled(g, lib, 1, lambda: lib.linear(x, w, stream=stream.cuda_stream))
+    torch.cuda._sleep(1_000_000_000)  # half a second of the default stream
+    busy = torch.cuda.Event()
+    busy.record()
+    assert lib.device_status(stream=stream.cuda_stream) == g.GEMM_ERR_DEVICE_TIMEOUT
+    assert lib.device_status(stream=stream.cuda_stream) == g.GEMM_OK
+    assert not busy.query()
+    torch.cuda.synchronize()
