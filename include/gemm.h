@@ -430,7 +430,9 @@ typedef enum {
                                 16-byte aligned with lda, ldb % 4 == 0, else GEMM_ERR_ALIGNMENT).  Auto:
                                 M<=32 skinny (4, else 3), M<=64 2, else 5 when its alignment holds, else 1 */
     GEMM_OPT_SPLIT_K = 2,    /* 0 auto, else the split-K factor for fp32 kernels (1..1024) */
-    GEMM_OPT_WAIT_LIMIT_US = 3, /* 0 default (2 s), else the bounded-wait limit of device waits in microseconds */
+    GEMM_OPT_WAIT_LIMIT_US = 3, /* 0 default (2 s), else the bounded-wait limit of device waits in microseconds
+                                   (linear layers: without a step of the pipeline or a tile finished, however
+                                   long the launch takes) */
     GEMM_OPT_TC_CHUNK = 4,      /* 0 default (16), else the tensor-core accumulation chunk in 64-wide k-blocks
                                    (1..4096): the tensor core's fp32 accumulator is restarted every chunk and
                                    chunk sums are added in fp32 round-to-nearest (linear layers: rounded up to

@@ -469,6 +469,21 @@ __device__ __forceinline__ void add_db(const LinParams& p, const int* off, int l
     }
 }
 
+// A wait that lasts for other roles' many steps, of which each has waits of its own: the limit
+// counts from the last step seen (`progress`, which moves with the tiles), not from its start, or
+// it would be a limit to a healthy launch's time.
+__device__ __forceinline__ bool mbar_wait_while(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag,
+                                                volatile int* progress)
+{
+    int seen = *progress;
+    while (!mbar_wait_cluster(bar, parity, limit_ns, abort_flag)) {
+        const int now = *progress;
+        if (now == seen || (abort_flag && *abort_flag)) return false;
+        seen = now;
+    }
+    return true;
+}
+
 // KPS: k-blocks of a stage, which are waited for and committed together.
 template <int MODE, bool GATED, bool BF16, bool CHUNKED, int KPS>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -494,6 +509,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tfull_bar + 6);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_holder + 2);
+    volatile int* progress = reinterpret_cast<volatile int*>(tmem_holder + 3);  // accumulators the epilogue has had
     int* off = reinterpret_cast<int*>(tmem_holder + 4);
     int* cum = off + p.G + 1;
 
@@ -518,6 +534,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         mbar_init(smem_u32(drain_bar), 1);
         mbar_init(smem_u32(never_bar), 1);
         *abort_flag = 0;
+        *progress = 0;
         mbar_fence_init();
         if (p.kb > 0) {
             prefetch_tensormap(&tmA);
@@ -697,7 +714,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 if (elect_one()) umma_commit_mask(smem_u32(drain_bar), pair_mask);
                 __syncwarp();
             }
-            if (!mbar_wait_cluster(smem_u32(drain_bar), 0, p.limit_ns, nullptr)) {
+            // (the odd CTA's warp is here from the start)
+            if (!mbar_wait_while(smem_u32(drain_bar), 0, p.limit_ns, nullptr, progress)) {
                 record_error(p.status, kDevTimeoutDrain, abort_flag);
                 aborted = true;
             }
@@ -717,7 +735,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 stage = (stage + nk) % p.stages;
                 if (r >= BK) continue;
                 const uint32_t parity = (used >> s) & 1;
-                ok = mbar_wait(smem_u32(&tail_bar[s]), parity, p.limit_ns, abort_flag);
+                // (whole tiles go by unseen before it)
+                ok = mbar_wait_while(smem_u32(&tail_bar[s]), parity, p.limit_ns, abort_flag, progress);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) {
                     if (lane == 0) record_error(p.status, kDevTimeoutMma, abort_flag);
@@ -786,6 +805,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                     if (lane == 0) record_error(p.status, kDevTimeoutEpilogue, abort_flag);
                     dead = true;
                 }
+                if (ok && warp == EPI_WARP0 && lane == 0) *progress = *progress + 1;
                 tc_fence_after();
             };
             const auto release = [&] {

@@ -124,3 +124,24 @@ def test_status_waits_for_its_own_stream_only(g, lib):
     assert lib.device_status(stream=stream.cuda_stream) == g.GEMM_OK
     assert not busy.query()
     torch.cuda.synchronize()
+
+
+def test_wait_limit_is_none_of_the_launch(g, lib):
+    """A launch may last far longer than the limit as long as its tiles come along.  Forward: one of the
+    pair's CTAs has a warp that waits for the whole launch.  Gradient of W over groups: the
+    groups' last rows are waited for past every whole tile."""
+    x, w = randn(41, 16384, 8192), randn(42, 8192, 16384)
+    lib.set_option(g.GEMM_OPT_WAIT_LIMIT_US, 0)
+    off = torch.tensor([0, 16384 - 64, 16384 - 31], dtype=torch.int32, device="cuda")
+    want = lib.linear(x, w)
+    _, want_dw, _ = lib.grouped_linear_backward(want, x, w.view(1, 8192, 16384).expand(2, -1, -1).contiguous(), off,
+                                                need_dx=False)
+    w2 = torch.empty(2, 8192, 16384, device="cuda", dtype=torch.bfloat16)
+    assert lib.device_status() == g.GEMM_OK
+    lib.set_option(g.GEMM_OPT_WAIT_LIMIT_US, 400)
+    y = lib.linear(x, w)
+    assert lib.device_status() == g.GEMM_OK
+    assert torch.equal(y, want)
+    _, dw, _ = lib.grouped_linear_backward(want, x, w2, off, need_dx=False)
+    assert lib.device_status() == g.GEMM_OK
+    assert torch.equal(dw, want_dw)
