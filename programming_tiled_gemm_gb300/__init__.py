@@ -13,7 +13,7 @@ import struct
 from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
-# GEMM_GB300_DEBUG=1 loads the debug build (every computed global index checked in the
+# GEMM_GB300_DEBUG=1 loads the debug build (computed global indices checked in the
 # kernels; a failed check is reported by gemm_get_device_status as GEMM_ERR_DEVICE_BOUNDS).
 DEBUG = os.environ.get("GEMM_GB300_DEBUG") == "1"
 LIB_PATH = os.path.join(_PKG, "lib", "libgemm_gb300_debug.so" if DEBUG else "libgemm_gb300.so")

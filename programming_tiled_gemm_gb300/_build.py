@@ -2,7 +2,7 @@
 
 Output: ``programming_tiled_gemm_gb300/lib/libgemm_gb300.so`` (sm_103a only), and with
 ``debug=True`` ``lib/libgemm_gb300_debug.so``: the same sources built with -DGEMM_DEBUG,
-whose kernels check every computed global index before the access (see internal.h).
+whose kernels check the global indices they compute before the access (see internal.h).
 Object files go to ``programming_tiled_gemm_gb300/_build/`` (``_build/debug/``).  Nothing is
 installed.
 """

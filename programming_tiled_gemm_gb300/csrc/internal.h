@@ -27,9 +27,10 @@ bool log_enabled();
 void glog(const char* fmt, ...) __attribute__((format(printf, 1, 2)));
 
 // ------------------------------------------------------------------ debug builds
-// Built with -DGEMM_DEBUG (lib/libgemm_gb300_debug.so), every global access a kernel makes
-// through an index it computed is checked against the extent of its operand first: a check
-// that fails raises the bounds flag of the kernel's translation unit and the access is
+// Built with -DGEMM_DEBUG (lib/libgemm_gb300_debug.so), global accesses that a kernel makes
+// through an index it computed or read from device memory (a pick's slot, row or expert) are
+// checked against the extent of their operand first, unless the index is a loop's that ends
+// there or a tensor-map copy's: a check that fails raises the bounds flag of the kernel's translation unit and the access is
 // skipped (no trap, no assert; the thread carries on, so every barrier is still reached).
 // gemm_get_device_status reads and clears the flags of all translation units and reports
 // GEMM_ERR_DEVICE_BOUNDS.  The flags belong to the process and the device, not to a handle.

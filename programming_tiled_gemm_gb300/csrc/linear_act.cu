@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 3) linear_act_kernel(ActParams p)
             float t = 0.f;
 #pragma unroll
             for (int q = 0; q < WARPS; ++q) t += sums[q][threadIdx.x / 8 * 9 + threadIdx.x % 8];
-            if (c < p.N) dst[h * p.N + c] = t;
+            if (c < p.N && in_range(item, p.items) && in_range(h * p.N + c, Nw)) dst[h * p.N + c] = t;
         }
     }
 }
@@ -259,13 +259,13 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) linear_db_kernel(ActParams p, 
     const float* src = p.ws + (int64_t)cum[g] * Nw + c;
     const int pieces = cum[g + 1] - cum[g];
     float t = 0.f;
-    if (c < Nw) {
+    if (c < Nw && (pieces == 0 || in_range(cum[g + 1] - 1, p.items))) {
 #pragma unroll 8
         for (int i = warp; i < pieces; i += SUM_WARPS) t += __ldcg(src + (int64_t)i * Nw);
     }
     sums[warp][lane] = t;
     __syncthreads();
-    if (warp == 0 && c < Nw) {
+    if (warp == 0 && c < Nw && in_range(g, p.G)) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < SUM_WARPS; ++w) v += sums[w][lane];

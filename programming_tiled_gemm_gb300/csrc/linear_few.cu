@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
     const int cl = lane % 8, kr = lane / 8;
     const int first = out0 + (GATED ? cl % 4 : cl) * 8;
     const int ncol = max(0, min(8, p.N - first));
-    const uint16_t* W = p.W + (ncol > 0 ? first + (GATED && cl >= 4 ? p.N : 0) : 0);
+    const int wcol = ncol > 0 ? first + (GATED && cl >= 4 ? p.N : 0) : 0;
+    const uint16_t* W = p.W + wcol;
     float2 acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -97,11 +98,12 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
             const int k0 = b * BATCH + kr * DEEP;
 #pragma unroll
             for (int u = 0; u < DEEP; ++u) {
-                const bool in = k0 + u < p.K;
+                const bool in = k0 + u < p.K && (ncol == 0 || (in_range(k0 + u, p.K) && in_range(wcol + ncol - 1, p.Nw)));
                 copy_8(at + u * 512 + lane * 16, W + (in ? (int64_t)(k0 + u) * p.ldw : 0), in ? ncol : 0);
             }
             if (cl < MT) {
-                const int n = cl < p.M ? max(0, min(8, p.K - k0)) : 0;
+                int n = cl < p.M ? max(0, min(8, p.K - k0)) : 0;
+                if (n > 0 && (!in_range(cl, p.M) || !in_range(k0 + n - 1, p.K))) n = 0;
                 copy_8(at + DEEP * 512 + (cl * 4 + kr) * 16, p.X + (n > 0 ? cl * p.ldx + k0 : 0), n);
             }
         }
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
     };
     for (int e = rank * THREADS + threadIdx.x; e < p.M * OUT; e += C * THREADS) {
         const int m = e / OUT, j = e % OUT, n = out0 + j;
-        if (n >= p.N || !in_range(m, p.M)) continue;
+        if (n >= p.N || !in_range(m, p.M) || !in_range(n, p.N) || !in_range(GATED ? p.N + n : n, p.Nw)) continue;
         float v[1] = {total(m * COLS + j)};
         if (p.bias) v[0] += from_16<BF16>(p.bias[n]);
         uint16_t* z = p.Z ? p.Z + m * p.ldz + n : nullptr;

@@ -898,7 +898,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
             const int nf = dead ? 0 : p.F - fw;
             const int zw = GATED && q >= 2 ? p.F + fw : fw;
             float bias = 0.f;
-            if (MODE == kLinFwd && p.bias && lane < nf)
+            if (MODE == kLinFwd && p.bias && lane < nf && in_range(it.g, p.G) && in_range(zw + lane, p.bias_stride))
                 bias = from_16<BF16>(static_cast<const uint16_t*>(p.bias)[it.g * p.bias_stride + zw + lane]);
             const int64_t out0 = MODE == kLinDw ? it.g * p.out_stride : 0;
             constexpr int OUT_N = GATED ? 16 : 32;       // rows a warp finishes of 32 (gated: the pair shares them)

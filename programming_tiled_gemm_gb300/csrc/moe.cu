@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = 32 * c + lane;
-            v[c] = e < E ? D::get(l[e]) : -INFINITY;
+            v[c] = e < E && in_range(t, p.T) ? D::get(l[e]) : -INFINITY;
         }
     };
     int picks[R_EACH], ranks[R_EACH];  // lane j: the j-th pick of each token
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
         ranks[q] = have ? mine[pick]++ : 0;
         picks[q] = pick;
         __syncwarp();
-        if (lane < k) {
+        if (lane < k && in_range(t, p.T)) {
             const int64_t i = (int64_t)t * k + lane;
             p.weights[i] = have ? ex / rest : 0.f;
             p.experts[i] = pick;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(32 * route_warps(C)) route_kernel(RouteParams 
             int slot = -1;
             if (picks[q] >= 0) {
                 slot = own_counts[picks[q]] + mine[picks[q]] + ranks[q];
-                p.rows[slot] = i;
+                if (in_range(slot, (int64_t)p.T * k)) p.rows[slot] = i;
             }
             p.slots[i] = slot;
         }
@@ -324,7 +324,7 @@ __global__ void route_place_kernel(RouteParams p)
     if (i >= n) return;
     const int e = p.experts[i];
     int slot = -1;
-    if (e >= 0) {
+    if (e >= 0 && in_range(e, p.E) && in_range(i / p.k / p.tokens, p.nblk)) {
         slot = p.base[(i / p.k / p.tokens) * p.E + e] + p.slots[i];
         if (in_range(slot, n)) p.rows[slot] = (int)i;
     }
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(32 * G_WARPS) route_grad_kernel(RouteGradParam
     for (int e = lane; e < p.E; e += 32) g[e] = 0.f;
     __syncwarp();
     int e = lane < p.k ? p.experts[t * p.k + lane] : -1;
-    if (e >= p.E) e = -1;
+    if (e >= 0 && (!in_range(e, p.E) || e >= p.E)) e = -1;
     const bool have = e >= 0;
     const float dw = have ? p.dweights[t * p.k + lane] : 0.f;
     const float x = have ? D::get(l[e]) : -INFINITY;
@@ -432,7 +432,7 @@ __global__ void dispatch_kernel(DispatchArgs a)
     const int64_t r = blockIdx.x;
     const int at = a.rows[r];
     const int64_t t = at >= 0 ? at / a.k : -1;
-    if (t >= a.T) return;  // (no row of x)
+    if (at >= 0 && (!in_range(t, a.T) || t >= a.T)) return;  // (no row of x)
     // four accesses in flight a thread; x's row is read again for the token's other experts,
     // the copies are not.  (8192 x 4096 bf16 to four experts: 59 us, 5.7 TB/s; x comes from DRAM
     // 2.1 times, each die's L2 fetching it once, whatever the order of the rows.)
@@ -441,13 +441,13 @@ __global__ void dispatch_kernel(DispatchArgs a)
         Vec<D, V> v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (c + i * step < a.N) {
+            if (c + i * step < a.N && in_range(c + i * step + V - 1, a.N)) {
                 if (t >= 0) v[i].load(a.x, t * a.ldx + c + i * step);
                 else v[i].zero();
             }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (c + i * step < a.N) v[i].store_once(a.xr, r * a.ldxr + c + i * step);
+            if (c + i * step < a.N && in_range(c + i * step + V - 1, a.N)) v[i].store_once(a.xr, r * a.ldxr + c + i * step);
     }
 }
 
@@ -464,11 +464,12 @@ __global__ void combine_kernel(CombineArgs a)
     const int64_t t = blockIdx.x;
     if (threadIdx.x < a.k) {
         const int s = a.slots[t * a.k + threadIdx.x];
-        slot[threadIdx.x] = s < a.rows_y ? s : -1;
+        slot[threadIdx.x] = s >= 0 && in_range(s, a.rows_y) && s < a.rows_y ? s : -1;
         w[threadIdx.x] = a.weights ? a.weights[t * a.k + threadIdx.x] : 1.f;
     }
     __syncthreads();
     for (int c = threadIdx.x * V; c < a.N; c += blockDim.x * V) {
+        if (!in_range(c + V - 1, a.N)) break;
         float s[V] = {};
         int j = 0;
         // four rows in flight, added in order
@@ -515,11 +516,13 @@ __global__ void combine_grad_kernel(CombineGradArgs a)
     for (int j = 0; j < a.k; ++j) {
         const int64_t i = t * a.k + j;
         int s = a.slots[i];
-        if (s >= a.T * a.k) s = -1;
+        if (s >= 0 && (!in_range(s, a.T * a.k) || s >= a.T * a.k)) s = -1;
         const float w = a.weights[i];
         float dot = 0.f;
         const bool none = a.rows[i] < 0;  // row i of dy (not of this token) holds nothing
+        if (!none) (void)in_range(a.rows[i], a.T * a.k);
         for (int c = threadIdx.x * V; c < a.N; c += blockDim.x * V) {
+            if (!in_range(c + V - 1, a.N)) break;
             Vec<D, V> g, y;
             if (s >= 0) {
                 g.load(a.dout, t * a.lddo + c);
