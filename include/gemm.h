@@ -251,9 +251,13 @@ int conv4d_forward_tc(gemm_handle_t h, const void* x, int64_t C_in, const int64_
  * row-major as B is in gemm_run.
  *
  * Operands are bf16 or fp16 (GEMM_F32 is GEMM_ERR_UNSUPPORTED: these run on the tensor
- * cores only).  Products of 16-bit values accumulate in fp32 as in gemm_run; bias,
- * activation and residual are applied in fp32 and the result is rounded once.  Results
- * are deterministic.
+ * cores only).  Products of 16-bit values accumulate in fp32; bias, activation and residual
+ * are applied in fp32 and the result is rounded once.  Results are deterministic.
+ * The tensor core's accumulator truncates: up to 2^-23 of the partial sum every 16 of the
+ * reduced dimension.  fp32 results, and all results of more than 16384 of it, restart it
+ * every 1024 as gemm_run does.  16-bit results of up to 16384 do not: they lose up to 2^-13 of
+ * the largest partial sum there (2^-17 at 1024), which shows where sums cancel.
+ * GEMM_OPT_TC_CHUNK restarts it for them too (128-row tiles: 1.1 to 1.6 times the time).
  *
  * Workspace and CUDA graphs, of the calls here and of moe_route below: calls on one handle
  * share its workspace, so calls on different streams (and replays of graphs) must not overlap
@@ -436,7 +440,7 @@ typedef enum {
     GEMM_OPT_TC_CHUNK = 4,      /* 0 default (16), else the tensor-core accumulation chunk in 64-wide k-blocks
                                    (1..4096): the tensor core's fp32 accumulator is restarted every chunk and
                                    chunk sums are added in fp32 round-to-nearest (linear layers: rounded up to
-                                   an even number) */
+                                   an even number; by default no chunks for 16-bit results of up to 16384) */
     GEMM_OPT_TC_PAIR = 5,       /* tensor-core tiles: 0 choose (default: pairs when M > 128; for M <= 128 with
                                    128x256 tiles that fill under half the SMs, K split into 2 to 16 slices,
                                    one CTA each, on a cluster per tile that adds the fp32 partial tiles in

@@ -19,12 +19,17 @@
 //
 // Pipeline, as in the plain product's CTA-pair kernel: TMA producers, a ring of stages, one
 // warp a pair that issues MMAs, eight epilogue warps a CTA.  The tensor core's fp32
-// accumulation rounds toward zero: 2^-24 of the sum lost per 16 of K.  For fp32 results, and
-// for more than 16384 of K, it is cut into chunks of `kc` k-blocks (16: 1024 of K, as in the
-// plain product), each in a fresh TMEM accumulator, added in fp32 round-to-nearest registers
-// in order (CHUNKED).  Otherwise one accumulator takes all of K: at 16384 that is 2^-14 of
-// the sum, an eighth of an fp16 result's own rounding and 1/64 of a bf16 result's, and the
-// epilogue, which takes its sums straight from TMEM, overlaps the whole next tile.
+// accumulation rounds toward zero: up to 2^-23 of the PARTIAL sum is lost per 16 of K.  For fp32
+// results, and for more than 16384 of K, it is cut into chunks of `kc` k-blocks (16: 1024 of K, as
+// in the plain product), each in a fresh TMEM accumulator, added in fp32 round-to-nearest
+// registers in order (CHUNKED).  Otherwise one accumulator takes all of K (or of a slice), and
+// the epilogue, which takes its sums straight from TMEM, overlaps the whole next tile.  At 16384
+// that loses 2^-13 of the largest partial sum at most, a quarter of an fp16 result's own
+// rounding and 1/32 of a bf16 result's where the sum does not cancel (measured, products of one
+// sign: 1.0e-4, 2^-13.2; in chunks 5.4e-6).  Sums of random signs lose far less, as their partial
+// sums stay small.  Where a sum cancels, the loss is still of the large partial sum: halves that
+// cancel to 1/230 were off by 3.9e-3 (fp16) and 4.1e-3 (bf16) of the result, 2.1e-4 and 1.7e-3
+// in chunks, which GEMM_OPT_TC_CHUNK asks for.
 //
 // Work: tiles are walked round robin by the persistent pairs.  The tiles of the last,
 // partial wave (all tiles, when there are fewer than pairs) may be cut along K into slices,

@@ -249,3 +249,27 @@ def test_groups_cut_along_k(lib, counts, act, dt):
                 check_forward(y[sl], z[sl], x[sl], w[e], b[e], act, None)
         again = lib.grouped_linear(x, w, off, bias=b, act=act, out_dtype=out_dtype)
         assert torch.equal(again, y)
+
+
+# ------------------------------------------------------------------------------------------------ long sums
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("signs", ["same", "halves cancel"])
+def test_one_accumulator_over_16384(g, lib, signs, dt):
+    """16-bit results of whole tiles keep one accumulator over all of K: off by 2^-23 of the largest
+    partial sum at most every 16 of K, however small the sum ends.  Largest partial sum: the sum
+    itself, or of a first half that the second takes back.  In chunks of 1024: the same of each
+    chunk's own partial sums, and one fp32 addition a chunk."""
+    dtype, K = DTYPES[dt], 16384
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    x = (torch.rand(1024, K, generator=gen, device="cuda") * 0.5 + 0.5).to(dtype)
+    w = ((torch.rand(K, 4864, generator=gen, device="cuda") * 0.5 + 0.5) / K).to(dtype)
+    if signs != "same":
+        w[K // 2:] *= -1
+    z = x.double() @ w.double()
+    largest = z if signs == "same" else x[:, :K // 2].double() @ w[:K // 2].double()
+    rounded(lib.linear(x, w), z, K / 16 * 2.0 ** -23 * largest)
+    lib.set_option(g.GEMM_OPT_TC_CHUNK, 16)
+    chunk = x[:, :1024].double() @ w[:1024].double() * 2  # (twice the first's: every chunk's, by the factors' range)
+    rounded(lib.linear(x, w), z, K / 16 * 2.0 ** -23 * chunk + 16 * 2.0 ** -24 * largest)
+    lib.set_option(g.GEMM_OPT_TC_CHUNK, 0)
