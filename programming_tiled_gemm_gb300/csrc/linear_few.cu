@@ -240,9 +240,21 @@ cudaError_t launch_rows(const FewParams& p, int rows, int blocks, cudaStream_t s
 }  // namespace
 
 // One row costs W's bytes alone; more are bound by the FMAs in time, and large W are then as fast
-// or faster on the tensor cores.  us here and there: 1 row 4096 x 28672 40 and 42, 8192 x 28672
-// 77 and 75; 4 rows 8192 x 8192 25 and 27, 4096 x 16384 gated 55 and 47; 8 rows 4096 x 4096 11.8
-// and 12.7, 8192 x 8192 35 and 27.
+// or faster on the tensor cores.  3 rows run the kernel of 4, 5 to 7 that of 8, each at its
+// time (bf16; every row count was timed).  us here and on the tensor cores, K x columns of W:
+//                         1 row       2           3, 4        5 to 8
+//   2048 x 2048           4.4   9.4   4.6   9.4   5.2   9.4   6.3   9.4
+//   4096 x 4096           7.7  12.9   8.1  12.9   9.1  12.8  11.6  12.8
+//   16384 x 1024          9.5  13.7  10.7  13.7  13.4  13.7  19.0  13.7
+//   4096 x 8192          12.9  17.4  13.5  17.5  14.5  17.5  19.7  17.5
+//   8192 x 8192          23.2  27.4  24.5  27.4  25.6  27.4  34.8  27.4
+//   4096 x 16384 gated   22.5  24.2  24.1  24.3  27.4  24.3  36.0  24.3
+//   4096 x 28672         40.1  41.5  40.0  41.6  39.7  41.6  50.7  41.8
+//   8192 x 16384         44.3  42.6  46.1  42.9  46.6  42.8  64.5  42.9
+//   8192 x 28672         76.7  74.4  77.1  74.4  76.3  74.5  95.3  74.8
+// The limits are of W's size alone: beside them the kernel not chosen is up to 8 % faster for
+// one or two rows, 11 % for three or four; for five to eight, 11 % where K is short and a third at
+// 16384 x 1024, where 128 CTAs leave a part of the FMAs idle.
 bool linear_is_few(const LinArgs& a)
 {
     if (a.mode != kLinFwd || a.G != 0) return false;
