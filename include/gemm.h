@@ -342,7 +342,12 @@ typedef struct gemm_linear_grad_args {
  *   activation's input (unread for GEMM_ACT_NONE).  dX [M][K]: `dtype`.  dW [K][Nw] (per
  *   group at dw_stride elements): `dw_dtype`, `dtype` or GEMM_F32.  db [Nw] (per group
  *   contiguous): fp32.  All are overwritten; a group without rows gets zeros.
- * dZ is rounded once to `dtype` for the two products; db sums it before that rounding.
+ * dZ is rounded once to `dtype` for the two products, as their operand; db sums it before that
+ * rounding.  So dX and dW are off by 1.4 times their own rounding (bf16: 2.3e-3 instead of
+ * 1.7e-3 in norm), and in GEMM_F16 an element of dZ above 65504 becomes infinite and one below
+ * 2^-25 zero: scale dY (the loss) accordingly.  GEMM_ACT_NONE reads dY itself.
+ * The handle keeps dZ's buffer, M x Nw 16-bit values (Nw to a multiple of 8), until
+ * gemm_destroy.
  * dY, Z, X and W must be 16-byte aligned with leading dimensions (and w_stride) multiples
  * of 8, the outputs aligned to their elements.  Groups, errors and limits as in
  * gemm_linear; dX's rows from offsets[groups] on are not written.

@@ -44,7 +44,8 @@
 //
 // Measured (GB300, bf16; the plain product's measured rate is 1878 TFLOP/s, copies 6.79 TB/s):
 //   8192^3, bias, gelu_tanh and residual: 575 us in a burst, 1912 TFLOP/s, tensor pipe busy;
-//     664 us (1656 TFLOP/s) back to back under the power limit
+//     (the plain product 571) and 680 to 700 us (1570 to 1620 TFLOP/s) back to back under the
+//     power limit
 //   4096^3: dX 74 us, dW 81 us, with the full epilogue 81 us (tensor pipe 90, 88, 81 % active)
 //   16 x 8192 x 8192: 27 us, 4.9 TB/s; 16 x 8192 x 28672: 75 us, 6.3 TB/s (HBM)
 //   16 x 2048 x 2048: 9.6 us, latency: 5 us of launch, set-up, first loads and drain, then
