@@ -409,6 +409,45 @@ int moe_combine_backward(gemm_handle_t h, int64_t T, int64_t N, int64_t k, const
                          const void* y, int64_t ldy, int dtype, const int32_t* slots, const int32_t* rows,
                          const float* weights, void* dy, int64_t lddy, float* dweights, void* stream);
 
+/* ------------------------------------------------------------------ token log probabilities
+ *
+ * What is asked of a model's logits [rows][V] once its last product has made them.  dtype is
+ * GEMM_F32, GEMM_BF16 or GEMM_F16; sums are held in fp32 and added in a fixed order.  No
+ * workspace; calls on different streams may overlap.  Rows may start on any element (`ld`: no
+ * multiple is asked for).  V <= 2^30, rows < 2^31 - 1024, else GEMM_ERR_UNSUPPORTED. */
+
+/* With u_j = logits[r][j] / temperature and p = softmax(u):
+ *   logprobs[r] = ln p_t for t = tokens[r], 0 where t is outside 0 .. V-1 (none is given);
+ *   entropy[r] = -sum p_j ln p_j (or NULL: not computed);
+ *   stats[r] = {the largest logit m, ln sum exp((logits[r][j] - m) / temperature)}, for
+ *     token_logprobs_backward; ln sum exp(u) = stats[r][0] / temperature + stats[r][1];
+ *   top_tokens[r][i], top_logprobs[r][i], i < top: the `top` most likely tokens in order, equal
+ *     logits (and +0, -0) by the lower index, and their ln p; -1 and -inf where there are no more.
+ * A logit of -inf is a token that cannot come: p = 0, never among the alternatives.  A row of
+ * -inf only has entropy 0, no alternatives and, where a token is given, logprob -inf.  A row that holds
+ * NaN or +inf: NaN, and no alternatives.
+ * logits, logprobs, entropy, stats and top_logprobs are aligned to their elements, tokens and
+ * top_tokens to 8 bytes (GEMM_ERR_ALIGNMENT).  temperature must be positive and finite, with a
+ * finite reciprocal, V >= 1, 0 <= top (GEMM_ERR_INVALID_ARG) <= 32 (GEMM_ERR_UNSUPPORTED).
+ * top == 0: top_logprobs and top_tokens are ignored.  rows == 0: nothing is done.
+ * The pages have no counterpart to it. */
+int token_logprobs(gemm_handle_t h, int64_t rows, int64_t V, const void* logits, int64_t ld, int dtype,
+                   const int64_t* tokens, float temperature, float* logprobs, float* entropy, float* stats,
+                   int64_t top, float* top_logprobs, int64_t* top_tokens, void* stream);
+
+/* The gradient of the logits for g = dlogprobs[r] and h = dentropy[r] (either may be NULL: zero):
+ *   dlogits[r][j] = (g (delta_jt - p_j) - h p_j (ln p_j + entropy[r])) / temperature
+ * with stats and entropy as token_logprobs left them (entropy is read where dentropy is given),
+ * and g taken as 0 where no token is given.  dlogits has the logits' type and is overwritten; it
+ * may be the logits themselves (the same address and leading dimension), not a part of them.
+ * Rows whose g and h are both 0 get zeros without being read, rows of -inf only get zeros, rows
+ * that hold NaN or +inf get NaN.  GEMM_F16: p g below 2^-25 is 0; scale the loss accordingly.
+ * Alignment, limits and errors as in token_logprobs.
+ * The pages have no counterpart to it. */
+int token_logprobs_backward(gemm_handle_t h, int64_t rows, int64_t V, const void* logits, int64_t ld, int dtype,
+                            const int64_t* tokens, float temperature, const float* stats, const float* entropy,
+                            const float* dlogprobs, const float* dentropy, void* dlogits, int64_t ldd, void* stream);
+
 /* Synchronise `stream`, then read and clear the handle's device status word (and, in the
  * debug library, the kernels' bounds-check flags).  This is
  * the wait of "Learning to develop for GPU with GEMM as the example", section "Writing a

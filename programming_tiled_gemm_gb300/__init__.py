@@ -39,7 +39,7 @@ EXPORTS = ["gemm_create", "gemm_destroy", "gemm_run", "gemm_run_ex", "gemm_run_h
            "gemm_get_device_status", "gemm_set_option", "gemm_launch_count", "gemm_status_string",
            "gemm_run_f32_skinny_noalloc",
            "gemm_linear", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
-           "moe_combine_backward"]
+           "moe_combine_backward", "token_logprobs", "token_logprobs_backward"]
 
 GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_SILU, GEMM_ACT_SWIGLU = 0, 1, 2, 3, 4, 5
 ACTIVATIONS = {"none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU, "gelu": GEMM_ACT_GELU, "gelu_tanh": GEMM_ACT_GELU_TANH,
@@ -83,6 +83,15 @@ class Routing(NamedTuple):
     offsets: object  # int32 [E + 1], the groups of grouped_linear
 
 
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs leaves: torch tensors, see include/gemm.h."""
+    logprobs: object      # fp32 [rows], of the given tokens; 0 where none is given
+    entropy: object       # fp32 [rows], or None
+    stats: object         # fp32 [rows, 2]: the largest logit m and ln sum exp((z - m) / temperature)
+    top_logprobs: object  # fp32 [rows, top], or None
+    top_tokens: object    # int64 [rows, top], -1: no more; or None
+
+
 class GemmError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -116,6 +125,8 @@ def _load():
     lib.moe_dispatch.argtypes = [p, i64, i64, i64, p, i64, i32, p, p, i64, p]
     lib.moe_combine.argtypes = [p, i64, i64, i64, p, i64, i64, i32, p, p, p, i64, p, i64, p]
     lib.moe_combine_backward.argtypes = [p, i64, i64, i64, p, i64, p, i64, i32, p, p, p, p, i64, p, p]
+    lib.token_logprobs.argtypes = [p, i64, i64, p, i64, i32, p, f32, p, p, p, i64, p, p, p]
+    lib.token_logprobs_backward.argtypes = [p, i64, i64, p, i64, i32, p, f32, p, p, p, p, p, i64, p]
     lib.gemm_status_string.argtypes = [i32]
     lib.gemm_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -218,6 +229,18 @@ def moe_combine_backward(h, T, N, k, dout, lddo, y, ldy, dtype, slots, rows, wei
                          stream=0) -> int:
     return _lib.moe_combine_backward(h, T, N, k, dout, lddo, y, ldy, dtype, slots, rows, weights, dy, lddy, dweights,
                                      stream)
+
+
+def token_logprobs(h, rows, V, logits, ld, dtype, tokens, temperature, logprobs, entropy, stats, top, top_logprobs,
+                   top_tokens, stream=0) -> int:
+    return _lib.token_logprobs(h, rows, V, logits, ld, dtype, tokens, temperature, logprobs, entropy, stats, top,
+                               top_logprobs, top_tokens, stream)
+
+
+def token_logprobs_backward(h, rows, V, logits, ld, dtype, tokens, temperature, stats, entropy, dlogprobs, dentropy,
+                            dlogits, ldd, stream=0) -> int:
+    return _lib.token_logprobs_backward(h, rows, V, logits, ld, dtype, tokens, temperature, stats, entropy, dlogprobs,
+                                        dentropy, dlogits, ldd, stream)
 
 
 def gemm_get_device_status(h, stream=0) -> int:
@@ -725,6 +748,64 @@ class Gemm:
             raise GemmError(rc, "moe_combine_backward")
         return dy, dweights
 
+    # ---- token log probabilities
+
+    def token_logprobs(self, logits, tokens, top=0, entropy=False, temperature=1.0, stream=None):
+        """Log probabilities of tokens (int64 [rows]; outside 0 .. V - 1, as -100: none is given) under
+        softmax(logits / temperature), with the entropy and the `top` (up to 32) most likely
+        tokens: a TokenLogprobs.  logits [rows, V], float32, bf16 or fp16; -inf marks a token that cannot come."""
+        import torch
+        if logits.dim() != 2:
+            raise ValueError("logits must be [rows, V]")
+        rows, V = logits.shape
+        top = int(top)
+        dcode = _dtype_code(logits)
+        ld = self._mat(logits, "logits", rows, V, logits.dtype)
+        if V < 1 or top < 0:
+            raise ValueError("logits need a column, and top must not be negative")
+        at_tokens = self._flat(tokens, "tokens", (rows,), torch.int64)
+        f32 = torch.float32
+        r = TokenLogprobs(self._new((rows,), f32, stream), self._new((rows,), f32, stream) if entropy else None,
+                          self._new((rows, 2), f32, stream), self._new((rows, top), f32, stream) if top else None,
+                          self._new((rows, top), torch.int64, stream) if top else None)
+        rc = _lib.token_logprobs(self.handle, rows, V, logits.data_ptr(), ld, dcode, at_tokens, temperature,
+                                 r.logprobs.data_ptr(), _ptr(r.entropy), r.stats.data_ptr(), top, _ptr(r.top_logprobs),
+                                 _ptr(r.top_tokens), self._stream(stream))
+        if rc != GEMM_OK:
+            raise GemmError(rc, "token_logprobs")
+        return r
+
+    def token_logprobs_backward(self, dlogprobs, logits, tokens, result, dentropy=None, temperature=1.0, out=None,
+                                stream=None):
+        """The gradient of the logits for the gradients dlogprobs and dentropy (float32 [rows], either may
+        be None) of what token_logprobs returned as `result`.  out may be logits itself."""
+        import torch
+        if logits.dim() != 2:
+            raise ValueError("logits must be [rows, V]")
+        rows, V = logits.shape
+        dt = logits.dtype
+        dcode = _dtype_code(logits)
+        ld = self._mat(logits, "logits", rows, V, dt)
+        f32 = torch.float32
+        if dentropy is not None and result.entropy is None:
+            raise ValueError("dentropy needs a result with the entropy")
+        at_tokens = self._flat(tokens, "tokens", (rows,), torch.int64)
+        at_stats = self._flat(result.stats, "result.stats", (rows, 2), f32)
+        at_g = self._flat(dlogprobs, "dlogprobs", (rows,), f32) if dlogprobs is not None else 0
+        at_h = at_entropy = 0
+        if dentropy is not None:
+            at_h = self._flat(dentropy, "dentropy", (rows,), f32)
+            at_entropy = self._flat(result.entropy, "result.entropy", (rows,), f32)
+        if out is None:
+            out, ldo = self._new((rows, V), dt, stream), V
+        else:
+            ldo = self._mat(out, "out", rows, V, dt)
+        rc = _lib.token_logprobs_backward(self.handle, rows, V, logits.data_ptr(), ld, dcode, at_tokens, temperature,
+                                          at_stats, at_entropy, at_g, at_h, out.data_ptr(), ldo, self._stream(stream))
+        if rc != GEMM_OK:
+            raise GemmError(rc, "token_logprobs_backward")
+        return out
+
     def launch_count(self) -> int:
         return gemm_launch_count(self.handle)
 
@@ -739,5 +820,6 @@ __all__ = ["Gemm", "GemmError", "HostProblem", "gemm_create", "gemm_destroy", "g
            "conv4d_im2col", "conv4d_forward", "conv4d_forward_cl", "conv4d_forward_tc", "gemm_get_device_status", "gemm_set_option", "gemm_launch_count",
            "gemm_status_string",
            "gemm_linear", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
-           "moe_combine_backward", "LinearArgs", "LinearGradArgs", "Routing", "ACTIVATIONS",
+           "moe_combine_backward", "token_logprobs", "token_logprobs_backward", "LinearArgs", "LinearGradArgs", "Routing",
+           "TokenLogprobs", "ACTIVATIONS",
            "status_string", "library", "LIB_PATH", "EXPORTS"]

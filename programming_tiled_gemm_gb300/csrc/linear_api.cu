@@ -2,6 +2,7 @@
 // workspaces and the order of the launches.
 #include <cstdio>
 
+#include "api_checks.h"
 #include "context.h"
 #include "linear.h"
 #include "moe.h"
@@ -9,26 +10,6 @@
 using namespace gemm_gb300;
 
 namespace {
-
-constexpr int64_t kLim32 = 0x7fffffffLL - 1024;  // the kernels index sizes in 32 bits
-
-bool is_16(int dtype) { return dtype == GEMM_BF16 || dtype == GEMM_F16; }
-int size_of(int dtype) { return dtype == GEMM_F32 ? 4 : 2; }
-bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-
-// A matrix of `rows` rows of `cols` used elements: null or a leading dimension below the
-// row's length is refused, unless there is nothing to access.
-bool bad_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld)
-{
-    if (rows == 0 || cols == 0) return false;
-    return !p || ld < cols || ld > kLim32;
-}
-
-// TMA and 16-byte vector operands: aligned base, row stride a multiple of 16 bytes.
-bool bad_rows16(const void* p, int64_t rows, int64_t cols, int64_t ld)
-{
-    return rows > 0 && cols > 0 && (misaligned(p, 16) || ld % 8 != 0);
-}
 
 // Grows the workspace to what the product needs, which *need tells run_product.
 int reserve_product(gemm_handle_t h, const LinArgs& a, cudaStream_t s, size_t* need)
@@ -204,8 +185,6 @@ int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* 
     return dw ? run_product(h, w, need_dw, s) : GEMM_OK;
 }
 
-bool known_dtype(int d) { return d == GEMM_F32 || is_16(d); }
-
 int check_routing(int64_t T, int64_t k)
 {
     if (T < 0 || k < 1) return GEMM_ERR_INVALID_ARG;
@@ -330,12 +309,6 @@ int combine_backward_impl(gemm_handle_t h, int64_t T, int64_t N, int64_t k, cons
     const int rc2 = launch_moe_combine_grad(a, dtype, s, &n);
     h->launches += n;
     return rc2;
-}
-
-int told(const char* what, int rc)
-{
-    if (rc != GEMM_OK) glog("%s refused: %s (%d)", what, gemm_status_string(rc), rc);
-    return rc;
 }
 
 }  // namespace
