@@ -1,19 +1,21 @@
 // Log probabilities of given tokens, the entropy and the best alternatives of rows of logits,
 // and the logits' gradient.
 //
-// With u_j = (z_j - m) / T, m the row's largest logit: S = sum exp(u_j), ln p_j = u_j - ln S,
-// H = ln S - sum exp(u_j) u_j / S.  One pass: every thread keeps its own m, S and Q = sum
-// exp(u) u (in units of ln 2, for ex2) and rescales them when m grows,
-//     S' = f S,  Q' = f (Q + d S),  d = (m - m') / T,  f = exp(d),
-// and the threads' triples are joined the same way.  u is taken as (z - m) times 1 / T, never as
-// z / T - m / T: that loses what the two share and overflows at the type's lowest value.  As a
-// factor of exp(u), u is clamped at -1e4, far below where exp is 0: 0 * -inf is 0 there.
+// With c = 1 / (T ln 2) and a reference R, the row's largest logit m times c as it rounds:
+// t_j = z_j c - R (one rounding, of a small number), S = sum 2^t_j, Q = sum 2^t_j t_j,
+//     ln p_j = (z_j - m) / T - ln S',   ln S' = ln S - ln 2 (m c - R),   H = ln S - ln 2 Q / S.
+// One pass: every thread keeps its own m, R, S and Q and rescales them when m grows,
+//     S' = f S,  Q' = f (Q + d S),  d = R - R',  f = 2^d,
+// and the threads' sums are joined the same way.  As a factor, t is clamped at -1e4, far below
+// where 2^t is 0: 0 * -inf is 0 there.  Where m c is beyond 1e29 ("far": a row of a type's lowest
+// value), z c would overflow; any logit but m itself is then further off than exp can tell, so
+// p is 1 / n at the n logits that equal m.
 //
-// Alternatives: a warp keeps the `top` best it has seen, one a lane, in order.  A logit is looked
-// at only if it beats the warp's last one and is no worse than a bound that all warps of the CTA
-// raise; a first bound is the top-th largest of the lanes' maxima of the first batch (at least
-// `top` logits are no worse), so some `top` insertions a warp remain.  A warp meets its logits in
-// the order of their index, so equal ones keep that order.
+// Alternatives: the threads' maxima are there already.  The `top` best logits of a CTA's part all
+// belong to threads whose maximum is among the `top` largest maxima, and none of them is below the
+// smallest of these.  So only those threads' logits are read again (20 of 256, from L2); the few
+// that are no worse than that bound wait in shared memory until a warp has 32, which it sorts and
+// merges with its best in 20 exchanges of 64-bit keys of logit and index.
 //
 // A cluster of up to 8 CTAs shares a row where there are few (their sums and lists go to the
 // first CTA's shared memory); rows are read with 16-byte loads from the first 16-byte boundary
@@ -64,6 +66,17 @@ struct LF32 {
         z[0] = __uint_as_float(v.x), z[1] = __uint_as_float(v.y);
         z[2] = __uint_as_float(v.z), z[3] = __uint_as_float(v.w);
     }
+    // the largest of FLY vectors (NaN left out)
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&v)[N])
+    {
+        float h = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            h = fmaxf(fmaxf(h, fmaxf(__uint_as_float(v[u].x), __uint_as_float(v[u].y))),
+                      fmaxf(__uint_as_float(v[u].z), __uint_as_float(v[u].w)));
+        return h;
+    }
     static __device__ __forceinline__ uint4 pack(const float (&z)[PER])
     {
         return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
@@ -83,6 +96,21 @@ struct LBF16 {
             z[2 * i] = __uint_as_float(w[i] << 16);
             z[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&v)[N])
+    {
+        using P = __nv_bfloat162;
+        const uint32_t low = LOW;
+        P h = *reinterpret_cast<const P*>(&low);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h = __hmax2(h, *reinterpret_cast<const P*>(&w[i]));
+        }
+        const float lo = __low2float(h), hi = __high2float(h);
+        return fmaxf(lo, hi);
     }
     static __device__ __forceinline__ uint4 pack(const float (&z)[PER])
     {
@@ -110,6 +138,21 @@ struct LF16 {
             z[2 * i] = f.x, z[2 * i + 1] = f.y;
         }
     }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&v)[N])
+    {
+        using P = __half2;
+        const uint32_t low = LOW;
+        P h = *reinterpret_cast<const P*>(&low);
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h = __hmax2(h, *reinterpret_cast<const P*>(&w[i]));
+        }
+        const float lo = __low2float(h), hi = __high2float(h);
+        return fmaxf(lo, hi);
+    }
     static __device__ __forceinline__ uint4 pack(const float (&z)[PER])
     {
         uint32_t w[4];
@@ -130,23 +173,28 @@ __device__ __forceinline__ int head_of(const typename D::T* row, int V)
     return min(V, off ? D::PER - off : 0);
 }
 
-struct Triple {
-    float m, s, q;  // largest logit, sum exp(u), sum exp(u) u / ln 2, with u = (z - m) / T
+// The reference of a largest logit; sums without a logit have the least, -1e38, which is far from all.
+__device__ __forceinline__ float reference(float m, float c) { return fminf(fmaxf(m * c, -1e38f), 1e38f); }
+// Whether m c is out of the exponents' range.
+__device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m) < INFINITY && fabsf(m) * c >= 1e29f; }
+
+struct Sums {
+    float m, s, q;  // largest logit, sum 2^t, sum 2^t t with t = z c - reference(m)
 };
 
 // Everything relative to the larger m.
 template <bool ENT>
-__device__ __forceinline__ Triple rescale(const Triple& a, float m, float c)
+__device__ __forceinline__ Sums rescale(const Sums& a, float m, float c)
 {
-    if (a.m == m || a.m == -INFINITY) return {m, a.s, a.q};  // (without logits there is nothing to scale)
-    const float d = fmaxf((a.m - m) * c, FLOOR), f = ex2(d);
+    if (a.m == m) return a;
+    const float d = fmaxf(reference(a.m, c) - reference(m, c), FLOOR), f = ex2(d);
     return {m, a.s * f, ENT ? f * (a.q + d * a.s) : 0.f};
 }
 template <bool ENT>
-__device__ __forceinline__ Triple join(const Triple& a, const Triple& b, float c)
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c)
 {
     const float m = fmaxf(a.m, b.m);
-    const Triple x = rescale<ENT>(a, m, c), y = rescale<ENT>(b, m, c);
+    const Sums x = rescale<ENT>(a, m, c), y = rescale<ENT>(b, m, c);
     return {m, x.s + y.s, x.q + y.q};
 }
 
@@ -154,15 +202,43 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t at, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
-__device__ __forceinline__ void st_cluster_u32(uint32_t at, uint32_t v)
+__device__ __forceinline__ void st_cluster_u64(uint32_t at, uint64_t v)
 {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+
+// A logit and its index as one number: larger ones first, equal ones by the lower index; 0: none.
+// One key a lane, sorted over the warp, largest first (bitonic: every compare-exchange is of lanes
+// 2^b apart).
+__device__ __forceinline__ uint64_t exchange(uint64_t k, int d, bool larger)
+{
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, k, d);
+    return (k > o) == larger ? k : o;
+}
+__device__ __forceinline__ uint64_t sort_keys(uint64_t k)
+{
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int n = 2; n <= 32; n *= 2)
+#pragma unroll
+        for (int d = n / 2; d > 0; d /= 2) k = exchange(k, d, ((lane & d) == 0) == ((lane & n) == 0 || n == 32));
+    return k;
+}
+// The 32 largest of two sorted warps of keys, sorted.
+__device__ __forceinline__ uint64_t merge_best(uint64_t a, uint64_t b)
+{
+    const int lane = threadIdx.x % 32;
+    const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
+    uint64_t k = a > r ? a : r;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) k = exchange(k, d, (lane & d) == 0);
+    return k;
 }
 
 struct LogprobsParams {
     const void* logits;
     int64_t ld;
-    int V, top, cluster;
+    int V, top, cluster, threads;
     const int64_t* tokens;
     float inv_t, c;  // 1 / T and 1 / (T ln 2)
     float* logprobs;
@@ -178,13 +254,17 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     constexpr int PER = D::PER;
     constexpr int LISTS = MAX_CLUSTER * WARPS;
     __shared__ float part_m[LISTS], part_s[LISTS], part_q[LISTS];
-    __shared__ float list_v[TOP ? LISTS : 1][TOP ? kMaxTop : 1];
-    __shared__ uint32_t list_i[TOP ? LISTS : 1][TOP ? kMaxTop : 1];
-    __shared__ uint32_t bound;  // a key: `top` logits of the row are no worse
+    __shared__ uint64_t lists_best[TOP ? LISTS : 1][TOP ? kMaxTop : 1];
+    __shared__ uint64_t waiting[TOP ? WARPS : 1][TOP ? 64 : 1];
+    __shared__ __align__(16) float high_of[TOP ? THREADS : 4];  // each thread's largest logit
+    __shared__ uint16_t chosen[TOP ? THREADS : 1];              // threads with the largest of them
+    __shared__ int chosen_n;
+    __shared__ uint32_t bound;  // the key of the smallest of these: `top` logits are no worse
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int C = p.cluster, rank = blockIdx.x % C;
     const int64_t r = blockIdx.x / C;
-    if (TOP && threadIdx.x == 0) bound = 0;
+    const int nthreads = blockDim.x, warps = nthreads / 32;
+    if (TOP && threadIdx.x == 0) bound = 0xffffffffu, chosen_n = 0;
     if (C > 1) cluster_sync_all();  // (the first CTA's shared memory is written by the others)
     else if (TOP) __syncthreads();
     grid_dependency_wait();
@@ -204,58 +284,15 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     const int v0 = (int)((int64_t)vecs * rank / C), v1 = (int)((int64_t)vecs * (rank + 1) / C);
     const uint4* body = reinterpret_cast<const uint4*>(row + head);
 
-    Triple a = {-INFINITY, 0.f, 0.f};
-    // the warp's best: lane i the i-th
-    float best = -INFINITY;
-    int best_i = -1;
-    float last = -INFINITY;  // the top-th, in every lane
-    float floor_v = -INFINITY;
-    const auto insert = [&](float v, int i) {
-        const int at = __popc(__ballot_sync(0xffffffffu, best >= v));  // (equal ones came earlier: lower indices)
-        const float up = __shfl_up_sync(0xffffffffu, best, 1);
-        const int up_i = __shfl_up_sync(0xffffffffu, best_i, 1);
-        if (lane > at) best = up, best_i = up_i;
-        if (lane == at) best = v, best_i = i;
-        last = __shfl_sync(0xffffffffu, best, p.top - 1);
-    };
-    // N logits of each lane, in the order of the lanes
-    const auto offer = [&](const auto& z, int first, int n) {
-        constexpr int N = sizeof(z) / sizeof(float);
-        for (;;) {
-            unsigned mask = 0;
-#pragma unroll
-            for (int j = 0; j < N; ++j) mask |= (j < n && z[j] > last && z[j] >= floor_v) ? 1u << j : 0u;
-            const unsigned who = __ballot_sync(0xffffffffu, mask != 0);
-            if (who == 0) break;
-            const int src = __ffs(who) - 1;
-            // that lane's candidates in order; each is taken off before the next look
-            unsigned left = __shfl_sync(0xffffffffu, mask, src);
-            while (left) {
-                const int j = __ffs(left) - 1;
-                left &= left - 1;
-                float v = z[0];
-#pragma unroll
-                for (int k = 1; k < N; ++k)
-                    if (k == j) v = z[k];
-                v = __shfl_sync(0xffffffffu, v, src);
-                if (v > last) insert(v, __shfl_sync(0xffffffffu, first, src) + j);
-            }
-            if (lane <= src) n = 0;  // those before it had none
-        }
-    };
-    const auto add = [&](float z, float m) {
-        const float t = (z - m) * c, e = ex2(t);  // (NaN where z is NaN or +inf)
-        a.s += e;
-        if (ENT) a.q += e * fmaxf(t, FLOOR);
-    };
+    Sums a = {-INFINITY, 0.f, 0.f};
     // a few elements outside the 16-byte vectors
     const auto edge = [&](int first, int n) {
-        float z[1] = {(int)threadIdx.x < n ? D::get(row[first + threadIdx.x]) : -INFINITY};
-        if ((int)threadIdx.x < n) {
-            if (z[0] > a.m) a = rescale<ENT>(a, z[0], c);
-            add(z[0], a.m == -INFINITY ? 0.f : a.m);
-        }
-        if (TOP && warp == 0) offer(z, first + (int)threadIdx.x, (int)threadIdx.x < n);
+        if ((int)threadIdx.x >= n) return;
+        const float z = D::get(row[first + threadIdx.x]);
+        if (z > a.m) a = rescale<ENT>(a, z, c);
+        const float t = __fmaf_rn(z, c, -reference(a.m, c)), e = ex2(t);
+        a.s += e;
+        if (ENT) a.q += e * fmaxf(t, FLOOR);
     };
     if (rank == 0 && head > 0) edge(0, head);
 
@@ -263,143 +300,209 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     const auto fetch = [&](int v) {
 #pragma unroll
         for (int u = 0; u < FLY; ++u) {
-            const int i = v + u * THREADS;
+            const int i = v + u * nthreads;
             next[u] = i < v1 ? __ldcs(body + i) : make_uint4(D::LOW, D::LOW, D::LOW, D::LOW);
         }
     };
-    bool begun = false;
     int v = v0 + (int)threadIdx.x;
     fetch(v);
-    for (int b = v0; b < v1; b += FLY * THREADS, v += FLY * THREADS) {
+    for (int b = v0; b < v1; b += FLY * nthreads, v += FLY * nthreads) {
         uint4 cur[FLY];
 #pragma unroll
         for (int u = 0; u < FLY; ++u) cur[u] = next[u];
-        if (b + FLY * THREADS < v1) fetch(v + FLY * THREADS);
-        float high = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < FLY; ++u) {
-            float z[PER];
-            D::unpack(cur[u], z);
-#pragma unroll
-            for (int j = 0; j < PER; ++j) high = fmaxf(high, z[j]);
-        }
+        if (b + FLY * nthreads < v1) fetch(v + FLY * nthreads);
+        const float high = D::largest(cur);
         if (high > a.m) a = rescale<ENT>(a, high, c);
-        const float m = a.m == -INFINITY ? 0.f : a.m;
+        const float ref = -reference(a.m, c);
+        const float2 ref2 = make_float2(ref, ref), c2 = make_float2(c, c);
+        float2 s2 = make_float2(0.f, 0.f), q2 = s2;
 #pragma unroll
         for (int u = 0; u < FLY; ++u) {
             float z[PER];
             D::unpack(cur[u], z);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) add(z[j], m);
-        }
-        if (TOP) {
-            if (!begun) {
-                // the top-th largest of the lanes' maxima
-                begun = true;
-                int better = 0;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float o = __shfl_sync(0xffffffffu, high, i);
-                    better += o > high || (o == high && i < lane);
+            for (int j = 0; j < PER; j += 2) {
+                float2 t = __ffma2_rn(make_float2(z[j], z[j + 1]), c2, ref2);
+                const float2 e = make_float2(ex2(t.x), ex2(t.y));  // (NaN or inf where z is NaN or +inf)
+                s2 = __fadd2_rn(s2, e);
+                if (ENT) {
+                    t.x = fmaxf(t.x, FLOOR), t.y = fmaxf(t.y, FLOOR);
+                    q2 = __ffma2_rn(e, t, q2);
                 }
-                const float kth = __shfl_sync(0xffffffffu, high,
-                                              __ffs(__ballot_sync(0xffffffffu, better == p.top - 1)) - 1);
-                if (lane == 0) atomicMax(&bound, order_key(kth));
-                floor_v = kth;
-            }
-            floor_v = fmaxf(floor_v, key_value(*(volatile uint32_t*)&bound));
-            if (__any_sync(0xffffffffu, high > last && high >= floor_v)) {
-#pragma unroll
-                for (int u = 0; u < FLY; ++u) {
-                    float z[PER];
-                    D::unpack(cur[u], z);
-                    offer(z, head + (v + u * THREADS) * PER, v + u * THREADS < v1 ? PER : 0);
-                }
-                if (lane == 0 && last > -INFINITY) atomicMax(&bound, order_key(last));
             }
         }
+        a.s += s2.x + s2.y;
+        if (ENT) a.q += q2.x + q2.y;
     }
     if (rank == C - 1 && tail0 < p.V) edge(tail0, p.V - tail0);
+    uint64_t best = 0;  // lane i: the warp's i-th best
+    if constexpr (TOP) {
+        // the threads with the `top` largest maxima (more where they tie): all of the best are theirs
+        high_of[threadIdx.x] = a.m;
+        __syncthreads();
+        int better = 0;
+#pragma unroll 8
+        for (int i = 0; i < nthreads; i += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(&high_of[i]);
+            better += (o.x > a.m) + (o.y > a.m) + (o.z > a.m) + (o.w > a.m);
+        }
+        const bool is = better < p.top && a.m > -INFINITY;
+        const unsigned who = __ballot_sync(0xffffffffu, is);
+        int first = 0;
+        if (lane == 0 && who) first = atomicAdd(&chosen_n, __popc(who));
+        first = __shfl_sync(0xffffffffu, first, 0);
+        if (is) {
+            chosen[first + __popc(who & ((1u << lane) - 1))] = (uint16_t)threadIdx.x;
+            // (the smallest of them: the bound)
+            atomicMin(&bound, order_key(a.m));
+        }
+        __syncthreads();
+        const int n = chosen_n, each = (v1 - v0 + nthreads - 1) / nthreads;  // vectors of a thread
+        const float floor_v = n >= p.top ? key_value(bound) : -INFINITY;  // (fewer: everything they have)
+        uint64_t* const wait = waiting[warp];
+        int pending = 0;
+        float last = -INFINITY;  // the warp's top-th: its value and its index
+        int last_i = -1;
+        const auto flush = [&] {
+            __syncwarp();
+            best = merge_best(best, sort_keys(lane < pending ? wait[lane] : 0ull));
+            __syncwarp();
+            if (lane + 32 < pending) wait[lane] = wait[lane + 32];
+            pending = max(pending - 32, 0);
+            const uint64_t k = __shfl_sync(0xffffffffu, best, p.top - 1);
+            last = key_value((uint32_t)(k >> 32));
+            last_i = (int)~(uint32_t)k;
+        };
+        // a logit of each lane (-inf: none)
+        const auto offer = [&](float v, int i) {
+            const bool in = v >= floor_v && (v > last || (v == last && i < last_i));
+            const unsigned w = __ballot_sync(0xffffffffu, in);
+            if (w == 0) return;
+            if (in) wait[pending + __popc(w & ((1u << lane) - 1))] = (uint64_t)order_key(v) << 32 | (uint32_t)~i;
+            pending += __popc(w);
+            if (pending >= 32) flush();
+        };
+        // their vectors once more, from L2, AHEAD vectors of a thread in flight
+        constexpr int AHEAD = 4;
+        const unsigned items = (unsigned)n * each;
+        for (unsigned it0 = 0; it0 < items; it0 += AHEAD * nthreads) {
+            uint4 w[AHEAD];
+            int at[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const unsigned it = it0 + u * nthreads + threadIdx.x, vec = it / (unsigned)n;
+                at[u] = it < items ? v0 + (int)vec * nthreads + chosen[it - vec * n] : v1;
+                w[u] = at[u] < v1 ? body[at[u]] : make_uint4(D::LOW, D::LOW, D::LOW, D::LOW);
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                float z[PER];
+                D::unpack(w[u], z);
+                unsigned mask = 0;
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    mask |= z[j] >= floor_v && (z[j] > last || (z[j] == last && head + at[u] * PER + j < last_i)) ? 1u << j : 0u;
+                // one of each lane's at a time
+#pragma unroll 1
+                while (__any_sync(0xffffffffu, mask != 0)) {
+                    const int j = __ffs(mask) - 1;
+                    float x = mask ? z[0] : -INFINITY;
+#pragma unroll
+                    for (int k = 1; k < PER; ++k) x = k == j ? z[k] : x;
+                    offer(x, head + at[u] * PER + j);
+                    mask &= mask - 1;
+                }
+            }
+        }
+        // and what lies outside the vectors
+        if (warp == 0) {
+            const int i = lane < 16 ? lane : tail0 + lane - 16;
+            const bool in = lane < 16 ? rank == 0 && lane < head : rank == C - 1 && i < p.V;
+            offer(in ? D::get(row[i]) : -INFINITY, i);
+        }
+        if (pending > 0) flush();
+    }
 
     // the warps' sums and lists, at the first CTA
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) {
-        const Triple o = {__shfl_xor_sync(0xffffffffu, a.m, d), __shfl_xor_sync(0xffffffffu, a.s, d),
+        const Sums o = {__shfl_xor_sync(0xffffffffu, a.m, d), __shfl_xor_sync(0xffffffffu, a.s, d),
                           __shfl_xor_sync(0xffffffffu, a.q, d)};
         // (in the same order on both sides)
         a = (lane & d) ? join<ENT>(o, a, c) : join<ENT>(a, o, c);
     }
-    const int list = rank * WARPS + warp;
-    const auto at0 = [&](const void* q) { return C > 1 ? mapa_shared(smem_u32(q), 0) : smem_u32(q); };
+    const int list = rank * warps + warp;
+    const auto at_first = [&](const void* q) { return C > 1 ? mapa_shared(smem_u32(q), 0) : smem_u32(q); };
     if (C > 1) {
         if (lane == 0) {
-            st_cluster_f32(at0(&part_m[list]), a.m);
-            st_cluster_f32(at0(&part_s[list]), a.s);
-            if (ENT) st_cluster_f32(at0(&part_q[list]), a.q);
+            st_cluster_f32(at_first(&part_m[list]), a.m);
+            st_cluster_f32(at_first(&part_s[list]), a.s);
+            if (ENT) st_cluster_f32(at_first(&part_q[list]), a.q);
         }
-        if (TOP && lane < p.top) {
-            st_cluster_f32(at0(&list_v[list][lane]), best);
-            st_cluster_u32(at0(&list_i[list][lane]), (uint32_t)best_i);
-        }
+        if (TOP && lane < p.top) st_cluster_u64(at_first(&lists_best[list][lane]), best);
         cluster_sync_all();
     } else {
         if (lane == 0) {
             part_m[list] = a.m, part_s[list] = a.s;
             if (ENT) part_q[list] = a.q;
         }
-        if (TOP && lane < p.top) list_v[list][lane] = best, list_i[list][lane] = (uint32_t)best_i;
+        if (TOP && lane < p.top) lists_best[list][lane] = best;
         __syncthreads();
     }
     if (rank != 0 || warp != 0) return;
-    const int lists = C * WARPS;
-    Triple t = {-INFINITY, 0.f, 0.f};
+    const int lists = C * warps;
+    Sums t = {-INFINITY, 0.f, 0.f};
     for (int i = lane; i < lists; i += 32) {
-        const Triple o = {part_m[i], part_s[i], ENT ? part_q[i] : 0.f};
+        const Sums o = {part_m[i], part_s[i], ENT ? part_q[i] : 0.f};
         t = join<ENT>(t, o, c);
     }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) {
-        const Triple o = {__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d),
+        const Sums o = {__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d),
                           __shfl_xor_sync(0xffffffffu, t.q, d)};
         t = (lane & d) ? join<ENT>(o, t, c) : join<ENT>(t, o, c);
     }
+    float ln_r = logf(t.s), ln_s = ln_r - LN2 * __fmaf_rn(t.m, c, -reference(t.m, c));  // relative to R and to m
+    if (is_far(t.m, c)) {
+        int n = 0;
+        bool nan = false;
+        for (int i = lane; i < p.V; i += 32) {
+            const float z = D::get(row[i]);
+            n += z == t.m;
+            nan |= z != z;
+        }
+        ln_r = ln_s = __any_sync(0xffffffffu, nan) ? NAN : logf((float)__reduce_add_sync(0xffffffffu, n));
+        t.s = 1.f, t.q = 0.f;
+    }
+    if (t.m == INFINITY) ln_r = ln_s = NAN;
     const bool none = t.m == -INFINITY && t.s == 0.f;  // (a row of NaN has NaN sums)
-    const float ln_s = none ? 0.f : logf(t.s);
+    if (none) ln_s = 0.f;
     if (lane == 0) {
         p.stats[2 * r] = t.m;
         p.stats[2 * r + 1] = ln_s;
         float lp = 0.f;
         if (have) lp = none ? -INFINITY : (given - t.m) * p.inv_t - ln_s;
         p.logprobs[r] = lp;
-        if (ENT) p.entropy[r] = none ? 0.f : ln_s - LN2 * (t.q / t.s);
+        if (ENT) p.entropy[r] = none ? 0.f : ln_r - LN2 * (t.q / t.s);
     }
     if constexpr (TOP) {
         // the best head of all lists, `top` times: a lane holds the heads of two lists
         const bool bad = ln_s != ln_s;
-        uint32_t key[2], idx[2];
-        int at[2] = {0, 0};
-        const auto head_key = [&](int h) {
-            const int l = lane + 32 * h;
-            const bool in = l < lists && at[h] < p.top;
-            key[h] = in ? order_key(list_v[l][at[h]]) : 0u;
-            idx[h] = in ? list_i[l][at[h]] : 0xffffffffu;
-        };
-        head_key(0);
-        head_key(1);
-        float val = -INFINITY;
-        int64_t tok = -1;
+        int at0 = 0, at1 = 0;
+        const auto head_key = [&](int l, int at) { return l < lists && at < p.top ? lists_best[l][at] : 0ull; };
+        uint64_t key0 = head_key(lane, 0), key1 = head_key(lane + 32, 0), mine = 0;
         for (int j = 0; j < p.top && !bad; ++j) {
-            const int h = key[1] > key[0] || (key[1] == key[0] && idx[1] < idx[0]);
-            const uint32_t k = h ? key[1] : key[0], i = h ? idx[1] : idx[0];
-            const uint32_t m = __reduce_max_sync(0xffffffffu, k);
+            const uint64_t k = key1 > key0 ? key1 : key0;
+            const uint32_t m = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
             if (m == 0) break;
-            const uint32_t w = __reduce_min_sync(0xffffffffu, k == m ? i : 0xffffffffu);
-            if (k == m && i == w) {
-                ++at[h];
-                head_key(h);
-            }
-            if (lane == j) val = key_value(m), tok = (int64_t)w;
+            const uint32_t i = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == m ? (uint32_t)k : 0u);
+            const uint64_t w = (uint64_t)m << 32 | i;
+            if (key0 == w) key0 = head_key(lane, ++at0);
+            else if (key1 == w) key1 = head_key(lane + 32, ++at1);
+            if (lane == j) mine = w;
         }
+        const float val = key_value((uint32_t)(mine >> 32));
+        const int64_t tok = mine ? (int64_t)(uint32_t)~(uint32_t)mine : -1;
         if (lane < p.top) {
             p.top_logprobs[r * p.top + lane] = bad ? ln_s : tok < 0 ? -INFINITY : (val - t.m) * p.inv_t - ln_s;
             p.top_tokens[r * p.top + lane] = tok;
@@ -414,7 +517,7 @@ struct LogprobsGradParams {
     int64_t ld;
     int V, blocks;  // blocks of a row
     const int64_t* tokens;
-    float inv_t;
+    float inv_t, c;
     const float* stats;
     const float* entropy;
     const float* dlogprobs;
@@ -425,7 +528,8 @@ struct LogprobsGradParams {
 
 constexpr int GRAD_FLY = 4;
 
-// dz_j = (g (delta_jt - p_j) - h p_j (ln p_j + H)) / T = p_j (A + B ln p_j) + delta_jt g / T
+// dz_j = (g (delta_jt - p_j) - h p_j (ln p_j + H)) / T = p_j (A + B log2 p_j) + delta_jt g / T,
+// log2 p_j = (z_j c - R) - L, L = ln S' / ln 2 + (m c - R)
 template <typename D, bool ENT>
 __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradParams p)
 {
@@ -438,51 +542,69 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradPara
     const T* row = static_cast<const T*>(p.logits) + r * p.ld;
     T* out = static_cast<T*>(p.dlogits) + r * p.ldd;
     const int64_t tok = p.tokens[r];
-    const float m = p.stats[2 * r], ln_s = p.stats[2 * r + 1];
+    const float m = p.stats[2 * r], ln_s = p.stats[2 * r + 1], c = p.c;
     const bool have = tok >= 0 && tok < p.V;
     const float g = have && p.dlogprobs ? p.dlogprobs[r] : 0.f, h = ENT ? p.dentropy[r] : 0.f;
     const bool zero = (g == 0.f && h == 0.f) || (m == -INFINITY && ln_s == ln_s);
-    const float B = -h * p.inv_t, A = ENT ? -(g + h * p.entropy[r]) * p.inv_t : -g * p.inv_t;
+    const float B = -h * p.inv_t * LN2, A = ENT ? -(g + h * p.entropy[r]) * p.inv_t : -g * p.inv_t;
     const float gt = g * p.inv_t;
     const int t = have ? (int)tok : -1;
+    const float ref = reference(m, c), log_s = ln_s * LOG2E + __fmaf_rn(m, c, -ref);
+    const bool far = is_far(m, c);
     const auto grad = [&](float z, int j) {
         if (zero) return 0.f;
-        const float l = fmaxf((z - m) * p.inv_t - ln_s, FLOOR);
-        // (16-bit results: l * log2 e rounds by 2^-24 |l|, far below theirs)
-        const float e = PER == 4 ? expf(l) : ex2(l * LOG2E);
-        const float v = ENT ? e * (A + B * l) : e * A;
+        if (ln_s != ln_s) return ln_s;  // a row with NaN
+        float l = __fmaf_rn(z, c, -ref) - log_s;
+        if (far) l = z == m ? -ln_s * LOG2E : -INFINITY;
+        const float e = ex2(l);
+        const float v = ENT ? e * (A + B * fmaxf(l, FLOOR)) : e * A;
         return j == t ? v + gt : v;
     };
     const int head = head_of<D>(row, p.V), vecs = (p.V - head) / PER;
     const bool aligned = ((reinterpret_cast<uintptr_t>(out + head)) & 15) == 0;
-    const int n = (p.V + p.blocks - 1) / p.blocks;  // (unaligned: elements of this block)
-    const bool bad = ln_s != ln_s;                   // a row with NaN: all of it
-    if (!aligned || bad) {
-        const int j1 = min(p.V, (part + 1) * n);
+    if (!aligned || far || ln_s != ln_s) {
+        const int n = (p.V + p.blocks - 1) / p.blocks, j1 = min(p.V, (part + 1) * n);
         for (int j = part * n + (int)threadIdx.x; j < j1; j += THREADS)
-            out[j] = D::put(bad && !zero ? ln_s : grad(zero ? 0.f : D::get(row[j]), j));
+            out[j] = D::put(grad(zero ? 0.f : D::get(row[j]), j));
         return;
     }
     const int v0 = (int)((int64_t)vecs * part / p.blocks), v1 = (int)((int64_t)vecs * (part + 1) / p.blocks);
     const uint4* src = reinterpret_cast<const uint4*>(row + head);
     uint4* dst = reinterpret_cast<uint4*>(out + head);
-    for (int v = v0 + (int)threadIdx.x; v < v1; v += GRAD_FLY * THREADS) {
-        uint4 in[GRAD_FLY];
-        if (!zero) {
+    if (zero) {
+        for (int v = v0 + (int)threadIdx.x; v < v1; v += THREADS) __stcs(dst + v, make_uint4(0, 0, 0, 0));
+    } else {
+        const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref), log2 = make_float2(-log_s, -log_s);
+        const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
+        for (int v = v0 + (int)threadIdx.x; v < v1; v += GRAD_FLY * THREADS) {
+            uint4 in[GRAD_FLY];
 #pragma unroll
             for (int u = 0; u < GRAD_FLY; ++u)
                 if (v + u * THREADS < v1) in[u] = __ldcs(src + v + u * THREADS);
-        }
 #pragma unroll
-        for (int u = 0; u < GRAD_FLY; ++u) {
-            if (v + u * THREADS >= v1) break;
-            float z[PER];
-            if (zero) in[u] = make_uint4(0, 0, 0, 0);
-            D::unpack(in[u], z);
-            const int j0 = head + (v + u * THREADS) * PER;
+            for (int u = 0; u < GRAD_FLY; ++u) {
+                if (v + u * THREADS >= v1) break;
+                float z[PER];
+                D::unpack(in[u], z);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) z[j] = grad(z[j], j0 + j);
-            __stcs(dst + v + u * THREADS, D::pack(z));
+                for (int j = 0; j < PER; j += 2) {
+                    float2 l = __fadd2_rn(__ffma2_rn(make_float2(z[j], z[j + 1]), c2, ref2), log2);
+                    const float2 e = make_float2(ex2(l.x), ex2(l.y));
+                    float2 w = A2;
+                    if (ENT) {
+                        l.x = fmaxf(l.x, FLOOR), l.y = fmaxf(l.y, FLOOR);
+                        w = __ffma2_rn(B2, l, A2);
+                    }
+                    const float2 d = __fmul2_rn(e, w);
+                    z[j] = d.x, z[j + 1] = d.y;
+                }
+                const unsigned at = (unsigned)(t - (head + (v + u * THREADS) * PER));
+                if (at < (unsigned)PER)
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        if (j == (int)at) z[j] += gt;
+                __stcs(dst + v + u * THREADS, D::pack(z));
+            }
         }
     }
     if (part == 0 && (int)threadIdx.x < head)
@@ -496,7 +618,7 @@ cudaError_t launch_rows(const LogprobsParams& p, int64_t rows, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * p.cluster), 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.blockDim = dim3(p.threads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -537,11 +659,17 @@ int launch_logprobs(const LogprobsArgs& a, int num_sms, cudaStream_t s, int* lau
     p.c = (float)(1.4426950408889634 / a.temperature);
     p.logprobs = a.logprobs, p.entropy = a.entropy, p.stats = a.stats;
     p.top_logprobs = a.top_logprobs, p.top_tokens = a.top_tokens;
-    // CTAs a row: as many as are resident at once (six an SM) and have a batch to read
-    const int batch = FLY * THREADS * 16 / (a.dtype == GEMM_F32 ? 4 : 2);
+    const int batch = FLY * THREADS / 2 * 16 / (a.dtype == GEMM_F32 ? 4 : 2);
+    // CTAs a row: as many as are resident at once (nine an SM, by their registers) and have two batches
+    // to read
     p.cluster = 1;
-    while (p.cluster < MAX_CLUSTER && a.rows * 2 * p.cluster <= 6 * (int64_t)num_sms && a.V > p.cluster * batch / 2)
+    while (p.cluster < MAX_CLUSTER && a.rows * 2 * p.cluster <= 9 * (int64_t)num_sms && a.V > p.cluster * batch)
         p.cluster *= 2;
+    // Four warps a CTA: more of them are resident and less of the last wave is idle.  Eight where long rows
+    // do not fill the SMs and the loads in flight count.  us with four and eight warps (bf16, entropy):
+    //   4000 x 12000 29 48, 2000 x 50257 43 52, 4096 x 131072 159 166; 1000 x 131072 55 47
+    const int few = THREADS / 2;
+    p.threads = a.rows * p.cluster < 8 * (int64_t)num_sms && a.V / p.cluster > 1 << 16 ? THREADS : few;
     const cudaError_t e = a.dtype == GEMM_F32    ? launch_typed<LF32>(p, a.rows, s)
                           : a.dtype == GEMM_BF16 ? launch_typed<LBF16>(p, a.rows, s)
                                                  : launch_typed<LF16>(p, a.rows, s);
@@ -560,6 +688,7 @@ int launch_logprobs_grad(const LogprobsGradArgs& a, cudaStream_t s, int* launche
     p.blocks = (a.V + batch - 1) / batch;
     p.tokens = a.tokens;
     p.inv_t = 1.f / a.temperature;
+    p.c = (float)(1.4426950408889634 / a.temperature);
     p.stats = a.stats, p.entropy = a.entropy;
     p.dlogprobs = a.dlogprobs, p.dentropy = a.dentropy;
     p.dlogits = a.dlogits, p.ldd = a.ldd;

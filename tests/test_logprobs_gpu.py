@@ -108,6 +108,8 @@ def check_backward(logits, tokens, temperature, gain, dh, got):
     want = (gd[:, None] * (delta - p) - hd[:, None] * p * (lp + h[:, None])) / temperature
     size = (gd.abs()[:, None] * (delta + p) + hd.abs()[:, None] * p * (lp.abs() + h[:, None])) / temperature
     fp32 = (slack(V, eu)[:, None] + 4 * U * lp.abs() + 8 * U) * size + 1e-38
+    # ex2's results below 2^-126, the least normal number, are 0: up to that of p is lost
+    fp32 += 2.0 ** -126 * ((gd.abs()[:, None] + hd.abs()[:, None] * (lp.abs() + h[:, None])) / temperature)
     # the entropy itself is off by its own tolerance, which p multiplies
     fp32 += hd.abs()[:, None] * p * (slack(V, eu) * (1 + h + eu))[:, None] / temperature
     dt = got.dtype
