@@ -409,6 +409,47 @@ int moe_combine_backward(gemm_handle_t h, int64_t T, int64_t N, int64_t k, const
                          const void* y, int64_t ldy, int dtype, const int32_t* slots, const int32_t* rows,
                          const float* weights, void* dy, int64_t lddy, float* dweights, void* stream);
 
+/* The arguments of moe_layer. */
+typedef struct moe_layer_args {
+    int64_t T, E, k, D, F;
+    const void* logits;
+    int64_t ldl;
+    const void* X;
+    int64_t ldx;
+    const void* W1;
+    int64_t ldw1;
+    int64_t w1_stride;
+    const void* b1;
+    const void* W2;
+    int64_t ldw2;
+    int64_t w2_stride;
+    const void* b2;
+    const void* R;
+    int64_t ldr;
+    void* Y;
+    int64_t ldy;
+    int dtype, logits_dtype, y_dtype, act, renormalize;
+} moe_layer_args;
+
+/* A whole layer for a few tokens, T <= 64, in two kernels: the picks and their weights are those
+ * of moe_route, and
+ *   Y[t] = sum over j of weights[t][j] * (act(X[t] W1[e] + b1[e]) W2[e] + b2[e]) + R[t],  e = e_j,
+ * what moe_route, moe_dispatch, two grouped calls of gemm_linear and moe_combine give.
+ *   logits [T][E] of type logits_dtype (any); X [T][D], W1 [E][D][Fw] (matrix e at e * w1_stride
+ *   elements; Fw = F columns, 2 F for GEMM_ACT_SWIGLU, gate then up), b1 [E][Fw], W2 [E][F][D], b2
+ *   [E][D] of type dtype, GEMM_BF16 or GEMM_F16; R and Y [T][D] of type y_dtype, dtype or GEMM_F32.
+ *   b1, b2 and R may be NULL; R may be Y itself.  A token without picks is R (or 0).
+ * The activation's results are rounded to dtype once, as the second product's operand (GEMM_F16: beyond
+ * 65504 infinite); the picks' products and their sum, in the order of j, are held in fp32 and rounded
+ * once.  Only the picked experts' weights are read.  Deterministic.
+ * X, W1 and W2 must be 16-byte aligned with leading dimensions (and strides) multiples of 8, F a
+ * multiple of 8 for GEMM_ACT_SWIGLU; the others aligned to their elements (GEMM_ERR_ALIGNMENT).
+ * GEMM_ERR_UNSUPPORTED for GEMM_F32 operands, T > 64 (use the calls named above, which are faster
+ * there), k > 32, E > 1024, D > 262144 or F > 2^24.  T == 0 or D == 0: nothing is done.  F >= 1.
+ * The handle's workspace holds T * k rows of F 16-bit and D fp32 values, under the rules above.
+ * The pages have no counterpart to it. */
+int moe_layer(gemm_handle_t h, const moe_layer_args* args, void* stream);
+
 /* ------------------------------------------------------------------ token log probabilities
  *
  * What is asked of a model's logits [rows][V] once its last product has made them.  dtype is

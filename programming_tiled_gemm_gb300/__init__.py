@@ -39,7 +39,7 @@ EXPORTS = ["gemm_create", "gemm_destroy", "gemm_run", "gemm_run_ex", "gemm_run_h
            "gemm_get_device_status", "gemm_set_option", "gemm_launch_count", "gemm_status_string",
            "gemm_run_f32_skinny_noalloc",
            "gemm_linear", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
-           "moe_combine_backward", "token_logprobs", "token_logprobs_backward"]
+           "moe_combine_backward", "moe_layer", "token_logprobs", "token_logprobs_backward"]
 
 GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_SILU, GEMM_ACT_SWIGLU = 0, 1, 2, 3, 4, 5
 ACTIVATIONS = {"none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU, "gelu": GEMM_ACT_GELU, "gelu_tanh": GEMM_ACT_GELU_TANH,
@@ -72,6 +72,18 @@ class LinearGradArgs(ctypes.Structure):
                 ("dw_stride", ctypes.c_int64), ("db", ctypes.c_void_p), ("groups", ctypes.c_int64),
                 ("offsets", ctypes.c_void_p), ("dtype", ctypes.c_int), ("dw_dtype", ctypes.c_int),
                 ("act", ctypes.c_int)]
+
+
+class MoeLayerArgs(ctypes.Structure):
+    """moe_layer_args."""
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("F", ctypes.c_int64), ("logits", ctypes.c_void_p), ("ldl", ctypes.c_int64), ("X", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("W1", ctypes.c_void_p), ("ldw1", ctypes.c_int64),
+                ("w1_stride", ctypes.c_int64), ("b1", ctypes.c_void_p), ("W2", ctypes.c_void_p),
+                ("ldw2", ctypes.c_int64), ("w2_stride", ctypes.c_int64), ("b2", ctypes.c_void_p),
+                ("R", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("logits_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("renormalize", ctypes.c_int)]
 
 
 class Routing(NamedTuple):
@@ -125,6 +137,7 @@ def _load():
     lib.moe_dispatch.argtypes = [p, i64, i64, i64, p, i64, i32, p, p, i64, p]
     lib.moe_combine.argtypes = [p, i64, i64, i64, p, i64, i64, i32, p, p, p, i64, p, i64, p]
     lib.moe_combine_backward.argtypes = [p, i64, i64, i64, p, i64, p, i64, i32, p, p, p, p, i64, p, p]
+    lib.moe_layer.argtypes = [p, ctypes.POINTER(MoeLayerArgs), p]
     lib.token_logprobs.argtypes = [p, i64, i64, p, i64, i32, p, f32, p, p, p, i64, p, p, p]
     lib.token_logprobs_backward.argtypes = [p, i64, i64, p, i64, i32, p, f32, p, p, p, p, p, i64, p]
     lib.gemm_status_string.argtypes = [i32]
@@ -231,6 +244,10 @@ def moe_combine_backward(h, T, N, k, dout, lddo, y, ldy, dtype, slots, rows, wei
                                      stream)
 
 
+def moe_layer(h, args: MoeLayerArgs, stream=0) -> int:
+    return _lib.moe_layer(h, args, stream)
+
+
 def token_logprobs(h, rows, V, logits, ld, dtype, tokens, temperature, logprobs, entropy, stats, top, top_logprobs,
                    top_tokens, stream=0) -> int:
     return _lib.token_logprobs(h, rows, V, logits, ld, dtype, tokens, temperature, logprobs, entropy, stats, top,
@@ -293,8 +310,10 @@ def _ptr(t):
 # fields takes several microseconds to build), and entry points that take their addresses.
 _LINEAR = struct.Struct("@qqqPqPqqPPqPqPqqPiii")
 _LINEAR_GRAD = struct.Struct("@qqqPqPqPqqPqPqPqqPqPiii")
+_LAYER = struct.Struct("@qqqqqPqPqPqqPPqqPPqPqiiiii")
 _raw = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
 _linear_raw, _linear_backward_raw = _raw(("gemm_linear", _lib)), _raw(("gemm_linear_backward", _lib))
+_moe_layer_raw = _raw(("moe_layer", _lib))
 
 
 class Gemm:
@@ -303,7 +322,7 @@ class Gemm:
     def __init__(self, device: int = 0):
         self.device = int(device)
         self.handle = gemm_create(self.device)
-        self._args = ctypes.create_string_buffer(max(_LINEAR.size, _LINEAR_GRAD.size) + 8)
+        self._args = ctypes.create_string_buffer(max(_LINEAR.size, _LINEAR_GRAD.size, _LAYER.size) + 8)
         self._args_at = ctypes.addressof(self._args)
         self._dev = None
 
@@ -748,6 +767,50 @@ class Gemm:
             raise GemmError(rc, "moe_combine_backward")
         return dy, dweights
 
+    def _experts(self, w, name, E, K, N, dtype):
+        """(leading dimension, stride) of a matrix an expert, [E, K, N]."""
+        if w.shape != (E, K, N):
+            raise ValueError("%s must have shape %s, got %s" % (name, (E, K, N), tuple(w.shape)))
+        return self._mat(w[0], name, K, N, dtype), w.stride(0)
+
+    def moe_layer(self, x, logits, w1, w2, k, act="swiglu", b1=None, b2=None, renormalize=True, residual=None, out=None,
+                  out_dtype=None, stream=None):
+        """A whole mixture-of-experts layer for up to 64 tokens: moe_route of logits [T, E], and
+        sum over j of weights[t, j] * (act(x[t] @ w1[e] + b1[e]) @ w2[e] + b2[e]) + residual[t], e the
+        token's j-th pick.  x [T, D], w1 [E, D, F] ([E, D, 2 F] for "swiglu": gate columns, then up
+        columns), b1 [E, F], w2 [E, F, D], b2 [E, D], bf16 or fp16; logits of any type, -inf for an expert that
+        is not there.  The result (of x's type, or float32) has shape [T, D]."""
+        code = ACTIVATIONS[act]
+        if x.dim() != 2 or logits.dim() != 2 or w1.dim() != 3 or w2.dim() != 3:
+            raise ValueError("x must be [T, D], logits [T, E], w1 [E, D, F] and w2 [E, F, D]")
+        T, D = x.shape
+        E, F, _ = w2.shape
+        k = int(k)
+        if not 1 <= k <= E:
+            raise ValueError("k must be between 1 and the number of experts")
+        dt = x.dtype
+        dcode, lcode = _dtype_code(x), _dtype_code(logits)
+        ldx, ldl = self._mat(x, "x", T, D, dt), self._mat(logits, "logits", T, E, logits.dtype)
+        Fw = 2 * F if code == GEMM_ACT_SWIGLU else F
+        ldw1, s1 = self._experts(w1, "w1", E, D, Fw, dt)
+        ldw2, s2 = self._experts(w2, "w2", E, F, D, dt)
+        at_b1 = self._flat(b1, "b1", (E, Fw), dt) if b1 is not None else 0
+        at_b2 = self._flat(b2, "b2", (E, D), dt) if b2 is not None else 0
+        if out is None:
+            out, ldy = self._new((T, D), out_dtype or (residual.dtype if residual is not None else dt), stream), D
+        else:
+            ldy = self._mat(out, "out", T, D, out.dtype)
+        ldr = at_r = 0
+        if residual is not None:
+            ldr, at_r = self._mat(residual, "residual", T, D, out.dtype), residual.data_ptr()
+        _LAYER.pack_into(self._args, 0, T, E, k, D, F, logits.data_ptr(), ldl, x.data_ptr(), ldx, w1.data_ptr(), ldw1, s1,
+                         at_b1, w2.data_ptr(), ldw2, s2, at_b2, at_r, ldr, out.data_ptr(), ldy, dcode, lcode,
+                         dcode if out.dtype is dt else _dtype_code(out), code, 1 if renormalize else 0)
+        rc = _moe_layer_raw(self.handle, self._args_at, self._stream(stream))
+        if rc != GEMM_OK:
+            raise GemmError(rc, "moe_layer")
+        return out
+
     # ---- token log probabilities
 
     def token_logprobs(self, logits, tokens, top=0, entropy=False, temperature=1.0, stream=None):
@@ -820,6 +883,7 @@ __all__ = ["Gemm", "GemmError", "HostProblem", "gemm_create", "gemm_destroy", "g
            "conv4d_im2col", "conv4d_forward", "conv4d_forward_cl", "conv4d_forward_tc", "gemm_get_device_status", "gemm_set_option", "gemm_launch_count",
            "gemm_status_string",
            "gemm_linear", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
-           "moe_combine_backward", "token_logprobs", "token_logprobs_backward", "LinearArgs", "LinearGradArgs", "Routing",
+           "moe_combine_backward", "moe_layer", "token_logprobs", "token_logprobs_backward", "LinearArgs", "LinearGradArgs",
+           "MoeLayerArgs", "Routing",
            "TokenLogprobs", "ACTIVATIONS",
            "status_string", "library", "LIB_PATH", "EXPORTS"]

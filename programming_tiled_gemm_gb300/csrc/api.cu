@@ -16,6 +16,7 @@
 #include "context.h"
 #include "internal.h"
 #include "linear.h"
+#include "moe.h"
 
 using namespace gemm_gb300;
 
@@ -181,7 +182,7 @@ static int gemm_create_impl(gemm_handle_t* out, int device)
     h->device = device;
     h->num_sms = sms;
     // (cudaMemset runs on the legacy stream: done before any other stream may use the words)
-    const size_t counters = (size_t)(linear_counters(sms) + 1) * sizeof(unsigned);
+    const size_t counters = (size_t)(linear_counters(sms) + 1 + kLayerCounters) * sizeof(unsigned);
     if (cudaMalloc(&h->d_status, sizeof(int)) != cudaSuccess || cudaMalloc(&h->lin_counters, counters) != cudaSuccess ||
         cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess || cudaMemset(h->lin_counters, 0, counters) != cudaSuccess ||
         cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
@@ -217,6 +218,7 @@ int gemm_destroy(gemm_handle_t h)
     if (h->lin_dz) cudaFree(h->lin_dz);
     if (h->lin_sums) cudaFree(h->lin_sums);
     if (h->route_counts) cudaFree(h->route_counts);
+    if (h->layer) cudaFree(h->layer);
     while (gemm_ctx::KeptBuffer* k = h->kept) {
         h->kept = k->next;
         cudaFree(k->p);
@@ -731,7 +733,8 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
     for (auto take : {bounds_flag_take_ffma, bounds_flag_take_ffma_tma, bounds_flag_take_skinny,
                       bounds_flag_take_skinny_tma, bounds_flag_take_im2col, bounds_flag_take_conv_implicit,
                       bounds_flag_take_conv_tc, bounds_flag_take_tc_gemm, bounds_flag_take_linear_tc,
-                      bounds_flag_take_linear_act, bounds_flag_take_linear_few, bounds_flag_take_moe}) {
+                      bounds_flag_take_linear_act, bounds_flag_take_linear_few, bounds_flag_take_moe,
+                      bounds_flag_take_moe_layer}) {
         const int r = take();
         if (r < 0) return GEMM_ERR_CUDA;
         bad |= r;

@@ -42,8 +42,10 @@ struct gemm_ctx {
     size_t lin_sums_bytes = 0;
     void* route_counts = nullptr;
     size_t route_counts_bytes = 0;
+    void* layer = nullptr;  // moe_layer: the picks' rows between and after the two products
+    size_t layer_bytes = 0;
     // arrival counters, zero after every launch: linear_counters(num_sms) of the products, then
-    // the router's.  Made with the handle, so that they never move
+    // the router's, then kLayerCounters of moe_layer.  Made with the handle, so that they never move
     unsigned* lin_counters = nullptr;
     bool captured = false;    // a graph holds addresses of the buffers that grow
     struct KeptBuffer {

@@ -68,18 +68,6 @@ struct RouteParams {
     unsigned* cnt;
 };
 
-// Larger values have larger keys; NaN (as the largest) before +inf, 0 for -inf.  +0 = -0.
-__device__ __forceinline__ uint32_t order_key(float v)
-{
-    if (v != v) return 0xffffffffu;
-    if (v == -INFINITY) return 0u;
-    const uint32_t u = __float_as_uint(v + 0.f);
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-}
-
-// The value of a key (a NaN for any NaN's).
-__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
-
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

@@ -8,6 +8,18 @@ namespace gemm_gb300 {
 constexpr int kMaxExperts = 1024;  // logits of a token in a warp's registers
 constexpr int kMaxTopK = 32;       // one lane a pick
 
+// Larger values have larger keys; NaN (as the largest) before +inf, 0 for -inf.  +0 = -0.
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    if (v != v) return 0xffffffffu;
+    if (v == -INFINITY) return 0u;
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// The value of a key (a NaN for any NaN's).
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
+
 struct RouteArgs {
     const void* logits;  // [T][E], row stride ld
     int64_t ld, T, E;
@@ -72,5 +84,33 @@ struct CombineGradArgs {
     float* dweights;  // [T][k]
 };
 int launch_moe_combine_grad(const CombineGradArgs& a, int dtype, cudaStream_t s, int* launches);
+
+// A whole layer for a few tokens (moe_layer.cu).
+constexpr int kLayerTokens = 64;
+constexpr int kLayerSlab = 64;       // columns of W2 that one counter stands for
+constexpr int kLayerCounters = 4096;  // and the counters there are, zero before and after every launch
+
+struct LayerArgs {
+    int T, E, k, D, F, Fw;  // Fw columns of W1 (2 F when gated)
+    const void* logits;     // [T][E] of type logits_dtype
+    int64_t ldl;
+    int logits_dtype, renormalize;
+    const void* x;  // [T][D]
+    int64_t ldx;
+    const void* w1;  // [E][D][Fw]
+    int64_t ldw1, w1_stride;
+    const void* b1;  // [E][Fw] or null
+    const void* w2;  // [E][F][D]
+    int64_t ldw2, w2_stride;
+    const void* b2;  // [E][D] or null
+    const void* R;   // [T][D] or null
+    int64_t ldr;
+    void* out;  // [T][D]
+    int64_t ldo;
+    int act;
+    bool bf16, out_f32;
+};
+size_t moe_layer_ws_bytes(const LayerArgs& a);
+int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_sms, cudaStream_t s, int* launches);
 
 }  // namespace gemm_gb300

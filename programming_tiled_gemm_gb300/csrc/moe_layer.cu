@@ -1,0 +1,511 @@
+// A whole mixture-of-experts layer for up to 64 tokens, in two kernels:
+//   out[t] = sum_j w[t][j] (act(x[t] W1[e] + b1[e]) W2[e] + b2[e]) + R[t],   e = e[t][j], the router's picks.
+//
+// Bound by the picked experts' weights, which are streamed once: 64 tokens are too few rows to keep
+// the tensor cores busy.  Each kernel's CTAs walk (expert, 64 columns of its matrix) items; an
+// item's weights come through a ring of asynchronous copies, 64 of the reduced dimension a stage,
+// and are multiplied with the expert's rows by mma.sync: the features on the M side, eight rows an
+// MMA on the N side, so that a single row costs one MMA of 16 x 16 weights.  (tcgen05's set-up, tile
+// of 128 features and drain take longer than such an item; FMAs would bound three rows and more.)
+//
+// Every CTA routes for itself: the picks are some hundred instructions of a warp a token, less than
+// a launch and a trip through memory.  A pick's row of H and of the partial outputs is its index
+// t k + j, so nothing is sorted and CTAs need not agree on more than that; an expert's rows are the
+// picks that name it, in order.  The second kernel is launched early, routes and fills its ring with
+// weights while the first one ends, and waits for it only before it reads H.  It leaves every pick's
+// product in fp32; the CTA that finishes a slab of columns last adds each token's picks in the order
+// of j, the residual last.  Nothing waits for another CTA, and no sum depends on their order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "linear.h"
+#include "linear_math.h"
+#include "moe.h"
+#include "ptx.h"
+
+namespace gemm_gb300 {
+
+GEMM_DEBUG_UNIT(moe_layer)
+
+namespace {
+
+constexpr int WARPS = 8, THREADS = 32 * WARPS;
+constexpr int SLAB = kLayerSlab;  // columns of W an item
+constexpr int DEPTH = 64;         // of the reduced dimension a stage
+constexpr int W_BYTES = DEPTH * SLAB * 2;
+constexpr int ROW_BYTES = DEPTH * 2;  // of X or H a stage
+constexpr int PAD = SLAB + 4;         // floats of a row of sums
+constexpr int MAX_TILES = kLayerTokens / 8;
+constexpr uint16_t NONE = 0xffff;
+
+struct LayerParams {
+    int T, E, k, D, F, Fw;
+    const void* logits;
+    int64_t ldl;
+    int logits_dtype, renorm;
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* w;  // this kernel's matrices
+    int64_t ldw, w_stride;
+    const uint16_t* bias;
+    const void* R;
+    int64_t ldr;
+    void* out;
+    int64_t ldo;
+    int act, out_f32;
+    uint16_t* h;  // [T k][Fp]
+    int Fp;
+    float* y;  // [T k][Dp]
+    int Dp;
+    unsigned* counters;
+    int slabs, stages, rows_cap;  // rows_cap: rows of a stage, T to a multiple of 8
+};
+
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The router's outcome, in shared memory.
+struct Routes {
+    float* weight;      // [T k]
+    uint16_t* expert;   // [T k], NONE: no pick
+    uint16_t* pick;     // [T k]: the picks by expert, each expert's in order
+    int* count;         // [E]
+    uint16_t* active;   // [E]: experts with picks
+    int* first;         // [E + 1]: their first pick in `pick`
+    int* n_active;
+};
+__host__ __device__ inline int routes_bytes(int picks, int E)
+{
+    return 16 + 4 * (E + 1) + 4 * E + 4 * picks + 2 * picks * 2 + 2 * E + 16;
+}
+__device__ __forceinline__ Routes carve(uint8_t* at, int picks, int E)
+{
+    Routes r;
+    r.n_active = reinterpret_cast<int*>(at);
+    r.first = r.n_active + 4;
+    r.count = r.first + E + 1;
+    r.weight = reinterpret_cast<float*>(r.count + E);
+    r.expert = reinterpret_cast<uint16_t*>(r.weight + picks);
+    r.pick = r.expert + picks;
+    r.active = r.pick + picks;
+    return r;
+}
+
+// (read past L1: the second kernel does so before it has waited for the first)
+__device__ __forceinline__ float logit(const LayerParams& p, int t, int e)
+{
+    const int64_t i = (int64_t)t * p.ldl + e;
+    if (p.logits_dtype == GEMM_F32) return __ldcg(static_cast<const float*>(p.logits) + i);
+    const uint16_t v = __ldcg(static_cast<const uint16_t*>(p.logits) + i);
+    return p.logits_dtype == GEMM_BF16 ? from_16<true>(v) : from_16<false>(v);
+}
+
+// The picks of all tokens as moe_route makes them.  `scratch`: WARPS * E words.
+__device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uint32_t* scratch)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = p.E, k = p.k, picks = p.T * k;
+    for (int e = threadIdx.x; e < E; e += THREADS) r.count[e] = 0;
+    uint32_t* key = scratch + warp * E;
+    for (int t = warp; t < p.T; t += WARPS) {
+        for (int e = lane; e < E; e += 32) key[e] = order_key(logit(p, t, e));
+        __syncwarp();
+        int pick = -1;
+        float val = 0.f, top = 0.f, all = 0.f;
+        for (int j = 0; j < k; ++j) {
+            uint32_t best = 0;
+            int at = 0;
+            for (int e = lane; e < E; e += 32)
+                if (key[e] > best) best = key[e], at = e;
+            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+            if (m == 0) break;  // no expert is left
+            const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (unsigned)at : 0xffffffffu);
+            const float v = key_value(m);
+            if (j == 0) {
+                top = v;
+                if (!p.renorm)
+                    for (int i = lane; i < E; i += 32)
+                        if (key[i] != 0) all += expf(key_value(key[i]) - top);
+            }
+            __syncwarp();
+            if (best == m && at == e) key[e] = 0;
+            if (lane == j) pick = e, val = v;
+            __syncwarp();
+        }
+        const float ex = pick >= 0 ? expf(val - top) : 0.f;
+        float sum = p.renorm ? ex : all;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane < k) {
+            r.expert[t * k + lane] = pick >= 0 ? (uint16_t)pick : NONE;
+            r.weight[t * k + lane] = pick >= 0 ? ex / sum : 0.f;
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < picks; i += THREADS)
+        if (r.expert[i] != NONE) atomicAdd(&r.count[r.expert[i]], 1);
+    __syncthreads();
+    if (warp == 0) {
+        int n = 0, sum = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane, c = e < E ? r.count[e] : 0;
+            const unsigned on = __ballot_sync(0xffffffffu, c > 0);
+            int before = c;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, before, d);
+                if (lane >= d) before += o;
+            }
+            if (c > 0) {
+                const int a = n + __popc(on & ((1u << lane) - 1));
+                r.active[a] = (uint16_t)e;
+                r.first[a] = sum + before - c;
+            }
+            n += __popc(on);
+            sum += __shfl_sync(0xffffffffu, before, 31);
+        }
+        if (lane == 0) *r.n_active = n, r.first[n] = sum;
+    }
+    __syncthreads();
+    const int n = *r.n_active;
+    for (int a = warp; a < n; a += WARPS) {
+        const int e = r.active[a];
+        int at = r.first[a];
+        for (int i0 = 0; i0 < picks; i0 += 32) {
+            const bool is = i0 + lane < picks && r.expert[i0 + lane] == e;
+            const unsigned who = __ballot_sync(0xffffffffu, is);
+            if (is) r.pick[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(i0 + lane);
+            at += __popc(who);
+        }
+    }
+    __syncthreads();
+}
+
+// The tokens' sums of a slab of 64 columns: 8 columns of a token a thread.
+template <bool BF16>
+__device__ __forceinline__ void combine(const LayerParams& p, const Routes& r, int slab)
+{
+    for (int i = threadIdx.x; i < p.T * (SLAB / 8); i += THREADS) {
+        const int t = i / (SLAB / 8), col = slab * SLAB + i % (SLAB / 8) * 8, n = min(8, p.D - col);
+        if (n <= 0) continue;
+        float v[8] = {};
+#pragma unroll 4
+        for (int j = 0; j < p.k; ++j) {
+            const int q = t * p.k + j;
+            if (r.expert[q] == NONE || !in_range(q, p.T * p.k)) continue;
+            const float w = r.weight[q];
+            const float4* src = reinterpret_cast<const float4*>(p.y + (int64_t)q * p.Dp + col);
+            const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
+            float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if (p.bias) {
+                const uint16_t* b = p.bias + (int64_t)r.expert[q] * p.D + col;
+                for (int c = 0; c < n; ++c) y[c] += from_16<BF16>(b[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] += w * y[c];
+        }
+        if (p.out_f32) {
+            const float* R = p.R ? static_cast<const float*>(p.R) + (int64_t)t * p.ldr + col : nullptr;
+            float* o = static_cast<float*>(p.out) + (int64_t)t * p.ldo + col;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < n) o[c] = R ? v[c] + R[c] : v[c];
+        } else {
+            const uint16_t* R = p.R ? static_cast<const uint16_t*>(p.R) + (int64_t)t * p.ldr + col : nullptr;
+            uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)t * p.ldo + col;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < n) o[c] = to_16<BF16>(R ? v[c] + from_16<BF16>(R[c]) : v[c]);
+        }
+    }
+}
+
+// UP: H = act(X W1 + b1), else Y = H W2 and the tokens' sums.  Stage: [64 of the reduced
+// dimension][64 columns] of W, then [row][64] of X or H, 16-byte chunks of a 128-byte line exchanged
+// by the line's number (no bank conflicts).  GATED (UP): 32 columns of the gate, then 32 of the up half.
+template <bool UP, bool GATED, bool BF16>
+__global__ void __launch_bounds__(THREADS, 2) layer_kernel(LayerParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int stage_bytes = W_BYTES + p.rows_cap * ROW_BYTES;
+    uint8_t* const ring = smem;
+    float* const sums = reinterpret_cast<float*>(smem + p.stages * stage_bytes);  // [rows_cap][PAD]
+    const Routes r = carve(reinterpret_cast<uint8_t*>(sums + p.rows_cap * PAD), p.T * p.k, p.E);
+    __shared__ int is_last;
+    if (UP) {
+        grid_dependency_wait();
+        grid_dependents_launch();
+    }
+    // (the second kernel starts once every CTA of the first has got here: what came before that one,
+    // the logits among it, is complete, and only H is not)
+    route(p, r, reinterpret_cast<uint32_t*>(ring));
+
+    const int n_act = *r.n_active;
+    const int K = UP ? p.D : p.F, N = UP ? p.F : p.D;
+    const int steps = (K + DEPTH - 1) / DEPTH;
+    const int items = n_act * p.slabs;
+    constexpr int COLS = GATED ? SLAB / 2 : SLAB;  // output columns of an item
+
+    // the loader: its item and step, some stages ahead of the MMAs'
+    int l_item = blockIdx.x, l_step = 0, l_stage = 0;
+    const auto load = [&](bool weights, bool rows) {
+        if (l_item < items) {
+            const int a = l_item / p.slabs, slab = l_item - a * p.slabs;
+            const uint32_t at = smem_u32(ring + l_stage * stage_bytes);
+            const int k0 = l_step * DEPTH;
+            if (weights) {
+                const uint16_t* W = p.w + r.active[a] * p.w_stride;
+#pragma unroll
+                for (int i = 0; i < DEPTH * SLAB / 8 / THREADS; ++i) {
+                    const int q = threadIdx.x + i * THREADS, kr = q / 8, c = q % 8;
+                    const int f = slab * COLS + (GATED ? c % 4 : c) * 8;
+                    int n = k0 + kr < K ? max(0, min(8, N - f)) : 0;
+                    const int col = f + (GATED && c >= 4 ? p.F : 0);
+                    if (n > 0 && (!in_range(k0 + kr, K) || !in_range(col + n - 1, UP ? p.Fw : p.D))) n = 0;
+                    copy_16(at + kr * 128 + ((c ^ (kr & 7)) * 16), n > 0 ? W + (int64_t)(k0 + kr) * p.ldw + col : p.w, 2 * n);
+                }
+            }
+            if (rows) {
+                const int first = r.first[a], n_rows = r.first[a + 1] - first;
+                for (int q = threadIdx.x; q < (n_rows + 7) / 8 * 64; q += THREADS) {
+                    const int row = q / 8, c = q % 8, kk = k0 + c * 8;
+                    int n = row < n_rows ? max(0, min(8, (UP ? K : p.Fp) - kk)) : 0;
+                    const int pick = row < n_rows ? r.pick[first + row] : 0;
+                    if (n > 0 && !in_range(pick, p.T * p.k)) n = 0;
+                    const uint16_t* src = UP ? p.x + (int64_t)(pick / p.k) * p.ldx + kk : p.h + (int64_t)pick * p.Fp + kk;
+                    copy_16(at + W_BYTES + row * 128 + ((c ^ (row & 7)) * 16), n > 0 ? src : p.w, 2 * n);
+                }
+            }
+        }
+    };
+    const auto advance = [&](int& item, int& step, int& stage) {
+        if (++step == steps) step = 0, item += gridDim.x;
+        if (++stage == p.stages) stage = 0;
+    };
+    if (!UP) {
+        // weights ahead of the first kernel's end, then the rows of these stages
+        const int item0 = l_item, step0 = l_step;
+        for (int s = 0; s < p.stages - 1; ++s) {
+            load(true, false);
+            advance(l_item, l_step, l_stage);
+        }
+        grid_dependency_wait();
+        grid_dependents_launch();
+        l_item = item0, l_step = step0, l_stage = 0;
+    }
+    for (int s = 0; s < p.stages - 1; ++s) {
+        load(UP, true);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        advance(l_item, l_step, l_stage);
+    }
+
+    const int fg = warp % 4, kh = warp / 4;  // 16 columns, half of a stage's depth
+    int stage = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int a = item / p.slabs, slab = item - a * p.slabs;
+        const int first = r.first[a], n_rows = r.first[a + 1] - first, tiles = (n_rows + 7) / 8;
+        float acc[MAX_TILES][4];
+#pragma unroll
+        for (int t = 0; t < MAX_TILES; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+        for (int step = 0; step < steps; ++step) {
+            // (p.stages - 2 groups may be under way; the count is a constant of the instruction)
+            switch (p.stages) {
+            case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+            case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+            case 5: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+            default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+            }
+            __syncthreads();
+            load(true, true);  // into the stage that was multiplied before the barrier
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            advance(l_item, l_step, l_stage);
+            const uint32_t at = smem_u32(ring + stage * stage_bytes);
+            uint32_t wf[2][4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                // matrices (k 0..7, f 0..7), (k 0..7, f 8..15), (k 8..15, f 0..7), (k 8..15, f 8..15)
+                const int kr = kh * 32 + s * 16 + (lane / 16) * 8 + lane % 8, c = fg * 2 + lane / 8 % 2;
+                ldsm_x4_trans(at + kr * 128 + ((c ^ (kr & 7)) * 16), wf[s]);
+            }
+#pragma unroll
+            for (int t = 0; t < MAX_TILES; ++t) {
+                if (t >= tiles) break;
+                uint32_t xf[4];  // rows 8 t .. 8 t + 7, four chunks of 8 of k
+                const int row = t * 8 + lane % 8, c = kh * 4 + lane / 8;
+                ldsm_x4(at + W_BYTES + row * 128 + ((c ^ (row & 7)) * 16), xf);
+                mma_16816<BF16>(acc[t], wf[0], xf[0], xf[1]);
+                mma_16816<BF16>(acc[t], wf[1], xf[2], xf[3]);
+            }
+            if (++stage == p.stages) stage = 0;
+        }
+        // the two halves of the depth, [row][column]
+        const int f = fg * 16 + lane / 4, row = lane % 4 * 2;
+        if (kh == 1)
+#pragma unroll
+            for (int t = 0; t < MAX_TILES; ++t)
+                if (t < tiles) {
+                    float* s = sums + (t * 8 + row) * PAD + f;
+                    s[0] = acc[t][0], s[PAD] = acc[t][1], s[8] = acc[t][2], s[PAD + 8] = acc[t][3];
+                }
+        __syncthreads();
+        if (kh == 0)
+#pragma unroll
+            for (int t = 0; t < MAX_TILES; ++t)
+                if (t < tiles) {
+                    float* s = sums + (t * 8 + row) * PAD + f;
+                    s[0] += acc[t][0], s[PAD] += acc[t][1], s[8] += acc[t][2], s[PAD + 8] += acc[t][3];
+                }
+        __syncthreads();
+        for (int q = threadIdx.x; q < n_rows * (COLS / 8); q += THREADS) {
+            const int i = q / (COLS / 8), c0 = q % (COLS / 8) * 8, pick = r.pick[first + i], col = slab * COLS + c0;
+            if (!in_range(pick, p.T * p.k)) continue;
+            const float* s = sums + i * PAD + c0;
+            float v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = s[c];
+            if constexpr (UP) {
+                const int e = r.active[a];
+                if (p.bias)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (col + c < p.F) v[c] += from_16<BF16>(p.bias[(int64_t)e * p.Fw + col + c]);
+                if constexpr (GATED) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float up = s[SLAB / 2 + c];
+                        if (p.bias && col + c < p.F) up += from_16<BF16>(p.bias[(int64_t)e * p.Fw + p.F + col + c]);
+                        v[c] = silu(v[c]) * up;
+                    }
+                } else {
+                    activate(v, p.act);
+                }
+                // (columns past F are zero: zero weights, no bias, act(0) = 0)
+                uint32_t w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    w[c] = to_16<BF16>(v[2 * c]) | (uint32_t)to_16<BF16>(v[2 * c + 1]) << 16;
+                if (in_range(col + 7, p.Fp))
+                    *reinterpret_cast<uint4*>(p.h + (int64_t)pick * p.Fp + col) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else if (in_range(col + 7, p.Dp)) {
+                float4* o = reinterpret_cast<float4*>(p.y + (int64_t)pick * p.Dp + col);
+                __stcg(o, make_float4(v[0], v[1], v[2], v[3]));
+                __stcg(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+            }
+        }
+        if constexpr (!UP) {
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const int last = atomicAdd(p.counters + slab, 1u) == (unsigned)(n_act - 1);
+                if (last) p.counters[slab] = 0;  // ready for the next launch
+                __threadfence();
+                is_last = last;
+            }
+            __syncthreads();
+            if (is_last) {
+                __threadfence();
+                combine<BF16>(p, r, slab);
+            }
+        }
+    }
+    if constexpr (!UP) {
+        if (n_act == 0)  // no token goes anywhere
+            for (int slab = blockIdx.x; slab < p.slabs; slab += gridDim.x) combine<BF16>(p, r, slab);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <bool UP, bool GATED, bool BF16>
+cudaError_t launch_typed(const LayerParams& p, int grid, int smem, cudaStream_t s)
+{
+    auto kern = layer_kernel<UP, GATED, BF16>;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(kern, 112 * 1024, allowed);
+    return e != cudaSuccess ? e : launch_dependent(kern, dim3(grid), dim3(THREADS), smem, s, p);
+}
+
+int padded(int n) { return (n + DEPTH - 1) / DEPTH * DEPTH; }
+
+}  // namespace
+
+size_t moe_layer_ws_bytes(const LayerArgs& a)
+{
+    return (size_t)a.T * a.k * (padded(a.F) * sizeof(uint16_t) + padded(a.D) * sizeof(float));
+}
+
+int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_sms, cudaStream_t s, int* launches)
+{
+    LayerParams p = {};
+    p.T = a.T, p.E = a.E, p.k = a.k, p.D = a.D, p.F = a.F, p.Fw = a.Fw;
+    p.logits = a.logits, p.ldl = a.ldl, p.logits_dtype = a.logits_dtype, p.renorm = a.renormalize;
+    p.x = static_cast<const uint16_t*>(a.x), p.ldx = a.ldx;
+    p.R = a.R, p.ldr = a.ldr;
+    p.out = a.out, p.ldo = a.ldo;
+    p.act = a.act, p.out_f32 = a.out_f32 ? 1 : 0;
+    p.Fp = padded(a.F), p.Dp = padded(a.D);
+    const int picks = a.T * a.k;
+    p.y = static_cast<float*>(ws);
+    p.h = reinterpret_cast<uint16_t*>(p.y + (size_t)picks * p.Dp);
+    p.counters = counters;
+    p.rows_cap = (a.T + 7) / 8 * 8;
+    // two CTAs an SM; the router's keys lie in the ring
+    const int stage = W_BYTES + p.rows_cap * ROW_BYTES, fixed = p.rows_cap * PAD * 4 + routes_bytes(picks, a.E);
+    p.stages = (108 * 1024 - fixed) / stage;
+    if (p.stages > 6) p.stages = 6;
+    if (p.stages < 3 || p.stages * stage < WARPS * a.E * 4) return GEMM_ERR_UNSUPPORTED;
+    const int smem = p.stages * stage + fixed;
+    const bool gated = a.act == GEMM_ACT_SWIGLU;
+    const int most = a.E < picks ? a.E : picks;  // experts that can be active
+    const auto grid = [&](int slabs) {
+        const int64_t items = (int64_t)most * slabs, fit = 2 * num_sms;
+        return (int)(items < fit ? items : fit);
+    };
+    p.w = static_cast<const uint16_t*>(a.w1), p.ldw = a.ldw1, p.w_stride = a.w1_stride;
+    p.bias = static_cast<const uint16_t*>(a.b1);
+    p.slabs = p.Fp / (gated ? SLAB / 2 : SLAB);
+    cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true, true>(p, grid(p.slabs), smem, s)
+                                    : launch_typed<true, false, true>(p, grid(p.slabs), smem, s))
+                           : (gated ? launch_typed<true, true, false>(p, grid(p.slabs), smem, s)
+                                    : launch_typed<true, false, false>(p, grid(p.slabs), smem, s));
+    if (e != cudaSuccess) return GEMM_ERR_CUDA;
+    *launches += 1;
+    p.w = static_cast<const uint16_t*>(a.w2), p.ldw = a.ldw2, p.w_stride = a.w2_stride;
+    p.bias = static_cast<const uint16_t*>(a.b2);
+    p.slabs = p.Dp / SLAB;
+    e = a.bf16 ? launch_typed<false, false, true>(p, grid(p.slabs), smem, s)
+               : launch_typed<false, false, false>(p, grid(p.slabs), smem, s);
+    if (e != cudaSuccess) return GEMM_ERR_CUDA;
+    *launches += 1;
+    return GEMM_OK;
+}
+
+}  // namespace gemm_gb300
