@@ -111,6 +111,7 @@ struct LayerArgs {
     bool bf16, out_f32;
 };
 size_t moe_layer_ws_bytes(const LayerArgs& a);
-int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_sms, cudaStream_t s, int* launches);
+int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_sms, int* dev_status, uint64_t limit_ns,
+                     int test_stall, cudaStream_t s, int* launches);
 
 }  // namespace gemm_gb300

@@ -2,11 +2,12 @@
 //   out[t] = sum_j w[t][j] (act(x[t] W1[e] + b1[e]) W2[e] + b2[e]) + R[t],   e = e[t][j], the router's picks.
 //
 // Bound by the picked experts' weights, which are streamed once: 64 tokens are too few rows to keep
-// the tensor cores busy.  Each kernel's CTAs walk (expert, 64 columns of its matrix) items; an
-// item's weights come through a ring of asynchronous copies, 64 of the reduced dimension a stage,
-// and are multiplied with the expert's rows by mma.sync: the features on the M side, eight rows an
-// MMA on the N side, so that a single row costs one MMA of 16 x 16 weights.  (tcgen05's set-up, tile
-// of 128 features and drain take longer than such an item; FMAs would bound three rows and more.)
+// the tensor cores busy.  Each kernel's CTAs walk (expert, 64 columns of its matrix) items; one warp
+// keeps a ring of stages filled across the items, 128 of the reduced dimension a stage: the weights by
+// TMA, the expert's rows by 16-byte copies.  Eight warps multiply with mma.sync: the features on the M
+// side, eight rows an MMA on the N side, so that a single row costs one MMA of 16 x 16 weights.
+// (tcgen05's set-up, tile of 128 features and drain take longer than such an item; FMAs would bound
+// three rows and more.)
 //
 // Every CTA routes for itself: the picks are some hundred instructions of a warp a token, less than
 // a launch and a trip through memory.  A pick's row of H and of the partial outputs is its index
@@ -15,6 +16,8 @@
 // weights while the first one ends, and waits for it only before it reads H.  It leaves every pick's
 // product in fp32; the CTA that finishes a slab of columns last adds each token's picks in the order
 // of j, the residual last.  Nothing waits for another CTA, and no sum depends on their order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,11 +32,13 @@ GEMM_DEBUG_UNIT(moe_layer)
 
 namespace {
 
-constexpr int WARPS = 8, THREADS = 32 * WARPS;
+constexpr int MMA_WARPS = 8, WARPS = MMA_WARPS + 1, THREADS = 32 * WARPS;  // the last warp loads
 constexpr int SLAB = kLayerSlab;  // columns of W an item
-constexpr int DEPTH = 64;         // of the reduced dimension a stage
+constexpr int DEPTH = 128;        // of the reduced dimension a stage
 constexpr int W_BYTES = DEPTH * SLAB * 2;
-constexpr int ROW_BYTES = DEPTH * 2;  // of X or H a stage
+constexpr int ROW_BYTES = DEPTH * 2 + 16;  // of X or H a stage: rows 16 bytes apart in the banks
+constexpr int MAX_STAGES = 6;
+constexpr int SMEM_TWO = 112 * 1024, SMEM_ONE = 224 * 1024;  // of a CTA, two or one an SM
 constexpr int PAD = SLAB + 4;         // floats of a row of sums
 constexpr int MAX_TILES = kLayerTokens / 8;
 constexpr uint16_t NONE = 0xffff;
@@ -45,9 +50,7 @@ struct LayerParams {
     int logits_dtype, renorm;
     const uint16_t* x;
     int64_t ldx;
-    const uint16_t* w;  // this kernel's matrices
-    int64_t ldw, w_stride;
-    const uint16_t* bias;
+    const uint16_t* bias;  // this kernel's
     const void* R;
     int64_t ldr;
     void* out;
@@ -59,12 +62,11 @@ struct LayerParams {
     int Dp;
     unsigned* counters;
     int slabs, stages, rows_cap;  // rows_cap: rows of a stage, T to a multiple of 8
+    int* status;
+    uint64_t limit_ns;
+    int test_stall;
 };
 
-__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, int bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void ldsm_x4(uint32_t at, uint32_t (&r)[4])
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -211,7 +213,7 @@ __device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uin
 template <bool BF16>
 __device__ __forceinline__ void combine(const LayerParams& p, const Routes& r, int slab)
 {
-    for (int i = threadIdx.x; i < p.T * (SLAB / 8); i += THREADS) {
+    for (int i = threadIdx.x; i < p.T * (SLAB / 8); i += 32 * MMA_WARPS) {
         const int t = i / (SLAB / 8), col = slab * SLAB + i % (SLAB / 8) * 8, n = min(8, p.D - col);
         if (n <= 0) continue;
         float v[8] = {};
@@ -246,88 +248,115 @@ __device__ __forceinline__ void combine(const LayerParams& p, const Routes& r, i
     }
 }
 
-// UP: H = act(X W1 + b1), else Y = H W2 and the tokens' sums.  Stage: [64 of the reduced
-// dimension][64 columns] of W, then [row][64] of X or H, 16-byte chunks of a 128-byte line exchanged
-// by the line's number (no bank conflicts).  GATED (UP): 32 columns of the gate, then 32 of the up half.
+// UP: H = act(X W1 + b1), else Y = H W2 and the tokens' sums.  Stage: [128 of the reduced
+// dimension][64 columns] of W, swizzled by the TMA (128-byte rows; GATED, UP only: 32 columns of the gate,
+// then 32 of the up half, each in 64-byte rows), and [row][128] of X or H.
 template <bool UP, bool GATED, bool BF16>
-__global__ void __launch_bounds__(THREADS, 2) layer_kernel(LayerParams p)
+__global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant__ CUtensorMap tmW, LayerParams p)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int COLS = GATED ? SLAB / 2 : SLAB;  // output columns of an item
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int stage_bytes = W_BYTES + p.rows_cap * ROW_BYTES;
-    uint8_t* const ring = smem;
-    float* const sums = reinterpret_cast<float*>(smem + p.stages * stage_bytes);  // [rows_cap][PAD]
+    const uint32_t ring_w = smem_u32(smem), ring_x = ring_w + p.stages * W_BYTES;
+    const int x_bytes = p.rows_cap * ROW_BYTES;
+    float* const sums = reinterpret_cast<float*>(smem + p.stages * (W_BYTES + x_bytes));  // [rows_cap][PAD]
     const Routes r = carve(reinterpret_cast<uint8_t*>(sums + p.rows_cap * PAD), p.T * p.k, p.E);
+    __shared__ uint64_t full_bar[MAX_STAGES], empty_bar[MAX_STAGES], never_bar;
     __shared__ int is_last;
+    __shared__ volatile int abort_flag;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(smem_u32(&full_bar[i]), 1 + 32);  // the weights' bytes, and each loading lane's copies
+            mbar_init(smem_u32(&empty_bar[i]), MMA_WARPS);
+        }
+        mbar_init(smem_u32(&never_bar), 1);
+        abort_flag = 0;
+        mbar_fence_init();
+        prefetch_tensormap(&tmW);
+    }
     if (UP) {
         grid_dependency_wait();
         grid_dependents_launch();
     }
     // (the second kernel starts once every CTA of the first has got here: what came before that one,
     // the logits among it, is complete, and only H is not)
-    route(p, r, reinterpret_cast<uint32_t*>(ring));
+    route(p, r, reinterpret_cast<uint32_t*>(smem));
+    fence_proxy_async_shared();  // (the router's words lie where the TMA writes)
+    __syncthreads();
 
     const int n_act = *r.n_active;
-    const int K = UP ? p.D : p.F, N = UP ? p.F : p.D;
+    const int K = UP ? p.D : p.F;
     const int steps = (K + DEPTH - 1) / DEPTH;
     const int items = n_act * p.slabs;
-    constexpr int COLS = GATED ? SLAB / 2 : SLAB;  // output columns of an item
+    const auto gave_up = [&](int code) {
+        if (lane == 0) atomicCAS(p.status, 0, code);
+        abort_flag = 1;
+    };
+    bool dead = false;
 
-    // the loader: its item and step, some stages ahead of the MMAs'
-    int l_item = blockIdx.x, l_step = 0, l_stage = 0;
-    const auto load = [&](bool weights, bool rows) {
-        if (l_item < items) {
-            const int a = l_item / p.slabs, slab = l_item - a * p.slabs;
-            const uint32_t at = smem_u32(ring + l_stage * stage_bytes);
-            const int k0 = l_step * DEPTH;
-            if (weights) {
-                const uint16_t* W = p.w + r.active[a] * p.w_stride;
-#pragma unroll
-                for (int i = 0; i < DEPTH * SLAB / 8 / THREADS; ++i) {
-                    const int q = threadIdx.x + i * THREADS, kr = q / 8, c = q % 8;
-                    const int f = slab * COLS + (GATED ? c % 4 : c) * 8;
-                    int n = k0 + kr < K ? max(0, min(8, N - f)) : 0;
-                    const int col = f + (GATED && c >= 4 ? p.F : 0);
-                    if (n > 0 && (!in_range(k0 + kr, K) || !in_range(col + n - 1, UP ? p.Fw : p.D))) n = 0;
-                    copy_16(at + kr * 128 + ((c ^ (kr & 7)) * 16), n > 0 ? W + (int64_t)(k0 + kr) * p.ldw + col : p.w, 2 * n);
-                }
+    if (warp == MMA_WARPS) {
+        // ---------------------------------------------------------------- loads
+        const auto weights = [&](int item, int step, int stage) {
+            if (!elect_one()) return;
+            const int a = item / p.slabs, f = (item - a * p.slabs) * COLS, e = r.active[a];
+            const uint32_t bar = smem_u32(&full_bar[stage]), at = ring_w + stage * W_BYTES;
+            mbar_arrive_expect_tx(bar, W_BYTES);
+            tma_load_3d(at, &tmW, bar, f, step * DEPTH, e);
+            if (GATED) tma_load_3d(at + W_BYTES / 2, &tmW, bar, p.F + f, step * DEPTH, e);
+        };
+        int early = 0;  // stages whose weights are under way before the first kernel has ended
+        if (!UP) {
+            int item = blockIdx.x, step = 0;
+            while (early < p.stages && item < items) {
+                weights(item, step, early);
+                ++early;
+                if (++step == steps) step = 0, item += gridDim.x;
             }
-            if (rows) {
-                const int first = r.first[a], n_rows = r.first[a + 1] - first;
-                for (int q = threadIdx.x; q < (n_rows + 7) / 8 * 64; q += THREADS) {
-                    const int row = q / 8, c = q % 8, kk = k0 + c * 8;
-                    int n = row < n_rows ? max(0, min(8, (UP ? K : p.Fp) - kk)) : 0;
-                    const int pick = row < n_rows ? r.pick[first + row] : 0;
-                    if (n > 0 && !in_range(pick, p.T * p.k)) n = 0;
+            __syncwarp();
+            grid_dependency_wait();
+            grid_dependents_launch();
+        }
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int item = blockIdx.x; item < items && !dead; item += gridDim.x) {
+            const int a = item / p.slabs, first = r.first[a], n_rows = r.first[a + 1] - first;
+            const int chunks = (n_rows + 7) / 8 * 8 * (DEPTH / 8);  // 16-byte chunks of the rows, a line of 16 a row
+            for (int step = 0; step < steps; ++step) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, &abort_flag))) {
+                    gave_up(kDevTimeoutProducer);
+                    dead = true;
+                    break;
+                }
+                if (early > 0) --early;
+                else weights(item, step, stage);
+                __syncwarp();
+                const int c = lane % (DEPTH / 8), kk = step * DEPTH + c * 8;
+                const int n = max(0, min(8, (UP ? K : p.Fp) - kk));  // of this lane's chunk in every row
+                const uint32_t at = ring_x + stage * x_bytes + c * 16;
+#pragma unroll 4
+                for (int q = lane; q < chunks; q += 32) {
+                    const int row = q / (DEPTH / 8), pick = row < n_rows ? r.pick[first + row] : 0;
+                    const bool in = row < n_rows && n > 0 && in_range(pick, p.T * p.k);
                     const uint16_t* src = UP ? p.x + (int64_t)(pick / p.k) * p.ldx + kk : p.h + (int64_t)pick * p.Fp + kk;
-                    copy_16(at + W_BYTES + row * 128 + ((c ^ (row & 7)) * 16), n > 0 ? src : p.w, 2 * n);
+                    copy_async_16(at + row * ROW_BYTES, in ? src : (UP ? p.x : p.h), in ? 2 * n : 0);
                 }
+                copy_async_arrive(smem_u32(&full_bar[stage]));
+                if (++stage == p.stages) stage = 0, phase ^= 1;
             }
         }
-    };
-    const auto advance = [&](int& item, int& step, int& stage) {
-        if (++step == steps) step = 0, item += gridDim.x;
-        if (++stage == p.stages) stage = 0;
-    };
-    if (!UP) {
-        // weights ahead of the first kernel's end, then the rows of these stages
-        const int item0 = l_item, step0 = l_step;
-        for (int s = 0; s < p.stages - 1; ++s) {
-            load(true, false);
-            advance(l_item, l_step, l_stage);
-        }
-        grid_dependency_wait();
-        grid_dependents_launch();
-        l_item = item0, l_step = step0, l_stage = 0;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+    // -------------------------------------------------------------------- products
+    if (!UP) grid_dependency_wait();  // (the limit of the waits below starts when the first kernel has ended)
+    if (p.test_stall) {
+        (void)mbar_wait(smem_u32(&never_bar), 0, p.limit_ns);
+        gave_up(kDevTimeoutEpilogue);
+        dead = true;
     }
-    for (int s = 0; s < p.stages - 1; ++s) {
-        load(UP, true);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        advance(l_item, l_step, l_stage);
-    }
-
     const int fg = warp % 4, kh = warp / 4;  // 16 columns, half of a stage's depth
     int stage = 0;
+    uint32_t phase = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int a = item / p.slabs, slab = item - a * p.slabs;
         const int first = r.first[a], n_rows = r.first[a + 1] - first, tiles = (n_rows + 7) / 8;
@@ -336,36 +365,37 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(LayerParams p)
         for (int t = 0; t < MAX_TILES; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
-        for (int step = 0; step < steps; ++step) {
-            // (p.stages - 2 groups may be under way; the count is a constant of the instruction)
-            switch (p.stages) {
-            case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-            case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-            case 5: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-            default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        for (int step = 0; step < steps && !dead; ++step) {
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, &abort_flag))) {
+                gave_up(kDevTimeoutMma);
+                dead = true;
+                break;
             }
-            __syncthreads();
-            load(true, true);  // into the stage that was multiplied before the barrier
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            advance(l_item, l_step, l_stage);
-            const uint32_t at = smem_u32(ring + stage * stage_bytes);
-            uint32_t wf[2][4];
+            const uint32_t at_w = ring_w + stage * W_BYTES, at_x = ring_x + stage * x_bytes;
+            uint32_t wf[4][4];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < 4; ++s) {
                 // matrices (k 0..7, f 0..7), (k 0..7, f 8..15), (k 8..15, f 0..7), (k 8..15, f 8..15)
-                const int kr = kh * 32 + s * 16 + (lane / 16) * 8 + lane % 8, c = fg * 2 + lane / 8 % 2;
-                ldsm_x4_trans(at + kr * 128 + ((c ^ (kr & 7)) * 16), wf[s]);
+                const int kr = kh * (DEPTH / 2) + s * 16 + lane / 16 * 8 + lane % 8, c = lane / 8 % 2;
+                if (GATED)
+                    ldsm_x4_trans(at_w + fg / 2 * (W_BYTES / 2) + kr * 64 + (((fg % 2 * 2 + c) ^ (kr / 2 & 3)) * 16), wf[s]);
+                else
+                    ldsm_x4_trans(at_w + kr * 128 + (((fg * 2 + c) ^ (kr & 7)) * 16), wf[s]);
             }
 #pragma unroll
             for (int t = 0; t < MAX_TILES; ++t) {
                 if (t >= tiles) break;
-                uint32_t xf[4];  // rows 8 t .. 8 t + 7, four chunks of 8 of k
-                const int row = t * 8 + lane % 8, c = kh * 4 + lane / 8;
-                ldsm_x4(at + W_BYTES + row * 128 + ((c ^ (row & 7)) * 16), xf);
-                mma_16816<BF16>(acc[t], wf[0], xf[0], xf[1]);
-                mma_16816<BF16>(acc[t], wf[1], xf[2], xf[3]);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    uint32_t xf[4];  // rows 8 t .. 8 t + 7, four chunks of 8 of k
+                    ldsm_x4(at_x + (t * 8 + lane % 8) * ROW_BYTES + (kh * 8 + s * 4 + lane / 8) * 16, xf);
+                    mma_16816<BF16>(acc[t], wf[2 * s], xf[0], xf[1]);
+                    mma_16816<BF16>(acc[t], wf[2 * s + 1], xf[2], xf[3]);
+                }
             }
-            if (++stage == p.stages) stage = 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty_bar[stage]));
+            if (++stage == p.stages) stage = 0, phase ^= 1;
         }
         // the two halves of the depth, [row][column]
         const int f = fg * 16 + lane / 4, row = lane % 4 * 2;
@@ -376,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(LayerParams p)
                     float* s = sums + (t * 8 + row) * PAD + f;
                     s[0] = acc[t][0], s[PAD] = acc[t][1], s[8] = acc[t][2], s[PAD + 8] = acc[t][3];
                 }
-        __syncthreads();
+        named_barrier(1, 32 * MMA_WARPS);
         if (kh == 0)
 #pragma unroll
             for (int t = 0; t < MAX_TILES; ++t)
@@ -384,8 +414,8 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(LayerParams p)
                     float* s = sums + (t * 8 + row) * PAD + f;
                     s[0] += acc[t][0], s[PAD] += acc[t][1], s[8] += acc[t][2], s[PAD + 8] += acc[t][3];
                 }
-        __syncthreads();
-        for (int q = threadIdx.x; q < n_rows * (COLS / 8); q += THREADS) {
+        named_barrier(1, 32 * MMA_WARPS);
+        for (int q = threadIdx.x; q < n_rows * (COLS / 8) && !dead; q += 32 * MMA_WARPS) {
             const int i = q / (COLS / 8), c0 = q % (COLS / 8) * 8, pick = r.pick[first + i], col = slab * COLS + c0;
             if (!in_range(pick, p.T * p.k)) continue;
             const float* s = sums + i * PAD + c0;
@@ -408,7 +438,10 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(LayerParams p)
                 } else {
                     activate(v, p.act);
                 }
-                // (columns past F are zero: zero weights, no bias, act(0) = 0)
+                // (columns past F are zero, whatever W holds there: the gate's next ones are the up half's)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (col + c >= p.F) v[c] = 0.f;
                 uint32_t w[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -423,37 +456,53 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(LayerParams p)
         }
         if constexpr (!UP) {
             __threadfence();
-            __syncthreads();
+            named_barrier(1, 32 * MMA_WARPS);
             if (threadIdx.x == 0) {
                 const int last = atomicAdd(p.counters + slab, 1u) == (unsigned)(n_act - 1);
                 if (last) p.counters[slab] = 0;  // ready for the next launch
                 __threadfence();
                 is_last = last;
             }
-            __syncthreads();
-            if (is_last) {
+            named_barrier(1, 32 * MMA_WARPS);
+            if (is_last && !dead) {
                 __threadfence();
                 combine<BF16>(p, r, slab);
             }
         }
     }
     if constexpr (!UP) {
-        if (n_act == 0)  // no token goes anywhere
+        if (n_act == 0 && !dead)  // no token goes anywhere
             for (int slab = blockIdx.x; slab < p.slabs; slab += gridDim.x) combine<BF16>(p, r, slab);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    if (__syncthreads_or(dead ? 1 : 0)) grace_period(2000000ull);  // (copies under way land before the exit)
+}
+
+// One matrix an expert, [E][K][N] with N contiguous: boxes of DEPTH rows of `box` columns.
+bool encode_experts(CUtensorMap* map, const void* w, bool bf16, int64_t N, int64_t K, int64_t E, int64_t ld, int64_t stride,
+                    int box)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)K, (cuuint64_t)E};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(E > 1 ? stride : K * ld) * 2};
+    const cuuint32_t boxes[3] = {(cuuint32_t)box, DEPTH, 1}, estr[3] = {1, 1, 1};
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(w), dims,
+               strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box == SLAB ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool UP, bool GATED, bool BF16>
-cudaError_t launch_typed(const LayerParams& p, int grid, int smem, cudaStream_t s)
+cudaError_t launch_typed(const CUtensorMap& map, const LayerParams& p, int grid, int smem, cudaStream_t s)
 {
     auto kern = layer_kernel<UP, GATED, BF16>;
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(kern, 112 * 1024, allowed);
-    return e != cudaSuccess ? e : launch_dependent(kern, dim3(grid), dim3(THREADS), smem, s, p);
+    const cudaError_t e = allow_smem(kern, SMEM_ONE, allowed);
+    return e != cudaSuccess ? e : launch_dependent(kern, dim3(grid), dim3(THREADS), smem, s, map, p);
 }
 
-int padded(int n) { return (n + DEPTH - 1) / DEPTH * DEPTH; }
+int padded(int n) { return (n + SLAB - 1) / SLAB * SLAB; }
 
 }  // namespace
 
@@ -462,7 +511,8 @@ size_t moe_layer_ws_bytes(const LayerArgs& a)
     return (size_t)a.T * a.k * (padded(a.F) * sizeof(uint16_t) + padded(a.D) * sizeof(float));
 }
 
-int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_sms, cudaStream_t s, int* launches)
+int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_sms, int* dev_status, uint64_t limit_ns,
+                     int test_stall, cudaStream_t s, int* launches)
 {
     LayerParams p = {};
     p.T = a.T, p.E = a.E, p.k = a.k, p.D = a.D, p.F = a.F, p.Fw = a.Fw;
@@ -472,37 +522,42 @@ int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_s
     p.out = a.out, p.ldo = a.ldo;
     p.act = a.act, p.out_f32 = a.out_f32 ? 1 : 0;
     p.Fp = padded(a.F), p.Dp = padded(a.D);
+    p.status = dev_status, p.limit_ns = limit_ns, p.test_stall = test_stall;
     const int picks = a.T * a.k;
     p.y = static_cast<float*>(ws);
     p.h = reinterpret_cast<uint16_t*>(p.y + (size_t)picks * p.Dp);
     p.counters = counters;
     p.rows_cap = (a.T + 7) / 8 * 8;
-    // two CTAs an SM; the router's keys lie in the ring
-    const int stage = W_BYTES + p.rows_cap * ROW_BYTES, fixed = p.rows_cap * PAD * 4 + routes_bytes(picks, a.E);
-    p.stages = (108 * 1024 - fixed) / stage;
-    if (p.stages > 6) p.stages = 6;
-    if (p.stages < 3 || p.stages * stage < WARPS * a.E * 4) return GEMM_ERR_UNSUPPORTED;
+    // two CTAs an SM where each has three stages or more, else one
+    const int stage = W_BYTES + p.rows_cap * ROW_BYTES, fixed = 1024 + p.rows_cap * PAD * 4 + routes_bytes(picks, a.E);
+    int per_sm = 2;
+    p.stages = (SMEM_TWO - fixed) / stage;
+    if (p.stages < 3) per_sm = 1, p.stages = (SMEM_ONE - fixed) / stage;
+    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+    if (p.stages < 2 || p.stages * stage < WARPS * a.E * 4) return GEMM_ERR_UNSUPPORTED;  // (the router's keys lie in the ring)
     const int smem = p.stages * stage + fixed;
     const bool gated = a.act == GEMM_ACT_SWIGLU;
     const int most = a.E < picks ? a.E : picks;  // experts that can be active
     const auto grid = [&](int slabs) {
-        const int64_t items = (int64_t)most * slabs, fit = 2 * num_sms;
+        const int64_t items = (int64_t)most * slabs, fit = per_sm * num_sms;
         return (int)(items < fit ? items : fit);
     };
-    p.w = static_cast<const uint16_t*>(a.w1), p.ldw = a.ldw1, p.w_stride = a.w1_stride;
+    CUtensorMap up, down;
+    if (!encode_experts(&up, a.w1, a.bf16, a.Fw, a.D, a.E, a.ldw1, a.w1_stride, gated ? SLAB / 2 : SLAB) ||
+        !encode_experts(&down, a.w2, a.bf16, a.D, a.F, a.E, a.ldw2, a.w2_stride, SLAB))
+        return GEMM_ERR_CUDA;
     p.bias = static_cast<const uint16_t*>(a.b1);
     p.slabs = p.Fp / (gated ? SLAB / 2 : SLAB);
-    cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true, true>(p, grid(p.slabs), smem, s)
-                                    : launch_typed<true, false, true>(p, grid(p.slabs), smem, s))
-                           : (gated ? launch_typed<true, true, false>(p, grid(p.slabs), smem, s)
-                                    : launch_typed<true, false, false>(p, grid(p.slabs), smem, s));
+    cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true, true>(up, p, grid(p.slabs), smem, s)
+                                    : launch_typed<true, false, true>(up, p, grid(p.slabs), smem, s))
+                           : (gated ? launch_typed<true, true, false>(up, p, grid(p.slabs), smem, s)
+                                    : launch_typed<true, false, false>(up, p, grid(p.slabs), smem, s));
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
-    p.w = static_cast<const uint16_t*>(a.w2), p.ldw = a.ldw2, p.w_stride = a.w2_stride;
     p.bias = static_cast<const uint16_t*>(a.b2);
     p.slabs = p.Dp / SLAB;
-    e = a.bf16 ? launch_typed<false, false, true>(p, grid(p.slabs), smem, s)
-               : launch_typed<false, false, false>(p, grid(p.slabs), smem, s);
+    e = a.bf16 ? launch_typed<false, false, true>(down, p, grid(p.slabs), smem, s)
+               : launch_typed<false, false, false>(down, p, grid(p.slabs), smem, s);
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
     return GEMM_OK;

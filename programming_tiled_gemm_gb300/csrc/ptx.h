@@ -476,6 +476,27 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// 3-D tiled load global -> shared; completes on `bar`.  Out-of-range elements read zeros.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// 16 bytes global -> shared past L1, of which the first `bytes` are read and the others zero.
+__device__ __forceinline__ void copy_async_16(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Arrive on `bar` (one of its expected arrivals) once this thread's copy_async_16 so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Arrive on a barrier of this cluster (cluster address) without ordering earlier global
 // stores before it, as the cluster-scope form does by waiting for them: for arrivals that
 // hand over tensor memory already read (tcgen05.wait::ld), not data in memory.

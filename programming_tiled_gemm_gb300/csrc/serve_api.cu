@@ -56,7 +56,8 @@ int layer_impl(gemm_handle_t h, const moe_layer_args* a, void* stream)
     int rc = grow_buffer(h, &h->layer, &h->layer_bytes, moe_layer_ws_bytes(l), s);
     if (rc != GEMM_OK) return rc;
     int n = 0;
-    rc = launch_moe_layer(l, h->layer, h->lin_counters + linear_counters(h->num_sms) + 1, h->num_sms, s, &n);
+    rc = launch_moe_layer(l, h->layer, h->lin_counters + linear_counters(h->num_sms) + 1, h->num_sms, h->d_status,
+                          h->wait_limit_ns, h->opt_test_stall, s, &n);
     h->launches += n;
     return rc;
 }

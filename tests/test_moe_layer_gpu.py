@@ -344,3 +344,20 @@ def test_refusals(lib, g):
                dict(F=28, ldw1=64), dict(logits=l.data_ptr() + 2), dict(b1=x.data_ptr() + 1), dict(Y=x.data_ptr() + 1)):
         assert call(**kw) == g.GEMM_ERR_ALIGNMENT, kw
     assert lib.launch_count() == n
+
+
+def test_a_wait_that_runs_out_is_reported(g):
+    lib = g.Gemm(0)
+    s = make(4, 6, 8, 256, 128, BF16)
+    want = lib.moe_layer(s["x"], s["logits"], s["w1"], s["w2"], 2)
+    lib.set_option(g.GEMM_OPT_WAIT_LIMIT_US, 20000)
+    lib.set_option(g.GEMM_OPT_TEST_STALL, 1)
+    out = torch.full_like(want, 3.0)
+    lib.moe_layer(s["x"], s["logits"], s["w1"], s["w2"], 2, out=out)
+    assert lib.device_status() == g.GEMM_ERR_DEVICE_TIMEOUT
+    assert bool((out == 3).all())
+    lib.set_option(g.GEMM_OPT_TEST_STALL, 0)
+    for _ in range(2):  # (and the counters are zero again)
+        assert torch.equal(lib.moe_layer(s["x"], s["logits"], s["w1"], s["w2"], 2), want)
+    assert lib.device_status() == g.GEMM_OK
+    lib.close()
