@@ -37,10 +37,11 @@ constexpr int SLAB = kLayerSlab;  // columns of W an item
 constexpr int DEPTH = 128;        // of the reduced dimension a stage
 constexpr int W_BYTES = DEPTH * SLAB * 2;
 constexpr int ROW_BYTES = DEPTH * 2 + 16;  // of X or H a stage: rows 16 bytes apart in the banks
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 8;  // (an even number of them: each belongs to one half of the warps, which sees its every phase)
 constexpr int SMEM_TWO = 112 * 1024, SMEM_ONE = 224 * 1024;  // of a CTA, two or one an SM
 constexpr int PAD = SLAB + 4;         // floats of a row of sums
-constexpr int MAX_TILES = kLayerTokens / 8;
+constexpr int MAX_ROWS = 32;           // of an item: an expert with more has several
+constexpr int MAX_TILES = MAX_ROWS / 8;
 constexpr uint16_t NONE = 0xffff;
 
 struct LayerParams {
@@ -61,7 +62,7 @@ struct LayerParams {
     float* y;  // [T k][Dp]
     int Dp;
     unsigned* counters;
-    int slabs, stages, rows_cap;  // rows_cap: rows of a stage, T to a multiple of 8
+    int slabs, stages, rows_cap;  // rows_cap: rows of a stage, T to a multiple of 8, or MAX_ROWS
     int* status;
     uint64_t limit_ns;
     int test_stall;
@@ -98,20 +99,21 @@ struct Routes {
     uint16_t* expert;   // [T k], NONE: no pick
     uint16_t* pick;     // [T k]: the picks by expert, each expert's in order
     int* count;         // [E]
-    uint16_t* active;   // [E]: experts with picks
-    int* first;         // [E + 1]: their first pick in `pick`
+    uint16_t* active;   // [most_groups]: experts with picks, once for each MAX_ROWS of them
+    int* first;         // [most_groups + 1]: the groups' first pick in `pick`
     int* n_active;
 };
+__host__ __device__ inline int most_groups(int picks, int E) { return (E < picks ? E : picks) + picks / MAX_ROWS; }
 __host__ __device__ inline int routes_bytes(int picks, int E)
 {
-    return 16 + 4 * (E + 1) + 4 * E + 4 * picks + 2 * picks * 2 + 2 * E + 16;
+    return 16 + 4 * (most_groups(picks, E) + 1) + 4 * E + 4 * picks + 2 * picks * 2 + 2 * most_groups(picks, E) + 16;
 }
 __device__ __forceinline__ Routes carve(uint8_t* at, int picks, int E)
 {
     Routes r;
     r.n_active = reinterpret_cast<int*>(at);
     r.first = r.n_active + 4;
-    r.count = r.first + E + 1;
+    r.count = r.first + most_groups(picks, E) + 1;
     r.weight = reinterpret_cast<float*>(r.count + E);
     r.expert = reinterpret_cast<uint16_t*>(r.weight + picks);
     r.pick = r.expert + picks;
@@ -176,21 +178,21 @@ __device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uin
     if (warp == 0) {
         int n = 0, sum = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane, c = e < E ? r.count[e] : 0;
-            const unsigned on = __ballot_sync(0xffffffffu, c > 0);
-            int before = c;
+            const int e = e0 + lane, c = e < E ? r.count[e] : 0, groups = (c + MAX_ROWS - 1) / MAX_ROWS;
+            int before = c << 16 | groups;  // both running sums at once (below 2^15 each)
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
                 const int o = __shfl_up_sync(0xffffffffu, before, d);
                 if (lane >= d) before += o;
             }
-            if (c > 0) {
-                const int a = n + __popc(on & ((1u << lane) - 1));
+            for (int i = 0; i < groups; ++i) {
+                const int a = n + (before & 0xffff) - groups + i;
                 r.active[a] = (uint16_t)e;
-                r.first[a] = sum + before - c;
+                r.first[a] = sum + (before >> 16) - c + i * MAX_ROWS;
             }
-            n += __popc(on);
-            sum += __shfl_sync(0xffffffffu, before, 31);
+            const int all = __shfl_sync(0xffffffffu, before, 31);
+            n += all & 0xffff;
+            sum += all >> 16;
         }
         if (lane == 0) *r.n_active = n, r.first[n] = sum;
     }
@@ -198,6 +200,7 @@ __device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uin
     const int n = *r.n_active;
     for (int a = warp; a < n; a += WARPS) {
         const int e = r.active[a];
+        if (a > 0 && r.active[a - 1] == e) continue;  // (written with the expert's first group)
         int at = r.first[a];
         for (int i0 = 0; i0 < picks; i0 += 32) {
             const bool is = i0 + lane < picks && r.expert[i0 + lane] == e;
@@ -248,6 +251,35 @@ __device__ __forceinline__ void combine(const LayerParams& p, const Routes& r, i
     }
 }
 
+// A stage's products for 16 columns and N tiles of 8 rows.
+template <bool GATED, bool BF16, int N>
+__device__ __forceinline__ void products(float (&acc)[MAX_TILES][2][4], uint32_t at_w, uint32_t at_x, int fg, int lane)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t wf[4][4], xf[N][2][4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            // matrices (k 0..7, f 0..7), (k 0..7, f 8..15), (k 8..15, f 0..7), (k 8..15, f 8..15)
+            const int kr = h * (DEPTH / 2) + s * 16 + lane / 16 * 8 + lane % 8, c = lane / 8 % 2;
+            if (GATED)
+                ldsm_x4_trans(at_w + fg / 2 * (W_BYTES / 2) + kr * 64 + (((fg % 2 * 2 + c) ^ (kr / 2 & 3)) * 16), wf[s]);
+            else
+                ldsm_x4_trans(at_w + kr * 128 + (((fg * 2 + c) ^ (kr & 7)) * 16), wf[s]);
+        }
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)  // rows 8 t .. 8 t + 7, four chunks of 8 of k
+                ldsm_x4(at_x + (t * 8 + lane % 8) * ROW_BYTES + (h * 8 + s * 4 + lane / 8) * 16, xf[t][s]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+                mma_16816<BF16>(acc[t][s & 1], wf[s], xf[t][s / 2][s % 2 * 2], xf[t][s / 2][s % 2 * 2 + 1]);
+    }
+}
+
 // UP: H = act(X W1 + b1), else Y = H W2 and the tokens' sums.  Stage: [128 of the reduced
 // dimension][64 columns] of W, swizzled by the TMA (128-byte rows; GATED, UP only: 32 columns of the gate,
 // then 32 of the up half, each in 64-byte rows), and [row][128] of X or H.
@@ -268,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(smem_u32(&full_bar[i]), 1 + 32);  // the weights' bytes, and each loading lane's copies
-            mbar_init(smem_u32(&empty_bar[i]), MMA_WARPS);
+            mbar_init(smem_u32(&empty_bar[i]), MMA_WARPS / 2);
         }
         mbar_init(smem_u32(&never_bar), 1);
         abort_flag = 0;
@@ -354,57 +386,49 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
         gave_up(kDevTimeoutEpilogue);
         dead = true;
     }
-    const int fg = warp % 4, kh = warp / 4;  // 16 columns, half of a stage's depth
+    // a warp has 16 columns of every second stage: its latencies are another stage's time
+    const int fg = warp % 4, kh = warp / 4;
     int stage = 0;
     uint32_t phase = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int a = item / p.slabs, slab = item - a * p.slabs;
         const int first = r.first[a], n_rows = r.first[a + 1] - first, tiles = (n_rows + 7) / 8;
-        float acc[MAX_TILES][4];
+        float acc[MAX_TILES][2][4];  // even and odd steps of 16: an MMA takes 60 cycles to the next of its sum
 #pragma unroll
         for (int t = 0; t < MAX_TILES; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+            for (int i = 0; i < 8; ++i) acc[t][i / 4][i % 4] = 0.f;
         for (int step = 0; step < steps && !dead; ++step) {
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, &abort_flag))) {
-                gave_up(kDevTimeoutMma);
-                dead = true;
-                break;
-            }
-            const uint32_t at_w = ring_w + stage * W_BYTES, at_x = ring_x + stage * x_bytes;
-            uint32_t wf[4][4];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                // matrices (k 0..7, f 0..7), (k 0..7, f 8..15), (k 8..15, f 0..7), (k 8..15, f 8..15)
-                const int kr = kh * (DEPTH / 2) + s * 16 + lane / 16 * 8 + lane % 8, c = lane / 8 % 2;
-                if (GATED)
-                    ldsm_x4_trans(at_w + fg / 2 * (W_BYTES / 2) + kr * 64 + (((fg % 2 * 2 + c) ^ (kr / 2 & 3)) * 16), wf[s]);
-                else
-                    ldsm_x4_trans(at_w + kr * 128 + (((fg * 2 + c) ^ (kr & 7)) * 16), wf[s]);
-            }
-#pragma unroll
-            for (int t = 0; t < MAX_TILES; ++t) {
-                if (t >= tiles) break;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    uint32_t xf[4];  // rows 8 t .. 8 t + 7, four chunks of 8 of k
-                    ldsm_x4(at_x + (t * 8 + lane % 8) * ROW_BYTES + (kh * 8 + s * 4 + lane / 8) * 16, xf);
-                    mma_16816<BF16>(acc[t], wf[2 * s], xf[0], xf[1]);
-                    mma_16816<BF16>(acc[t], wf[2 * s + 1], xf[2], xf[3]);
+            if ((stage & 1) == kh) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, &abort_flag))) {
+                    gave_up(kDevTimeoutMma);
+                    dead = true;
+                    break;
                 }
+                const uint32_t at_w = ring_w + stage * W_BYTES, at_x = ring_x + stage * x_bytes;
+                switch (tiles) {
+                case 1: products<GATED, BF16, 1>(acc, at_w, at_x, fg, lane); break;
+                case 2: products<GATED, BF16, 2>(acc, at_w, at_x, fg, lane); break;
+                case 3: products<GATED, BF16, 3>(acc, at_w, at_x, fg, lane); break;
+                default: products<GATED, BF16, 4>(acc, at_w, at_x, fg, lane); break;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&empty_bar[stage]));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&empty_bar[stage]));
             if (++stage == p.stages) stage = 0, phase ^= 1;
         }
-        // the two halves of the depth, [row][column]
+#pragma unroll
+        for (int t = 0; t < MAX_TILES; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][0][i] += acc[t][1][i];
+        // the even and the odd stages, [row][column]
         const int f = fg * 16 + lane / 4, row = lane % 4 * 2;
         if (kh == 1)
 #pragma unroll
             for (int t = 0; t < MAX_TILES; ++t)
                 if (t < tiles) {
                     float* s = sums + (t * 8 + row) * PAD + f;
-                    s[0] = acc[t][0], s[PAD] = acc[t][1], s[8] = acc[t][2], s[PAD + 8] = acc[t][3];
+                    s[0] = acc[t][0][0], s[PAD] = acc[t][0][1], s[8] = acc[t][0][2], s[PAD + 8] = acc[t][0][3];
                 }
         named_barrier(1, 32 * MMA_WARPS);
         if (kh == 0)
@@ -412,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
             for (int t = 0; t < MAX_TILES; ++t)
                 if (t < tiles) {
                     float* s = sums + (t * 8 + row) * PAD + f;
-                    s[0] += acc[t][0], s[PAD] += acc[t][1], s[8] += acc[t][2], s[PAD + 8] += acc[t][3];
+                    s[0] += acc[t][0][0], s[PAD] += acc[t][0][1], s[8] += acc[t][0][2], s[PAD + 8] += acc[t][0][3];
                 }
         named_barrier(1, 32 * MMA_WARPS);
         for (int q = threadIdx.x; q < n_rows * (COLS / 8) && !dead; q += 32 * MMA_WARPS) {
@@ -454,7 +478,9 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
                 __stcg(o + 1, make_float4(v[4], v[5], v[6], v[7]));
             }
         }
-        if constexpr (!UP) {
+        if constexpr (UP) {
+            named_barrier(1, 32 * MMA_WARPS);  // (the sums are read before the next item's are written)
+        } else {
             __threadfence();
             named_barrier(1, 32 * MMA_WARPS);
             if (threadIdx.x == 0) {
@@ -527,17 +553,17 @@ int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_s
     p.y = static_cast<float*>(ws);
     p.h = reinterpret_cast<uint16_t*>(p.y + (size_t)picks * p.Dp);
     p.counters = counters;
-    p.rows_cap = (a.T + 7) / 8 * 8;
-    // two CTAs an SM where each has three stages or more, else one
+    p.rows_cap = a.T < MAX_ROWS ? (a.T + 7) / 8 * 8 : MAX_ROWS;
+    // two CTAs an SM where each has four stages or more, else one
     const int stage = W_BYTES + p.rows_cap * ROW_BYTES, fixed = 1024 + p.rows_cap * PAD * 4 + routes_bytes(picks, a.E);
     int per_sm = 2;
     p.stages = (SMEM_TWO - fixed) / stage;
-    if (p.stages < 3) per_sm = 1, p.stages = (SMEM_ONE - fixed) / stage;
-    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+    if (p.stages < 4) per_sm = 1, p.stages = (SMEM_ONE - fixed) / stage;
+    p.stages = p.stages > MAX_STAGES ? MAX_STAGES : p.stages / 2 * 2;
     if (p.stages < 2 || p.stages * stage < WARPS * a.E * 4) return GEMM_ERR_UNSUPPORTED;  // (the router's keys lie in the ring)
     const int smem = p.stages * stage + fixed;
     const bool gated = a.act == GEMM_ACT_SWIGLU;
-    const int most = a.E < picks ? a.E : picks;  // experts that can be active
+    const int most = most_groups(picks, a.E);
     const auto grid = [&](int slabs) {
         const int64_t items = (int64_t)most * slabs, fit = per_sm * num_sms;
         return (int)(items < fit ? items : fit);
