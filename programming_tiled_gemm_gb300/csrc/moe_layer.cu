@@ -98,7 +98,8 @@ struct Routes {
     float* weight;      // [T k]
     uint16_t* expert;   // [T k], NONE: no pick
     uint16_t* pick;     // [T k]: the picks by expert, each expert's in order
-    int* count;         // [E]
+    unsigned* tokens;   // [E][2]: a bit a token that picked it
+    int* base;          // [E]: its first pick in `pick`
     uint16_t* active;   // [most_groups]: experts with picks, once for each MAX_ROWS of them
     int* first;         // [most_groups + 1]: the groups' first pick in `pick`
     int* n_active;
@@ -106,15 +107,16 @@ struct Routes {
 __host__ __device__ inline int most_groups(int picks, int E) { return (E < picks ? E : picks) + picks / MAX_ROWS; }
 __host__ __device__ inline int routes_bytes(int picks, int E)
 {
-    return 16 + 4 * (most_groups(picks, E) + 1) + 4 * E + 4 * picks + 2 * picks * 2 + 2 * most_groups(picks, E) + 16;
+    return 16 + 4 * (most_groups(picks, E) + 1) + 12 * E + 4 * picks + 2 * picks * 2 + 2 * most_groups(picks, E) + 16;
 }
 __device__ __forceinline__ Routes carve(uint8_t* at, int picks, int E)
 {
     Routes r;
     r.n_active = reinterpret_cast<int*>(at);
     r.first = r.n_active + 4;
-    r.count = r.first + most_groups(picks, E) + 1;
-    r.weight = reinterpret_cast<float*>(r.count + E);
+    r.base = r.first + most_groups(picks, E) + 1;
+    r.tokens = reinterpret_cast<unsigned*>(r.base + E);
+    r.weight = reinterpret_cast<float*>(r.tokens + 2 * E);
     r.expert = reinterpret_cast<uint16_t*>(r.weight + picks);
     r.pick = r.expert + picks;
     r.active = r.pick + picks;
@@ -130,84 +132,152 @@ __device__ __forceinline__ float logit(const LayerParams& p, int t, int e)
     return p.logits_dtype == GEMM_BF16 ? from_16<true>(v) : from_16<false>(v);
 }
 
-// The picks of all tokens as moe_route makes them.  `scratch`: WARPS * E words.
-__device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uint32_t* scratch)
+// One pick: the largest key over the warp, the lowest expert that has it (-1: none is left).
+__device__ __forceinline__ int pick_of(uint32_t best, int at, uint32_t& key)
 {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = p.E, k = p.k, picks = p.T * k;
-    for (int e = threadIdx.x; e < E; e += THREADS) r.count[e] = 0;
-    uint32_t* key = scratch + warp * E;
-    for (int t = warp; t < p.T; t += WARPS) {
-        for (int e = lane; e < E; e += 32) key[e] = order_key(logit(p, t, e));
-        __syncwarp();
-        int pick = -1;
-        float val = 0.f, top = 0.f, all = 0.f;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = 0;
-            int at = 0;
-            for (int e = lane; e < E; e += 32)
-                if (key[e] > best) best = key[e], at = e;
-            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-            if (m == 0) break;  // no expert is left
-            const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (unsigned)at : 0xffffffffu);
-            const float v = key_value(m);
-            if (j == 0) {
-                top = v;
-                if (!p.renorm)
-                    for (int i = lane; i < E; i += 32)
-                        if (key[i] != 0) all += expf(key_value(key[i]) - top);
-            }
-            __syncwarp();
-            if (best == m && at == e) key[e] = 0;
-            if (lane == j) pick = e, val = v;
-            __syncwarp();
-        }
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    key = m;
+    if (m == 0) return -1;
+    const unsigned who = __ballot_sync(0xffffffffu, best == m);
+    if (who & (who - 1)) return (int)__reduce_min_sync(0xffffffffu, best == m ? (unsigned)at : 0xffffffffu);
+    return __shfl_sync(0xffffffffu, at, __ffs(who) - 1);
+}
+
+// What a token's picks leave: its experts, the experts' tokens and, where they are wanted, the weights
+// (`all`: a lane's part of the sum over all experts).
+template <bool WEIGHTS>
+__device__ __forceinline__ void record(const LayerParams& p, const Routes& r, int t, int pick, float val, float top, float all)
+{
+    const int lane = threadIdx.x % 32, k = p.k;
+    if (lane < k) {
+        r.expert[t * k + lane] = pick >= 0 ? (uint16_t)pick : NONE;
+        if (pick >= 0) atomicOr(&r.tokens[2 * pick + t / 32], 1u << (t % 32));
+    }
+    if (WEIGHTS) {
         const float ex = pick >= 0 ? expf(val - top) : 0.f;
         float sum = p.renorm ? ex : all;
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane < k) {
-            r.expert[t * k + lane] = pick >= 0 ? (uint16_t)pick : NONE;
-            r.weight[t * k + lane] = pick >= 0 ? ex / sum : 0.f;
-        }
-        __syncwarp();
+        if (lane < k) r.weight[t * k + lane] = pick >= 0 ? ex / sum : 0.f;
     }
+}
+
+// The picks of all tokens as moe_route makes them, a warp a token.  Up to 256 experts a lane keeps its keys
+// in registers; more lie in `scratch` (WARPS * E words).
+template <bool WEIGHTS>
+__device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uint32_t* scratch)
+{
+    constexpr int REG = 8;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, E = p.E, k = p.k, picks = p.T * k;
+    for (int e = threadIdx.x; e < 2 * E; e += THREADS) r.tokens[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < picks; i += THREADS)
-        if (r.expert[i] != NONE) atomicAdd(&r.count[r.expert[i]], 1);
+    if (E <= 32 * REG) {
+        float next[REG];
+        const auto fetch = [&](int t) {
+#pragma unroll
+            for (int c = 0; c < REG; ++c) {
+                if (32 * c >= E) break;
+                next[c] = 32 * c + lane < E ? logit(p, t, 32 * c + lane) : -INFINITY;
+            }
+        };
+        if (warp < p.T) fetch(warp);
+        for (int t = warp; t < p.T; t += WARPS) {
+            uint32_t key[REG] = {};
+            float l[REG];
+#pragma unroll
+            for (int c = 0; c < REG; ++c) {
+                if (32 * c >= E) break;
+                l[c] = next[c];
+                key[c] = order_key(l[c]);
+            }
+            if (t + WARPS < p.T) fetch(t + WARPS);
+            int pick = -1;
+            float val = 0.f, top = 0.f, all = 0.f;
+            for (int j = 0; j < k; ++j) {
+                uint32_t best = key[0], m;
+                int at = lane;
+#pragma unroll
+                for (int c = 1; c < REG; ++c)
+                    if (key[c] > best) best = key[c], at = 32 * c + lane;
+                const int e = pick_of(best, at, m);
+                if (e < 0) break;
+#pragma unroll
+                for (int c = 0; c < REG; ++c)
+                    if (32 * c + lane == e) key[c] = 0;
+                if (j == 0) top = key_value(m);
+                if (lane == j) pick = e, val = key_value(m);
+            }
+            if (WEIGHTS && !p.renorm) {
+#pragma unroll
+                for (int c = 0; c < REG; ++c) {
+                    if (32 * c >= E) break;
+                    if (l[c] != -INFINITY) all += expf(l[c] - top);
+                }
+            }
+            record<WEIGHTS>(p, r, t, pick, val, top, all);
+        }
+    } else {
+        uint32_t* key = scratch + warp * E;
+        for (int t = warp; t < p.T; t += WARPS) {
+            for (int e = lane; e < E; e += 32) key[e] = order_key(logit(p, t, e));
+            __syncwarp();
+            int pick = -1;
+            float val = 0.f, top = 0.f, all = 0.f;
+            for (int j = 0; j < k; ++j) {
+                uint32_t best = 0, m;
+                int at = 0;
+                for (int e = lane; e < E; e += 32)
+                    if (key[e] > best) best = key[e], at = e;
+                const int e = pick_of(best, at, m);
+                if (e < 0) break;
+                if (j == 0) {
+                    top = key_value(m);
+                    if (WEIGHTS && !p.renorm)
+                        for (int i = lane; i < E; i += 32)
+                            if (key[i] != 0) all += expf(key_value(key[i]) - top);
+                }
+                __syncwarp();
+                if (e % 32 == lane) key[e] = 0;
+                if (lane == j) pick = e, val = key_value(m);
+                __syncwarp();
+            }
+            record<WEIGHTS>(p, r, t, pick, val, top, all);
+            __syncwarp();
+        }
+    }
     __syncthreads();
     if (warp == 0) {
-        int n = 0, sum = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane, c = e < E ? r.count[e] : 0, groups = (c + MAX_ROWS - 1) / MAX_ROWS;
-            int before = c << 16 | groups;  // both running sums at once (below 2^15 each)
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xffffffffu, before, d);
-                if (lane >= d) before += o;
-            }
-            for (int i = 0; i < groups; ++i) {
-                const int a = n + (before & 0xffff) - groups + i;
-                r.active[a] = (uint16_t)e;
-                r.first[a] = sum + (before >> 16) - c + i * MAX_ROWS;
-            }
-            const int all = __shfl_sync(0xffffffffu, before, 31);
-            n += all & 0xffff;
-            sum += all >> 16;
+        // the experts' first picks and groups: a lane has `each` neighbouring experts
+        const int each = (E + 31) / 32, e0 = min(lane * each, E), e1 = min(e0 + each, E);
+        const auto count = [&](int e) { return __popc(r.tokens[2 * e]) + __popc(r.tokens[2 * e + 1]); };
+        int own = 0;  // picks in the upper half, groups in the lower (both below 2^15)
+        for (int e = e0; e < e1; ++e) {
+            const int c = count(e);
+            own += c << 16 | (c + MAX_ROWS - 1) / MAX_ROWS;
         }
-        if (lane == 0) *r.n_active = n, r.first[n] = sum;
+        int before = own;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d) before += o;
+        }
+        if (lane == 31) *r.n_active = before & 0xffff, r.first[before & 0xffff] = before >> 16;
+        before -= own;
+        int a = before & 0xffff, at = before >> 16;
+        for (int e = e0; e < e1; ++e) {
+            const int c = count(e);
+            r.base[e] = at;
+            for (int i = 0; i < c; i += MAX_ROWS, ++a) r.active[a] = (uint16_t)e, r.first[a] = at + i;
+            at += c;
+        }
     }
     __syncthreads();
-    const int n = *r.n_active;
-    for (int a = warp; a < n; a += WARPS) {
-        const int e = r.active[a];
-        if (a > 0 && r.active[a - 1] == e) continue;  // (written with the expert's first group)
-        int at = r.first[a];
-        for (int i0 = 0; i0 < picks; i0 += 32) {
-            const bool is = i0 + lane < picks && r.expert[i0 + lane] == e;
-            const unsigned who = __ballot_sync(0xffffffffu, is);
-            if (is) r.pick[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(i0 + lane);
-            at += __popc(who);
-        }
+    // every pick's place: its token's rank among the expert's
+    for (int i = threadIdx.x; i < picks; i += THREADS) {
+        const int e = r.expert[i], t = i / k;
+        if (e == NONE) continue;
+        const unsigned lo = r.tokens[2 * e], hi = r.tokens[2 * e + 1], below = (1u << (t % 32)) - 1;
+        r.pick[r.base[e] + (t < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below))] = (uint16_t)i;
     }
     __syncthreads();
 }
@@ -219,7 +289,14 @@ __device__ __forceinline__ void combine(const LayerParams& p, const Routes& r, i
     for (int i = threadIdx.x; i < p.T * (SLAB / 8); i += 32 * MMA_WARPS) {
         const int t = i / (SLAB / 8), col = slab * SLAB + i % (SLAB / 8) * 8, n = min(8, p.D - col);
         if (n <= 0) continue;
-        float v[8] = {};
+        float v[8] = {}, res[8] = {};
+        if (p.R) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < n)
+                    res[c] = p.out_f32 ? static_cast<const float*>(p.R)[(int64_t)t * p.ldr + col + c]
+                                       : from_16<BF16>(static_cast<const uint16_t*>(p.R)[(int64_t)t * p.ldr + col + c]);
+        }
 #pragma unroll 4
         for (int j = 0; j < p.k; ++j) {
             const int q = t * p.k + j;
@@ -235,18 +312,19 @@ __device__ __forceinline__ void combine(const LayerParams& p, const Routes& r, i
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] += w * y[c];
         }
+        if (p.R)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] += res[c];
         if (p.out_f32) {
-            const float* R = p.R ? static_cast<const float*>(p.R) + (int64_t)t * p.ldr + col : nullptr;
             float* o = static_cast<float*>(p.out) + (int64_t)t * p.ldo + col;
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                if (c < n) o[c] = R ? v[c] + R[c] : v[c];
+                if (c < n) o[c] = v[c];
         } else {
-            const uint16_t* R = p.R ? static_cast<const uint16_t*>(p.R) + (int64_t)t * p.ldr + col : nullptr;
             uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)t * p.ldo + col;
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                if (c < n) o[c] = to_16<BF16>(R ? v[c] + from_16<BF16>(R[c]) : v[c]);
+                if (c < n) o[c] = to_16<BF16>(v[c]);
         }
     }
 }
@@ -313,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
     }
     // (the second kernel starts once every CTA of the first has got here: what came before that one,
     // the logits among it, is complete, and only H is not)
-    route(p, r, reinterpret_cast<uint32_t*>(smem));
+    route<!UP>(p, r, reinterpret_cast<uint32_t*>(smem));
     fence_proxy_async_shared();  // (the router's words lie where the TMA writes)
     __syncthreads();
 
@@ -481,19 +559,17 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
         if constexpr (UP) {
             named_barrier(1, 32 * MMA_WARPS);  // (the sums are read before the next item's are written)
         } else {
-            __threadfence();
+            // (one fence orders what every thread before the barrier has written)
             named_barrier(1, 32 * MMA_WARPS);
             if (threadIdx.x == 0) {
+                __threadfence();
                 const int last = atomicAdd(p.counters + slab, 1u) == (unsigned)(n_act - 1);
                 if (last) p.counters[slab] = 0;  // ready for the next launch
                 __threadfence();
                 is_last = last;
             }
             named_barrier(1, 32 * MMA_WARPS);
-            if (is_last && !dead) {
-                __threadfence();
-                combine<BF16>(p, r, slab);
-            }
+            if (is_last && !dead) combine<BF16>(p, r, slab);
         }
     }
     if constexpr (!UP) {
@@ -554,16 +630,24 @@ int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_s
     p.h = reinterpret_cast<uint16_t*>(p.y + (size_t)picks * p.Dp);
     p.counters = counters;
     p.rows_cap = a.T < MAX_ROWS ? (a.T + 7) / 8 * 8 : MAX_ROWS;
-    // two CTAs an SM where each has four stages or more, else one
+    // Two CTAs an SM where each has four stages or more, else one.  Few items (not an SM's one) need the
+    // depth that two CTAs have together: eight stages of the first kernel and, beside it on the SM, four
+    // of the second.
     const int stage = W_BYTES + p.rows_cap * ROW_BYTES, fixed = 1024 + p.rows_cap * PAD * 4 + routes_bytes(picks, a.E);
-    int per_sm = 2;
-    p.stages = (SMEM_TWO - fixed) / stage;
-    if (p.stages < 4) per_sm = 1, p.stages = (SMEM_ONE - fixed) / stage;
-    p.stages = p.stages > MAX_STAGES ? MAX_STAGES : p.stages / 2 * 2;
-    if (p.stages < 2 || p.stages * stage < WARPS * a.E * 4) return GEMM_ERR_UNSUPPORTED;  // (the router's keys lie in the ring)
-    const int smem = p.stages * stage + fixed;
     const bool gated = a.act == GEMM_ACT_SWIGLU;
     const int most = most_groups(picks, a.E);
+    const int up_slabs = p.Fp / (gated ? SLAB / 2 : SLAB), down_slabs = p.Dp / SLAB;
+    int per_sm = 2, stages = (SMEM_TWO - fixed) / stage;
+    if (stages < 4) per_sm = 1, stages = (SMEM_ONE - fixed) / stage;
+    stages = stages > MAX_STAGES ? MAX_STAGES : stages / 2 * 2;
+    if (per_sm == 2 && stages > 4) stages = 4;
+    if (stages < 2 || stages * stage < WARPS * a.E * 4) return GEMM_ERR_UNSUPPORTED;  // (the router's keys lie in the ring)
+    int up_stages = stages;
+    if (per_sm == 2 && (int64_t)most * up_slabs <= num_sms) {
+        up_stages = (2 * SMEM_TWO - stages * stage - 2 * fixed) / stage / 2 * 2;
+        if (up_stages > MAX_STAGES) up_stages = MAX_STAGES;
+    }
+    const auto smem = [&](int n) { return n * stage + fixed; };
     const auto grid = [&](int slabs) {
         const int64_t items = (int64_t)most * slabs, fit = per_sm * num_sms;
         return (int)(items < fit ? items : fit);
@@ -573,17 +657,17 @@ int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_s
         !encode_experts(&down, a.w2, a.bf16, a.D, a.F, a.E, a.ldw2, a.w2_stride, SLAB))
         return GEMM_ERR_CUDA;
     p.bias = static_cast<const uint16_t*>(a.b1);
-    p.slabs = p.Fp / (gated ? SLAB / 2 : SLAB);
-    cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true, true>(up, p, grid(p.slabs), smem, s)
-                                    : launch_typed<true, false, true>(up, p, grid(p.slabs), smem, s))
-                           : (gated ? launch_typed<true, true, false>(up, p, grid(p.slabs), smem, s)
-                                    : launch_typed<true, false, false>(up, p, grid(p.slabs), smem, s));
+    p.slabs = up_slabs, p.stages = up_stages;
+    cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true, true>(up, p, grid(p.slabs), smem(p.stages), s)
+                                    : launch_typed<true, false, true>(up, p, grid(p.slabs), smem(p.stages), s))
+                           : (gated ? launch_typed<true, true, false>(up, p, grid(p.slabs), smem(p.stages), s)
+                                    : launch_typed<true, false, false>(up, p, grid(p.slabs), smem(p.stages), s));
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
     p.bias = static_cast<const uint16_t*>(a.b2);
-    p.slabs = p.Dp / SLAB;
-    e = a.bf16 ? launch_typed<false, false, true>(down, p, grid(p.slabs), smem, s)
-               : launch_typed<false, false, false>(down, p, grid(p.slabs), smem, s);
+    p.slabs = down_slabs, p.stages = stages;
+    e = a.bf16 ? launch_typed<false, false, true>(down, p, grid(p.slabs), smem(p.stages), s)
+               : launch_typed<false, false, false>(down, p, grid(p.slabs), smem(p.stages), s);
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
     return GEMM_OK;
