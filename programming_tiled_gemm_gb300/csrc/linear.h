@@ -57,14 +57,17 @@ struct LinWorkspace {
 size_t linear_partials_bytes(const LinArgs& a, int num_sms, int kc);
 int64_t linear_counters(int num_sms);
 // Lets `kern` have `bytes` of shared memory on the current device: asked for once a device (`done`
-// has a bit for each), as it takes 0.4 us of a call.
+// has a bit for each), as it takes 0.4 us of a call.  `all`: the SM's whole memory is laid out for sharing,
+// so that another kernel's CTAs find room beside this one's.
 template <typename Kernel>
-cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done)
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done, bool all = false)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && all)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
     return e;
 }

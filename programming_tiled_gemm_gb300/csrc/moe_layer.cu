@@ -32,7 +32,7 @@ GEMM_DEBUG_UNIT(moe_layer)
 
 namespace {
 
-constexpr int MMA_WARPS = 8, WARPS = MMA_WARPS + 1, THREADS = 32 * WARPS;  // the last warp loads
+constexpr int MMA_WARPS = 8, WARPS = MMA_WARPS + 2, THREADS = 32 * WARPS;  // the last two load weights and rows
 constexpr int SLAB = kLayerSlab;  // columns of W an item
 constexpr int DEPTH = 128;        // of the reduced dimension a stage
 constexpr int W_BYTES = DEPTH * SLAB * 2;
@@ -174,11 +174,24 @@ __device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uin
     if (E <= 32 * REG) {
         float next[REG];
         const auto fetch = [&](int t) {
+            // (all of a token's loads before the first use)
+            uint32_t raw[REG] = {};
+            const int64_t at = (int64_t)t * p.ldl + lane;
+            if (p.logits_dtype == GEMM_F32) {
 #pragma unroll
-            for (int c = 0; c < REG; ++c) {
-                if (32 * c >= E) break;
-                next[c] = 32 * c + lane < E ? logit(p, t, 32 * c + lane) : -INFINITY;
+                for (int c = 0; c < REG; ++c)
+                    if (32 * c + lane < E) raw[c] = __ldcg(static_cast<const uint32_t*>(p.logits) + at + 32 * c);
+            } else {
+#pragma unroll
+                for (int c = 0; c < REG; ++c)
+                    if (32 * c + lane < E) raw[c] = __ldcg(static_cast<const uint16_t*>(p.logits) + at + 32 * c);
             }
+#pragma unroll
+            for (int c = 0; c < REG; ++c)
+                next[c] = 32 * c + lane >= E               ? -INFINITY
+                          : p.logits_dtype == GEMM_F32  ? __uint_as_float(raw[c])
+                          : p.logits_dtype == GEMM_BF16 ? from_16<true>((uint16_t)raw[c])
+                                                        : from_16<false>((uint16_t)raw[c]);
         };
         if (warp < p.T) fetch(warp);
         for (int t = warp; t < p.T; t += WARPS) {
@@ -186,7 +199,7 @@ __device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uin
             float l[REG];
 #pragma unroll
             for (int c = 0; c < REG; ++c) {
-                if (32 * c >= E) break;
+                if (32 * c >= E) break;  // (the same for all threads, here and below)
                 l[c] = next[c];
                 key[c] = order_key(l[c]);
             }
@@ -197,13 +210,17 @@ __device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uin
                 uint32_t best = key[0], m;
                 int at = lane;
 #pragma unroll
-                for (int c = 1; c < REG; ++c)
+                for (int c = 1; c < REG; ++c) {
+                    if (32 * c >= E) break;
                     if (key[c] > best) best = key[c], at = 32 * c + lane;
+                }
                 const int e = pick_of(best, at, m);
                 if (e < 0) break;
 #pragma unroll
-                for (int c = 0; c < REG; ++c)
+                for (int c = 0; c < REG; ++c) {
+                    if (32 * c >= E) break;
                     if (32 * c + lane == e) key[c] = 0;
+                }
                 if (j == 0) top = key_value(m);
                 if (lane == j) pick = e, val = key_value(m);
             }
@@ -297,20 +314,30 @@ __device__ __forceinline__ void combine(const LayerParams& p, const Routes& r, i
                     res[c] = p.out_f32 ? static_cast<const float*>(p.R)[(int64_t)t * p.ldr + col + c]
                                        : from_16<BF16>(static_cast<const uint16_t*>(p.R)[(int64_t)t * p.ldr + col + c]);
         }
-#pragma unroll 4
-        for (int j = 0; j < p.k; ++j) {
-            const int q = t * p.k + j;
-            if (r.expert[q] == NONE || !in_range(q, p.T * p.k)) continue;
-            const float w = r.weight[q];
-            const float4* src = reinterpret_cast<const float4*>(p.y + (int64_t)q * p.Dp + col);
-            const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
-            float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            if (p.bias) {
-                const uint16_t* b = p.bias + (int64_t)r.expert[q] * p.D + col;
-                for (int c = 0; c < n; ++c) y[c] += from_16<BF16>(b[c]);
+        // (four picks' rows under way at once; those of picks that are none are there and left out)
+        for (int j0 = 0; j0 < p.k; j0 += 4) {
+            float4 lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = t * p.k + min(j0 + i, p.k - 1);
+                const float4* src = reinterpret_cast<const float4*>(p.y + (in_range(q, p.T * p.k) ? (int64_t)q * p.Dp : 0) + col);
+                lo[i] = __ldcg(src), hi[i] = __ldcg(src + 1);
             }
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] += w * y[c];
+            for (int i = 0; i < 4; ++i) {
+                const int q = t * p.k + min(j0 + i, p.k - 1);
+                if (j0 + i >= p.k || r.expert[q] == NONE) continue;
+                const float w = r.weight[q];
+                float y[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+                if (p.bias) {
+                    const uint16_t* b = p.bias + (int64_t)r.expert[q] * p.D + col;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < n) y[c] += from_16<BF16>(b[c]);
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] += w * y[c];
+            }
         }
         if (p.R)
 #pragma unroll
@@ -377,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
     __shared__ volatile int abort_flag;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(smem_u32(&full_bar[i]), 1 + 32);  // the weights' bytes, and each loading lane's copies
+            mbar_init(smem_u32(&full_bar[i]), 1 + 32);  // the weights' bytes, and each lane's copies of rows
             mbar_init(smem_u32(&empty_bar[i]), MMA_WARPS / 2);
         }
         mbar_init(smem_u32(&never_bar), 1);
@@ -406,51 +433,65 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
     bool dead = false;
 
     if (warp == MMA_WARPS) {
-        // ---------------------------------------------------------------- loads
-        const auto weights = [&](int item, int step, int stage) {
-            if (!elect_one()) return;
-            const int a = item / p.slabs, f = (item - a * p.slabs) * COLS, e = r.active[a];
-            const uint32_t bar = smem_u32(&full_bar[stage]), at = ring_w + stage * W_BYTES;
-            mbar_arrive_expect_tx(bar, W_BYTES);
-            tma_load_3d(at, &tmW, bar, f, step * DEPTH, e);
-            if (GATED) tma_load_3d(at + W_BYTES / 2, &tmW, bar, p.F + f, step * DEPTH, e);
-        };
-        int early = 0;  // stages whose weights are under way before the first kernel has ended
-        if (!UP) {
-            int item = blockIdx.x, step = 0;
-            while (early < p.stages && item < items) {
-                weights(item, step, early);
-                ++early;
-                if (++step == steps) step = 0, item += gridDim.x;
-            }
-            __syncwarp();
-            grid_dependency_wait();
-            grid_dependents_launch();
-        }
+        // ---------------------------------------------------------------- weights
+        // (whole warps walk and one elected lane issues)
         int stage = 0;
         uint32_t phase = 0;
         for (int item = blockIdx.x; item < items && !dead; item += gridDim.x) {
-            const int a = item / p.slabs, first = r.first[a], n_rows = r.first[a + 1] - first;
-            const int chunks = (n_rows + 7) / 8 * 8 * (DEPTH / 8);  // 16-byte chunks of the rows, a line of 16 a row
+            const int a = item / p.slabs, f = (item - a * p.slabs) * COLS, e = r.active[a];
             for (int step = 0; step < steps; ++step) {
                 if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, &abort_flag))) {
                     gave_up(kDevTimeoutProducer);
                     dead = true;
                     break;
                 }
-                if (early > 0) --early;
-                else weights(item, step, stage);
-                __syncwarp();
-                const int c = lane % (DEPTH / 8), kk = step * DEPTH + c * 8;
-                const int n = max(0, min(8, (UP ? K : p.Fp) - kk));  // of this lane's chunk in every row
-                const uint32_t at = ring_x + stage * x_bytes + c * 16;
-#pragma unroll 4
-                for (int q = lane; q < chunks; q += 32) {
-                    const int row = q / (DEPTH / 8), pick = row < n_rows ? r.pick[first + row] : 0;
-                    const bool in = row < n_rows && n > 0 && in_range(pick, p.T * p.k);
-                    const uint16_t* src = UP ? p.x + (int64_t)(pick / p.k) * p.ldx + kk : p.h + (int64_t)pick * p.Fp + kk;
-                    copy_async_16(at + row * ROW_BYTES, in ? src : (UP ? p.x : p.h), in ? 2 * n : 0);
+                if (elect_one()) {
+                    const uint32_t bar = smem_u32(&full_bar[stage]), at = ring_w + stage * W_BYTES;
+                    mbar_arrive_expect_tx(bar, W_BYTES);
+                    tma_load_3d(at, &tmW, bar, f, step * DEPTH, e);
+                    if (GATED) tma_load_3d(at + W_BYTES / 2, &tmW, bar, p.F + f, step * DEPTH, e);
                 }
+                __syncwarp();
+                if (++stage == p.stages) stage = 0, phase ^= 1;
+            }
+        }
+    } else if (warp == MMA_WARPS + 1) {
+        // ---------------------------------------------------------------- rows
+        if (!UP) {
+            grid_dependency_wait();  // (the weights do not: they are under way before the first kernel has ended)
+            grid_dependents_launch();
+        }
+        constexpr int LINE = DEPTH / 8;  // 16-byte chunks of a row: a lane has the same one of every second row
+        const int c = lane % LINE, r0 = lane / LINE;
+        const uint16_t* const rows = UP ? p.x : p.h;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int item = blockIdx.x; item < items && !dead; item += gridDim.x) {
+            const int a = item / p.slabs, first = r.first[a], n_rows = r.first[a + 1] - first, n8 = (n_rows + 7) / 8 * 8;
+            const auto source = [&](int row) {
+                const int pick = r.pick[first + min(row, n_rows - 1)];
+                const int64_t at = UP ? (int64_t)(pick / p.k) * p.ldx : (int64_t)pick * p.Fp;
+                return rows + (in_range(pick, p.T * p.k) ? at : 0) + c * 8;
+            };
+            const uint16_t* src[4];  // of the first eight rows
+#pragma unroll
+            for (int i = 0; i < 4; ++i) src[i] = source(r0 + 2 * i);
+            for (int step = 0; step < steps; ++step) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, &abort_flag))) {
+                    gave_up(kDevTimeoutProducer);
+                    dead = true;
+                    break;
+                }
+                const int bytes = 2 * max(0, min(8, (UP ? K : p.Fp) - step * DEPTH - c * 8));  // of this chunk
+                const uint32_t at = ring_x + stage * x_bytes + c * 16;
+                const auto copy = [&](int row, const uint16_t* from) {
+                    const int n = row < n_rows ? bytes : 0;
+                    copy_async_16(at + row * ROW_BYTES, n > 0 ? from + step * DEPTH : rows, n);
+                };
+#pragma unroll
+                for (int i = 0; i < 4; ++i) copy(r0 + 2 * i, src[i]);
+#pragma unroll 4
+                for (int row = r0 + 8; row < n8; row += 2) copy(row, source(row));
                 copy_async_arrive(smem_u32(&full_bar[stage]));
                 if (++stage == p.stages) stage = 0, phase ^= 1;
             }
@@ -600,7 +641,7 @@ cudaError_t launch_typed(const CUtensorMap& map, const LayerParams& p, int grid,
 {
     auto kern = layer_kernel<UP, GATED, BF16>;
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(kern, SMEM_ONE, allowed);
+    const cudaError_t e = allow_smem(kern, SMEM_ONE, allowed, true);
     return e != cudaSuccess ? e : launch_dependent(kern, dim3(grid), dim3(THREADS), smem, s, map, p);
 }
 
@@ -630,9 +671,10 @@ int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_s
     p.h = reinterpret_cast<uint16_t*>(p.y + (size_t)picks * p.Dp);
     p.counters = counters;
     p.rows_cap = a.T < MAX_ROWS ? (a.T + 7) / 8 * 8 : MAX_ROWS;
-    // Two CTAs an SM where each has four stages or more, else one.  Few items (not an SM's one) need the
-    // depth that two CTAs have together: eight stages of the first kernel and, beside it on the SM, four
-    // of the second.
+    // Bytes in flight decide: 128 KiB of weights an SM.  The second kernel has two CTAs of four stages an SM.
+    // The first has one of six or eight, which leaves room for the first half of the second kernel's CTAs: they route
+    // and fill their rings meanwhile.  With stages too large for that (more than 16 tokens): two CTAs of four
+    // stages each, or one of as many as fit.
     const int stage = W_BYTES + p.rows_cap * ROW_BYTES, fixed = 1024 + p.rows_cap * PAD * 4 + routes_bytes(picks, a.E);
     const bool gated = a.act == GEMM_ACT_SWIGLU;
     const int most = most_groups(picks, a.E);
@@ -640,16 +682,14 @@ int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_s
     int per_sm = 2, stages = (SMEM_TWO - fixed) / stage;
     if (stages < 4) per_sm = 1, stages = (SMEM_ONE - fixed) / stage;
     stages = stages > MAX_STAGES ? MAX_STAGES : stages / 2 * 2;
-    if (per_sm == 2 && stages > 4) stages = 4;
+    if (per_sm == 2) stages = 4;
     if (stages < 2 || stages * stage < WARPS * a.E * 4) return GEMM_ERR_UNSUPPORTED;  // (the router's keys lie in the ring)
-    int up_stages = stages;
-    if (per_sm == 2 && (int64_t)most * up_slabs <= num_sms) {
-        up_stages = (2 * SMEM_TWO - stages * stage - 2 * fixed) / stage / 2 * 2;
-        if (up_stages > MAX_STAGES) up_stages = MAX_STAGES;
-    }
+    int up_stages = stages, up_per_sm = per_sm;
+    const int beside = (2 * SMEM_TWO - (stages * stage + fixed) - fixed) / stage / 2 * 2;
+    if (per_sm == 2 && beside >= 6) up_stages = beside < MAX_STAGES ? beside : MAX_STAGES, up_per_sm = 1;
     const auto smem = [&](int n) { return n * stage + fixed; };
-    const auto grid = [&](int slabs) {
-        const int64_t items = (int64_t)most * slabs, fit = per_sm * num_sms;
+    const auto grid = [&](int slabs, int ctas) {
+        const int64_t items = (int64_t)most * slabs, fit = ctas * num_sms;
         return (int)(items < fit ? items : fit);
     };
     CUtensorMap up, down;
@@ -658,16 +698,16 @@ int launch_moe_layer(const LayerArgs& a, void* ws, unsigned* counters, int num_s
         return GEMM_ERR_CUDA;
     p.bias = static_cast<const uint16_t*>(a.b1);
     p.slabs = up_slabs, p.stages = up_stages;
-    cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true, true>(up, p, grid(p.slabs), smem(p.stages), s)
-                                    : launch_typed<true, false, true>(up, p, grid(p.slabs), smem(p.stages), s))
-                           : (gated ? launch_typed<true, true, false>(up, p, grid(p.slabs), smem(p.stages), s)
-                                    : launch_typed<true, false, false>(up, p, grid(p.slabs), smem(p.stages), s));
+    cudaError_t e = a.bf16 ? (gated ? launch_typed<true, true, true>(up, p, grid(p.slabs, up_per_sm), smem(p.stages), s)
+                                    : launch_typed<true, false, true>(up, p, grid(p.slabs, up_per_sm), smem(p.stages), s))
+                           : (gated ? launch_typed<true, true, false>(up, p, grid(p.slabs, up_per_sm), smem(p.stages), s)
+                                    : launch_typed<true, false, false>(up, p, grid(p.slabs, up_per_sm), smem(p.stages), s));
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
     p.bias = static_cast<const uint16_t*>(a.b2);
     p.slabs = down_slabs, p.stages = stages;
-    e = a.bf16 ? launch_typed<false, false, true>(down, p, grid(p.slabs), smem(p.stages), s)
-               : launch_typed<false, false, false>(down, p, grid(p.slabs), smem(p.stages), s);
+    e = a.bf16 ? launch_typed<false, false, true>(down, p, grid(p.slabs, per_sm), smem(p.stages), s)
+               : launch_typed<false, false, false>(down, p, grid(p.slabs, per_sm), smem(p.stages), s);
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
     return GEMM_OK;
