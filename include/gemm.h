@@ -312,6 +312,37 @@ typedef struct gemm_linear_args {
  * The pages have no counterpart to it: it is the layer large language models are built of. */
 int gemm_linear(gemm_handle_t h, const gemm_linear_args* args, void* stream);
 
+/* The low-rank adapters of gemm_linear_adapted. */
+typedef struct gemm_adapter_args {
+    int64_t n, r;
+    const void* A;
+    int64_t lda;
+    int64_t a_stride;
+    const void* B;
+    int64_t ldb;
+    int64_t b_stride;
+    const int32_t* adapters;
+    const float* scales;
+} gemm_adapter_args;
+
+/* gemm_linear beside a low-rank adapter of each row's choice, as a server runs the requests of many
+ * adapters over one shared projection:
+ *   Y[m] = act(X[m] W + scales[i] (X[m] A_i) B_i + bias) + R[m],  i = adapters[m].
+ *   n adapters of rank r: A [n][K][r] (adapter i at i * a_stride elements), B [n][r][Nw] (b_stride), of
+ *   type dtype; scales fp32 [n] or NULL (ones); adapters [M] device memory, read by the kernels in any order
+ *   of rows; a row with an index outside 0 .. n-1 (as -1) has none.  n == 0: gemm_linear.
+ * U = scales[i] X A_i is rounded to dtype once, as the second product's operand (relative to the adapter's
+ * part 2^-9 in bf16, 2^-12 in fp16, where |U| above 65504 is infinite); everything else is summed in fp32
+ * with X W in one accumulator and rounded once.  Two launches, the first small.
+ * Infinities and NaN in a row of X stay in that row.  An adapter whose A or B holds some reaches its own rows
+ * only, which become NaN where it falls, or in all columns.
+ * args as in gemm_linear with groups == 0 and Z == NULL (else GEMM_ERR_INVALID_ARG: this is the form for
+ * serving); GEMM_ERR_UNSUPPORTED for y_dtype other than dtype, K > 16384, r > 128 or n > 2^20.
+ * GEMM_OPT_TC_CHUNK does not apply.  A and B must be 16-byte aligned with leading dimensions, strides and r
+ * multiples of 8 (GEMM_ERR_ALIGNMENT; pad the rank with zeros).
+ * The pages have no counterpart to it. */
+int gemm_linear_adapted(gemm_handle_t h, const gemm_linear_args* args, const gemm_adapter_args* adapters, void* stream);
+
 /* The arguments of gemm_linear_backward. */
 typedef struct gemm_linear_grad_args {
     int64_t M, K, N;

@@ -38,8 +38,8 @@ EXPORTS = ["gemm_create", "gemm_destroy", "gemm_run", "gemm_run_ex", "gemm_run_h
            "conv4d_forward", "conv4d_forward_cl", "conv4d_forward_tc",
            "gemm_get_device_status", "gemm_set_option", "gemm_launch_count", "gemm_status_string",
            "gemm_run_f32_skinny_noalloc",
-           "gemm_linear", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
-           "moe_combine_backward", "moe_layer", "token_logprobs", "token_logprobs_backward"]
+           "gemm_linear", "gemm_linear_adapted", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch",
+           "moe_combine", "moe_combine_backward", "moe_layer", "token_logprobs", "token_logprobs_backward"]
 
 GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_SILU, GEMM_ACT_SWIGLU = 0, 1, 2, 3, 4, 5
 ACTIVATIONS = {"none": GEMM_ACT_NONE, "relu": GEMM_ACT_RELU, "gelu": GEMM_ACT_GELU, "gelu_tanh": GEMM_ACT_GELU_TANH,
@@ -72,6 +72,13 @@ class LinearGradArgs(ctypes.Structure):
                 ("dw_stride", ctypes.c_int64), ("db", ctypes.c_void_p), ("groups", ctypes.c_int64),
                 ("offsets", ctypes.c_void_p), ("dtype", ctypes.c_int), ("dw_dtype", ctypes.c_int),
                 ("act", ctypes.c_int)]
+
+
+class AdapterArgs(ctypes.Structure):
+    """gemm_adapter_args."""
+    _fields_ = [("n", ctypes.c_int64), ("r", ctypes.c_int64), ("A", ctypes.c_void_p), ("lda", ctypes.c_int64),
+                ("a_stride", ctypes.c_int64), ("B", ctypes.c_void_p), ("ldb", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("adapters", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class MoeLayerArgs(ctypes.Structure):
@@ -137,6 +144,7 @@ def _load():
     lib.moe_dispatch.argtypes = [p, i64, i64, i64, p, i64, i32, p, p, i64, p]
     lib.moe_combine.argtypes = [p, i64, i64, i64, p, i64, i64, i32, p, p, p, i64, p, i64, p]
     lib.moe_combine_backward.argtypes = [p, i64, i64, i64, p, i64, p, i64, i32, p, p, p, p, i64, p, p]
+    lib.gemm_linear_adapted.argtypes = [p, ctypes.POINTER(LinearArgs), ctypes.POINTER(AdapterArgs), p]
     lib.moe_layer.argtypes = [p, ctypes.POINTER(MoeLayerArgs), p]
     lib.token_logprobs.argtypes = [p, i64, i64, p, i64, i32, p, f32, p, p, p, i64, p, p, p]
     lib.token_logprobs_backward.argtypes = [p, i64, i64, p, i64, i32, p, f32, p, p, p, p, p, i64, p]
@@ -244,6 +252,10 @@ def moe_combine_backward(h, T, N, k, dout, lddo, y, ldy, dtype, slots, rows, wei
                                      stream)
 
 
+def gemm_linear_adapted(h, args: LinearArgs, adapters: AdapterArgs, stream=0) -> int:
+    return _lib.gemm_linear_adapted(h, args, adapters, stream)
+
+
 def moe_layer(h, args: MoeLayerArgs, stream=0) -> int:
     return _lib.moe_layer(h, args, stream)
 
@@ -310,10 +322,15 @@ def _ptr(t):
 # fields takes several microseconds to build), and entry points that take their addresses.
 _LINEAR = struct.Struct("@qqqPqPqqPPqPqPqqPiii")
 _LINEAR_GRAD = struct.Struct("@qqqPqPqPqqPqPqPqqPqPiii")
+_ADAPTERS = struct.Struct("@qqPqqPqqPP")
 _LAYER = struct.Struct("@qqqqqPqPqPqqPPqqPPqPqiiiii")
 _raw = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
 _linear_raw, _linear_backward_raw = _raw(("gemm_linear", _lib)), _raw(("gemm_linear_backward", _lib))
 _moe_layer_raw = _raw(("moe_layer", _lib))
+_linear_adapted_raw = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p)(("gemm_linear_adapted", _lib))
+# (the adapters' structure behind the linear layer's)
+_ADAPTERS_AT = (_LINEAR.size + 15) // 16 * 16
 
 
 class Gemm:
@@ -322,7 +339,8 @@ class Gemm:
     def __init__(self, device: int = 0):
         self.device = int(device)
         self.handle = gemm_create(self.device)
-        self._args = ctypes.create_string_buffer(max(_LINEAR.size, _LINEAR_GRAD.size, _LAYER.size) + 8)
+        self._args = ctypes.create_string_buffer(max(_LINEAR_GRAD.size, _LAYER.size,
+                                                       _ADAPTERS_AT + _ADAPTERS.size) + 8)
         self._args_at = ctypes.addressof(self._args)
         self._dev = None
 
@@ -607,6 +625,50 @@ class Gemm:
             raise ValueError("grouped_linear needs offsets")
         return self._linear(x, w, offsets, bias, act, residual, out, out_dtype, save_preact, stream)
 
+    def adapted_linear(self, x, w, a, b, adapters, scales=None, bias=None, act="none", residual=None, out=None,
+                       stream=None):
+        """act(x @ w + scales[i] * (x @ a[i]) @ b[i] + bias) + residual, i = adapters[m] for row m: linear with a
+        low-rank adapter of each row's choice.  x [M, K], w [K, N] ([K, 2 N] for "swiglu"), a [n, K, r],
+        b [n, r, N], bf16 or fp16, r a multiple of 8 up to 128; adapters int32 [M] (-1: none), scales float32
+        [n] or None.  The result has x's type and shape [M, N]."""
+        import torch
+        code = ACTIVATIONS[act]
+        if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+            raise ValueError("x must be [M, K], a [n, K, r] and b [n, r, N]")
+        M, K = x.shape
+        dt = x.dtype
+        dcode = _dtype_code(x)
+        ldx = self._mat(x, "x", M, K, dt)
+        _, ldw, _, Nw = self._weights(w, K, dt, None)
+        n, _, r = a.shape
+        if code == GEMM_ACT_SWIGLU and Nw % 2:
+            raise ValueError("swiglu needs an even number of columns of w (gate, then up)")
+        N = Nw // 2 if code == GEMM_ACT_SWIGLU else Nw
+        lda = ldb = sa = sb = 0
+        if n:
+            lda, sa = self._experts(a, "a", n, K, r, dt)
+            ldb, sb = self._experts(b, "b", n, r, Nw, dt)
+        elif a.shape[1] != K or b.shape != (0, r, Nw):
+            raise ValueError("a and b must be [n, K, r] and [n, r, N]")
+        at_adapters = self._flat(adapters, "adapters", (M,), torch.int32)
+        at_scales = self._flat(scales, "scales", (n,), torch.float32) if scales is not None else 0
+        at_bias = self._flat(bias, "bias", (Nw,), dt) if bias is not None else 0
+        if out is None:
+            out, ldy = self._new((M, N), dt, stream), N
+        else:
+            ldy = self._mat(out, "out", M, N, dt)
+        ldr = at_r = 0
+        if residual is not None:
+            ldr, at_r = self._mat(residual, "residual", M, N, dt), residual.data_ptr()
+        _LINEAR.pack_into(self._args, 0, M, K, N, x.data_ptr(), ldx, w.data_ptr(), ldw, 0, at_bias, at_r, ldr, 0, Nw,
+                          out.data_ptr(), ldy, 0, 0, dcode, dcode, code)
+        _ADAPTERS.pack_into(self._args, _ADAPTERS_AT, n, r, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, at_adapters,
+                            at_scales)
+        rc = _linear_adapted_raw(self.handle, self._args_at, self._args_at + _ADAPTERS_AT, self._stream(stream))
+        if rc != GEMM_OK:
+            raise GemmError(rc, "gemm_linear_adapted")
+        return out
+
     def _linear_backward(self, dy, x, w, offsets, z, act, bias, need_dx, need_dw, dw_dtype, stream):
         import torch
         code = ACTIVATIONS[act]
@@ -882,8 +944,8 @@ __all__ = ["Gemm", "GemmError", "HostProblem", "gemm_create", "gemm_destroy", "g
            "gemm_run_host", "gemm_run_host_batch",
            "conv4d_im2col", "conv4d_forward", "conv4d_forward_cl", "conv4d_forward_tc", "gemm_get_device_status", "gemm_set_option", "gemm_launch_count",
            "gemm_status_string",
-           "gemm_linear", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
-           "moe_combine_backward", "moe_layer", "token_logprobs", "token_logprobs_backward", "LinearArgs", "LinearGradArgs",
-           "MoeLayerArgs", "Routing",
+           "gemm_linear", "gemm_linear_adapted", "gemm_linear_backward", "moe_route", "moe_route_backward", "moe_dispatch",
+           "moe_combine", "moe_combine_backward", "moe_layer", "token_logprobs", "token_logprobs_backward", "LinearArgs", "LinearGradArgs",
+           "AdapterArgs", "MoeLayerArgs", "Routing",
            "TokenLogprobs", "ACTIVATIONS",
            "status_string", "library", "LIB_PATH", "EXPORTS"]

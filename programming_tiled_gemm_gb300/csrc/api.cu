@@ -219,6 +219,7 @@ int gemm_destroy(gemm_handle_t h)
     if (h->lin_sums) cudaFree(h->lin_sums);
     if (h->route_counts) cudaFree(h->route_counts);
     if (h->layer) cudaFree(h->layer);
+    if (h->adapt) cudaFree(h->adapt);
     while (gemm_ctx::KeptBuffer* k = h->kept) {
         h->kept = k->next;
         cudaFree(k->p);
@@ -734,7 +735,7 @@ int gemm_get_device_status(gemm_handle_t h, void* stream)
                       bounds_flag_take_skinny_tma, bounds_flag_take_im2col, bounds_flag_take_conv_implicit,
                       bounds_flag_take_conv_tc, bounds_flag_take_tc_gemm, bounds_flag_take_linear_tc,
                       bounds_flag_take_linear_act, bounds_flag_take_linear_few, bounds_flag_take_moe,
-                      bounds_flag_take_moe_layer}) {
+                      bounds_flag_take_moe_layer, bounds_flag_take_linear_adapted, bounds_flag_take_adapters}) {
         const int r = take();
         if (r < 0) return GEMM_ERR_CUDA;
         bad |= r;

@@ -44,6 +44,8 @@ struct gemm_ctx {
     size_t route_counts_bytes = 0;
     void* layer = nullptr;  // moe_layer: the picks' rows between and after the two products
     size_t layer_bytes = 0;
+    void* adapt = nullptr;  // adapters: the rows' narrow products and the row tiles' lists
+    size_t adapt_bytes = 0;
     // arrival counters, zero after every launch: linear_counters(num_sms) of the products, then
     // the router's, then kLayerCounters of moe_layer.  Made with the handle, so that they never move
     unsigned* lin_counters = nullptr;

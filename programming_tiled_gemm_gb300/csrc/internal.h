@@ -71,6 +71,8 @@ int bounds_flag_take_linear_act();
 int bounds_flag_take_linear_few();
 int bounds_flag_take_moe();
 int bounds_flag_take_moe_layer();
+int bounds_flag_take_linear_adapted();
+int bounds_flag_take_adapters();
 #else
 #define GEMM_DEBUG_UNIT(name) \
     static __device__ __forceinline__ constexpr bool in_range(int64_t, int64_t) { return true; }

@@ -16,6 +16,26 @@ constexpr int kMaxGroups = 1024;  // the kernels keep two words a group in share
 //   kLinDw   dW = X^T dZ             f: columns of W, t: columns of X, reduced over the rows
 enum LinMode { kLinFwd = 0, kLinDx = 1, kLinDw = 2 };
 
+// Low-rank adapters beside a forward product: row m adds s_i (X[m] A_i) B_i, i = adapters[m].
+constexpr int kMaxAdapterRank = 128;
+constexpr int kAdapterParts = 8;  // CTAs that look a used adapter's B through, each with a word of `bad`
+struct LinAdapt {
+    int n, r, rs;  // adapters, their rank, and the rank to 16, 32, 64 or 128: a row's length in `u`
+    const void* A;  // [n][K][r]
+    int64_t lda, a_stride;
+    const void* B;  // [n][r][Nw]
+    int64_t ldb, b_stride;
+    const int32_t* adapters;  // [M]; outside 0 .. n - 1: the row has none
+    const float* scales;      // [n] or null: ones
+    // made by launch_shrink for the product
+    uint16_t* u;       // [M][rs]: s_i X A_i of the rows that have an adapter
+    int* tiles;        // the row tiles' lists of adapters (adapter_list_words(rows) words each)
+    uint16_t* slot;    // [M]: the row's adapter's place in its tile's list, or 0xffff
+    int* bad;          // [n][kAdapterParts]: whether a used adapter's B holds infinities or NaN
+    int tile_rows;     // of the product's row tiles; 0: the few-row kernel, which needs none of the last three
+};
+inline int adapter_list_words(int tile_rows) { return 1 + tile_rows; }
+
 struct LinArgs {
     int mode;
     int64_t M, K, N, Nw;  // N outputs a row, Nw columns of W (2 N when gated)
@@ -41,6 +61,7 @@ struct LinArgs {
     float* db;
     const float* db_ws;
     int db_piece;
+    const LinAdapt* adapt;  // kLinFwd without groups, or null
 };
 
 // Forward products of a few rows without groups stream W through a kernel of their own.
@@ -75,6 +96,13 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done, bool
 // Returns GEMM_OK or a negative gemm_status_t.
 int launch_linear(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* dev_status, uint64_t limit_ns, int kc,
                   int test_stall, cudaStream_t stream, int* launches);
+
+// The same with adapters (16-bit results, K up to 16384), whose part is there once launch_shrink's kernel
+// before it has run.  The rows of its tiles, for LinAdapt::tile_rows.
+int linear_tile_rows(const LinArgs& a, int num_sms);
+int launch_linear_adapted(const LinArgs& a, const LinWorkspace& ws, int num_sms, int* dev_status, uint64_t limit_ns,
+                          int test_stall, cudaStream_t stream, int* launches);
+int launch_shrink(const LinArgs& a, const LinAdapt& ad, int num_sms, cudaStream_t stream, int* launches);
 
 // dZ = dY act'(Z) and db = column sums of dZ, per group.
 struct LinActArgs {

@@ -14,7 +14,7 @@ namespace {
 // Grows the workspace to what the product needs, which *need tells run_product.
 int reserve_product(gemm_handle_t h, const LinArgs& a, cudaStream_t s, size_t* need)
 {
-    *need = linear_partials_bytes(a, h->num_sms, h->opt_tc_chunk);
+    *need = linear_partials_bytes(a, h->num_sms, a.adapt ? 0 : h->opt_tc_chunk);
     return *need == 0 ? GEMM_OK : grow_buffer(h, reinterpret_cast<void**>(&h->lin_partials), &h->lin_partials_bytes, *need, s);
 }
 
@@ -25,7 +25,8 @@ int run_product(gemm_handle_t h, const LinArgs& a, size_t need, cudaStream_t s)
     ws.counters = h->lin_counters;
     int n = 0;
     const int stall = !h->opt_test_stall ? 0 : h->opt_test_stall_pair > 0 ? h->opt_test_stall_pair : -1;
-    const int rc = launch_linear(a, ws, h->num_sms, h->d_status, h->wait_limit_ns, h->opt_tc_chunk, stall, s, &n);
+    const int rc = a.adapt ? launch_linear_adapted(a, ws, h->num_sms, h->d_status, h->wait_limit_ns, stall, s, &n)
+                           : launch_linear(a, ws, h->num_sms, h->d_status, h->wait_limit_ns, h->opt_tc_chunk, stall, s, &n);
     h->launches += n;
     return rc;
 }
@@ -48,7 +49,41 @@ bool bad_stride(int64_t groups, int64_t K, int64_t ld, int64_t stride)
     return groups > 1 && K > 0 && (stride < (K - 1) * ld + 1 || stride > ((int64_t)1 << 38));
 }
 
-int linear_impl(gemm_handle_t h, const gemm_linear_args* a, void* stream)
+// What gemm_linear_adapted checks of its adapters.
+int check_adapters(const gemm_linear_args* a, const gemm_adapter_args* d, int64_t Nw)
+{
+    if (d->n < 0 || d->r < 1 || a->groups != 0 || a->Z) return GEMM_ERR_INVALID_ARG;
+    if (a->y_dtype != a->dtype || a->K > 16384 || d->n > (1 << 20) || d->r > kMaxAdapterRank) return GEMM_ERR_UNSUPPORTED;
+    if (d->n == 0 || a->M == 0 || a->N == 0) return GEMM_OK;
+    if (!d->adapters || bad_matrix(d->A, a->K, d->r, d->lda) || bad_matrix(d->B, d->r, Nw, d->ldb) ||
+        bad_stride(d->n, a->K, d->lda, d->a_stride) || (d->n > 1 && d->a_stride < (a->K - 1) * d->lda + d->r) ||
+        bad_stride(d->n, d->r, d->ldb, d->b_stride) || (d->n > 1 && d->b_stride < (d->r - 1) * d->ldb + Nw))
+        return GEMM_ERR_INVALID_ARG;
+    if (d->r % 8 != 0 || bad_rows16(d->A, a->K, d->r, d->lda) || bad_rows16(d->B, d->r, Nw, d->ldb) ||
+        (d->n > 1 && (d->a_stride % 8 != 0 || d->b_stride % 8 != 0)) || misaligned(d->adapters, 4) || misaligned(d->scales, 4))
+        return GEMM_ERR_ALIGNMENT;
+    return GEMM_OK;
+}
+
+// The workspace of the adapters' narrow half: the rows' U, the row tiles' lists, which B are bad, the slots.
+int reserve_adapters(gemm_handle_t h, const LinArgs& l, LinAdapt& ad, cudaStream_t s)
+{
+    const auto up = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
+    const size_t tiles = ad.tile_rows > 0 ? (size_t)((l.M + ad.tile_rows - 1) / ad.tile_rows) : 0;
+    const size_t u = up((size_t)l.M * ad.rs * 2), lists = up(tiles * adapter_list_words(ad.tile_rows) * 4);
+    const size_t bad = tiles ? up((size_t)ad.n * kAdapterParts * 4) : 0, slots = tiles ? up((size_t)l.M * 2) : 0;
+    const int rc = grow_buffer(h, &h->adapt, &h->adapt_bytes, u + lists + bad + slots, s);
+    if (rc != GEMM_OK) return rc;
+    char* at = static_cast<char*>(h->adapt);
+    ad.u = reinterpret_cast<uint16_t*>(at);
+    ad.tiles = reinterpret_cast<int*>(at + u);
+    ad.bad = reinterpret_cast<int*>(at + u + lists);
+    ad.slot = reinterpret_cast<uint16_t*>(at + u + lists + bad);
+    return GEMM_OK;
+}
+
+// `d`: adapters, or null.
+int linear_impl(gemm_handle_t h, const gemm_linear_args* a, const gemm_adapter_args* d, void* stream)
 {
     if (!h || !a) return GEMM_ERR_INVALID_ARG;
     int rc = check_shape(a->M, a->K, a->N, a->act, a->dtype, a->groups, a->offsets);
@@ -60,6 +95,7 @@ int linear_impl(gemm_handle_t h, const gemm_linear_args* a, void* stream)
         (a->R && bad_matrix(a->R, M, N, a->ldr)) || (a->Z && bad_matrix(a->Z, M, Nw, a->ldz)) ||
         bad_stride(G, K, a->ldw, a->w_stride))
         return GEMM_ERR_INVALID_ARG;
+    if (d && (rc = check_adapters(a, d, Nw)) != GEMM_OK) return rc;
     if (M == 0 || N == 0) return GEMM_OK;
     const int ys = size_of(a->y_dtype);
     if (bad_rows16(a->X, M, K, a->ldx) || bad_rows16(a->W, K, Nw, a->ldw) || (G > 1 && K > 0 && a->w_stride % 8 != 0) ||
@@ -84,16 +120,36 @@ int linear_impl(gemm_handle_t h, const gemm_linear_args* a, void* stream)
     const bool few = linear_is_few(l);
     glog("gemm_linear %s %lldx%lldx%lld, %lld groups, activation %d: %s kernel", dtype_name(a->dtype), (long long)M,
          (long long)N, (long long)K, (long long)a->groups, a->act, few ? "few-row linear" : "tensor-core linear");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    size_t need = 0;
+    int n = 0;
+    LinAdapt ad = {};
+    if (d && d->n > 0 && K > 0) {
+        ad.n = (int)d->n, ad.r = (int)d->r;
+        ad.rs = ad.r <= 16 ? 16 : ad.r <= 32 ? 32 : ad.r <= 64 ? 64 : 128;
+        ad.A = d->A, ad.lda = d->lda, ad.a_stride = d->a_stride;
+        ad.B = d->B, ad.ldb = d->ldb, ad.b_stride = d->b_stride;
+        ad.adapters = d->adapters, ad.scales = d->scales;
+        l.adapt = &ad;
+        if (!few) ad.tile_rows = linear_tile_rows(l, h->num_sms);
+    }
+    if (!few) {
+        rc = reserve_product(h, l, s, &need);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (l.adapt) {
+        if ((rc = reserve_adapters(h, l, ad, s)) != GEMM_OK) return rc;
+        rc = launch_shrink(l, ad, h->num_sms, s, &n);
+        h->launches += n;
+        if (rc != GEMM_OK) return rc;
+        n = 0;
+    }
     if (few) {
-        int n = 0;
-        rc = launch_linear_few(l, h->num_sms, reinterpret_cast<cudaStream_t>(stream), &n);
+        rc = launch_linear_few(l, h->num_sms, s, &n);
         h->launches += n;
         return rc;
     }
-    size_t need = 0;
-    rc = reserve_product(h, l, reinterpret_cast<cudaStream_t>(stream), &need);
-    if (rc != GEMM_OK) return rc;
-    return run_product(h, l, need, reinterpret_cast<cudaStream_t>(stream));
+    return run_product(h, l, need, s);
 }
 
 int linear_backward_impl(gemm_handle_t h, const gemm_linear_grad_args* a, void* stream)
@@ -317,7 +373,12 @@ extern "C" {
 
 int gemm_linear(gemm_handle_t h, const gemm_linear_args* args, void* stream)
 {
-    return told("gemm_linear", linear_impl(h, args, stream));
+    return told("gemm_linear", linear_impl(h, args, nullptr, stream));
+}
+
+int gemm_linear_adapted(gemm_handle_t h, const gemm_linear_args* args, const gemm_adapter_args* adapters, void* stream)
+{
+    return told("gemm_linear_adapted", adapters ? linear_impl(h, args, adapters, stream) : GEMM_ERR_INVALID_ARG);
 }
 
 int gemm_linear_backward(gemm_handle_t h, const gemm_linear_grad_args* args, void* stream)

@@ -7,6 +7,9 @@
 // until the end.  A warp covers 64 columns x 32 of K.  A CTA holds 64 columns (gated: 32 of
 // the gate and the 32 of the up half that belong to them); a cluster of up to 8 CTAs shares K
 // and adds its sums through distributed shared memory, in order.
+// ADAPT: a low-rank adapter of each row's choice, U = s_i X A_i from the kernel before (adapters.cu).
+// Behind the batches of X and W come those of U and the rows' B, `rank` of K for every row, which count for
+// that row only.  The kernel starts as that one's dependent and waits for it before it copies U.
 // Measured (bf16, one row): 2048 x 64 2.5 us, 2048 x 2048 4.0 (tensor-core kernel 8.4 and 9.6),
 // 4096 x 4096 7.4 (12.7), 8192 x 8192 23.3, 5.8 TB/s (27.3).  Dropped: loads kept in registers
 // instead of the ring (4096 x 4096 12.8, and 100 us for 4 rows of 8192 x 28672); three CTAs of two
@@ -54,6 +57,14 @@ struct FewParams {
     int act, out_f32, cluster;
 };
 
+struct FewAdapt {
+    const uint16_t* u;  // [M][rs]
+    int rs, r, n;
+    const uint16_t* B;  // [n][r][Nw]
+    int64_t ldb, b_stride;
+    const int32_t* adapters;
+};
+
 // 16 bytes to shared memory, of which the first n (of 16-bit values, 0 .. 8) are read and the
 // others zero.
 __device__ __forceinline__ void copy_8(uint32_t dst, const uint16_t* src, int n)
@@ -68,13 +79,13 @@ __device__ __forceinline__ float2 two(uint32_t u)
     return __half22float2(*reinterpret_cast<__half2*>(&u));
 }
 
-template <int MT, bool GATED, bool BF16>
-__global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams p)
+template <int MT, bool GATED, bool BF16, bool ADAPT>
+__global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams p, FewAdapt ad)
 {
     constexpr int OUT = GATED ? COLS / 2 : COLS;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float part[MT * COLS];
-    grid_dependency_wait();
+    if (!ADAPT) grid_dependency_wait();
     grid_dependents_launch();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int C = p.cluster, rank = blockIdx.x % C, out0 = blockIdx.x / C * OUT;
@@ -89,11 +100,23 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][i] = make_float2(0.f, 0.f);
-    const int batches = (p.K + BATCH - 1) / BATCH, step = C * WARPS;
+    const int base = (p.K + BATCH - 1) / BATCH, step = C * WARPS;
+    const int batches = base + (ADAPT ? (p.M * ad.r + BATCH - 1) / BATCH : 0);
     uint8_t* mine = ring + warp * STAGES * stage_bytes(MT);
     // every lane copies what it multiplies itself of W; lane (kr, m) row m's eight values of X
     const auto fetch = [&](int b, int s) {
-        if (b < batches) {
+        if (ADAPT && b >= base && b < batches) {
+            // eight of K of one row's adapter
+            const uint32_t at = smem_u32(mine + s * stage_bytes(MT));
+            const int k = (b - base) * BATCH + kr * DEEP, m = k / ad.r, k0 = k - m * ad.r;
+            const int id = m < p.M ? ad.adapters[m] : -1;
+            const bool on = id >= 0 && id < ad.n && (ncol == 0 || in_range(wcol + ncol - 1, p.Nw));
+            const uint16_t* B = ad.B + (on ? id * ad.b_stride + (int64_t)k0 * ad.ldb + wcol : 0);
+#pragma unroll
+            for (int u = 0; u < DEEP; ++u) copy_8(at + u * 512 + lane * 16, B + (on ? u * ad.ldb : 0), on ? ncol : 0);
+            grid_dependency_wait();
+            if (cl < MT) copy_8(at + DEEP * 512 + (cl * 4 + kr) * 16, ad.u + (on ? m * ad.rs + k0 : 0), on && cl == m ? 8 : 0);
+        } else if (b < base) {
             const uint32_t at = smem_u32(mine + s * stage_bytes(MT));
             const int k0 = b * BATCH + kr * DEEP;
 #pragma unroll
@@ -118,6 +141,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
         __syncwarp();
         const uint4* w = reinterpret_cast<const uint4*>(mine + s * stage_bytes(MT)) + lane;
         const uint4* xs = reinterpret_cast<const uint4*>(mine + s * stage_bytes(MT) + DEEP * 512) + kr;
+        const int row = ADAPT && b >= base ? ((b - base) * BATCH + kr * DEEP) / ad.r : -1;  // whose adapter's batch it is
         uint32_t x[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -130,6 +154,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
             const float2 wf[4] = {two<BF16>(v.x), two<BF16>(v.y), two<BF16>(v.z), two<BF16>(v.w)};
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
+                if (ADAPT && m != row && row >= 0) continue;  // (another row's adapter: not even its NaN)
                 const float2 pair = two<BF16>(x[m][u / 2]);
                 const float f = u % 2 ? pair.y : pair.x;
 #pragma unroll
@@ -142,6 +167,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
         if (++s == STAGES) s = 0;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (ADAPT) grid_dependency_wait();  // (a CTA without such a batch too: the kernel before has ended when this one has)
     __syncthreads();  // the ring is free
     float(*red)[MT * COLS] = reinterpret_cast<float(*)[MT * COLS]>(ring);
     // the warp's four parts of K, then the warps' and the cluster's sums in order
@@ -205,8 +231,8 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
     if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
 }
 
-template <int MT, bool GATED, bool BF16>
-cudaError_t launch_typed(const FewParams& p, int blocks, cudaStream_t s)
+template <int MT, bool GATED, bool BF16, bool ADAPT>
+cudaError_t launch_typed(const FewParams& p, const FewAdapt& ad, int blocks, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks * p.cluster, 1, 1);
@@ -214,7 +240,7 @@ cudaError_t launch_typed(const FewParams& p, int blocks, cudaStream_t s)
     cfg.stream = s;
     cfg.dynamicSmemBytes = smem_bytes(MT);
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(linear_few_kernel<MT, GATED, BF16>, smem_bytes(MT), allowed);
+    const cudaError_t e = allow_smem(linear_few_kernel<MT, GATED, BF16, ADAPT>, smem_bytes(MT), allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -225,16 +251,26 @@ cudaError_t launch_typed(const FewParams& p, int blocks, cudaStream_t s)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, linear_few_kernel<MT, GATED, BF16>, p);
+    return cudaLaunchKernelEx(&cfg, linear_few_kernel<MT, GATED, BF16, ADAPT>, p, ad);
 }
 
-template <bool GATED, bool BF16>
-cudaError_t launch_rows(const FewParams& p, int rows, int blocks, cudaStream_t s)
+template <bool GATED, bool BF16, bool ADAPT>
+cudaError_t launch_rows(const FewParams& p, const FewAdapt& ad, int rows, int blocks, cudaStream_t s)
 {
-    if (rows == 1) return launch_typed<1, GATED, BF16>(p, blocks, s);
-    if (rows == 2) return launch_typed<2, GATED, BF16>(p, blocks, s);
-    if (rows == 4) return launch_typed<4, GATED, BF16>(p, blocks, s);
-    return launch_typed<8, GATED, BF16>(p, blocks, s);
+    if (rows == 1) return launch_typed<1, GATED, BF16, ADAPT>(p, ad, blocks, s);
+    if (rows == 2) return launch_typed<2, GATED, BF16, ADAPT>(p, ad, blocks, s);
+    if (rows == 4) return launch_typed<4, GATED, BF16, ADAPT>(p, ad, blocks, s);
+    return launch_typed<8, GATED, BF16, ADAPT>(p, ad, blocks, s);
+}
+
+template <bool ADAPT>
+cudaError_t launch_form(const LinArgs& a, const FewParams& p, const FewAdapt& ad, int rows, int blocks, cudaStream_t s)
+{
+    const bool gated = a.act == GEMM_ACT_SWIGLU;
+    return a.bf16 ? (gated ? launch_rows<true, true, ADAPT>(p, ad, rows, blocks, s)
+                           : launch_rows<false, true, ADAPT>(p, ad, rows, blocks, s))
+                  : (gated ? launch_rows<true, false, ADAPT>(p, ad, rows, blocks, s)
+                           : launch_rows<false, false, ADAPT>(p, ad, rows, blocks, s));
 }
 
 }  // namespace
@@ -281,10 +317,13 @@ int launch_linear_few(const LinArgs& a, int num_sms, cudaStream_t stream, int* l
     while (p.cluster < MAX_CLUSTER && 2 * p.cluster * blocks <= RESIDENT * num_sms &&
            2 * p.cluster * WARPS <= batches + WARPS - 1)
         p.cluster *= 2;
-    const cudaError_t e = a.bf16 ? (gated ? launch_rows<true, true>(p, rows, blocks, stream)
-                                          : launch_rows<false, true>(p, rows, blocks, stream))
-                                 : (gated ? launch_rows<true, false>(p, rows, blocks, stream)
-                                          : launch_rows<false, false>(p, rows, blocks, stream));
+    FewAdapt ad = {};
+    if (a.adapt) {
+        const LinAdapt& l = *a.adapt;
+        ad = {l.u, l.rs, l.r, l.n, static_cast<const uint16_t*>(l.B), l.ldb, l.b_stride, l.adapters};
+    }
+    const cudaError_t e = a.adapt ? launch_form<true>(a, p, ad, rows, blocks, stream)
+                                  : launch_form<false>(a, p, ad, rows, blocks, stream);
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;
     return GEMM_OK;
