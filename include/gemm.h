@@ -337,7 +337,7 @@ typedef struct gemm_adapter_args {
  * Infinities and NaN in a row of X stay in that row.  An adapter whose A or B holds some reaches its own rows
  * only, which become NaN where it falls, or in all columns.
  * args as in gemm_linear with groups == 0 and Z == NULL (else GEMM_ERR_INVALID_ARG: this is the form for
- * serving); GEMM_ERR_UNSUPPORTED for y_dtype other than dtype, K > 16384, r > 128 or n > 2^20.
+ * serving); GEMM_ERR_UNSUPPORTED for y_dtype other than dtype, K > 16384, r > 128 or n > 8192.
  * GEMM_OPT_TC_CHUNK does not apply.  A and B must be 16-byte aligned with leading dimensions, strides and r
  * multiples of 8 (GEMM_ERR_ALIGNMENT; pad the rank with zeros).
  * The pages have no counterpart to it. */

@@ -3,11 +3,11 @@
 // for that product's tiles the lists of their adapters and which of these have a B with infinities or NaN.
 //
 // Few rows (shrink_rows_kernel): a cluster a row, K shared by its CTAs, FMAs in fp32; bound by the reads of
-// A, 16 bytes a thread.  Many rows (shrink_tiles_kernel): a cluster takes 64 rows and shares K; each CTA
-// keeps its part of X in shared memory and multiplies it with the A of every adapter that the tile has, on
-// mma.sync (the rank is too narrow a side for tcgen05's 128 or 256); a row takes the sums of its own adapter
-// only, so that no adapter's NaN reaches another's rows.  Bound by X's bytes where requests lie together.
-// The CTAs' parts of K are added in order through distributed shared memory.
+// A, 16 bytes a thread.  Many rows (shrink_tiles_kernel): a cluster takes 64 rows and shares K; a ring of
+// asynchronous copies brings 64 of K of X and of an adapter's A, for one adapter of the tile's rows after the
+// other, and mma.sync multiplies them (the rank is too narrow a side for tcgen05's 128 or 256); a row takes the
+// sums of its own adapter only, so that no adapter's NaN reaches another's rows.  Bound by X's bytes where
+// requests lie together.  The CTAs' parts of K are added in order through distributed shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -23,7 +23,6 @@ namespace {
 
 constexpr int WARPS = 8, THREADS = 32 * WARPS;
 constexpr int MAX_CLUSTER = 8;
-static_assert(kAdapterParts == MAX_CLUSTER, "a part of B a CTA of the cluster");
 
 struct ShrinkParams {
     int M, K, Nw, n, r, rs;
@@ -38,7 +37,7 @@ struct ShrinkParams {
     uint16_t* u;
     int* tiles;
     uint16_t* slot;
-    int* bad;
+    uint8_t* bad;
     int tile_rows, cluster, work;  // work: clusters of U; those after them make the lists
 };
 
@@ -81,36 +80,78 @@ __device__ __forceinline__ void make_list(const ShrinkParams& p, int tile)
     if (j < p.tile_rows && row < p.M && in_range(row, p.M)) p.slot[row] = id >= 0 ? (uint16_t)place[first] : (uint16_t)0xffff;
 }
 
-// Whether a part of adapter `id`'s B holds infinities or NaN (exponents of ones).
+// Whether B holds infinities or NaN (exponents of ones): the used adapters' parts, shared by all CTAs of the
+// launch.  (It brings them into L2 for the product, too.)
 template <bool BF16>
-__device__ __forceinline__ void look_through(const ShrinkParams& p, int id, int rank)
+__device__ __forceinline__ void look_through(const ShrinkParams& p)
 {
     constexpr uint32_t EXP = BF16 ? 0x7f807f80u : 0x7c007c00u;
-    // (a cluster of fewer CTAs writes every part all the same)
-    for (int part = rank; part < kAdapterParts; part += p.cluster) {
-        const int c0 = (int)((int64_t)p.Nw * part / kAdapterParts) / 8 * 8,
-                  c1 = part + 1 == kAdapterParts ? p.Nw : (int)((int64_t)p.Nw * (part + 1) / kAdapterParts) / 8 * 8;
-        const int chunks = (c1 - c0 + 7) / 8;
+    constexpr int WORDS = kMaxAdapters / 32, FLY = 4;
+    static_assert(WORDS == THREADS, "a word of the adapters' bits a thread");
+    __shared__ unsigned used[WORDS];
+    __shared__ int upto[WARPS];  // used adapters of the warps' words, summed
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    __syncthreads();
+    used[threadIdx.x] = 0;
+    __syncthreads();
+    for (int m = threadIdx.x; m < p.M; m += THREADS) {
+        const int id = adapter_of(p, m);
+        if (id >= 0) atomicOr(&used[id / 32], 1u << (id % 32));
+    }
+    __syncthreads();
+    const int own = __popc(used[threadIdx.x]);
+    int before = own;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += o;
+    }
+    if (lane == 31) upto[warp] = before;
+    __syncthreads();
+    int all = 0;
+    before -= own;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += upto[w];
+        all += upto[w];
+    }
+    __shared__ int who;
+    for (int task = blockIdx.x; task < all * kAdapterParts; task += gridDim.x) {
+        // the task's adapter: the thread whose word holds it
+        const int nth = task / kAdapterParts, part = task % kAdapterParts;
+        if (nth >= before && nth < before + own) {
+            unsigned bits = used[threadIdx.x];
+            for (int i = before; i < nth; ++i) bits &= bits - 1;
+            who = threadIdx.x * 32 + __ffs(bits) - 1;
+        }
+        __syncthreads();
+        const int id = who, q0 = (p.Nw + 7) / 8 * part / kAdapterParts, chunks = (p.Nw + 7) / 8 * (part + 1) / kAdapterParts - q0;
         int hit = 0;
-        for (int q = threadIdx.x; q < p.r * chunks; q += THREADS) {
-            const int k = q / chunks, c = c0 + (q - k * chunks) * 8;
-            const uint16_t* b = p.B + id * p.b_stride + (int64_t)k * p.ldb + c;
-            if (!in_range(c, p.Nw)) continue;
-            uint32_t w[4] = {};
-            if (c + 8 <= p.Nw) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(b));
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            } else {
-                for (int i = 0; c + i < p.Nw; ++i) w[i / 2] |= (uint32_t)b[i] << (16 * (i & 1));
+        for (int q = threadIdx.x; q < p.r * chunks; q += FLY * THREADS) {
+            uint4 v[FLY];
+#pragma unroll
+            for (int i = 0; i < FLY; ++i) {
+                const int at = q + i * THREADS, k = at / max(chunks, 1), c = (q0 + at - k * chunks) * 8;
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (at >= p.r * chunks || !in_range(c, p.Nw)) continue;
+                const uint16_t* b = p.B + id * p.b_stride + (int64_t)k * p.ldb + c;
+                if (c + 8 <= p.Nw) {
+                    v[i] = __ldg(reinterpret_cast<const uint4*>(b));
+                } else {
+                    for (int j = 0; c + j < p.Nw; ++j) hit |= (b[j] & EXP & 0xffffu) == (EXP & 0xffffu);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t e = w[i] & EXP;
-                hit |= (e & 0xffffu) == (EXP & 0xffffu) || (e >> 16) == (EXP >> 16);
+            for (int i = 0; i < FLY; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t e = w[j] & EXP;
+                    hit |= (e & 0xffffu) == (EXP & 0xffffu) || (e >> 16) == (EXP >> 16);
+                }
             }
         }
         hit = __syncthreads_or(hit);
-        if (threadIdx.x == 0) p.bad[(int64_t)id * kAdapterParts + part] = hit;
+        if (threadIdx.x == 0) p.bad[(int64_t)id * kAdapterParts + part] = (uint8_t)(hit != 0);
     }
 }
 
@@ -133,10 +174,14 @@ __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
     const int C = p.cluster, rank = blockIdx.x % C, m = blockIdx.x / C;
     if (m >= p.work) {
         if (rank == 0) make_list(p, m - p.work);
+        if (p.bad) look_through<BF16>(p);
         return;
     }
     const int id = adapter_of(p, m);
-    if (id < 0) return;  // (the whole cluster)
+    if (id < 0) {  // (the whole cluster)
+        if (p.bad) look_through<BF16>(p);
+        return;
+    }
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // a lane has eight ranks of every `per`-th row of A
     const int chunks = p.r / 8;
@@ -202,22 +247,20 @@ __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
         }
         if (in_range(m, p.M)) p.u[(int64_t)m * p.rs + threadIdx.x] = to_16<BF16>(s);
     }
-    if (p.bad) {
-        int earlier = 0;  // rows before with this adapter: the first one's CTAs look its B through
-        for (int j = threadIdx.x; j < m; j += THREADS) earlier |= adapter_of(p, j) == id;
-        if (!__syncthreads_or(earlier)) look_through<BF16>(p, id, rank);
-    }
+    if (p.bad) look_through<BF16>(p);
     if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
 }
 
 // ------------------------------------------------------------------ a cluster 64 rows
 
 constexpr int ROWS = 64;
-constexpr int SUB = 512;                    // of K at a time
-constexpr int X_PITCH = SUB * 2 + 16;       // bytes of a row of X: rows 16 bytes apart in the banks
-constexpr int RING = 3;                     // stages of A, 64 of K each
+constexpr int DEPTH = 64;                  // of K a stage
+constexpr int X_PITCH = DEPTH * 2 + 16;    // bytes of a row of X: rows 16 bytes apart in the banks
+constexpr int RING = 4;                    // stages
 constexpr int a_pitch(int rs) { return rs * 2 + 16; }
-constexpr int tiles_smem(int rs) { return ROWS * X_PITCH + RING * 64 * a_pitch(rs); }
+constexpr int tile_stage(int rs) { return ROWS * X_PITCH + DEPTH * a_pitch(rs); }
+constexpr int tiles_smem(int rs) { return RING * tile_stage(rs); }
+static_assert(tiles_smem(16) >= ROWS * (16 + 1) * 4 && tiles_smem(128) >= ROWS * (128 + 1) * 4, "the sums lie in the ring");
 
 __device__ __forceinline__ void ldsm_x4(uint32_t at, uint32_t (&r)[4])
 {
@@ -257,6 +300,7 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
     const int C = p.cluster, rank = blockIdx.x % C, tile = blockIdx.x / C;
     if (tile >= p.work) {
         if (rank == 0) make_list(p, tile - p.work);
+        if (p.bad) look_through<BF16>(p);
         return;
     }
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row0 = tile * ROWS;
@@ -277,78 +321,78 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
     }
     __syncthreads();
     const int adapters = count;
-    if (adapters == 0) return;  // (the whole cluster)
-    const uint32_t xs = smem_u32(smem), as = xs + ROWS * X_PITCH;
-    const int kb = (p.K + 63) / 64, kb0 = kb * rank / C, kb1 = kb * (rank + 1) / C;
+    if (adapters == 0) {  // (the whole cluster)
+        if (p.bad) look_through<BF16>(p);
+        return;
+    }
+    const uint32_t ring = smem_u32(smem);
+    const int kb = (p.K + DEPTH - 1) / DEPTH, kb0 = kb * rank / C, nb = kb * (rank + 1) / C - kb0, steps = adapters * nb;
     const int rg = warp % 4, kh = warp / 4;
     const int id0 = ids[rg * 16 + lane / 4], id1 = ids[rg * 16 + lane / 4 + 8];  // of this thread's two rows
-    float sum[NT][4];
+    float sum[NT][4], acc[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[t][i] = 0.f;
-    for (int b0 = kb0; b0 < kb1; b0 += SUB / 64) {
-        const int nb = min(SUB / 64, kb1 - b0), steps = adapters * nb;
-        __syncthreads();  // the last part's X has been read
-        for (int q = threadIdx.x; q < ROWS * nb * 8; q += THREADS) {
-            const int row = q / (nb * 8), c = q - row * (nb * 8), k = b0 * 64 + c * 8;
-            int n = row0 + row < p.M ? max(0, min(8, p.K - k)) : 0;
-            if (n > 0 && !in_range(row0 + row, p.M)) n = 0;
-            copy_async_16(xs + row * X_PITCH + c * 16, n > 0 ? p.X + (int64_t)(row0 + row) * p.ldx + k : p.X, 2 * n);
-        }
-        const auto load = [&](int s) {
-            if (s < steps) {
-                const int d = s / nb, k0 = (b0 + s - d * nb) * 64;
-                const uint16_t* A = p.A + list[d] * p.a_stride;
-                const uint32_t at = as + s % RING * 64 * PITCH;
+    // the loader's adapter and k-block, RING - 1 stages ahead
+    int l_step = 0, l_adapter = 0, l_block = 0;
+    const auto load = [&] {
+        if (l_step < steps) {
+            const int k0 = (kb0 + l_block) * DEPTH;
+            const uint32_t at = ring + l_step % RING * tile_stage(RS);
 #pragma unroll
-                for (int q = threadIdx.x; q < 64 * NT; q += THREADS) {
-                    const int k = q / NT, c = q % NT;
-                    int n = k0 + k < p.K && c * 8 < p.r ? 8 : 0;
-                    if (n > 0 && !in_range(k0 + k, p.K)) n = 0;
-                    copy_async_16(at + k * PITCH + c * 16, n > 0 ? A + (int64_t)(k0 + k) * p.lda + c * 8 : p.A, 2 * n);
-                }
+            for (int i = 0; i < ROWS * 8 / THREADS; ++i) {
+                const int q = threadIdx.x + i * THREADS, row = q / 8, k = k0 + q % 8 * 8;
+                int n = row0 + row < p.M ? max(0, min(8, p.K - k)) : 0;
+                if (n > 0 && !in_range(row0 + row, p.M)) n = 0;
+                copy_async_16(at + row * X_PITCH + q % 8 * 16, n > 0 ? p.X + (int64_t)(row0 + row) * p.ldx + k : p.X, 2 * n);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        load(0);
-        load(1);
-        float acc[NT][4];
-        for (int s = 0; s < steps; ++s) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            const uint16_t* A = p.A + list[l_adapter] * p.a_stride;
+#pragma unroll
+            for (int q = threadIdx.x; q < DEPTH * NT; q += THREADS) {
+                const int k = q / NT, c = q % NT;
+                int n = k0 + k < p.K && c * 8 < p.r ? 8 : 0;
+                if (n > 0 && !in_range(k0 + k, p.K)) n = 0;
+                copy_async_16(at + ROWS * X_PITCH + k * PITCH + c * 16, n > 0 ? A + (int64_t)(k0 + k) * p.lda + c * 8 : p.A, 2 * n);
+            }
+            ++l_step;
+            if (++l_block == nb) l_block = 0, ++l_adapter;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < RING - 1; ++i) load();
+    for (int d = 0, s = 0; d < adapters && nb > 0; ++d) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+        for (int b = 0; b < nb; ++b, ++s) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
             __syncthreads();
-            load(s + 2);
-            const int d = s / nb, b = s - d * nb;
-            if (b == 0)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
-            const uint32_t at = as + s % RING * 64 * PITCH;
+            load();  // into the stage that was multiplied before the barrier
+            const uint32_t xs = ring + s % RING * tile_stage(RS), as = xs + ROWS * X_PITCH;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = kh * 32 + h * 16;
                 uint32_t xf[4];  // (rows 0..7, k 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
-                ldsm_x4(xs + (rg * 16 + lane % 16) * X_PITCH + (b * 64 + k + lane / 16 * 8) * 2, xf);
+                ldsm_x4(xs + (rg * 16 + lane % 16) * X_PITCH + (k + lane / 16 * 8) * 2, xf);
 #pragma unroll
                 for (int t = 0; t < NT; t += 2) {
                     uint32_t af[4];  // (k 0..7, ranks 0..7), (k 8..15, 0..7), (k 0..7, 8..15), (k 8..15, 8..15)
-                    ldsm_x4_trans(at + (k + lane % 16) * PITCH + (t * 8 + lane / 16 * 8) * 2, af);
+                    ldsm_x4_trans(as + (k + lane % 16) * PITCH + (t * 8 + lane / 16 * 8) * 2, af);
                     mma_16816<BF16>(acc[t], xf, af[0], af[1]);
                     mma_16816<BF16>(acc[t + 1], xf, af[2], af[3]);
                 }
             }
-            if (b == nb - 1) {
-                const int id = list[d];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (id0 == id) sum[t][0] += acc[t][0], sum[t][1] += acc[t][1];
-                    if (id1 == id) sum[t][2] += acc[t][2], sum[t][3] += acc[t][3];
-                }
-            }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        const int id = list[d];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (id0 == id) sum[t][0] = acc[t][0], sum[t][1] = acc[t][1];
+            if (id1 == id) sum[t][2] = acc[t][2], sum[t][3] = acc[t][3];
+        }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     // [row][rank] of both halves, then of the cluster's CTAs, in order
     float* part = reinterpret_cast<float*>(smem);
@@ -380,12 +424,7 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
         if (p.scales) v *= p.scales[id];
         if (in_range(row0 + i, p.M)) p.u[(int64_t)(row0 + i) * RS + c] = to_16<BF16>(c < p.r ? v : 0.f);
     }
-    if (p.bad)
-        for (int d = 0; d < adapters; ++d) {
-            int earlier = 0;  // the first tile with an adapter looks its B through
-            for (int j = threadIdx.x; j < row0; j += THREADS) earlier |= adapter_of(p, j) == list[d];
-            if (!__syncthreads_or(earlier)) look_through<BF16>(p, list[d], rank);
-        }
+    if (p.bad) look_through<BF16>(p);
     if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
 }
 
@@ -436,12 +475,10 @@ int launch_shrink(const LinArgs& a, const LinAdapt& ad, int num_sms, cudaStream_
     // A row's own cluster reads its A for itself: rows of one adapter read it again, from L2.
     const bool rows = a.M * a.K * ad.r <= (int64_t)16 << 20;
     p.work = rows ? p.M : (p.M + ROWS - 1) / ROWS;
-    // K is shared by as many CTAs as fit at once and have some 256 (a tile: 128) of it
+    // K is shared by as many CTAs as fit at once and have some 256 of it
     p.cluster = 1;
-    const int fit = rows ? 4 * num_sms : 2 * num_sms, least = rows ? 256 : 128;
-    while (p.cluster < MAX_CLUSTER && 2 * p.cluster * p.work <= fit && 2 * p.cluster * least <= p.K) p.cluster *= 2;
-    if (!rows)  // (and by so many that a CTA's part of X lies in shared memory at once)
-        while (p.cluster < MAX_CLUSTER && p.K > SUB * p.cluster) p.cluster *= 2;
+    const int fit = (rows ? 4 : 3) * num_sms;
+    while (p.cluster < MAX_CLUSTER && p.cluster * p.work < fit && 2 * p.cluster * 256 <= p.K) p.cluster *= 2;
     const int clusters = p.work + lists;
     cudaError_t e;
     if (rows) {

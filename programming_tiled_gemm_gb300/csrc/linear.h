@@ -18,7 +18,8 @@ enum LinMode { kLinFwd = 0, kLinDx = 1, kLinDw = 2 };
 
 // Low-rank adapters beside a forward product: row m adds s_i (X[m] A_i) B_i, i = adapters[m].
 constexpr int kMaxAdapterRank = 128;
-constexpr int kAdapterParts = 8;  // CTAs that look a used adapter's B through, each with a word of `bad`
+constexpr int kMaxAdapters = 8192;     // (which of them are used: a bit each in shared memory)
+constexpr int kAdapterParts = 32;      // of a used adapter's B, each looked through by a CTA, which leaves a byte of `bad`
 struct LinAdapt {
     int n, r, rs;  // adapters, their rank, and the rank to 16, 32, 64 or 128: a row's length in `u`
     const void* A;  // [n][K][r]
@@ -31,7 +32,7 @@ struct LinAdapt {
     uint16_t* u;       // [M][rs]: s_i X A_i of the rows that have an adapter
     int* tiles;        // the row tiles' lists of adapters (adapter_list_words(rows) words each)
     uint16_t* slot;    // [M]: the row's adapter's place in its tile's list, or 0xffff
-    int* bad;          // [n][kAdapterParts]: whether a used adapter's B holds infinities or NaN
+    uint8_t* bad;      // [n][kAdapterParts]: whether a used adapter's B holds infinities or NaN
     int tile_rows;     // of the product's row tiles; 0: the few-row kernel, which needs none of the last three
 };
 inline int adapter_list_words(int tile_rows) { return 1 + tile_rows; }

@@ -53,7 +53,7 @@ bool bad_stride(int64_t groups, int64_t K, int64_t ld, int64_t stride)
 int check_adapters(const gemm_linear_args* a, const gemm_adapter_args* d, int64_t Nw)
 {
     if (d->n < 0 || d->r < 1 || a->groups != 0 || a->Z) return GEMM_ERR_INVALID_ARG;
-    if (a->y_dtype != a->dtype || a->K > 16384 || d->n > (1 << 20) || d->r > kMaxAdapterRank) return GEMM_ERR_UNSUPPORTED;
+    if (a->y_dtype != a->dtype || a->K > 16384 || d->n > kMaxAdapters || d->r > kMaxAdapterRank) return GEMM_ERR_UNSUPPORTED;
     if (d->n == 0 || a->M == 0 || a->N == 0) return GEMM_OK;
     if (!d->adapters || bad_matrix(d->A, a->K, d->r, d->lda) || bad_matrix(d->B, d->r, Nw, d->ldb) ||
         bad_stride(d->n, a->K, d->lda, d->a_stride) || (d->n > 1 && d->a_stride < (a->K - 1) * d->lda + d->r) ||
@@ -71,13 +71,13 @@ int reserve_adapters(gemm_handle_t h, const LinArgs& l, LinAdapt& ad, cudaStream
     const auto up = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
     const size_t tiles = ad.tile_rows > 0 ? (size_t)((l.M + ad.tile_rows - 1) / ad.tile_rows) : 0;
     const size_t u = up((size_t)l.M * ad.rs * 2), lists = up(tiles * adapter_list_words(ad.tile_rows) * 4);
-    const size_t bad = tiles ? up((size_t)ad.n * kAdapterParts * 4) : 0, slots = tiles ? up((size_t)l.M * 2) : 0;
+    const size_t bad = tiles ? up((size_t)ad.n * kAdapterParts) : 0, slots = tiles ? up((size_t)l.M * 2) : 0;
     const int rc = grow_buffer(h, &h->adapt, &h->adapt_bytes, u + lists + bad + slots, s);
     if (rc != GEMM_OK) return rc;
     char* at = static_cast<char*>(h->adapt);
     ad.u = reinterpret_cast<uint16_t*>(at);
     ad.tiles = reinterpret_cast<int*>(at + u);
-    ad.bad = reinterpret_cast<int*>(at + u + lists);
+    ad.bad = reinterpret_cast<uint8_t*>(at + u + lists);
     ad.slot = reinterpret_cast<uint16_t*>(at + u + lists + bad);
     return GEMM_OK;
 }

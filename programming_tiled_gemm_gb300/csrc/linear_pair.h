@@ -502,7 +502,7 @@ struct AdaptParams {
     const uint16_t* u;   // [M][rs]
     const int* tiles;    // [row tile][words]: how many adapters the tile has, and which
     const uint16_t* slot;  // [M]: the row's adapter's place in its tile's list, or 0xffff
-    const int* bad;      // [n][kAdapterParts]: an adapter whose B holds infinities or NaN
+    const uint8_t* bad;  // [n][kAdapterParts]: an adapter whose B holds infinities or NaN
     int rs, n, words;    // of K an adapter takes; adapters
 };
 constexpr int ADAPT_SMEM = MAX_W / 2 * 2;  // the fixer's copy of its rows' slots
@@ -572,20 +572,33 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
     }
     if (!ADAPT) grid_dependency_wait();  // what follows reads what the kernel before this one wrote
     grid_dependents_launch();
-    // The blocks that a tile's adapters add to its last slice, and their list.  (Whole warps call it: first when
-    // the list is certain to be there, at the latest where it is needed.)
-    const auto adapters_of = [&](const Item& it) { return ad.tiles + (int64_t)(it.row0 / it.w) * ad.words; };
-    const auto extra_of = [&](const Item& it) {
-        if (it.kb1 != p.kb) return 0;
-        grid_dependency_wait();
-        return __ldcg(adapters_of(it));
+    // A tile's list of adapters: how many, then which.  It is there once the kernel before has ended, which every
+    // warp that reads it waits for where it first needs it: behind the first tile's own k-blocks.  Later tiles'
+    // words are asked for before their k-blocks.
+    bool listed = false;
+    const auto list_at = [&](const Item& it) { return ad.tiles + (int64_t)(it.row0 / it.w) * ad.words; };
+    const auto word_now = [](const int* q) {
+        int v;
+        asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(v) : "l"(q) : "memory");
+        return v;
     };
-    // Zero times infinity is NaN: such an adapter's B would reach every row of the tile.  It is read as zeros (TMA
-    // past the last adapter), and its own rows' U as NaN.
-    const auto is_bad = [&](int id) {
-        const int4* b = reinterpret_cast<const int4*>(ad.bad + (int64_t)id * kAdapterParts);
-        const int4 lo = __ldcg(b), hi = __ldcg(b + 1);
-        return (lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w) != 0;
+    const auto count_ahead = [&](const Item& it) { return ADAPT && listed && it.kb1 == p.kb ? word_now(list_at(it)) : 0; };
+    const auto count_of = [&](const Item& it, int ahead) {  // of the slice: none but the last has adapters
+        if (listed || it.kb1 != p.kb) return ahead;
+        grid_dependency_wait();
+        listed = true;
+        return word_now(list_at(it));
+    };
+    // Lane i: adapter first + i of the list, or ad.n (which TMA reads as zeros) where its B holds infinities or NaN:
+    // zero times these is NaN and would reach every row of the tile.  Its own rows' U is then NaN.
+    const auto usable = [&](const Item& it, int first, int count) {
+        const int at = first + (int)(threadIdx.x % 32);
+        if (at >= count || !in_range(at + 1, ad.words)) return ad.n;
+        const int id = word_now(list_at(it) + 1 + at);
+        if (!in_range(id, ad.n)) return ad.n;
+        const int4* f = reinterpret_cast<const int4*>(ad.bad + (int64_t)id * kAdapterParts);
+        const int4 lo = __ldcg(f), hi = __ldcg(f + 1);
+        return (lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w) != 0 ? ad.n : id;
     };
     if (MODE == kLinDw)
         group_table(p.offsets, p.G, p.M, 0, (p.rows + p.wcap - 1) / p.wcap * p.f_tiles, 0, off, cum);
@@ -622,6 +635,7 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                 // A's two boxes of 64 features (kLinDx: one of 128 rows of W)
                 const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
                 const int fa2 = GATED ? p.F + fa : fa + 64;
+                const int ahead = count_ahead(it);
                 for (int kb = it.kb0; kb < it.kb1; kb += KPS) {
                     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
                         record_error(p.status, kDevTimeoutProducer, abort_flag);
@@ -671,28 +685,32 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                     }
                 }
                 if constexpr (ADAPT) {
-                    const int count = ok ? extra_of(it) : 0, depth = min(ad.rs, BK);
-                    const int* list = adapters_of(it) + 1;
+                    const int count = ok ? count_of(it, ahead) : 0, depth = min(ad.rs, BK);
+                    int mine = 0;  // lane i: adapter 32 n + i of the list
                     for (int k = 0; k < count * ad.rs && ok; k += BK) {
+                        // the adapters of these 64 of K (one of them, or a part of one, from a rank of 64 on)
+                        const int s0 = k / ad.rs, n = min(BK / depth, count - s0), k0 = k - s0 * ad.rs;
+                        if (load_a && s0 % 32 == 0 && k0 == 0) mine = usable(it, s0, count);
                         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
                             record_error(p.status, kDevTimeoutProducer, abort_flag);
                             ok = false;
                             break;
                         }
-                        // the adapters of these 64 of K (one of them, or a part of one, from a rank of 64 on)
-                        const int s0 = k / ad.rs, n = min(BK / depth, count - s0), k0 = k - s0 * ad.rs;
+                        int ids[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ids[i] = __shfl_sync(0xffffffffu, mine, (s0 + i) % 32);
                         if (!load_a) {
                             // (this warp sees every stage; the one that writes U does not, and takes it from here)
                             if (elect_one()) mbar_arrive(smem_u32(&tail_bar[stage]));
                         } else if (elect_one()) {
                             const uint32_t bar = full0 + stage * 8, dst = a_base + stage * KPS * A_BYTES;
                             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * n * 2 * depth * 128);
-                            for (int i = 0; i < n; ++i) {
-                                int id = __ldcg(list + s0 + i);
-                                if (!in_range(id, ad.n) || is_bad(id)) id = ad.n;
-                                tma_load_3d_pair(dst + i * depth * 128, &tmE, bar, fa, k0, id);
-                                tma_load_3d_pair(dst + i * depth * 128 + BOX_BYTES, &tmE, bar, fa2, k0, id);
-                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i < n) {
+                                    tma_load_3d_pair(dst + i * depth * 128, &tmE, bar, fa, k0, ids[i]);
+                                    tma_load_3d_pair(dst + i * depth * 128 + BOX_BYTES, &tmE, bar, fa2, k0, ids[i]);
+                                }
                         }
                         __syncwarp();
                         if (++stage == p.stages) {
@@ -722,6 +740,7 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                 while (ok && walk.next(it)) {
                     const uint32_t idesc = p.idesc | ((uint32_t)(it.w >> 3) << 17);
                     const int kc = CHUNKED ? p.kc : it.kb1 - it.kb0;
+                    const int ahead = count_ahead(it);
                     for (int kb0 = it.kb0; kb0 < it.kb1 && ok; kb0 += kc) {
                         if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&tempty_bar[buf]), buf_phase ^ 1, p.limit_ns,
                                                                        abort_flag))) {
@@ -773,7 +792,7 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                             }
                         }
                         if constexpr (ADAPT) {
-                            const int count = ok ? extra_of(it) : 0;
+                            const int count = ok ? count_of(it, ahead) : 0;
                             for (int k = 0; k < count * ad.rs && ok; k += BK) {
                                 if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, abort_flag)) ||
                                     !__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&peer_bar[stage]), (tails >> stage) & 1,
@@ -875,7 +894,7 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
             while (ok && walk.next(it)) {
                 // the product's own stages go by unseen
                 stage = (int)(((unsigned)stage + (unsigned)(it.kb1 - it.kb0 + KPS - 1) / KPS) % (unsigned)p.stages);
-                const int count = extra_of(it), half = it.w / 2, first = (int)rank * half;
+                const int count = count_of(it, count_ahead(it)), half = it.w / 2, first = (int)rank * half;
                 if (count == 0) continue;
                 __syncwarp();
                 for (int j = lane; j < half; j += 32)
@@ -883,7 +902,23 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                                                                                             : (uint16_t)0xffff;
                 __syncwarp();
                 const int c = lane % 8;  // a lane has the same eight of K of every fourth row
+                int mine = 0;            // lane i: adapter 32 n + i of the list
+                // A stage whose copies have landed: an unusable adapter's rows, and on to the MMA warp.
+                const auto pass_on = [&](int at, int own, bool broken) {
+                    if (broken)
+                        for (int j = lane / 8; j < half; j += 4)
+                            if (slots[j] == own)
+                                *reinterpret_cast<uint4*>(smem_b + at * KPS * p.b_bytes + j * 128 + ((c ^ (j & 7)) << 4)) =
+                                    make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&peer_bar[at]), 0));
+                };
+                int last = -1, last_own = 0;  // the stage whose copies are under way
+                bool last_broken = false;
                 for (int k = 0; k < count * ad.rs; k += BK) {
+                    const int s0 = k / ad.rs;
+                    if (s0 % 32 == 0 && k == s0 * ad.rs) mine = usable(it, s0, count);
                     ok = __all_sync(0xffffffffu, mbar_wait_while(smem_u32(&tail_bar[stage]), (used >> stage) & 1, p.limit_ns,
                                                                  abort_flag, progress));
                     if (!ok) {
@@ -892,28 +927,25 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                         break;
                     }
                     used ^= 1u << stage;
-                    {
-                        const int own = (k + c * 8) / ad.rs, k0 = k + c * 8 - own * ad.rs;
-                        const bool broken = own < count && is_bad(__ldcg(adapters_of(it) + 1 + own));
-                        const uint32_t dst = b_base + stage * KPS * p.b_bytes;
-                        const uint16_t* src = ad.u + (int64_t)(it.row0 + first) * ad.rs + k0;
+                    const int own = (k + c * 8) / ad.rs, k0 = k + c * 8 - own * ad.rs;
+                    const bool broken = __shfl_sync(0xffffffffu, mine, own % 32) == ad.n && own < count;
+                    const uint32_t dst = b_base + stage * KPS * p.b_bytes;
+                    const uint16_t* src = ad.u + (int64_t)(it.row0 + first) * ad.rs + k0;
 #pragma unroll 4
-                        for (int j = lane / 8; j < half; j += 4) {
-                            const bool is = slots[j] == own;
-                            copy_async_16(dst + j * 128 + ((c ^ (j & 7)) << 4), is ? src + (int64_t)j * ad.rs : ad.u, is ? 16 : 0);
-                        }
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        if (broken)
-                            for (int j = lane / 8; j < half; j += 4)
-                                if (slots[j] == own)
-                                    *reinterpret_cast<uint4*>(smem_b + stage * KPS * p.b_bytes + j * 128 + ((c ^ (j & 7)) << 4)) =
-                                        make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    for (int j = lane / 8; j < half; j += 4) {
+                        const bool is = slots[j] == own;
+                        copy_async_16(dst + j * 128 + ((c ^ (j & 7)) << 4), is ? src + (int64_t)j * ad.rs : ad.u, is ? 16 : 0);
                     }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&peer_bar[stage]), 0));
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (last >= 0) {
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        pass_on(last, last_own, last_broken);
+                    }
+                    last = stage, last_own = own, last_broken = broken;
                     if (++stage == p.stages) stage = 0;
                 }
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                if (ok && last >= 0) pass_on(last, last_own, last_broken);
             }
             __syncwarp();
         } else if (MODE == kLinDx && warp == 2) {

@@ -368,7 +368,7 @@ def test_refusals(lib, g):
                dict(a_stride=64), dict(b_stride=64), dict(lin=dict(groups=1, offsets=ad.data_ptr())),
                dict(lin=dict(Z=x.data_ptr(), ldz=64))):
         assert call(**kw) == g.GEMM_ERR_INVALID_ARG, kw
-    for kw in (dict(lin=dict(y_dtype=g.GEMM_F32)), dict(lin=dict(K=16392, ldx=16392), a_stride=1 << 30), dict(n=(1 << 20) + 1),
+    for kw in (dict(lin=dict(y_dtype=g.GEMM_F32)), dict(lin=dict(K=16392, ldx=16392), a_stride=1 << 30), dict(n=8193),
                dict(r=136, lda=136, a_stride=1 << 20, b_stride=1 << 20)):
         assert call(**kw) == g.GEMM_ERR_UNSUPPORTED, kw
     for kw in (dict(A=a.data_ptr() + 8), dict(B=b.data_ptr() + 2), dict(lda=20, a_stride=2048), dict(ldb=68, b_stride=2048),
