@@ -38,7 +38,8 @@ struct ShrinkParams {
     int* tiles;
     uint16_t* slot;
     uint8_t* bad;
-    int tile_rows, cluster, work;  // work: clusters of U; those after them make the lists
+    // clusters of U; after their CTAs come `lists` that make a list each, and those that look B through
+    int tile_rows, cluster, work, lists;
 };
 
 __device__ __forceinline__ int adapter_of(const ShrinkParams& p, int m)
@@ -80,10 +81,10 @@ __device__ __forceinline__ void make_list(const ShrinkParams& p, int tile)
     if (j < p.tile_rows && row < p.M && in_range(row, p.M)) p.slot[row] = id >= 0 ? (uint16_t)place[first] : (uint16_t)0xffff;
 }
 
-// Whether B holds infinities or NaN (exponents of ones): the used adapters' parts, shared by all CTAs of the
-// launch.  (It brings them into L2 for the product, too.)
+// Whether B holds infinities or NaN (exponents of ones): the used adapters' parts, shared by `ctas` CTAs.
+// (It brings them into L2 for the product, too.)
 template <bool BF16>
-__device__ __forceinline__ void look_through(const ShrinkParams& p)
+__device__ __forceinline__ void look_through(const ShrinkParams& p, int cta, int ctas)
 {
     constexpr uint32_t EXP = BF16 ? 0x7f807f80u : 0x7c007c00u;
     constexpr int WORDS = kMaxAdapters / 32, FLY = 4;
@@ -91,12 +92,15 @@ __device__ __forceinline__ void look_through(const ShrinkParams& p)
     __shared__ unsigned used[WORDS];
     __shared__ int upto[WARPS];  // used adapters of the warps' words, summed
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    __syncthreads();
     used[threadIdx.x] = 0;
     __syncthreads();
-    for (int m = threadIdx.x; m < p.M; m += THREADS) {
-        const int id = adapter_of(p, m);
-        if (id >= 0) atomicOr(&used[id / 32], 1u << (id % 32));
+    for (int m = threadIdx.x; m < p.M; m += 8 * THREADS) {
+        int id[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) id[i] = adapter_of(p, m + i * THREADS);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (id[i] >= 0 && (i == 0 || id[i] != id[i - 1])) atomicOr(&used[id[i] / 32], 1u << (id[i] % 32));
     }
     __syncthreads();
     const int own = __popc(used[threadIdx.x]);
@@ -115,7 +119,7 @@ __device__ __forceinline__ void look_through(const ShrinkParams& p)
         all += upto[w];
     }
     __shared__ int who;
-    for (int task = blockIdx.x; task < all * kAdapterParts; task += gridDim.x) {
+    for (int task = cta; task < all * kAdapterParts; task += ctas) {
         // the task's adapter: the thread whose word holds it
         const int nth = task / kAdapterParts, part = task % kAdapterParts;
         if (nth >= before && nth < before + own) {
@@ -173,15 +177,13 @@ __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
     grid_dependents_launch();
     const int C = p.cluster, rank = blockIdx.x % C, m = blockIdx.x / C;
     if (m >= p.work) {
-        if (rank == 0) make_list(p, m - p.work);
-        if (p.bad) look_through<BF16>(p);
+        const int extra = blockIdx.x - p.work * C;
+        if (extra < p.lists) make_list(p, extra);
+        else if (p.bad) look_through<BF16>(p, extra - p.lists, gridDim.x - p.work * C - p.lists);
         return;
     }
     const int id = adapter_of(p, m);
-    if (id < 0) {  // (the whole cluster)
-        if (p.bad) look_through<BF16>(p);
-        return;
-    }
+    if (id < 0) return;  // (the whole cluster)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // a lane has eight ranks of every `per`-th row of A
     const int chunks = p.r / 8;
@@ -247,18 +249,17 @@ __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
         }
         if (in_range(m, p.M)) p.u[(int64_t)m * p.rs + threadIdx.x] = to_16<BF16>(s);
     }
-    if (p.bad) look_through<BF16>(p);
     if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
 }
 
 // ------------------------------------------------------------------ a cluster 64 rows
 
 constexpr int ROWS = 64;
-constexpr int DEPTH = 64;                  // of K a stage
-constexpr int X_PITCH = DEPTH * 2 + 16;    // bytes of a row of X: rows 16 bytes apart in the banks
-constexpr int RING = 4;                    // stages
+constexpr int RING = 3;                    // stages
+constexpr int depth_of(int rs) { return rs <= 64 ? 128 : 64; }  // of K a stage
+constexpr int x_pitch(int rs) { return depth_of(rs) * 2 + 16; }  // bytes of a row of X: rows 16 bytes apart in the banks
 constexpr int a_pitch(int rs) { return rs * 2 + 16; }
-constexpr int tile_stage(int rs) { return ROWS * X_PITCH + DEPTH * a_pitch(rs); }
+constexpr int tile_stage(int rs) { return ROWS * x_pitch(rs) + depth_of(rs) * a_pitch(rs); }
 constexpr int tiles_smem(int rs) { return RING * tile_stage(rs); }
 static_assert(tiles_smem(16) >= ROWS * (16 + 1) * 4 && tiles_smem(128) >= ROWS * (128 + 1) * 4, "the sums lie in the ring");
 
@@ -287,11 +288,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Warps: 16 rows (of 64) x half of every 64 of K.
+// Warps: 16 rows (of 64) x half of every stage's K.
 template <bool BF16, int RS>
 __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
 {
-    constexpr int NT = RS / 8, PITCH = a_pitch(RS);
+    constexpr int NT = RS / 8, PITCH = a_pitch(RS), DEPTH = depth_of(RS), X_PITCH = x_pitch(RS), LINE = DEPTH / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) int ids[ROWS];
     __shared__ int list[ROWS], count;
@@ -299,8 +300,9 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
     grid_dependents_launch();
     const int C = p.cluster, rank = blockIdx.x % C, tile = blockIdx.x / C;
     if (tile >= p.work) {
-        if (rank == 0) make_list(p, tile - p.work);
-        if (p.bad) look_through<BF16>(p);
+        const int extra = blockIdx.x - p.work * C;
+        if (extra < p.lists) make_list(p, extra);
+        else if (p.bad) look_through<BF16>(p, extra - p.lists, gridDim.x - p.work * C - p.lists);
         return;
     }
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row0 = tile * ROWS;
@@ -321,10 +323,7 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
     }
     __syncthreads();
     const int adapters = count;
-    if (adapters == 0) {  // (the whole cluster)
-        if (p.bad) look_through<BF16>(p);
-        return;
-    }
+    if (adapters == 0) return;  // (the whole cluster)
     const uint32_t ring = smem_u32(smem);
     const int kb = (p.K + DEPTH - 1) / DEPTH, kb0 = kb * rank / C, nb = kb * (rank + 1) / C - kb0, steps = adapters * nb;
     const int rg = warp % 4, kh = warp / 4;
@@ -341,11 +340,11 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
             const int k0 = (kb0 + l_block) * DEPTH;
             const uint32_t at = ring + l_step % RING * tile_stage(RS);
 #pragma unroll
-            for (int i = 0; i < ROWS * 8 / THREADS; ++i) {
-                const int q = threadIdx.x + i * THREADS, row = q / 8, k = k0 + q % 8 * 8;
+            for (int i = 0; i < ROWS * LINE / THREADS; ++i) {
+                const int q = threadIdx.x + i * THREADS, row = q / LINE, k = k0 + q % LINE * 8;
                 int n = row0 + row < p.M ? max(0, min(8, p.K - k)) : 0;
                 if (n > 0 && !in_range(row0 + row, p.M)) n = 0;
-                copy_async_16(at + row * X_PITCH + q % 8 * 16, n > 0 ? p.X + (int64_t)(row0 + row) * p.ldx + k : p.X, 2 * n);
+                copy_async_16(at + row * X_PITCH + q % LINE * 16, n > 0 ? p.X + (int64_t)(row0 + row) * p.ldx + k : p.X, 2 * n);
             }
             const uint16_t* A = p.A + list[l_adapter] * p.a_stride;
 #pragma unroll
@@ -372,8 +371,8 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
             load();  // into the stage that was multiplied before the barrier
             const uint32_t xs = ring + s % RING * tile_stage(RS), as = xs + ROWS * X_PITCH;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = kh * 32 + h * 16;
+            for (int h = 0; h < DEPTH / 32; ++h) {
+                const int k = kh * (DEPTH / 2) + h * 16;
                 uint32_t xf[4];  // (rows 0..7, k 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
                 ldsm_x4(xs + (rg * 16 + lane % 16) * X_PITCH + (k + lane / 16 * 8) * 2, xf);
 #pragma unroll
@@ -424,7 +423,6 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
         if (p.scales) v *= p.scales[id];
         if (in_range(row0 + i, p.M)) p.u[(int64_t)(row0 + i) * RS + c] = to_16<BF16>(c < p.r ? v : 0.f);
     }
-    if (p.bad) look_through<BF16>(p);
     if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
 }
 
@@ -471,7 +469,7 @@ int launch_shrink(const LinArgs& a, const LinAdapt& ad, int num_sms, cudaStream_
     p.adapters = ad.adapters, p.scales = ad.scales;
     p.u = ad.u, p.tile_rows = ad.tile_rows;
     if (ad.tile_rows > 0) p.tiles = ad.tiles, p.slot = ad.slot, p.bad = ad.bad;
-    const int lists = ad.tile_rows > 0 ? (p.M + ad.tile_rows - 1) / ad.tile_rows : 0;
+    p.lists = ad.tile_rows > 0 ? (p.M + ad.tile_rows - 1) / ad.tile_rows : 0;
     // A row's own cluster reads its A for itself: rows of one adapter read it again, from L2.
     const bool rows = a.M * a.K * ad.r <= (int64_t)16 << 20;
     p.work = rows ? p.M : (p.M + ROWS - 1) / ROWS;
@@ -479,7 +477,8 @@ int launch_shrink(const LinArgs& a, const LinAdapt& ad, int num_sms, cudaStream_
     p.cluster = 1;
     const int fit = (rows ? 4 : 3) * num_sms;
     while (p.cluster < MAX_CLUSTER && p.cluster * p.work < fit && 2 * p.cluster * 256 <= p.K) p.cluster *= 2;
-    const int clusters = p.work + lists;
+    // (B is looked through beside the rest, by a CTA an SM)
+    const int clusters = p.work + (p.lists > 0 ? (p.lists + num_sms + p.cluster - 1) / p.cluster : 0);
     cudaError_t e;
     if (rows) {
         e = a.bf16 ? launch(shrink_rows_kernel<true>, 0, nullptr, p, clusters, stream)

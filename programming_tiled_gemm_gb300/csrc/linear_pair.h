@@ -57,10 +57,12 @@
 // ADAPT (kLinFwd): a low-rank adapter of each row's choice, Z = X W + b + U B_i with U = s_i X A_i of
 // 16 bits from the kernel before (adapters.cu).  It is a longer reduction: after a tile's last
 // k-block of X and W come blocks of 64 more of K, in which the tile's adapters lie side by side, `rs` of
-// K each: TMA brings their rows of B as it brings W's, and the fixer warp writes the rows' U, zero outside the
-// row's own adapter.  So the sum stays in one accumulator, and a tile pays one block more for four adapters of
-// rank 16.  The kernel starts as the dependent of the one that makes U and waits for it only before these
-// blocks; X was complete before that one started.
+// K each: TMA brings their rows of B as it brings W's, and an otherwise idle warp copies the rows' U, zero
+// outside the row's own adapter.  So the sum stays in one accumulator, and a tile pays one block more for four
+// adapters of rank 16.  These blocks have one to four places of their own beside the ring, filled while the
+// tile's own k-blocks run: in the ring, they came 4 us after the tile's last one.  The kernel starts as the
+// dependent of the one that makes U and waits for it only before these blocks; X was complete before that one
+// started.
 #pragma once
 
 #include <cuda.h>
@@ -503,7 +505,8 @@ struct AdaptParams {
     const int* tiles;    // [row tile][words]: how many adapters the tile has, and which
     const uint16_t* slot;  // [M]: the row's adapter's place in its tile's list, or 0xffff
     const uint8_t* bad;  // [n][kAdapterParts]: an adapter whose B holds infinities or NaN
-    int rs, n, words;    // of K an adapter takes; adapters
+    int rs, n, words;    // of K an adapter takes; adapters; of a tile's list
+    int places;          // for blocks of 64 of K of the adapters
 };
 constexpr int ADAPT_SMEM = MAX_W / 2 * 2;  // the fixer's copy of its rows' slots
 
@@ -519,13 +522,16 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     uint8_t* smem_a = smem;
-    uint8_t* smem_b = smem + p.stages * KPS * A_BYTES;
-    uint8_t* after = smem_b + p.stages * KPS * p.b_bytes;
+    const int slots_all = p.stages * KPS + (ADAPT ? ad.places : 0);  // (the adapters' places lie behind the ring's)
+    uint8_t* smem_b = smem + slots_all * A_BYTES;
+    uint8_t* after = smem_b + slots_all * p.b_bytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(after + EPI_WARPS * STG_BYTES);
     uint64_t* full_bar = bars;                     // (used in the even CTA)
     uint64_t* empty_bar = bars + MAX_STAGES;       // (both CTAs, multicast)
-    uint64_t* tail_bar = bars + 2 * MAX_STAGES;    // kLinDw: a stage the fixer passes on; ADAPT: or takes (each CTA's own)
-    uint64_t* peer_bar = bars + 3 * MAX_STAGES;    // kLinDw: the odd CTA's fixer is done; ADAPT: both are (used in the even CTA)
+    uint64_t* tail_bar = bars + 2 * MAX_STAGES;    // kLinDw: a stage the fixer passes on (each CTA's own)
+    uint64_t* peer_bar = bars + 3 * MAX_STAGES;    // kLinDw: the odd CTA's fixer is done (used in the even CTA)
+    uint64_t* free_bar = tail_bar;                 // ADAPT: a place's MMAs are done (both CTAs, multicast)
+    uint64_t* there_bar = peer_bar;                // ADAPT: a place is filled: B by TMA, both CTAs' U (used in the even CTA)
     uint64_t* tfull_bar = bars + 4 * MAX_STAGES;   // [2] (both CTAs, multicast)
     uint64_t* tempty_bar = tfull_bar + 2;          // [2] (used in the even CTA)
     uint64_t* drain_bar = tfull_bar + 4;           // (both CTAs, multicast)
@@ -545,11 +551,11 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
     const int npairs = gridDim.x / 2;
 
     if (warp == 0 && lane == 0) {
-        for (int s = 0; s < p.stages; ++s) {
+        for (int s = 0; s < (ADAPT ? max(p.stages, ad.places) : p.stages); ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
             mbar_init(smem_u32(&empty_bar[s]), 1);
             mbar_init(smem_u32(&tail_bar[s]), 1);
-            mbar_init(smem_u32(&peer_bar[s]), ADAPT ? 2 : 1);
+            mbar_init(smem_u32(&peer_bar[s]), ADAPT ? 3 : 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&tfull_bar[a]), 1);
@@ -573,32 +579,28 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
     if (!ADAPT) grid_dependency_wait();  // what follows reads what the kernel before this one wrote
     grid_dependents_launch();
     // A tile's list of adapters: how many, then which.  It is there once the kernel before has ended, which every
-    // warp that reads it waits for where it first needs it: behind the first tile's own k-blocks.  Later tiles'
-    // words are asked for before their k-blocks.
-    bool listed = false;
+    // warp that reads it waits for where it first needs it.  Later tiles' words are asked for as the tile begins.
     const auto list_at = [&](const Item& it) { return ad.tiles + (int64_t)(it.row0 / it.w) * ad.words; };
     const auto word_now = [](const int* q) {
         int v;
         asm volatile("ld.global.cg.b32 %0, [%1];" : "=r"(v) : "l"(q) : "memory");
         return v;
     };
-    const auto count_ahead = [&](const Item& it) { return ADAPT && listed && it.kb1 == p.kb ? word_now(list_at(it)) : 0; };
-    const auto count_of = [&](const Item& it, int ahead) {  // of the slice: none but the last has adapters
-        if (listed || it.kb1 != p.kb) return ahead;
-        grid_dependency_wait();
-        listed = true;
-        return word_now(list_at(it));
+    // Lane i's adapter first + i of a list (or -1), and that adapter's flags.
+    const auto id_of = [&](const Item& it, int first) {
+        const int at = 1 + first + (int)(threadIdx.x % 32);
+        const int id = at < ad.words ? word_now(list_at(it) + at) : -1;
+        return id >= 0 && id < ad.n ? id : -1;  // (words past the list's end are anything)
     };
-    // Lane i: adapter first + i of the list, or ad.n (which TMA reads as zeros) where its B holds infinities or NaN:
-    // zero times these is NaN and would reach every row of the tile.  Its own rows' U is then NaN.
-    const auto usable = [&](const Item& it, int first, int count) {
-        const int at = first + (int)(threadIdx.x % 32);
-        if (at >= count || !in_range(at + 1, ad.words)) return ad.n;
-        const int id = word_now(list_at(it) + 1 + at);
-        if (!in_range(id, ad.n)) return ad.n;
-        const int4* f = reinterpret_cast<const int4*>(ad.bad + (int64_t)id * kAdapterParts);
-        const int4 lo = __ldcg(f), hi = __ldcg(f + 1);
-        return (lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w) != 0 ? ad.n : id;
+    const auto flags_of = [&](int id, uint4(&f)[2]) {
+        const uint8_t* q = ad.bad + (int64_t)max(id, 0) * kAdapterParts;
+        asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(f[0].x), "=r"(f[0].y), "=r"(f[0].z), "=r"(f[0].w) : "l"(q) : "memory");
+        asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(f[1].x), "=r"(f[1].y), "=r"(f[1].z), "=r"(f[1].w) : "l"(q + 16) : "memory");
+    };
+    // ad.n (which TMA reads as zeros) for an adapter whose B holds infinities or NaN: zero times these is NaN and would
+    // reach every row of the tile.  Its own rows' U is then NaN.
+    const auto usable = [&](int id, const uint4(&f)[2]) {
+        return id < 0 || (f[0].x | f[0].y | f[0].z | f[0].w | f[1].x | f[1].y | f[1].z | f[1].w) != 0 ? ad.n : id;
     };
     if (MODE == kLinDw)
         group_table(p.offsets, p.G, p.M, 0, (p.rows + p.wcap - 1) / p.wcap * p.f_tiles, 0, off, cum);
@@ -625,6 +627,10 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
             const bool load_a = warp == 0;
             const uint32_t a_base = smem_u32(smem_a), b_base = smem_u32(smem_b);
             const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0), tail_own = mapa_shared(smem_u32(tail_bar), rank);
+            const uint32_t there0 = mapa_shared(smem_u32(there_bar), 0);
+            bool listed = false;  // ADAPT: the lists are there
+            int place = 0;        // and the next block's place
+            uint32_t place_phase = 0;
             while (ok && walk.next(it)) {
                 const int f0 = it.f0 * TILE_F;
                 const int half = it.w / 2;
@@ -635,8 +641,55 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                 // A's two boxes of 64 features (kLinDx: one of 128 rows of W)
                 const int fa = GATED ? f0 + 64 * (int)rank : f0 + CTA_F * (int)rank;
                 const int fa2 = GATED ? p.F + fa : fa + 64;
-                const int ahead = count_ahead(it);
+                // ADAPT, warp 0: the list's words and flags are asked for ahead of their use
+                const bool adapts = ADAPT && load_a && it.kb1 == p.kb;
+                int count = 0, id = -1, mine = 0, block = 0, seen = 0;
+                uint4 flags[2] = {};
+                if (adapts && listed) count = word_now(list_at(it)), id = id_of(it, 0);
+                // blocks of 64 of K of the tile's adapters, up to the `to`-th
+                const auto adapter_blocks = [&](int to) {
+                    const int depth = min(ad.rs, BK);
+                    for (; block < to && block * BK < count * ad.rs && ok; ++block) {
+                        // the adapters of these 64 of K (one of them, or a part of one, from a rank of 64 on)
+                        const int k = block * BK, s0 = k / ad.rs, n = min(BK / depth, count - s0), k0 = k - s0 * ad.rs;
+                        if (s0 > 0 && s0 % 32 == 0 && k0 == 0) {
+                            id = id_of(it, s0);
+                            flags_of(id, flags);
+                        }
+                        if (s0 % 32 == 0 && k0 == 0) mine = usable(id, flags);
+                        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&free_bar[place]), place_phase ^ 1, p.limit_ns, abort_flag))) {
+                            record_error(p.status, kDevTimeoutProducer, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        int ids[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ids[i] = __shfl_sync(0xffffffffu, mine, (s0 + i) % 32);
+                        if (elect_one()) {
+                            const uint32_t bar = there0 + place * 8, dst = a_base + (p.stages * KPS + place) * A_BYTES;
+                            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&there_bar[place]), 2 * n * 2 * depth * 128);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i < n) {
+                                    tma_load_3d_pair(dst + i * depth * 128, &tmE, bar, fa, k0, ids[i]);
+                                    tma_load_3d_pair(dst + i * depth * 128 + BOX_BYTES, &tmE, bar, fa2, k0, ids[i]);
+                                }
+                        }
+                        __syncwarp();
+                        if (++place == ad.places) {
+                            place = 0;
+                            place_phase ^= 1;
+                        }
+                    }
+                };
                 for (int kb = it.kb0; kb < it.kb1; kb += KPS) {
+                    if (ADAPT && adapts) {
+                        // Once the ring has come round, the last tile's blocks have left their places (and there is
+                        // time enough until this tile's are needed).
+                        if (seen == 1 && listed) flags_of(id, flags);
+                        if (seen == p.stages && listed) adapter_blocks(ad.places);
+                        ++seen;
+                    }
                     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
                         record_error(p.status, kDevTimeoutProducer, abort_flag);
                         ok = false;
@@ -684,40 +737,15 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                         phase ^= 1;
                     }
                 }
-                if constexpr (ADAPT) {
-                    const int count = ok ? count_of(it, ahead) : 0, depth = min(ad.rs, BK);
-                    int mine = 0;  // lane i: adapter 32 n + i of the list
-                    for (int k = 0; k < count * ad.rs && ok; k += BK) {
-                        // the adapters of these 64 of K (one of them, or a part of one, from a rank of 64 on)
-                        const int s0 = k / ad.rs, n = min(BK / depth, count - s0), k0 = k - s0 * ad.rs;
-                        if (load_a && s0 % 32 == 0 && k0 == 0) mine = usable(it, s0, count);
-                        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
-                            record_error(p.status, kDevTimeoutProducer, abort_flag);
-                            ok = false;
-                            break;
-                        }
-                        int ids[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) ids[i] = __shfl_sync(0xffffffffu, mine, (s0 + i) % 32);
-                        if (!load_a) {
-                            // (this warp sees every stage; the one that writes U does not, and takes it from here)
-                            if (elect_one()) mbar_arrive(smem_u32(&tail_bar[stage]));
-                        } else if (elect_one()) {
-                            const uint32_t bar = full0 + stage * 8, dst = a_base + stage * KPS * A_BYTES;
-                            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * n * 2 * depth * 128);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (i < n) {
-                                    tma_load_3d_pair(dst + i * depth * 128, &tmE, bar, fa, k0, ids[i]);
-                                    tma_load_3d_pair(dst + i * depth * 128 + BOX_BYTES, &tmE, bar, fa2, k0, ids[i]);
-                                }
-                        }
-                        __syncwarp();
-                        if (++stage == p.stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                if (ADAPT && adapts && ok) {
+                    if (!listed) {
+                        grid_dependency_wait();
+                        listed = true;
+                        count = word_now(list_at(it)), id = id_of(it, 0);
+                        seen = 1;
                     }
+                    if (seen == 1) flags_of(id, flags);
+                    adapter_blocks(1 << 30);
                 }
             }
             if (!ok) aborted = true;
@@ -732,6 +760,9 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, buf_phase = 0;
                 uint32_t tails = 0;  // bit s: parity of stage s's next tail
+                bool listed = false;  // ADAPT: the lists are there
+                int place = 0;
+                uint32_t place_phase = 0;
                 bool ok = true;
                 // descriptors of stage 0; a stage or a step of 16 along K moves the start address
                 constexpr uint32_t A_STEP = A_MN ? UMMA_K * 128 : UMMA_K * 2, B_STEP = B_MN ? UMMA_K * 128 : UMMA_K * 2;
@@ -740,7 +771,8 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                 while (ok && walk.next(it)) {
                     const uint32_t idesc = p.idesc | ((uint32_t)(it.w >> 3) << 17);
                     const int kc = CHUNKED ? p.kc : it.kb1 - it.kb0;
-                    const int ahead = count_ahead(it);
+                    int count = 0;  // ADAPT: adapters of the tile
+                    if (ADAPT && listed && it.kb1 == p.kb) count = word_now(list_at(it));
                     for (int kb0 = it.kb0; kb0 < it.kb1 && ok; kb0 += kc) {
                         if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&tempty_bar[buf]), buf_phase ^ 1, p.limit_ns,
                                                                        abort_flag))) {
@@ -792,31 +824,34 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                             }
                         }
                         if constexpr (ADAPT) {
-                            const int count = ok ? count_of(it, ahead) : 0;
+                            if (ok && !listed && it.kb1 == p.kb) {
+                                grid_dependency_wait();
+                                listed = true;
+                                count = word_now(list_at(it));
+                            }
                             for (int k = 0; k < count * ad.rs && ok; k += BK) {
-                                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, abort_flag)) ||
-                                    !__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&peer_bar[stage]), (tails >> stage) & 1,
-                                                                               p.limit_ns, abort_flag))) {
+                                if (!__all_sync(0xffffffffu, mbar_wait_cluster(smem_u32(&there_bar[place]), place_phase, p.limit_ns,
+                                                                               abort_flag))) {
                                     record_error(p.status, kDevTimeoutMma, abort_flag);
                                     ok = false;
                                     break;
                                 }
-                                tails ^= 1u << stage;
                                 tc_fence_after();
-                                const int steps = min(BK, count * ad.rs - k) / UMMA_K;  // (the rest of the stage is not there)
+                                const int steps = min(BK, count * ad.rs - k) / UMMA_K;  // (the rest of the place is not there)
                                 if (elect_one()) {
-                                    const uint64_t a_desc = a_desc0 + (uint32_t)(stage * KPS * A_BYTES >> 4);
-                                    const uint64_t b_desc = b_desc0 + (uint32_t)(stage * KPS * p.b_bytes >> 4);
+                                    const int at = p.stages * KPS + place;
+                                    const uint64_t a_desc = a_desc0 + (uint32_t)(at * A_BYTES >> 4);
+                                    const uint64_t b_desc = b_desc0 + (uint32_t)(at * p.b_bytes >> 4);
 #pragma unroll
                                     for (int s = 0; s < BK / UMMA_K; ++s)
                                         if (s < steps)
                                             umma_f16_pair(d_tmem, a_desc + s * (A_STEP >> 4), b_desc + s * (B_STEP >> 4), idesc, 1u);
-                                    umma_commit_mask(smem_u32(&empty_bar[stage]), pair_mask);
+                                    umma_commit_mask(smem_u32(&free_bar[place]), pair_mask);
                                 }
                                 __syncwarp();
-                                if (++stage == p.stages) {
-                                    stage = 0;
-                                    phase ^= 1;
+                                if (++place == ad.places) {
+                                    place = 0;
+                                    place_phase ^= 1;
                                 }
                             }
                         }
@@ -886,15 +921,15 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
             // ---------------------------------------------------------------- the rows' U (both CTAs)
             Walk<MODE> walk(p, off, cum, pair, npairs);
             Item it;
-            int stage = 0;
-            uint32_t used = 0;  // bit s: parity of stage s's next hand-over
+            int place = 0;
+            uint32_t place_phase = 0;
             bool ok = true;
             uint16_t* const slots = reinterpret_cast<uint16_t*>(cum + p.G + 1);
-            const uint32_t b_base = smem_u32(smem_b);
+            uint8_t* const own_b = smem_b + p.stages * KPS * p.b_bytes;
+            grid_dependency_wait();
             while (ok && walk.next(it)) {
-                // the product's own stages go by unseen
-                stage = (int)(((unsigned)stage + (unsigned)(it.kb1 - it.kb0 + KPS - 1) / KPS) % (unsigned)p.stages);
-                const int count = count_of(it, count_ahead(it)), half = it.w / 2, first = (int)rank * half;
+                if (it.kb1 != p.kb) continue;
+                const int count = word_now(list_at(it)), half = it.w / 2, first = (int)rank * half;
                 if (count == 0) continue;
                 __syncwarp();
                 for (int j = lane; j < half; j += 32)
@@ -903,33 +938,43 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                 __syncwarp();
                 const int c = lane % 8;  // a lane has the same eight of K of every fourth row
                 int mine = 0;            // lane i: adapter 32 n + i of the list
-                // A stage whose copies have landed: an unusable adapter's rows, and on to the MMA warp.
+                // A place whose copies have landed: an unusable adapter's rows, and on to the MMA warp.
                 const auto pass_on = [&](int at, int own, bool broken) {
                     if (broken)
                         for (int j = lane / 8; j < half; j += 4)
                             if (slots[j] == own)
-                                *reinterpret_cast<uint4*>(smem_b + at * KPS * p.b_bytes + j * 128 + ((c ^ (j & 7)) << 4)) =
+                                *reinterpret_cast<uint4*>(own_b + at * p.b_bytes + j * 128 + ((c ^ (j & 7)) << 4)) =
                                     make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
                     fence_proxy_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&peer_bar[at]), 0));
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&there_bar[at]), 0));
                 };
-                int last = -1, last_own = 0;  // the stage whose copies are under way
+                int last = -1, last_own = 0;  // the place whose copies are under way
                 bool last_broken = false;
                 for (int k = 0; k < count * ad.rs; k += BK) {
                     const int s0 = k / ad.rs;
-                    if (s0 % 32 == 0 && k == s0 * ad.rs) mine = usable(it, s0, count);
-                    ok = __all_sync(0xffffffffu, mbar_wait_while(smem_u32(&tail_bar[stage]), (used >> stage) & 1, p.limit_ns,
-                                                                 abort_flag, progress));
+                    if (s0 % 32 == 0 && k == s0 * ad.rs) {
+                        uint4 flags[2];
+                        const int id = id_of(it, s0);
+                        flags_of(id, flags);
+                        mine = usable(id, flags);
+                    }
+                    // (a whole tile may go by before the place is free; with one place, what is under way must land first)
+                    if (last >= 0 && ad.places == 1) {
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        pass_on(last, last_own, last_broken);
+                        last = -1;
+                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait_while(smem_u32(&free_bar[place]), place_phase ^ 1, p.limit_ns, abort_flag,
+                                                                 progress));
                     if (!ok) {
                         if (lane == 0) record_error(p.status, kDevTimeoutProducer, abort_flag);
                         aborted = true;
                         break;
                     }
-                    used ^= 1u << stage;
                     const int own = (k + c * 8) / ad.rs, k0 = k + c * 8 - own * ad.rs;
                     const bool broken = __shfl_sync(0xffffffffu, mine, own % 32) == ad.n && own < count;
-                    const uint32_t dst = b_base + stage * KPS * p.b_bytes;
+                    const uint32_t dst = smem_u32(own_b + place * p.b_bytes);
                     const uint16_t* src = ad.u + (int64_t)(it.row0 + first) * ad.rs + k0;
 #pragma unroll 4
                     for (int j = lane / 8; j < half; j += 4) {
@@ -941,8 +986,11 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                         asm volatile("cp.async.wait_group 1;" ::: "memory");
                         pass_on(last, last_own, last_broken);
                     }
-                    last = stage, last_own = own, last_broken = broken;
-                    if (++stage == p.stages) stage = 0;
+                    last = place, last_own = own, last_broken = broken;
+                    if (++place == ad.places) {
+                        place = 0;
+                        place_phase ^= 1;
+                    }
                 }
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
                 if (ok && last >= 0) pass_on(last, last_own, last_broken);
@@ -1236,7 +1284,7 @@ bool encode(CUtensorMap* map, int rank, const void* base, bool bf16, int64_t d0,
 
 struct LinPlan {
     int rows, F, kb, f_tiles, wcap, wmax, pairs;
-    int bx, b_bytes, kps, stages, smem;
+    int bx, b_bytes, kps, stages, places, smem;  // places: beside the ring, for the adapters' blocks
     bool gated, ragged;
     int split_w;  // 0: the last wave is not cut
     int64_t tiles;  // an upper bound when the groups' rows are only known on the device
@@ -1304,9 +1352,10 @@ LinPlan plan(const LinArgs& a, int num_sms, bool chunked)
     // rows, 404 instead of 430 at 160; at 192 it would be 594 instead of 400: three stages).
     // dW's fixer counts stages by k-block.
     pl.kps = a.mode != kLinDw && pl.wmax <= 160 ? 2 : 1;
-    pl.stages = (SMEM_MAX - fixed) / (pl.kps * (A_BYTES + pl.b_bytes));
+    pl.places = !a.adapt ? 0 : pl.kps == 1 ? 1 : 4;
+    pl.stages = ((SMEM_MAX - fixed) / (A_BYTES + pl.b_bytes) - pl.places) / pl.kps;
     if (pl.stages > MAX_STAGES) pl.stages = MAX_STAGES;
-    pl.smem = fixed + pl.stages * pl.kps * (A_BYTES + pl.b_bytes);
+    pl.smem = fixed + (pl.stages * pl.kps + pl.places) * (A_BYTES + pl.b_bytes);
     // groups' dW tiles have lengths of their own and are not cut
     pl.split_w = a.mode == kLinDw && a.G > 0 ? 0 : pl.wmax;
     if (ragged && a.M > a.G) {
