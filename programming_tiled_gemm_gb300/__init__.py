@@ -830,10 +830,17 @@ class Gemm:
         return dy, dweights
 
     def _experts(self, w, name, E, K, N, dtype):
-        """(leading dimension, stride) of a matrix an expert, [E, K, N]."""
+        """(leading dimension, stride) of a row-major matrix an expert (or adapter), [E, K, N]."""
+        if w.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, w.dtype))
         if w.shape != (E, K, N):
             raise ValueError("%s must have shape %s, got %s" % (name, (E, K, N), tuple(w.shape)))
-        return self._mat(w[0], name, K, N, dtype), w.stride(0)
+        if w.get_device() != self.device:
+            raise ValueError("%s must be on cuda:%d, got %s" % (name, self.device, w.device))
+        stride, ld, step = w.stride()
+        if (step != 1 and N > 1) or (ld < N and K > 1):
+            raise ValueError("%s must be row-major (unit column stride), got strides %s" % (name, (stride, ld, step)))
+        return (ld if ld > N else (N or 1)), stride
 
     def moe_layer(self, x, logits, w1, w2, k, act="swiglu", b1=None, b2=None, renormalize=True, residual=None, out=None,
                   out_dtype=None, stream=None):

@@ -473,10 +473,11 @@ int launch_shrink(const LinArgs& a, const LinAdapt& ad, int num_sms, cudaStream_
     // A row's own cluster reads its A for itself: rows of one adapter read it again, from L2.
     const bool rows = a.M * a.K * ad.r <= (int64_t)16 << 20;
     p.work = rows ? p.M : (p.M + ROWS - 1) / ROWS;
-    // K is shared by as many CTAs as fit at once and have some 256 of it
+    // K is shared by as many CTAs as fit at once and have some 256 of it.  (8192 rows of 4096: 128 tiles by two
+    // CTAs each; by four, which is more than fit, FOUR)
     p.cluster = 1;
-    const int fit = (rows ? 4 : 3) * num_sms;
-    while (p.cluster < MAX_CLUSTER && p.cluster * p.work < fit && 2 * p.cluster * 256 <= p.K) p.cluster *= 2;
+    const int fit = (rows ? 4 : 2) * num_sms;
+    while (p.cluster < MAX_CLUSTER && 2 * p.cluster * p.work <= fit && 2 * p.cluster * 256 <= p.K) p.cluster *= 2;
     // (B is looked through beside the rest, by a CTA an SM)
     const int clusters = p.work + (p.lists > 0 ? (p.lists + num_sms + p.cluster - 1) / p.cluster : 0);
     cudaError_t e;
