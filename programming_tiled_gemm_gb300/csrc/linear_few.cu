@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) linear_few_kernel(FewParams
             // eight of K of one row's adapter
             const uint32_t at = smem_u32(mine + s * stage_bytes(MT));
             const int k = (b - base) * BATCH + kr * DEEP, m = k / ad.r, k0 = k - m * ad.r;
-            const int id = m < p.M ? ad.adapters[m] : -1;
+            const int id = m < p.M ? __ldcg(ad.adapters + m) : -1;
             const bool on = id >= 0 && id < ad.n && (ncol == 0 || in_range(wcol + ncol - 1, p.Nw));
             const uint16_t* B = ad.B + (on ? id * ad.b_stride + (int64_t)k0 * ad.ldb + wcol : 0);
 #pragma unroll

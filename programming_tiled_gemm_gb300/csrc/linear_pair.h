@@ -629,7 +629,8 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
             const uint32_t full0 = mapa_shared(smem_u32(full_bar), 0), tail_own = mapa_shared(smem_u32(tail_bar), rank);
             const uint32_t there0 = mapa_shared(smem_u32(there_bar), 0);
             bool listed = false;  // ADAPT: the lists are there
-            int place = 0;        // and the next block's place
+            bool first_tile = true;
+            int place = 0;  // the next block's place
             uint32_t place_phase = 0;
             while (ok && walk.next(it)) {
                 const int f0 = it.f0 * TILE_F;
@@ -686,8 +687,16 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                     if (ADAPT && adapts) {
                         // Once the ring has come round, the last tile's blocks have left their places (and there is
                         // time enough until this tile's are needed).
-                        if (seen == 1 && listed) flags_of(id, flags);
-                        if (seen == p.stages && listed) adapter_blocks(ad.places);
+                        if (seen == p.stages && !listed) {
+                            grid_dependency_wait();
+                            listed = true;
+                            count = word_now(list_at(it)), id = id_of(it, 0);
+                            seen = 0;
+                        } else if (seen == 1 && listed) {
+                            flags_of(id, flags);
+                        } else if (seen == (first_tile ? 2 : p.stages) && listed) {
+                            adapter_blocks(ad.places);
+                        }
                         ++seen;
                     }
                     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, abort_flag))) {
@@ -746,7 +755,10 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                     }
                     if (seen == 1) flags_of(id, flags);
                     adapter_blocks(1 << 30);
+                    first_tile = false;
                 }
+                // (what the next waits are for waits for the kernel before: their limit starts when it has ended)
+                if (ADAPT && !load_a) grid_dependency_wait();
             }
             if (!ok) aborted = true;
             __syncwarp();
@@ -784,6 +796,11 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAX_W);
                         const int kb1 = min(kb0 + kc, it.kb1);
                         for (int kb = kb0; kb < kb1; kb += KPS) {
+                            if (ADAPT && kb == kb0 + p.stages * KPS && !listed && it.kb1 == p.kb) {
+                                grid_dependency_wait();
+                                listed = true;
+                                count = word_now(list_at(it));
+                            }
                             if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, abort_flag))) {
                                 record_error(p.status, kDevTimeoutMma, abort_flag);
                                 ok = false;
@@ -869,6 +886,7 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                 __syncwarp();
             }
             // (the odd CTA's warp is here from the start)
+            if (ADAPT) grid_dependency_wait();
             if (!mbar_wait_while(smem_u32(drain_bar), 0, p.limit_ns, nullptr, progress)) {
                 record_error(p.status, kDevTimeoutDrain, abort_flag);
                 aborted = true;
@@ -1003,6 +1021,9 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
         // ---------------------------------------------------------------- epilogue (both CTAs)
+        // ADAPT: bias and residual are read through L1, which is certain to be fresh only behind this; and the limit
+        // of the first wait starts when the kernel before has ended.
+        if (ADAPT) grid_dependency_wait();
         const int q = warp & 3;             // TMEM lane quarter
         const int group = (warp - EPI_WARP0) / 4;   // takes column blocks group, group + 2, ...
         const int e = threadIdx.x - 32 * EPI_WARP0;

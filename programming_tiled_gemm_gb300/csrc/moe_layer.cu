@@ -440,6 +440,8 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
         for (int item = blockIdx.x; item < items && !dead; item += gridDim.x) {
             const int a = item / p.slabs, f = (item - a * p.slabs) * COLS, e = r.active[a];
             for (int step = 0; step < steps; ++step) {
+                // (a full ring is emptied once the first kernel has ended: the wait's limit starts there)
+                if (!UP && stage == 0 && phase == 1) grid_dependency_wait();
                 if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1, p.limit_ns, &abort_flag))) {
                     gave_up(kDevTimeoutProducer);
                     dead = true;

@@ -331,6 +331,18 @@ def test_a_wait_that_runs_out_is_reported(g):
     lib.close()
 
 
+def test_wait_limit_is_none_of_the_first_kernels_time(g):
+    """the product's waits may begin while the kernel that makes U is busy for longer than their limit"""
+    lib = g.Gemm(0)
+    s = make(5, 65536, 2048, 256, 6, 128, BF16, order="requests")
+    want = run(lib, s, "none")
+    lib.set_option(g.GEMM_OPT_WAIT_LIMIT_US, 60)
+    for _ in range(3):
+        assert torch.equal(run(lib, s, "none"), want)
+    assert lib.device_status() == g.GEMM_OK
+    lib.close()
+
+
 def test_refusals(lib, g):
     s = make(1, 12, 64, 64, 3, 16, BF16)
     x, w, a, b, ad = s["x"], s["w"], s["a"], s["b"], s["adapters"]

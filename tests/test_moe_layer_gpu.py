@@ -294,6 +294,18 @@ def test_back_to_back_calls_read_the_last_ones_results(lib):
     assert checked >= 4
 
 
+def test_wait_limit_is_none_of_the_first_kernels_time(g):
+    """the second kernel starts early, and may wait for the first for longer than its waits' limit"""
+    lib = g.Gemm(0)
+    s = make(7, 8, 16, 4096, 4096, BF16)
+    want = lib.moe_layer(s["x"], s["logits"], s["w1"], s["w2"], 8)
+    lib.set_option(g.GEMM_OPT_WAIT_LIMIT_US, 40)  # (the first kernel takes some 150)
+    for _ in range(3):
+        assert torch.equal(lib.moe_layer(s["x"], s["logits"], s["w1"], s["w2"], 8), want)
+    assert lib.device_status() == g.GEMM_OK
+    lib.close()
+
+
 def test_refusals(lib, g):
     s = make(1, 4, 8, 64, 32, BF16)
     x, l, w1, w2 = s["x"], s["logits"], s["w1"], s["w2"]
