@@ -2,12 +2,13 @@
 // adapter, rounded to 16 bits as an operand of the product that follows (linear_pair.h, linear_few.cu), and
 // for that product's tiles the lists of their adapters and which of these have a B with infinities or NaN.
 //
-// Few rows (shrink_rows_kernel): a cluster a row, K shared by its CTAs, FMAs in fp32; bound by the reads of
-// A, 16 bytes a thread.  Many rows (shrink_tiles_kernel): a cluster takes 64 rows and shares K; a ring of
-// asynchronous copies brings 64 of K of X and of an adapter's A, for one adapter of the tile's rows after the
-// other, and mma.sync multiplies them (the rank is too narrow a side for tcgen05's 128 or 256); a row takes the
-// sums of its own adapter only, so that no adapter's NaN reaches another's rows.  Bound by X's bytes where
-// requests lie together.  The CTAs' parts of K are added in order through distributed shared memory.
+// A few rows or a short K (shrink_rows_kernel): a cluster a row, K shared by its CTAs, FMAs in fp32; bound by the
+// reads of A, 16 bytes a thread.  More (shrink_groups_kernel): a cluster takes up to 64 rows of ONE adapter,
+// wherever they lie, and shares K; so every A and every row of X is read once, whatever the rows' order.
+// Which rows is found by every CTA for itself, by two passes over the rows' indices.  A ring of asynchronous
+// copies brings them, 128 of K a stage, and mma.sync multiplies (rows of other adapters would only be masked
+// on tcgen05's 128 or 256 rows, and the rank is narrower still).  The CTAs' parts of K are added in order
+// through distributed shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -252,16 +253,16 @@ __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
     if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
 }
 
-// ------------------------------------------------------------------ a cluster 64 rows
+// ------------------------------------------------------------------ a cluster up to 64 rows of an adapter
 
 constexpr int ROWS = 64;
 constexpr int RING = 3;                    // stages
 constexpr int depth_of(int rs) { return rs <= 64 ? 128 : 64; }  // of K a stage
 constexpr int x_pitch(int rs) { return depth_of(rs) * 2 + 16; }  // bytes of a row of X: rows 16 bytes apart in the banks
 constexpr int a_pitch(int rs) { return rs * 2 + 16; }
-constexpr int tile_stage(int rs) { return ROWS * x_pitch(rs) + depth_of(rs) * a_pitch(rs); }
-constexpr int tiles_smem(int rs) { return RING * tile_stage(rs); }
-static_assert(tiles_smem(16) >= ROWS * (16 + 1) * 4 && tiles_smem(128) >= ROWS * (128 + 1) * 4, "the sums lie in the ring");
+constexpr int group_stage(int rs) { return ROWS * x_pitch(rs) + depth_of(rs) * a_pitch(rs); }
+constexpr int sums_bytes(int rs) { return (ROWS + WARPS * 16) * (rs + 1) * 4; }  // in the ring's place afterwards
+constexpr int groups_smem(int rs) { return RING * group_stage(rs) > sums_bytes(rs) ? RING * group_stage(rs) : sums_bytes(rs); }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t at, uint32_t (&r)[4])
 {
@@ -288,91 +289,209 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Warps: 16 rows (of 64) x half of every stage's K.
+// The sum over the block's threads before this one, and of all.
+__device__ __forceinline__ int sum_before(int v, int* per_warp, int& all)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += o;
+    }
+    if (lane == 31) per_warp[warp] = s;
+    __syncthreads();
+    all = 0;
+    s -= v;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) s += per_warp[w];
+        all += per_warp[w];
+    }
+    __syncthreads();
+    return s;
+}
+
+// The adapters of rows m .. m + 3 (m a multiple of 4), -1 past the last row.
+__device__ __forceinline__ int4 four_adapters(const ShrinkParams& p, int m)
+{
+    if (m + 4 > p.M || (reinterpret_cast<uintptr_t>(p.adapters) & 15) != 0)
+        return make_int4(adapter_of(p, m), adapter_of(p, m + 1), adapter_of(p, m + 2), adapter_of(p, m + 3));
+    int4 v = *reinterpret_cast<const int4*>(p.adapters + m);
+    v.x = v.x >= 0 && v.x < p.n ? v.x : -1, v.y = v.y >= 0 && v.y < p.n ? v.y : -1;
+    v.z = v.z >= 0 && v.z < p.n ? v.z : -1, v.w = v.w >= 0 && v.w < p.n ? v.w : -1;
+    return v;
+}
+
+// How many rows every adapter has: a word each in `counts`.
+__device__ __forceinline__ void count_rows(const ShrinkParams& p, int* counts)
+{
+    constexpr int FLY = 4;
+    for (int i = threadIdx.x; i < p.n; i += THREADS) counts[i] = 0;
+    __syncthreads();
+    for (int b = 0; b < p.M; b += FLY * 4 * THREADS) {
+        int4 v[FLY];
+#pragma unroll
+        for (int i = 0; i < FLY; ++i) v[i] = four_adapters(p, b + (i * THREADS + (int)threadIdx.x) * 4);
+#pragma unroll
+        for (int i = 0; i < FLY; ++i) {
+            // (a warp's 128 rows often have one adapter: one addition for all of them)
+            const int first = __shfl_sync(0xffffffffu, v[i].x, 0);
+            if (__all_sync(0xffffffffu, v[i].x == first && v[i].y == first && v[i].z == first && v[i].w == first)) {
+                if (first >= 0 && threadIdx.x % 32 == 0) atomicAdd(&counts[first], 128);
+                continue;
+            }
+            if (v[i].x >= 0) atomicAdd(&counts[v[i].x], 1);
+            if (v[i].y >= 0) atomicAdd(&counts[v[i].y], 1);
+            if (v[i].z >= 0) atomicAdd(&counts[v[i].z], 1);
+            if (v[i].w >= 0) atomicAdd(&counts[v[i].w], 1);
+        }
+    }
+    __syncthreads();
+}
+
+// The `group`-th of the adapters' groups of 64 rows: its adapter (-1: there are not as many), its rows in
+// `rows` and their number.
+__device__ __forceinline__ int find_group(const ShrinkParams& p, int group, const int* counts, int* rows, int& n_rows)
+{
+    __shared__ int per_warp[WARPS], found_id, found_chunk;
+    constexpr int FLY = 4;
+    if (threadIdx.x == 0) found_id = -1, found_chunk = 0;
+    __syncthreads();
+    // the adapter that holds the group: a thread has `each` neighbouring adapters
+    const int each = (p.n + THREADS - 1) / THREADS, i0 = min((int)threadIdx.x * each, p.n), i1 = min(i0 + each, p.n);
+    int own = 0, all;
+    for (int i = i0; i < i1; ++i) own += (counts[i] + ROWS - 1) / ROWS;
+    int before = sum_before(own, per_warp, all);
+    if (group >= before && group < before + own)
+        for (int i = i0; i < i1; ++i) {
+            const int g = (counts[i] + ROWS - 1) / ROWS;
+            if (group < before + g) {
+                found_id = i, found_chunk = group - before;
+                break;
+            }
+            before += g;
+        }
+    __syncthreads();
+    const int id = found_id;
+    if (id < 0) return -1;
+    // its rows, in order: a warp has a stretch of them, 128 at a time
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int skip = found_chunk * ROWS, stretch = (p.M + 128 * WARPS - 1) / (128 * WARPS) * 128, m0 = warp * stretch;
+    const int m1 = min(m0 + stretch, p.M);
+    int mine = 0;
+    for (int m = m0; m < m1; m += 128 * FLY) {
+        int4 v[FLY];
+#pragma unroll
+        for (int i = 0; i < FLY; ++i)
+            v[i] = m + 128 * i < m1 ? four_adapters(p, m + 128 * i + lane * 4) : make_int4(-1, -1, -1, -1);
+#pragma unroll
+        for (int i = 0; i < FLY; ++i) mine += (v[i].x == id) + (v[i].y == id) + (v[i].z == id) + (v[i].w == id);
+    }
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) per_warp[warp] = mine;
+    __syncthreads();
+    int at = -skip;
+    all = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) at += per_warp[w];
+        all += per_warp[w];
+    }
+    if (at + mine > 0)
+        for (int m = m0; m < m1 && at < ROWS; m += 128) {
+            const int4 v = four_adapters(p, m + lane * 4);
+            const bool is[4] = {v.x == id, v.y == id, v.z == id, v.w == id};
+            int place = at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const unsigned who = __ballot_sync(0xffffffffu, is[j]);
+                place += __popc(who & ((1u << lane) - 1));
+                at += __popc(who);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (is[j]) {
+                    if (place >= 0 && place < ROWS) rows[place] = m + lane * 4 + j;
+                    ++place;
+                }
+        }
+    n_rows = min(ROWS, all - skip);
+    __syncthreads();
+    return id;
+}
+
+// Warps: 16 of the rows x a part of every stage's K, more parts where there are fewer rows.
 template <bool BF16, int RS>
-__global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
+__global__ void __launch_bounds__(THREADS, RS <= 64 ? 2 : 1) shrink_groups_kernel(ShrinkParams p)
 {
     constexpr int NT = RS / 8, PITCH = a_pitch(RS), DEPTH = depth_of(RS), X_PITCH = x_pitch(RS), LINE = DEPTH / 8;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) int ids[ROWS];
-    __shared__ int list[ROWS], count;
+    __shared__ int rows[ROWS];
+    int* const counts = reinterpret_cast<int*>(smem + groups_smem(RS));
     grid_dependency_wait();
     grid_dependents_launch();
-    const int C = p.cluster, rank = blockIdx.x % C, tile = blockIdx.x / C;
-    if (tile >= p.work) {
+    const int C = p.cluster, rank = blockIdx.x % C;
+    if (blockIdx.x / C >= p.work) {
         const int extra = blockIdx.x - p.work * C;
         if (extra < p.lists) make_list(p, extra);
         else if (p.bad) look_through<BF16>(p, extra - p.lists, gridDim.x - p.work * C - p.lists);
         return;
     }
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row0 = tile * ROWS;
-    if ((int)threadIdx.x < ROWS) ids[threadIdx.x] = adapter_of(p, row0 + threadIdx.x);
-    __syncthreads();
-    if (warp == 0) {
-        // the tile's adapters, in the order of their first rows
-        int n = 0;
-        for (int h = 0; h < ROWS; h += 32) {
-            const int j = h + lane, id = ids[j];
-            bool is = id >= 0;
-            for (int i = 0; i < j; ++i) is = is && ids[i] != id;
-            const unsigned who = __ballot_sync(0xffffffffu, is);
-            if (is) list[n + __popc(who & ((1u << lane) - 1))] = id;
-            n += __popc(who);
-        }
-        if (lane == 0) count = n;
-    }
-    __syncthreads();
-    const int adapters = count;
-    if (adapters == 0) return;  // (the whole cluster)
-    const uint32_t ring = smem_u32(smem);
-    const int kb = (p.K + DEPTH - 1) / DEPTH, kb0 = kb * rank / C, nb = kb * (rank + 1) / C - kb0, steps = adapters * nb;
-    const int rg = warp % 4, kh = warp / 4;
-    const int id0 = ids[rg * 16 + lane / 4], id1 = ids[rg * 16 + lane / 4 + 8];  // of this thread's two rows
-    float sum[NT][4], acc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[t][i] = 0.f;
-    // the loader's adapter and k-block, RING - 1 stages ahead
-    int l_step = 0, l_adapter = 0, l_block = 0;
-    const auto load = [&] {
-        if (l_step < steps) {
-            const int k0 = (kb0 + l_block) * DEPTH;
-            const uint32_t at = ring + l_step % RING * tile_stage(RS);
-#pragma unroll
-            for (int i = 0; i < ROWS * LINE / THREADS; ++i) {
-                const int q = threadIdx.x + i * THREADS, row = q / LINE, k = k0 + q % LINE * 8;
-                int n = row0 + row < p.M ? max(0, min(8, p.K - k)) : 0;
-                if (n > 0 && !in_range(row0 + row, p.M)) n = 0;
-                copy_async_16(at + row * X_PITCH + q % LINE * 16, n > 0 ? p.X + (int64_t)(row0 + row) * p.ldx + k : p.X, 2 * n);
-            }
-            const uint16_t* A = p.A + list[l_adapter] * p.a_stride;
-#pragma unroll
-            for (int q = threadIdx.x; q < DEPTH * NT; q += THREADS) {
-                const int k = q / NT, c = q % NT;
-                int n = k0 + k < p.K && c * 8 < p.r ? 8 : 0;
-                if (n > 0 && !in_range(k0 + k, p.K)) n = 0;
-                copy_async_16(at + ROWS * X_PITCH + k * PITCH + c * 16, n > 0 ? A + (int64_t)(k0 + k) * p.lda + c * 8 : p.A, 2 * n);
-            }
-            ++l_step;
-            if (++l_block == nb) l_block = 0, ++l_adapter;
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    for (int i = 0; i < RING - 1; ++i) load();
-    for (int d = 0, s = 0; d < adapters && nb > 0; ++d) {
+    count_rows(p, counts);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int group = blockIdx.x / C;; group += p.work) {
+        int n_rows = 0;
+        const int id = find_group(p, group, counts, rows, n_rows);
+        if (id < 0) return;  // (the whole cluster)
+        const uint32_t ring = smem_u32(smem);
+        const int kb = (p.K + DEPTH - 1) / DEPTH, kb0 = kb * rank / C, steps = kb * (rank + 1) / C - kb0;
+        // 16 rows a warp, and `parts` warps share a stage's K
+        const int tiles = n_rows <= 16 ? 1 : n_rows <= 32 ? 2 : 4, parts = WARPS / tiles, rg = warp % tiles, part = warp / tiles;
+        float acc[NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
-        for (int b = 0; b < nb; ++b, ++s) {
+        // what a thread copies of every stage: the same 16 bytes of some rows of X and of some rows of A
+        constexpr int XS = ROWS * LINE / THREADS, AS = DEPTH * NT / THREADS > 0 ? DEPTH * NT / THREADS : 1;
+        const int xc = threadIdx.x % LINE, xr = threadIdx.x / LINE, ac = threadIdx.x % NT, ar = threadIdx.x / NT;
+        const uint16_t* xp[XS];
+#pragma unroll
+        for (int i = 0; i < XS; ++i) {
+            const int row = xr + i * (THREADS / LINE);
+            xp[i] = p.X + (row < n_rows && in_range(rows[row], p.M) ? (int64_t)rows[row] * p.ldx : 0) + (int64_t)kb0 * DEPTH + xc * 8;
+        }
+        const uint16_t* ap = p.A + id * p.a_stride + (int64_t)(kb0 * DEPTH + ar) * p.lda + ac * 8;
+        int l_step = 0;
+        const auto load = [&] {
+            if (l_step < steps) {
+                const int k0 = (kb0 + l_step) * DEPTH;
+                const uint32_t at = ring + l_step % RING * group_stage(RS);
+                const int nx = 2 * max(0, min(8, p.K - k0 - xc * 8));
+#pragma unroll
+                for (int i = 0; i < XS; ++i) {
+                    const int row = xr + i * (THREADS / LINE), n = row < n_rows ? nx : 0;
+                    if (row < tiles * 16) copy_async_16(at + row * X_PITCH + xc * 16, n > 0 ? xp[i] + l_step * DEPTH : p.X, n);
+                }
+#pragma unroll
+                for (int i = 0; i < AS; ++i) {
+                    const int k = ar + i * (THREADS / NT);
+                    if (DEPTH * NT < THREADS && k >= DEPTH) break;
+                    const int n = k0 + k < p.K && ac * 8 < p.r && in_range(k0 + k, p.K) ? 16 : 0;
+                    copy_async_16(at + ROWS * X_PITCH + k * PITCH + ac * 16,
+                                  n > 0 ? ap + (int64_t)(l_step * DEPTH + i * (THREADS / NT)) * p.lda : p.A, n);
+                }
+                ++l_step;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int i = 0; i < RING - 1; ++i) load();
+        for (int s = 0; s < steps; ++s) {
             asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
             __syncthreads();
             load();  // into the stage that was multiplied before the barrier
-            const uint32_t xs = ring + s % RING * tile_stage(RS), as = xs + ROWS * X_PITCH;
-#pragma unroll
-            for (int h = 0; h < DEPTH / 32; ++h) {
-                const int k = kh * (DEPTH / 2) + h * 16;
+            const uint32_t xs = ring + s % RING * group_stage(RS), as = xs + ROWS * X_PITCH;
+#pragma unroll 4
+            for (int k = part * 16; k < DEPTH; k += parts * 16) {
                 uint32_t xf[4];  // (rows 0..7, k 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
                 ldsm_x4(xs + (rg * 16 + lane % 16) * X_PITCH + (k + lane / 16 * 8) * 2, xf);
 #pragma unroll
@@ -384,53 +503,52 @@ __global__ void __launch_bounds__(THREADS) shrink_tiles_kernel(ShrinkParams p)
                 }
             }
         }
-        const int id = list[d];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (id0 == id) sum[t][0] = acc[t][0], sum[t][1] = acc[t][1];
-            if (id1 == id) sum[t][2] = acc[t][2], sum[t][3] = acc[t][3];
-        }
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-    // [row][rank] of both halves, then of the cluster's CTAs, in order
-    float* part = reinterpret_cast<float*>(smem);
-    const int row = rg * 16 + lane / 4, col = lane % 4 * 2;
-    constexpr int FP = RS + 1;
-    for (int h = 0; h < 2; ++h) {
-        if (kh == h)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float* o = part + (row + i / 2 * 8) * FP + t * 8 + col + i % 2;
-                    *o = h ? *o + sum[t][i] : sum[t][i];
-                }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-    }
-    if (C > 1) cluster_sync_all();
-    for (int q = rank * THREADS + threadIdx.x; q < ROWS * RS; q += C * THREADS) {
-        const int i = q / RS, c = q % RS, id = ids[i];
-        if (id < 0) continue;
-        const uint32_t at = smem_u32(part + i * FP + c);
-        float t[MAX_CLUSTER], v = 0.f;
+        // [row][rank] of the warps, of a stage's parts, then of the cluster's CTAs, in order
+        constexpr int FP = RS + 1;
+        float* const own = reinterpret_cast<float*>(smem) + ROWS * FP + warp * 16 * FP;
+        float* const sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int w = 0; w < MAX_CLUSTER; ++w)
-            if (w < C) t[w] = C > 1 ? ld_shared_cluster_f32(mapa_shared(at, w)) : part[i * FP + c];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int w = 0; w < MAX_CLUSTER; ++w)
-            if (w < C) v += t[w];
-        if (p.scales) v *= p.scales[id];
-        if (in_range(row0 + i, p.M)) p.u[(int64_t)(row0 + i) * RS + c] = to_16<BF16>(c < p.r ? v : 0.f);
+            for (int i = 0; i < 4; ++i) own[(lane / 4 + i / 2 * 8) * FP + t * 8 + lane % 4 * 2 + i % 2] = acc[t][i];
+        __syncthreads();
+        for (int q = threadIdx.x; q < n_rows * RS; q += THREADS) {
+            const int i = q / RS, c = q % RS;
+            const float* from = sums + ROWS * FP + i * FP + c;  // (row i: row i % 16 of warp i / 16)
+            float v = 0.f;
+            for (int h = 0; h < parts; ++h) v += from[h * tiles * 16 * FP];
+            sums[i * FP + c] = v;
+        }
+        __syncthreads();
+        if (C > 1) cluster_sync_all();
+        const float scale = p.scales ? p.scales[id] : 1.f;
+        for (int q = rank * THREADS + threadIdx.x; q < n_rows * RS; q += C * THREADS) {
+            const int i = q / RS, c = q % RS;
+            const uint32_t at = smem_u32(sums + i * FP + c);
+            float t[MAX_CLUSTER], v = 0.f;
+#pragma unroll
+            for (int w = 0; w < MAX_CLUSTER; ++w)
+                if (w < C) t[w] = C > 1 ? ld_shared_cluster_f32(mapa_shared(at, w)) : sums[i * FP + c];
+#pragma unroll
+            for (int w = 0; w < MAX_CLUSTER; ++w)
+                if (w < C) v += t[w];
+            if (in_range(rows[i], p.M)) p.u[(int64_t)rows[i] * RS + c] = to_16<BF16>(c < p.r ? v * scale : 0.f);
+        }
+        // (nobody leaves or writes over its sums while they are read)
+        if (C > 1) cluster_sync_all();
+        else __syncthreads();
     }
-    if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
 }
 
+// `most`: of shared memory, that any launch of the kernel takes.
 template <typename Kernel>
-cudaError_t launch(Kernel kern, int smem, std::atomic<uint64_t>* allowed, const ShrinkParams& p, int clusters, cudaStream_t s)
+cudaError_t launch(Kernel kern, int smem, int most, std::atomic<uint64_t>* allowed, const ShrinkParams& p, int clusters,
+                   cudaStream_t s)
 {
     if (allowed) {
-        const cudaError_t e = allow_smem(kern, smem, *allowed);
+        const cudaError_t e = allow_smem(kern, most, *allowed);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -451,10 +569,13 @@ cudaError_t launch(Kernel kern, int smem, std::atomic<uint64_t>* allowed, const 
 }
 
 template <bool BF16, int RS>
-cudaError_t launch_tiles(const ShrinkParams& p, int clusters, cudaStream_t s)
+cudaError_t launch_groups(const ShrinkParams& p, int clusters, cudaStream_t s)
 {
     static std::atomic<uint64_t> allowed{0};
-    return launch(shrink_tiles_kernel<BF16, RS>, tiles_smem(RS), &allowed, p, clusters, s);
+    // (behind the ring a word an adapter; as much as any number of them takes is asked for)
+    static_assert(groups_smem(RS) + kMaxAdapters * 4 <= 232448 - 4096, "shared memory of a CTA");
+    return launch(shrink_groups_kernel<BF16, RS>, groups_smem(RS) + p.n * 4, groups_smem(RS) + kMaxAdapters * 4, &allowed, p,
+                  clusters, s);
 }
 
 }  // namespace
@@ -470,30 +591,32 @@ int launch_shrink(const LinArgs& a, const LinAdapt& ad, int num_sms, cudaStream_
     p.u = ad.u, p.tile_rows = ad.tile_rows;
     if (ad.tile_rows > 0) p.tiles = ad.tiles, p.slot = ad.slot, p.bad = ad.bad;
     p.lists = ad.tile_rows > 0 ? (p.M + ad.tile_rows - 1) / ad.tile_rows : 0;
-    // A row's own cluster reads its A for itself: rows of one adapter read it again, from L2.
-    const bool rows = a.M * a.K * ad.r <= (int64_t)16 << 20;
-    p.work = rows ? p.M : (p.M + ROWS - 1) / ROWS;
-    // K is shared by as many CTAs as fit at once and have some 256 of it.  (8192 rows of 4096: 128 tiles by two
-    // CTAs each; by four, which is more than fit, FOUR)
+    // A cluster a row reads its A for itself, rows of one adapter again from L2, but is done sooner than the
+    // rows of an adapter are found.  us of the whole call with a cluster a row and with groups (adapters at
+    // random; M x K x rank): 32 x 4096 x 16 24.5 25.5, 77 x 1000 x 24 15.8 20.0, 256 x 1024 x 16 19.8 19.5,
+    // 64 x 4096 x 16 30.3 29.0, 256 x 4096 x 16 35.6 32.3, 32 x 4096 x 64 39.4 39.3, 128 x 4096 x 64 52.9 46.8
+    const bool rows = a.M * a.K * ad.r <= (int64_t)4 << 20 || ad.tile_rows == 0;
+    const int64_t groups = (a.M < ad.n ? a.M : ad.n) + a.M / ROWS, fit = (rows ? 4 : 2) * num_sms;  // at most, and CTAs
+    p.work = rows ? p.M : (int)(groups < fit ? groups : fit);
+    // K is shared by as many CTAs as fit at once and have some 256 (128) of it
     p.cluster = 1;
-    const int fit = (rows ? 4 : 2) * num_sms;
-    while (p.cluster < MAX_CLUSTER && 2 * p.cluster * p.work <= fit && 2 * p.cluster * 256 <= p.K) p.cluster *= 2;
+    while (p.cluster < MAX_CLUSTER && 2 * p.cluster * p.work <= fit && 2 * p.cluster * (rows ? 256 : 128) <= p.K) p.cluster *= 2;
     // (B is looked through beside the rest, by a CTA an SM)
     const int clusters = p.work + (p.lists > 0 ? (p.lists + num_sms + p.cluster - 1) / p.cluster : 0);
     cudaError_t e;
     if (rows) {
-        e = a.bf16 ? launch(shrink_rows_kernel<true>, 0, nullptr, p, clusters, stream)
-                   : launch(shrink_rows_kernel<false>, 0, nullptr, p, clusters, stream);
+        e = a.bf16 ? launch(shrink_rows_kernel<true>, 0, 0, nullptr, p, clusters, stream)
+                   : launch(shrink_rows_kernel<false>, 0, 0, nullptr, p, clusters, stream);
     } else {
-        const auto tiles = a.bf16 ? (p.rs == 16   ? launch_tiles<true, 16>
-                                     : p.rs == 32 ? launch_tiles<true, 32>
-                                     : p.rs == 64 ? launch_tiles<true, 64>
-                                                  : launch_tiles<true, 128>)
-                                  : (p.rs == 16   ? launch_tiles<false, 16>
-                                     : p.rs == 32 ? launch_tiles<false, 32>
-                                     : p.rs == 64 ? launch_tiles<false, 64>
-                                                  : launch_tiles<false, 128>);
-        e = tiles(p, clusters, stream);
+        const auto groups_of = a.bf16 ? (p.rs == 16   ? launch_groups<true, 16>
+                                         : p.rs == 32 ? launch_groups<true, 32>
+                                         : p.rs == 64 ? launch_groups<true, 64>
+                                                      : launch_groups<true, 128>)
+                                      : (p.rs == 16   ? launch_groups<false, 16>
+                                         : p.rs == 32 ? launch_groups<false, 32>
+                                         : p.rs == 64 ? launch_groups<false, 64>
+                                                      : launch_groups<false, 128>);
+        e = groups_of(p, clusters, stream);
     }
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     *launches += 1;

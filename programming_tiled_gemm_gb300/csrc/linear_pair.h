@@ -684,6 +684,8 @@ __device__ __forceinline__ void linear_pair_body(const CUtensorMap& tmA, const C
                     }
                 };
                 for (int kb = it.kb0; kb < it.kb1; kb += KPS) {
+                    if (ADAPT && !load_a && it.kb1 == p.kb && seen++ == p.stages)
+                        grid_dependency_wait();  // (the MMA warp does there: the next wait's limit starts behind it)
                     if (ADAPT && adapts) {
                         // Once the ring has come round, the last tile's blocks have left their places (and there is
                         // time enough until this tile's are needed).
