@@ -125,7 +125,7 @@ def check(got, s, act, rows=slice(None)):
     (8, 4096, 512, 40, 16, "silu", False, True, BF16, "random"),
     (7, 136, 1032, 3, 128, "none", True, False, F16, "one"),
     (4, 256, 256, 3, 16, "none", False, False, BF16, "none"),
-    # the tensor-core kernel, rows of U by a cluster each
+    # the tensor-core kernel, a cluster a row
     (9, 64, 64, 4, 8, "none", False, False, BF16, "random"),
     (16, 2048, 2048, 16, 16, "none", False, True, BF16, "random"),
     (33, 4096, 1024, 64, 16, "swiglu", False, False, BF16, "random"),
@@ -135,7 +135,7 @@ def check(got, s, act, rows=slice(None)):
     (130, 512, 512, 300, 16, "none", False, False, BF16, "random"),
     (40, 512, 256, 3, 128, "none", False, False, F16, "random"),
     (50, 512, 256, 3, 72, "swiglu", True, True, BF16, "requests"),
-    # the tensor-core kernel, tiles of 64 rows of U
+    # the tensor-core kernel, groups of 64 rows
     (300, 4096, 512, 6, 64, "none", False, False, BF16, "requests"),
     (1000, 2000, 1032, 8, 16, "silu", True, True, BF16, "requests"),
     (777, 1032, 776, 20, 48, "gelu", True, False, F16, "random"),
@@ -143,6 +143,10 @@ def check(got, s, act, rows=slice(None)):
     (520, 16384, 128, 2, 32, "none", False, False, BF16, "requests"),
     (4100, 1024, 2048, 8, 64, "swiglu", False, False, BF16, "requests"),
     (700, 1024, 512, 4, 16, "none", False, False, BF16, "none"),
+    # more groups than are under way at once, most of them small; none of any adapter but one
+    (5000, 512, 64, 600, 16, "none", False, False, BF16, "random"),
+    (300, 2048, 128, 8192, 8, "none", False, False, F16, "random"),
+    (1500, 1024, 256, 3, 32, "none", False, False, BF16, "one"),
 ])
 def test_adapted(lib, M, K, N, n, r, act, bias, residual, dtype, order):
     s = make(M + K + N, M, K, N, n, r, dtype, act, bias, residual, order)
@@ -212,6 +216,17 @@ def test_nan_stays_with_its_rows(lib, M, order, value):
         assert torch.equal(got[~mine], clean[~mine]), name
         if bool(mine.any()):
             assert not bool((got if name == "a" else got[:, 130])[mine].isfinite().any()), name
+
+
+def test_indices_that_start_anywhere(lib):
+    """rows' indices off every 16-byte boundary: the same results"""
+    s = make(8, 1001, 1024, 128, 5, 16, BF16, order="requests")
+    want = run(lib, s, "none")
+    check(want, s, "none")
+    for off in (1, 2, 3):
+        big = torch.full((1001 + 8,), 77, device="cuda", dtype=torch.int32)
+        big[off:off + 1001] = s["adapters"]
+        assert torch.equal(run(lib, dict(s, adapters=big[off:off + 1001]), "none"), want)
 
 
 @pytest.mark.parametrize("scales", [True, False])
