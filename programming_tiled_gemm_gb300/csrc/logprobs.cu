@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
         int last_i = -1;
         const auto flush = [&] {
             __syncwarp();
-            best = merge_best(best, sort_keys(lane < pending ? wait[lane] : 0ull));
+            const uint64_t sorted = sort_keys(lane < pending ? wait[lane] : 0ull);
+            best = last_i == -1 ? sorted : merge_best(best, sorted);  // (-1: the first; all but a warp's last flush are of 32)
             __syncwarp();
             if (lane + 32 < pending) wait[lane] = wait[lane + 32];
             pending = max(pending - 32, 0);
