@@ -11,15 +11,26 @@
 // value), z c would overflow; any logit but m itself is then further off than exp can tell, so
 // p is 1 / n at the n logits that equal m.
 //
-// Alternatives: the threads' maxima are there already.  The `top` best logits of a CTA's part all
-// belong to threads whose maximum is among the `top` largest maxima, and none of them is below the
-// smallest of these.  So only those threads' logits are read again (20 of 256, from L2); the few
-// that are no worse than that bound wait in shared memory until a warp has 32, which it sorts and
-// merges with its best in 20 exchanges of 64-bit keys of logit and index.
+// Alternatives: the pass leaves the maxima of units: 64 bytes (four lanes) of a row of the block's vectors, in one or
+// more of its batches, so that there are 32 to 256 units a CTA.  The `top` best logits of a CTA's part all belong to
+// units whose maximum is among the `top` largest, and none of them is below the smallest of these.  So only those
+// units are read again; the few logits that are no worse than that bound wait in shared memory until a warp has 32,
+// which it sorts and merges with its best in 6 exchanges of 64-bit keys of logit and index.
 //
 // A cluster of up to 8 CTAs shares a row where there are few (their sums and lists go to the
 // first CTA's shared memory); rows are read with 16-byte loads from the first 16-byte boundary
 // on, wherever they start.  One launch each, no workspace, sums in a fixed order.
+//
+// Bound by memory where the rows fill the SMs, next by the exponentials (16 a cycle and SM: two thirds of the
+// reading's time at 16 bits); short calls by latency.  Measured (GPU time; bf16 where not said otherwise):
+//   4096 x 131072: forward 158 us, 6.8 TB/s; with 1 or 20 alternatives 193 and 229; the gradient 309, 6.95 TB/s
+//   1000 x 50257 with entropy: 27 us, 3.7 TB/s (one wave of CTAs, 12 batches a thread), its gradient 34, 5.9 TB/s
+//   64 x 131072 with entropy: 8.7 us; with 20 alternatives 15.6; 1 x 32000 fp32: 4.9 and 10.8
+// Dropped: every logit offered to sorted lists as the row goes by (64 x 131072, 20 alternatives: 51 us); one maximum a
+// thread as the unit (its 16 bytes cost whole sectors again: 4096 x 131072 286 us); units ranked by counting (241, and
+// 144 instead of 109 for the best of 4096 x 32000 fp32); persistent blocks for the gradient (552 instead of 494 both
+// ways); logits through a ring of asynchronous copies two to four batches ahead instead of one in registers (1000 x
+// 50257: 27.5 to 29.3 instead of 27.1); sums two at a time (f32x2) take 161 us where single ones took 169.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,6 +44,7 @@ namespace {
 constexpr int WARPS = 8, THREADS = 32 * WARPS;
 constexpr int MAX_CLUSTER = 8;
 constexpr int FLY = 4;  // 16-byte loads of a thread in a batch
+constexpr int MAX_UNITS = 256;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float FLOOR = -1e4f;  // of exponents: exp2 is 0 there
 
@@ -224,6 +236,29 @@ __device__ __forceinline__ uint64_t sort_keys(uint64_t k)
         for (int d = n / 2; d > 0; d /= 2) k = exchange(k, d, ((lane & d) == 0) == ((lane & n) == 0 || n == 32));
     return k;
 }
+// The same with values alone (no NaN), and the 32 largest of two sorted warps of them, sorted.
+__device__ __forceinline__ float exchange(float v, int d, bool larger)
+{
+    const float o = __shfl_xor_sync(0xffffffffu, v, d);
+    return larger ? fmaxf(v, o) : fminf(v, o);
+}
+__device__ __forceinline__ float sort_values(float v)
+{
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int n = 2; n <= 32; n *= 2)
+#pragma unroll
+        for (int d = n / 2; d > 0; d /= 2) v = exchange(v, d, ((lane & d) == 0) == ((lane & n) == 0 || n == 32));
+    return v;
+}
+__device__ __forceinline__ float merge_values(float a, float b)
+{
+    const int lane = threadIdx.x % 32;
+    float v = fmaxf(a, __shfl_sync(0xffffffffu, b, 31 - lane));
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) v = exchange(v, d, (lane & d) == 0);
+    return v;
+}
 // The 32 largest of two sorted warps of keys, sorted.
 __device__ __forceinline__ uint64_t merge_best(uint64_t a, uint64_t b)
 {
@@ -256,15 +291,15 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     __shared__ float part_m[LISTS], part_s[LISTS], part_q[LISTS];
     __shared__ uint64_t lists_best[TOP ? LISTS : 1][TOP ? kMaxTop : 1];
     __shared__ uint64_t waiting[TOP ? WARPS : 1][TOP ? 64 : 1];
-    __shared__ __align__(16) float high_of[TOP ? THREADS : 4];  // each thread's largest logit
-    __shared__ uint16_t chosen[TOP ? THREADS : 1];              // threads with the largest of them
+    __shared__ __align__(16) float high_of[TOP ? MAX_UNITS : 4];  // each unit's largest logit
+    __shared__ uint16_t chosen[TOP ? MAX_UNITS : 1];              // units with the largest of them
     __shared__ int chosen_n;
-    __shared__ uint32_t bound;  // the key of the smallest of these: `top` logits are no worse
+    __shared__ float sorted_of[TOP ? WARPS : 1][TOP ? 32 : 1];  // each warp's units' largest
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int C = p.cluster, rank = blockIdx.x % C;
     const int64_t r = blockIdx.x / C;
     const int nthreads = blockDim.x, warps = nthreads / 32;
-    if (TOP && threadIdx.x == 0) bound = 0xffffffffu, chosen_n = 0;
+    if (TOP && threadIdx.x == 0) chosen_n = 0;
     if (C > 1) cluster_sync_all();  // (the first CTA's shared memory is written by the others)
     else if (TOP) __syncthreads();
     grid_dependency_wait();
@@ -296,6 +331,18 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     };
     if (rank == 0 && head > 0) edge(0, head);
 
+    // units: `in_row` next to each other in a row of vectors, the next ones `per_unit` batches on
+    const int in_row = nthreads / 4, batch = FLY * nthreads;
+    const int per_unit = TOP ? max(1, ((v1 - v0 + batch - 1) / batch + MAX_UNITS / in_row - 1) / (MAX_UNITS / in_row)) : 0;
+    int units = 0, in_unit = 0;
+    float unit_high = -INFINITY;
+    const auto end_unit = [&] {
+        unit_high = fmaxf(unit_high, __shfl_xor_sync(0xffffffffu, unit_high, 1));
+        unit_high = fmaxf(unit_high, __shfl_xor_sync(0xffffffffu, unit_high, 2));
+        if (lane % 4 == 0) high_of[units + threadIdx.x / 4] = unit_high;
+        units += in_row, in_unit = 0, unit_high = -INFINITY;
+    };
+
     uint4 next[FLY];
     const auto fetch = [&](int v) {
 #pragma unroll
@@ -306,12 +353,16 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     };
     int v = v0 + (int)threadIdx.x;
     fetch(v);
-    for (int b = v0; b < v1; b += FLY * nthreads, v += FLY * nthreads) {
+    for (int b = v0; b < v1; b += batch, v += batch) {
         uint4 cur[FLY];
 #pragma unroll
         for (int u = 0; u < FLY; ++u) cur[u] = next[u];
-        if (b + FLY * nthreads < v1) fetch(v + FLY * nthreads);
+        if (b + batch < v1) fetch(v + batch);
         const float high = D::largest(cur);
+        if constexpr (TOP) {
+            unit_high = fmaxf(unit_high, high);
+            if (++in_unit == per_unit) end_unit();
+        }
         if (high > a.m) a = rescale<ENT>(a, high, c);
         const float ref = -reference(a.m, c);
         const float2 ref2 = make_float2(ref, ref), c2 = make_float2(c, c);
@@ -337,28 +388,30 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     if (rank == C - 1 && tail0 < p.V) edge(tail0, p.V - tail0);
     uint64_t best = 0;  // lane i: the warp's i-th best
     if constexpr (TOP) {
-        // the threads with the `top` largest maxima (more where they tie): all of the best are theirs
-        high_of[threadIdx.x] = a.m;
+        // the units with the `top` largest maxima (more where they tie): all of the best in vectors are theirs
+        if (in_unit > 0) end_unit();
         __syncthreads();
-        int better = 0;
-#pragma unroll 8
-        for (int i = 0; i < nthreads; i += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(&high_of[i]);
-            better += (o.x > a.m) + (o.y > a.m) + (o.z > a.m) + (o.w > a.m);
+        float bound = -INFINITY;  // lane i: the i-th largest maximum, of the warp's units, then of all
+        for (int u = threadIdx.x; u < units; u += nthreads) {  // (units are a multiple of 32)
+            const float sorted = sort_values(high_of[u]);
+            bound = u < nthreads ? sorted : merge_values(bound, sorted);
         }
-        const bool is = better < p.top && a.m > -INFINITY;
-        const unsigned who = __ballot_sync(0xffffffffu, is);
-        int first = 0;
-        if (lane == 0 && who) first = atomicAdd(&chosen_n, __popc(who));
-        first = __shfl_sync(0xffffffffu, first, 0);
-        if (is) {
-            chosen[first + __popc(who & ((1u << lane) - 1))] = (uint16_t)threadIdx.x;
-            // (the smallest of them: the bound)
-            atomicMin(&bound, order_key(a.m));
+        sorted_of[warp][lane] = bound;
+        __syncthreads();
+        bound = sorted_of[0][lane];
+        for (int w = 1; w < min(warps, units / 32); ++w) bound = merge_values(bound, sorted_of[w][lane]);
+        const float floor_v = __shfl_sync(0xffffffffu, bound, p.top - 1);  // `top` logits are no worse (-inf: read all)
+        for (int u = threadIdx.x; u < units; u += nthreads) {
+            const float high = high_of[u];
+            const bool is = high >= floor_v && high > -INFINITY;
+            const unsigned who = __ballot_sync(0xffffffffu, is);
+            int first = 0;
+            if (lane == 0 && who) first = atomicAdd(&chosen_n, __popc(who));
+            first = __shfl_sync(0xffffffffu, first, 0);
+            if (is) chosen[first + __popc(who & ((1u << lane) - 1))] = (uint16_t)u;
         }
         __syncthreads();
-        const int n = chosen_n, each = (v1 - v0 + nthreads - 1) / nthreads;  // vectors of a thread
-        const float floor_v = n >= p.top ? key_value(bound) : -INFINITY;  // (fewer: everything they have)
+        const int n = chosen_n, each = per_unit * FLY;  // rows of four vectors of a unit
         uint64_t* const wait = waiting[warp];
         int pending = 0;
         float last = -INFINITY;  // the warp's top-th: its value and its index
@@ -383,16 +436,17 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
             pending += __popc(w);
             if (pending >= 32) flush();
         };
-        // their vectors once more, from L2, AHEAD vectors of a thread in flight
+        // their vectors once more, AHEAD vectors of a thread in flight
         constexpr int AHEAD = 4;
-        const unsigned items = (unsigned)n * each;
+        const unsigned items = 4u * n * each;
         for (unsigned it0 = 0; it0 < items; it0 += AHEAD * nthreads) {
             uint4 w[AHEAD];
             int at[AHEAD];
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
-                const unsigned it = it0 + u * nthreads + threadIdx.x, vec = it / (unsigned)n;
-                at[u] = it < items ? v0 + (int)vec * nthreads + chosen[it - vec * n] : v1;
+                const unsigned it = it0 + u * nthreads + threadIdx.x, j = it / 4, row = j / (unsigned)n;
+                const int unit = it < items ? chosen[j - row * n] : 0;
+                at[u] = it < items ? v0 + (unit / in_row * each + (int)row) * nthreads + (unit % in_row) * 4 + it % 4 : v1;
                 w[u] = at[u] < v1 ? body[at[u]] : make_uint4(D::LOW, D::LOW, D::LOW, D::LOW);
             }
 #pragma unroll
