@@ -52,7 +52,7 @@ int launch_linear_adapted(const LinArgs& a, const LinWorkspace& ws, int num_sms,
     int rc = set_up(a, pl, ws, dev_status, limit_ns, 0, test_stall, p, tmA, tmB);
     if (rc != GEMM_OK) return rc;
     AdaptParams ad = {l.u, l.tiles, l.slot, l.bad, l.rs, l.n, adapter_list_words(l.tile_rows), pl.places};
-    if (!encode(&tmE, 3, l.B, a.bf16, a.Nw, l.r, l.n, l.ldb, l.n > 1 ? l.b_stride : l.r * l.ldb, l.rs < BK ? l.rs : BK))
+    if (!encode(&tmE, 3, l.B, a.bf16, a.Nw, l.r, l.n, l.ldb, l.n > 1 ? l.b_stride : l.ldb, l.rs < BK ? l.rs : BK))
         return GEMM_ERR_CUDA;
     const auto launch = pl.gated ? (a.bf16 ? (pl.kps == 1 ? launch_typed<true, true, 1> : launch_typed<true, true, 2>)
                                            : (pl.kps == 1 ? launch_typed<true, false, 1> : launch_typed<true, false, 2>))
