@@ -337,7 +337,8 @@ typedef struct gemm_adapter_args {
  * Infinities and NaN in a row of X stay in that row.  An adapter whose A or B holds some reaches its own rows
  * only, which become NaN where it falls, or in all columns.
  * args as in gemm_linear with groups == 0 and Z == NULL (else GEMM_ERR_INVALID_ARG: this is the form for
- * serving); GEMM_ERR_UNSUPPORTED for y_dtype other than dtype, K > 16384, r > 128 or n > 8192.
+ * serving); GEMM_ERR_UNSUPPORTED for y_dtype other than dtype, K > 16384, r > 128, n > 8192 or
+ * M > 2^31 - 2^17.
  * GEMM_OPT_TC_CHUNK does not apply.  A and B must be 16-byte aligned with leading dimensions, strides and r
  * multiples of 8 (GEMM_ERR_ALIGNMENT; pad the rank with zeros).
  * The pages have no counterpart to it. */
@@ -475,8 +476,8 @@ typedef struct moe_layer_args {
  * once.  Only the picked experts' weights are read.  Deterministic.
  * X, W1 and W2 must be 16-byte aligned with leading dimensions (and strides) multiples of 8, F a
  * multiple of 8 for GEMM_ACT_SWIGLU; the others aligned to their elements (GEMM_ERR_ALIGNMENT).
- * GEMM_ERR_UNSUPPORTED for GEMM_F32 operands, T > 64 (use the calls named above, which are faster
- * there), k > 32, E > 1024, D > 262144 or F > 2^24.  T == 0 or D == 0: nothing is done.  F >= 1.
+ * GEMM_ERR_UNSUPPORTED for GEMM_F32 operands, T > 64 (use the calls named above), k > 32, E > 1024,
+ * D > 262144 or F > 2^24.  T == 0 or D == 0: nothing is done.  F >= 1.
  * The handle's workspace holds T * k rows of F 16-bit and D fp32 values, under the rules above.
  * The pages have no counterpart to it. */
 int moe_layer(gemm_handle_t h, const moe_layer_args* args, void* stream);
@@ -564,7 +565,8 @@ typedef enum {
                                    128x256 tile, 2 a pair of CTAs (cluster of two) per 256x256 tile.  Any
                                    other value (3 included) is GEMM_ERR_INVALID_ARG */
     GEMM_OPT_TEST_STALL = 6,    /* test hook for failure detection, 0 (default) or 1: the kernels with
-                                   bounded waits (tensor-core GEMMs, linear layers and convolution, TMA
+                                   bounded waits (tensor-core GEMMs, linear layers with and without adapters, expert layers
+                                   for a few tokens, tensor-core convolution, TMA
                                    skinny GEMM, persistent fp32 GEMM) first wait on a barrier nothing
                                    arrives on; the wait runs out after the wait limit, the
                                    kernel drains its copies and MMAs, frees its tensor memory, returns,

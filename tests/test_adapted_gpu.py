@@ -403,3 +403,17 @@ def test_refusals(lib, g):
         assert call(**kw) == g.GEMM_ERR_ALIGNMENT, kw
     assert g.library().gemm_linear_adapted(lib.handle, la, None, None) == g.GEMM_ERR_INVALID_ARG
     assert lib.launch_count() == n
+
+
+def test_rows_near_the_end_of_32_bits_are_refused(lib, g):
+    """The kernels look some rows past the last, in 32 bits: 2^31 - 1025 rows pass gemm_linear's own limit."""
+    s = make(1, 12, 64, 64, 3, 16, BF16)
+    la = g.LinearArgs(M=12, K=64, N=64, X=s["x"].data_ptr(), ldx=64, W=s["w"].data_ptr(), ldw=64, Y=s["x"].data_ptr(),
+                      ldy=64, dtype=g.GEMM_BF16, y_dtype=g.GEMM_BF16)
+    aa = g.AdapterArgs(n=3, r=16, A=s["a"].data_ptr(), lda=16, a_stride=64 * 16, B=s["b"].data_ptr(), ldb=64,
+                       b_stride=16 * 64, adapters=s["adapters"].data_ptr())
+    n = lib.launch_count()
+    for rows in (2 ** 31 - 1025, 2 ** 31 - 2 ** 16):
+        la.M = rows
+        assert g.gemm_linear_adapted(lib.handle, la, aa) == g.GEMM_ERR_UNSUPPORTED
+    assert lib.launch_count() == n
