@@ -19,7 +19,7 @@ enum LinMode { kLinFwd = 0, kLinDx = 1, kLinDw = 2 };
 // Low-rank adapters beside a forward product: row m adds s_i (X[m] A_i) B_i, i = adapters[m].
 constexpr int kMaxAdapterRank = 128;
 constexpr int kMaxAdapters = 8192;     // (which of them are used: a bit each in shared memory)
-constexpr int kAdapterParts = 32;      // of a used adapter's B, each looked through by a CTA, which leaves a byte of `bad`
+constexpr int kAdapterParts = 32;      // of a used adapter's B, which have a byte of `bad` each
 struct LinAdapt {
     int n, r, rs;  // adapters, their rank, and the rank to 16, 32, 64 or 128: a row's length in `u`
     const void* A;  // [n][K][r]

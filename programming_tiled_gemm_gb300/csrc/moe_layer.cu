@@ -451,12 +451,11 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
         int stage = 0;
         uint32_t phase = 0;
         for (int item = blockIdx.x; item < items && !dead; item += gridDim.x) {
-            const int a = item / p.slabs, first = r.first[a], n_rows = r.first[a + 1] - first, n8 = (n_rows + 7) / 8 * 8;
-            const auto source = [&](int row) {
-                const int pick = r.pick[first + min(row, n_rows - 1)];
-                const int64_t at = UP ? (int64_t)(pick / p.k) * p.ldx : (int64_t)pick * p.Fp;
-                return rows + (in_range(pick, p.T * p.k) ? at : 0) + c * 8;
-            };
+            const int a = item / p.slabs, first = r.first[a], n_rows = r.first[a + 1] - first;
+            // lane i: where row i starts
+            const int pick = r.pick[first + min(lane, n_rows - 1)];
+            const int64_t starts = !in_range(pick, p.T * p.k) ? 0 : UP ? (int64_t)(pick / p.k) * p.ldx : (int64_t)pick * p.Fp;
+            const auto source = [&](int row) { return rows + __shfl_sync(0xffffffffu, starts, row) + c * 8; };
             const uint16_t* src[4];  // of the first eight rows
 #pragma unroll
             for (int i = 0; i < 4; ++i) src[i] = source(r0 + 2 * i);
@@ -468,14 +467,14 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
                 }
                 const int bytes = 2 * max(0, min(8, (UP ? K : p.Fp) - step * DEPTH - c * 8));  // of this chunk
                 const uint32_t at = ring_x + stage * x_bytes + c * 16;
+                // (what lies in a tile's rows behind the last stays: their products are not read)
                 const auto copy = [&](int row, const uint16_t* from) {
-                    const int n = row < n_rows ? bytes : 0;
-                    copy_async_16(at + row * ROW_BYTES, n > 0 ? from + step * DEPTH : rows, n);
+                    if (row < n_rows) copy_async_16(at + row * ROW_BYTES, bytes > 0 ? from + step * DEPTH : rows, bytes);
                 };
 #pragma unroll
                 for (int i = 0; i < 4; ++i) copy(r0 + 2 * i, src[i]);
 #pragma unroll 4
-                for (int row = r0 + 8; row < n8; row += 2) copy(row, source(row));
+                for (int i = 8; i < n_rows; i += 2) copy(i + r0, source(i + r0));
                 copy_async_arrive(smem_u32(&full_bar[stage]));
                 if (++stage == p.stages) stage = 0, phase ^= 1;
             }
