@@ -62,7 +62,7 @@
 // adapters of rank 16.  These blocks have one to four places of their own beside the ring, filled while the
 // tile's own k-blocks run: in the ring, they came 4 us after the tile's last one.  The kernel starts as the
 // dependent of the one that makes U and waits for it only before these blocks; X was complete before that one
-// started.  Measured (bf16, both kernels): 32 x 4096 x 4096, 16 adapters of rank 16, 25 us (without adapters 14.5: U 5,
+// started.  Measured (bf16, both kernels): 32 x 4096 x 4096, 16 adapters of rank 16, 24 us (without adapters 14.5: U 4,
 // the adapters' blocks 3, their part of the slices 2); 8192 x 4096 x 4096 swiglu, 8 adapters of rank 64, 197 us (142; U
 // 30, the blocks the rest).
 #pragma once

@@ -25,7 +25,7 @@
 // reading's time at 16 bits); short calls by latency.  Measured (GPU time; bf16 where not said otherwise):
 //   4096 x 131072: forward 158 us, 6.8 TB/s; with 1 or 20 alternatives 193 and 229; the gradient 309, 6.95 TB/s
 //   1000 x 50257 with entropy: 27 us, 3.7 TB/s (one wave of CTAs, 12 batches a thread), its gradient 34, 5.9 TB/s
-//   64 x 131072 with entropy: 8.7 us; with 20 alternatives 15.6; 1 x 32000 fp32: 4.9 and 10.8
+//   64 x 131072 with entropy: 8.7 us; with 20 alternatives 15.6; 1 x 32000 fp32: 4.9 and 10.5
 // Dropped: every logit offered to sorted lists as the row goes by (64 x 131072, 20 alternatives: 51 us); one maximum a
 // thread as the unit (its 16 bytes cost whole sectors again: 4096 x 131072 286 us); units ranked by counting (241, and
 // 144 instead of 109 for the best of 4096 x 32000 fp32); persistent blocks for the gradient (552 instead of 494 both
