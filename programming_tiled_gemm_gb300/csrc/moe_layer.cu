@@ -145,64 +145,77 @@ __device__ __forceinline__ void record(const LayerParams& p, const Routes& r, in
     }
 }
 
-// N tokens of a warp at once, so that their latencies are one's (one after another, 48 tokens to 2 of 16
-// experts took 5.9 us of each kernel, ROUTEUS); up to 32 CH experts, a lane's keys in registers.
-template <bool WEIGHTS, int CH, int N>
+// G lanes a token, up to G x REG experts, a lane's keys in registers.  Eight lanes a token are 40 tokens at once.  (48
+// tokens to 2 of 16 experts, us of the two kernels: 2.6 and 3.6; a warp a token, one after another, 5.6 and 6.6; four of
+// a warp's together 3.6 and 4.9.  One token to 4 of 64: 1.5 and 1.5, with a warp to itself 1.0 and 1.0.)
+template <bool WEIGHTS, int G, int REG>
 __device__ __forceinline__ void route_few(const LayerParams& p, const Routes& r)
 {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int t0 = warp; t0 < p.T; t0 += WARPS * N) {
-        uint32_t key[N][CH] = {};
+    constexpr int PER_WARP = 32 / G;
+    const int warp = threadIdx.x / 32, sub = threadIdx.x % 32 / G, lane = threadIdx.x % G, k = p.k;
+    for (int t0 = warp * PER_WARP; t0 < p.T; t0 += WARPS * PER_WARP) {
+        const int t = t0 + sub;
+        const bool live = t < p.T;
+        uint32_t key[REG] = {};
         // (all of the loads before the first use)
-        const bool wide = p.logits_dtype == GEMM_F32;
+        const int64_t from = (int64_t)t * p.ldl + lane;
+        if (p.logits_dtype == GEMM_F32) {
 #pragma unroll
-        for (int u = 0; u < N; ++u)
+            for (int c = 0; c < REG; ++c)
+                if (live && G * c + lane < p.E) key[c] = __ldcg(static_cast<const uint32_t*>(p.logits) + from + G * c);
+        } else {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int t = t0 + u * WARPS, e = 32 * c + lane;
-                const int64_t at = (int64_t)t * p.ldl + e;
-                if (t < p.T && e < p.E)
-                    key[u][c] = wide ? __ldcg(static_cast<const uint32_t*>(p.logits) + at)
-                                     : __ldcg(static_cast<const uint16_t*>(p.logits) + at);
+            for (int c = 0; c < REG; ++c)
+                if (live && G * c + lane < p.E) key[c] = __ldcg(static_cast<const uint16_t*>(p.logits) + from + G * c);
+        }
+#pragma unroll
+        for (int c = 0; c < REG; ++c) {
+            const float l = p.logits_dtype == GEMM_F32    ? __uint_as_float(key[c])
+                            : p.logits_dtype == GEMM_BF16 ? from_16<true>((uint16_t)key[c])
+                                                          : from_16<false>((uint16_t)key[c]);
+            key[c] = live && G * c + lane < p.E ? order_key(l) : 0;
+        }
+        float top = 0.f, sum = 0.f;
+        for (int j = 0; j < k; ++j) {
+            // the largest key, the lowest expert that has it (0: none is left)
+            uint32_t best = key[0];
+            int at = lane;
+#pragma unroll
+            for (int c = 1; c < REG; ++c)
+                if (key[c] > best) best = key[c], at = G * c + lane;
+#pragma unroll
+            for (int d = G / 2; d > 0; d /= 2) {
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, best, d);
+                const int o_at = __shfl_xor_sync(0xffffffffu, at, d);
+                if (o > best || (o == best && o_at < at)) best = o, at = o_at;
             }
+            if (WEIGHTS && j == 0) {
+                top = best != 0 ? key_value(best) : 0.f;
+                if (!p.renorm) {
 #pragma unroll
-        for (int u = 0; u < N; ++u)
+                    for (int c = 0; c < REG; ++c)
+                        if (key[c] != 0) sum += expf(key_value(key[c]) - top);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const float l = wide                            ? __uint_as_float(key[u][c])
-                                : p.logits_dtype == GEMM_BF16 ? from_16<true>((uint16_t)key[u][c])
-                                                              : from_16<false>((uint16_t)key[u][c]);
-                key[u][c] = t0 + u * WARPS < p.T && 32 * c + lane < p.E ? order_key(l) : 0;
-            }
-        int pick[N];
-        float val[N], top[N], all[N];
-#pragma unroll
-        for (int u = 0; u < N; ++u) pick[u] = -1, val[u] = top[u] = all[u] = 0.f;
-        for (int j = 0; j < p.k; ++j)
-#pragma unroll
-            for (int u = 0; u < N; ++u) {
-                uint32_t best = key[u][0];
-                int at = lane;
-#pragma unroll
-                for (int c = 1; c < CH; ++c)
-                    if (key[u][c] > best) best = key[u][c], at = 32 * c + lane;
-                const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-                const int e = (int)__reduce_min_sync(0xffffffffu, best == m ? (unsigned)at : 0xffffffffu);
-                if (j == 0 && m != 0) {
-                    top[u] = key_value(m);
-                    if (WEIGHTS && !p.renorm)
-#pragma unroll
-                        for (int c = 0; c < CH; ++c)
-                            if (key[u][c] != 0) all[u] += expf(key_value(key[u][c]) - top[u]);
+                    for (int d = G / 2; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 }
-                if (lane == j && m != 0) pick[u] = e, val[u] = key_value(m);
-#pragma unroll
-                for (int c = 0; c < CH; ++c)
-                    if (32 * c + lane == e) key[u][c] = 0;
+            }
+            const float ex = WEIGHTS && best != 0 ? expf(key_value(best) - top) : 0.f;
+            if (WEIGHTS && p.renorm) sum += ex;
+            if (live && lane == 0) {
+                r.expert[t * k + j] = best != 0 ? (uint16_t)at : NONE;
+                if (WEIGHTS) r.weight[t * k + j] = ex;
+                if (best != 0) atomicOr(&r.tokens[2 * at + t / 32], 1u << (t % 32));
             }
 #pragma unroll
-        for (int u = 0; u < N; ++u)
-            if (t0 + u * WARPS < p.T) record<WEIGHTS>(p, r, t0 + u * WARPS, pick[u], val[u], top[u], all[u]);
+            for (int c = 0; c < REG; ++c)
+                if (G * c + lane == at) key[c] = 0;
+        }
+        if (WEIGHTS) {
+            __syncwarp();
+            if (live)
+                for (int j = lane; j < k; j += G)
+                    if (r.expert[t * k + j] != NONE) r.weight[t * k + j] /= sum;
+        }
     }
 }
 
@@ -215,10 +228,10 @@ __device__ __forceinline__ void route(const LayerParams& p, const Routes& r, uin
     for (int e = threadIdx.x; e < 2 * E; e += THREADS) r.tokens[e] = 0;
     __syncthreads();
     if (E <= 64) {
-        if (p.T <= WARPS) route_few<WEIGHTS, 2, 1>(p, r);
-        else route_few<WEIGHTS, 2, 4>(p, r);
+        if (p.T <= WARPS) route_few<WEIGHTS, 32, 2>(p, r);
+        else route_few<WEIGHTS, 8, 8>(p, r);
     } else if (E <= 256) {
-        route_few<WEIGHTS, 8, 1>(p, r);
+        route_few<WEIGHTS, 32, 8>(p, r);
     } else {
         uint32_t* key = scratch + warp * E;
         for (int t = warp; t < p.T; t += WARPS) {
@@ -587,13 +600,11 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
         if constexpr (UP) {
             named_barrier(1, 32 * MMA_WARPS);  // (the sums are read before the next item's are written)
         } else {
-            // (one fence orders what every thread before the barrier has written)
+            // (one addition orders what every thread before the barrier has written)
             named_barrier(1, 32 * MMA_WARPS);
             if (threadIdx.x == 0) {
-                __threadfence();
-                const int last = atomicAdd(p.counters + slab, 1u) == (unsigned)(n_act - 1);
+                const int last = add_acq_rel(p.counters + slab, 1u) == (unsigned)(n_act - 1);
                 if (last) p.counters[slab] = 0;  // ready for the next launch
-                __threadfence();
                 is_last = last;
             }
             named_barrier(1, 32 * MMA_WARPS);

@@ -546,6 +546,15 @@ __device__ __forceinline__ int tagged_arrive(unsigned long long* counter, uint32
     return 0;
 }
 
+// An addition that releases what this thread (and, over a barrier, its block) has written and acquires what
+// those before it released.
+__device__ __forceinline__ unsigned add_acq_rel(unsigned* at, unsigned v)
+{
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(at), "r"(v) : "memory");
+    return old;
+}
+
 // ---- warp MMAs: 8 x 8 matrices of 16 bits from shared memory, and a 16 x 8 product over 16
 
 __device__ __forceinline__ void ldsm_x4(uint32_t at, uint32_t (&r)[4])
