@@ -194,6 +194,26 @@ def test_routing_as_moe_route(lib, logits_dtype, renormalize, out_dtype):
     assert bool(((five.double() - got.double()).abs() <= 2 * tol).all())
 
 
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("T,E,k", [(3, 50, 6), (10, 64, 32), (11, 9, 9), (41, 64, 20), (64, 40, 11), (12, 65, 5),
+                                   (50, 256, 12), (30, 257, 9)])
+def test_routing_whatever_lanes_a_token_has(lib, T, E, k, renormalize):
+    """both sides of the limits at which a token has 8 or 32 lanes, keys in registers or not: ties, experts that
+    are not there, more picks than experts that are, tokens without any"""
+    s = make(T + E, T, E, 64, 32, BF16, "swiglu")
+    l = (s["logits"].float() * 2).round() / 2
+    l[::2, 1::3] = -math.inf
+    l[1::4, 3:] = -math.inf
+    l[2] = -math.inf
+    s["logits"] = l
+    got = lib.moe_layer(s["x"], l, s["w1"], s["w2"], k, renormalize=renormalize, out_dtype=F32)
+    check(got, s, k, "swiglu", renormalize=renormalize)
+    assert bool((got[2] == 0).all())
+    l[0, 5], l[-1, 0] = math.nan, math.inf  # a NaN is picked first, and the row is NaN; so is inf's, as inf - inf
+    got = lib.moe_layer(s["x"], l, s["w1"], s["w2"], k, renormalize=renormalize, out_dtype=F32)
+    assert bool(got[0].isnan().all()) and bool(got[-1].isnan().all()) and not bool(got[1:-1].isnan().any())
+
+
 def test_no_token_goes_anywhere(lib, g):
     s = make(1, 5, 8, 64, 32, BF16, residual=True)
     s["logits"][:] = -math.inf
