@@ -184,7 +184,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
 {
     __shared__ float red[WARPS][kMaxAdapterRank];
-    __shared__ float part[kMaxAdapterRank];
+    __shared__ float part[MAX_CLUSTER][kMaxAdapterRank];  // the CTAs' sums, in the first one's
     grid_dependency_wait();
     grid_dependents_launch();
     const int C = p.cluster, rank = blockIdx.x % C, m = blockIdx.x / C;
@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
     }
     const int id = adapter_of(p, m);
     if (id < 0) return;  // (the whole cluster)
+    if (C > 1) cluster_arrive();  // (the first CTA is there before the others write to it)
+    const float scale = p.scales ? p.scales[id] : 1.f;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     // a lane has eight ranks of every `per`-th row of A
     const int chunks = p.r / 8;
@@ -238,30 +240,26 @@ __global__ void __launch_bounds__(THREADS) shrink_rows_kernel(ShrinkParams p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) red[warp][lane * 8 + i] = acc[i];
     __syncthreads();
+    if (C > 1) cluster_wait();
     if ((int)threadIdx.x < p.r) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) s += red[w][threadIdx.x];
-        part[threadIdx.x] = s;
+        const uint32_t at = smem_u32(&part[rank][threadIdx.x]);
+        if (C > 1) st_shared_cluster_f32(mapa_shared(at, 0), s);
+        else part[0][threadIdx.x] = s;
     }
     if (C > 1) cluster_sync_all();
     else __syncthreads();
-    if (rank == 0 && (int)threadIdx.x < p.rs) {
-        float s = 0.f;
-        if ((int)threadIdx.x < p.r) {
-            const uint32_t at = smem_u32(&part[threadIdx.x]);
-            float t[MAX_CLUSTER];
+    if (rank != 0 || (int)threadIdx.x >= p.rs) return;
+    float s = 0.f;
+    if ((int)threadIdx.x < p.r) {
 #pragma unroll
-            for (int q = 0; q < MAX_CLUSTER; ++q)
-                if (q < C) t[q] = C > 1 ? ld_shared_cluster_f32(mapa_shared(at, q)) : part[threadIdx.x];
-#pragma unroll
-            for (int q = 0; q < MAX_CLUSTER; ++q)
-                if (q < C) s += t[q];
-            if (p.scales) s *= p.scales[id];
-        }
-        if (in_range(m, p.M)) p.u[(int64_t)m * p.rs + threadIdx.x] = to_16<BF16>(s);
+        for (int q = 0; q < MAX_CLUSTER; ++q)
+            if (q < C) s += part[q][threadIdx.x];
+        s *= scale;
     }
-    if (C > 1) cluster_sync_all();  // (nobody leaves while its sums are read)
+    if (in_range(m, p.M)) p.u[(int64_t)m * p.rs + threadIdx.x] = to_16<BF16>(s);
 }
 
 // ------------------------------------------------------------------ a cluster up to 64 rows of an adapter
@@ -428,6 +426,7 @@ __global__ void __launch_bounds__(THREADS, RS <= 64 ? 2 : 1) shrink_groups_kerne
         int n_rows = 0;
         const int id = find_group(p, group, counts, rows, n_rows);
         if (id < 0) return;  // (the whole cluster)
+        const float scale = p.scales ? p.scales[id] : 1.f;
         const uint32_t ring = smem_u32(smem);
         const int kb = (p.K + DEPTH - 1) / DEPTH, kb0 = kb * rank / C, steps = kb * (rank + 1) / C - kb0;
         // 16 rows a warp, and `parts` warps share a stage's K
@@ -509,7 +508,6 @@ __global__ void __launch_bounds__(THREADS, RS <= 64 ? 2 : 1) shrink_groups_kerne
         }
         __syncthreads();
         if (C > 1) cluster_sync_all();
-        const float scale = p.scales ? p.scales[id] : 1.f;
         for (int q = rank * THREADS + threadIdx.x; q < n_rows * RS; q += C * THREADS) {
             const int i = q / RS, c = q % RS;
             const uint32_t at = smem_u32(sums + i * FP + c);

@@ -210,10 +210,6 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c)
     return {m, x.s + y.s, x.q + y.q};
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t at, float v)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
-}
 __device__ __forceinline__ void st_cluster_u64(uint32_t at, uint64_t v)
 {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
@@ -490,9 +486,9 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     const auto at_first = [&](const void* q) { return C > 1 ? mapa_shared(smem_u32(q), 0) : smem_u32(q); };
     if (C > 1) {
         if (lane == 0) {
-            st_cluster_f32(at_first(&part_m[list]), a.m);
-            st_cluster_f32(at_first(&part_s[list]), a.s);
-            if (ENT) st_cluster_f32(at_first(&part_q[list]), a.q);
+            st_shared_cluster_f32(at_first(&part_m[list]), a.m);
+            st_shared_cluster_f32(at_first(&part_s[list]), a.s);
+            if (ENT) st_shared_cluster_f32(at_first(&part_q[list]), a.q);
         }
         if (TOP && lane < p.top) st_cluster_u64(at_first(&lists_best[list][lane]), best);
         cluster_sync_all();
