@@ -10,7 +10,7 @@
 // on tcgen05's 128 or 256 rows, and the rank is narrower still).  The CTAs' parts of K are added in order
 // through distributed shared memory.
 //
-// Measured (bf16, GPU time): 32 rows of 16 adapters, K 4096, rank 16: 5 us (2 MB of A: latency); 8192 rows in
+// Measured (bf16, GPU time): 32 rows of 16 adapters, K 4096, rank 16: 4 us (2 MB of A: latency); 8192 rows in
 // runs of one adapter, K 4096, rank 64: 30 us (71 MB, 2.4 TB/s: counting the rows 3.6, finding the group 3, the loop 16,
 // the sums 3).  Dropped: tiles of 64 neighbouring rows with all their adapters (512 rows of 16 adapters at random, with
 // the product: 94 us instead of 41); twice the CTAs a group for those rows (with the product 210 us instead of 200).

@@ -10,7 +10,7 @@
 // ADAPT: a low-rank adapter of each row's choice, U = s_i X A_i from the kernel before (adapters.cu).
 // Behind the batches of X and W come those of U and the rows' B, `rank` of K for every row, which count for
 // that row only.  The kernel starts as that one's dependent and waits for it before it copies U.
-// One row, 2048 x 2048, rank 16: 7.2 us with U's kernel (4.1 without an adapter).
+// One row, 2048 x 2048, rank 16: 6.8 us with U's kernel (4.1 without an adapter).
 // Measured (bf16, one row): 2048 x 64 2.5 us, 2048 x 2048 4.0 (tensor-core kernel 8.4 and 9.6),
 // 4096 x 4096 7.4 (12.7), 8192 x 8192 23.3, 5.8 TB/s (27.3).  Dropped: loads kept in registers
 // instead of the ring (4096 x 4096 12.8, and 100 us for 4 rows of 8192 x 28672); three CTAs of two
