@@ -20,7 +20,7 @@
 // Measured (bf16, swiglu, GPU time): 1 token to 4 of 64 experts, 2048 -> 1024 -> 2048, 19.8 us (50 MB, floor 7.4:
 // routing, first copies, the kernels' hand-over and the slabs' sums each take 1 to 4); 16 tokens 98 us (519 MB, 5.3
 // TB/s in all, 6.2 in the first kernel's loop); 64 tokens to 2 of 16, 4096 -> 4096 -> 4096, 280 to 287 us (1.6 GB, 5.7 TB/s;
-// DRAM 73 % busy in the first kernel).
+// DRAM 79 % busy in the first kernel).
 // Dropped: one warp for the weights' and the rows' copies (64 tokens: 330 us instead of 290); every warp at every stage
 // (476 instead of 332 then); weights by cp.async from all threads, a block barrier a stage (16 tokens: 184 instead of 103);
 // the second kernel's last round of items cut along its reduced dimension (64 tokens 292 instead of 280, one token 23).
