@@ -1,15 +1,17 @@
 // Log probabilities of given tokens, the entropy and the best alternatives of rows of logits,
 // and the logits' gradient.
 //
-// With c = 1 / (T ln 2) and a reference R, the row's largest logit m times c as it rounds:
-// t_j = z_j c - R (one rounding, of a small number), S = sum 2^t_j, Q = sum 2^t_j t_j,
-//     ln p_j = (z_j - m) / T - ln S',   ln S' = ln S - ln 2 (m c - R),   H = ln S - ln 2 Q / S.
-// One pass: every thread keeps its own m, R, S and Q and rescales them when m grows,
-//     S' = f S,  Q' = f (Q + d S),  d = R - R',  f = 2^d,
+// With c = 1 / (T ln 2) and the row's largest logit m: t_j = (z_j - m) c, S = sum 2^t_j, Q = sum 2^t_j t_j,
+//     ln p_j = (z_j - m) / T - ln S,   H = ln S - ln 2 Q / S.
+// The difference comes first: t is 0 at the largest logit and below 0 elsewhere, whatever their magnitude, so no
+// power overflows and S is 1 at least.  (z c less a rounded m c is one operation instead of two; but from |m| c = 2^31 on
+// what m c lost in rounding is beyond 2^t's range, and a masked value of -1e10 reaches that.)  With h = 1/2 it is
+// t = (z h - m h) (c / h), as the difference of two finite logits may be beyond fp32's range while t is not.  From c = 2
+// on such a t is below -2^128, so that h = 1 will do (and c / h stays finite).
+// One pass: every thread keeps its own m, S and Q and rescales them when m grows,
+//     S' = f S,  Q' = f (Q + d S),  d = (m - m') c,  f = 2^d,
 // and the threads' sums are joined the same way.  As a factor, t is clamped at -1e4, far below
-// where 2^t is 0: 0 * -inf is 0 there.  Where m c is beyond 1e29 ("far": a row of a type's lowest
-// value), z c would overflow; any logit but m itself is then further off than exp can tell, so
-// p is 1 / n at the n logits that equal m.
+// where 2^t is 0: 0 * -inf is 0 there.
 //
 // Alternatives: the pass leaves the maxima of units: 64 bytes (four lanes) of a row of the block's vectors, in one or
 // more of its batches, so that there are 32 to 256 units a CTA.  The `top` best logits of a CTA's part all belong to
@@ -33,6 +35,8 @@
 // 50257: 27.5 to 29.3 instead of 27.1); sums two at a time (f32x2) take 161 us where single ones took 169.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "logprobs.h"
 #include "ptx.h"
@@ -185,28 +189,36 @@ __device__ __forceinline__ int head_of(const typename D::T* row, int V)
     return min(V, off ? D::PER - off : 0);
 }
 
-// The reference of a largest logit; sums without a logit have the least, -1e38, which is far from all.
-__device__ __forceinline__ float reference(float m, float c) { return fminf(fmaxf(m * c, -1e38f), 1e38f); }
-// Whether m c is out of the exponents' range.
-__device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m) < INFINITY && fabsf(m) * c >= 1e29f; }
+// 1 / (T ln 2) as the exponents take it: t = (z h - reference(m, h)) c.
+struct Scale {
+    float h, c;
+};
+inline Scale scale_of(float temperature)
+{
+    const double c = 1.4426950408889634 / temperature;
+    return c < 2. ? Scale{0.5f, (float)(2. * c)} : Scale{1.f, (float)c};
+}
+
+// m h of a largest logit; sums without a logit have the least finite one, from which -inf is -inf off.
+__device__ __forceinline__ float reference(float m, float h) { return fmaxf(m, -FLT_MAX) * h; }
 
 struct Sums {
-    float m, s, q;  // largest logit, sum 2^t, sum 2^t t with t = z c - reference(m)
+    float m, s, q;  // largest logit, sum 2^t, sum 2^t t
 };
 
-// Everything relative to the larger m.
+// Everything relative to the larger m.  (s is one a logit at most: times 0 it is 0, or NaN where it was.)
 template <bool ENT>
-__device__ __forceinline__ Sums rescale(const Sums& a, float m, float c)
+__device__ __forceinline__ Sums rescale(const Sums& a, float m, Scale by)
 {
     if (a.m == m) return a;
-    const float d = fmaxf(reference(a.m, c) - reference(m, c), FLOOR), f = ex2(d);
+    const float d = fmaxf((reference(a.m, by.h) - reference(m, by.h)) * by.c, FLOOR), f = ex2(d);
     return {m, a.s * f, ENT ? f * (a.q + d * a.s) : 0.f};
 }
 template <bool ENT>
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c)
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, Scale by)
 {
     const float m = fmaxf(a.m, b.m);
-    const Sums x = rescale<ENT>(a, m, c), y = rescale<ENT>(b, m, c);
+    const Sums x = rescale<ENT>(a, m, by), y = rescale<ENT>(b, m, by);
     return {m, x.s + y.s, x.q + y.q};
 }
 
@@ -271,7 +283,8 @@ struct LogprobsParams {
     int64_t ld;
     int V, top, cluster, threads;
     const int64_t* tokens;
-    float inv_t, c;  // 1 / T and 1 / (T ln 2)
+    float inv_t;  // 1 / (T h)
+    Scale by;
     float* logprobs;
     float* entropy;
     float* stats;
@@ -301,7 +314,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     grid_dependency_wait();
     grid_dependents_launch();
     const typename D::T* row = static_cast<const typename D::T*>(p.logits) + r * p.ld;
-    const float c = p.c;
+    const Scale by = p.by;
     // the given token's logit, early
     float given = 0.f;
     bool have = false;
@@ -320,8 +333,8 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     const auto edge = [&](int first, int n) {
         if ((int)threadIdx.x >= n) return;
         const float z = D::get(row[first + threadIdx.x]);
-        if (z > a.m) a = rescale<ENT>(a, z, c);
-        const float t = __fmaf_rn(z, c, -reference(a.m, c)), e = ex2(t);
+        if (z > a.m) a = rescale<ENT>(a, z, by);
+        const float t = __fmaf_rn(z, by.h, -reference(a.m, by.h)) * by.c, e = ex2(t);
         a.s += e;
         if (ENT) a.q += e * fmaxf(t, FLOOR);
     };
@@ -359,9 +372,9 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
             unit_high = fmaxf(unit_high, high);
             if (++in_unit == per_unit) end_unit();
         }
-        if (high > a.m) a = rescale<ENT>(a, high, c);
-        const float ref = -reference(a.m, c);
-        const float2 ref2 = make_float2(ref, ref), c2 = make_float2(c, c);
+        if (high > a.m) a = rescale<ENT>(a, high, by);
+        const float ref = -reference(a.m, by.h);
+        const float2 ref2 = make_float2(ref, ref), h2 = make_float2(by.h, by.h), c2 = make_float2(by.c, by.c);
         float2 s2 = make_float2(0.f, 0.f), q2 = s2;
 #pragma unroll
         for (int u = 0; u < FLY; ++u) {
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
             D::unpack(cur[u], z);
 #pragma unroll
             for (int j = 0; j < PER; j += 2) {
-                float2 t = __ffma2_rn(make_float2(z[j], z[j + 1]), c2, ref2);
+                float2 t = __fmul2_rn(__ffma2_rn(make_float2(z[j], z[j + 1]), h2, ref2), c2);
                 const float2 e = make_float2(ex2(t.x), ex2(t.y));  // (NaN or inf where z is NaN or +inf)
                 s2 = __fadd2_rn(s2, e);
                 if (ENT) {
@@ -480,7 +493,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
         const Sums o = {__shfl_xor_sync(0xffffffffu, a.m, d), __shfl_xor_sync(0xffffffffu, a.s, d),
                           __shfl_xor_sync(0xffffffffu, a.q, d)};
         // (in the same order on both sides)
-        a = (lane & d) ? join<ENT>(o, a, c) : join<ENT>(a, o, c);
+        a = (lane & d) ? join<ENT>(o, a, by) : join<ENT>(a, o, by);
     }
     const int list = rank * warps + warp;
     const auto at_first = [&](const void* q) { return C > 1 ? mapa_shared(smem_u32(q), 0) : smem_u32(q); };
@@ -505,36 +518,25 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
     Sums t = {-INFINITY, 0.f, 0.f};
     for (int i = lane; i < lists; i += 32) {
         const Sums o = {part_m[i], part_s[i], ENT ? part_q[i] : 0.f};
-        t = join<ENT>(t, o, c);
+        t = join<ENT>(t, o, by);
     }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) {
         const Sums o = {__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d),
                           __shfl_xor_sync(0xffffffffu, t.q, d)};
-        t = (lane & d) ? join<ENT>(o, t, c) : join<ENT>(t, o, c);
+        t = (lane & d) ? join<ENT>(o, t, by) : join<ENT>(t, o, by);
     }
-    float ln_r = logf(t.s), ln_s = ln_r - LN2 * __fmaf_rn(t.m, c, -reference(t.m, c));  // relative to R and to m
-    if (is_far(t.m, c)) {
-        int n = 0;
-        bool nan = false;
-        for (int i = lane; i < p.V; i += 32) {
-            const float z = D::get(row[i]);
-            n += z == t.m;
-            nan |= z != z;
-        }
-        ln_r = ln_s = __any_sync(0xffffffffu, nan) ? NAN : logf((float)__reduce_add_sync(0xffffffffu, n));
-        t.s = 1.f, t.q = 0.f;
-    }
-    if (t.m == INFINITY) ln_r = ln_s = NAN;
+    float ln_s = t.m == INFINITY ? NAN : logf(t.s);
     const bool none = t.m == -INFINITY && t.s == 0.f;  // (a row of NaN has NaN sums)
     if (none) ln_s = 0.f;
+    const auto logprob = [&](float z) { return __fmaf_rn(z, by.h, -t.m * by.h) * p.inv_t - ln_s; };
     if (lane == 0) {
         p.stats[2 * r] = t.m;
         p.stats[2 * r + 1] = ln_s;
         float lp = 0.f;
-        if (have) lp = none ? -INFINITY : (given - t.m) * p.inv_t - ln_s;
+        if (have) lp = none ? -INFINITY : logprob(given);
         p.logprobs[r] = lp;
-        if (ENT) p.entropy[r] = none ? 0.f : ln_r - LN2 * (t.q / t.s);
+        if (ENT) p.entropy[r] = none ? 0.f : ln_s - LN2 * (t.q / t.s);
     }
     if constexpr (TOP) {
         // the best head of all lists, `top` times: a lane holds the heads of two lists
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(LogprobsParams p)
         const float val = key_value((uint32_t)(mine >> 32));
         const int64_t tok = mine ? (int64_t)(uint32_t)~(uint32_t)mine : -1;
         if (lane < p.top) {
-            p.top_logprobs[r * p.top + lane] = bad ? ln_s : tok < 0 ? -INFINITY : (val - t.m) * p.inv_t - ln_s;
+            p.top_logprobs[r * p.top + lane] = bad ? ln_s : tok < 0 ? -INFINITY : logprob(val);
             p.top_tokens[r * p.top + lane] = tok;
         }
     }
@@ -579,6 +581,10 @@ struct LogprobsGradParams {
 
 constexpr int GRAD_FLY = 4;
 
+// m c as it rounds, and whether it is out of the exponents' range
+__device__ __forceinline__ float rounded(float m, float c) { return fminf(fmaxf(m * c, -1e38f), 1e38f); }
+__device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m) < INFINITY && fabsf(m) * c >= 1e29f; }
+
 // dz_j = (g (delta_jt - p_j) - h p_j (ln p_j + H)) / T = p_j (A + B log2 p_j) + delta_jt g / T,
 // log2 p_j = (z_j c - R) - L, L = ln S' / ln 2 + (m c - R)
 template <typename D, bool ENT>
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradPara
     const float B = -h * p.inv_t * LN2, A = ENT ? -(g + h * p.entropy[r]) * p.inv_t : -g * p.inv_t;
     const float gt = g * p.inv_t;
     const int t = have ? (int)tok : -1;
-    const float ref = reference(m, c), log_s = ln_s * LOG2E + __fmaf_rn(m, c, -ref);
+    const float ref = rounded(m, c), log_s = ln_s * LOG2E + __fmaf_rn(m, c, -ref);
     const bool far = is_far(m, c);
     const auto grad = [&](float z, int j) {
         if (zero) return 0.f;
@@ -706,8 +712,8 @@ int launch_logprobs(const LogprobsArgs& a, int num_sms, cudaStream_t s, int* lau
     p.logits = a.logits, p.ld = a.ld;
     p.V = a.V, p.top = a.top;
     p.tokens = a.tokens;
-    p.inv_t = 1.f / a.temperature;
-    p.c = (float)(1.4426950408889634 / a.temperature);
+    p.by = scale_of(a.temperature);
+    p.inv_t = (float)(1. / p.by.h / a.temperature);
     p.logprobs = a.logprobs, p.entropy = a.entropy, p.stats = a.stats;
     p.top_logprobs = a.top_logprobs, p.top_tokens = a.top_tokens;
     const int batch = FLY * THREADS / 2 * 16 / (a.dtype == GEMM_F32 ? 4 : 2);

@@ -1,0 +1,144 @@
+"""Token log probabilities wherever the finite logits lie: finite masks, rows of nothing else, offsets at which
+neighbouring logits are far apart, temperatures down to the smallest; forward and backward, against 64 bits.
+
+The tolerances are those of test_logprobs_gpu.py: they count roundings of u = (z - m) / T, which has the same number
+whatever the magnitude of z and m.  Temperatures are fp32 values, so that both sides take the same one.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_logprobs_gpu import DTYPES, check_backward, check_forward, make
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = {"bf16": -3.3895313892515355e38, "f16": -65504.0, "f32": -3.4028234663852886e38}
+# fp16 has no larger mask than its lowest value; colder temperatures take it as far
+MASKED = ([("f32", v, t) for v in (-1e9, -1e10, -1e12, -1e20, -1e30, LOWEST["f32"]) for t in (0.1, 0.3, 1.0, 5.0, 30.0)] +
+          [("bf16", v, t) for v in (-1e9, -1e10, -1e12, -1e20, -1e30, LOWEST["bf16"]) for t in (0.1, 1.0, 5.0, 10.0)] +
+          [("f16", v, t) for v in (-6e4, LOWEST["f16"]) for t in (1e-6, 1e-4, 0.1, 1.0)])
+
+
+@pytest.fixture(scope="module")
+def g():
+    import programming_tiled_gemm_gb300 as g
+    return g
+
+
+@pytest.fixture(scope="module")
+def lib(g):
+    lib = g.Gemm(0)
+    yield lib
+    assert lib.device_status() == g.GEMM_OK
+    lib.close()
+
+
+def f32(v):
+    return float(np.float32(v))
+
+
+def masked_rows(dtype, value, rows, V):
+    """rows whose masked stretches leave: all but the first part, all but the last, one in the middle, one at either
+    end, a few, none, every other one"""
+    logits, tokens = make(rows + V, rows, V, DTYPES[dtype])
+    free = torch.zeros(rows, V, dtype=torch.bool, device="cuda")
+    at = torch.arange(V, device="cuda")
+    kinds = [at >= V * 3 // 4, at < V // 4, at == V // 2, at == 0, at == V - 1, (at > V // 3) & (at < V // 3 + 40),
+             at < 0, at % 2 == 0]
+    for r in range(rows):
+        free[r] = kinds[r % len(kinds)]
+    logits.masked_fill_(~free, value)
+    # a token that is left, where there is one, and a masked one in every third row
+    first = torch.where(free.any(1), free.float().argmax(1), torch.full_like(tokens, 3))
+    tokens = torch.where(torch.arange(rows, device="cuda") % 3 == 1, tokens, first)
+    return logits, tokens
+
+
+def gains(rows, temperature):
+    """gradients that leave the logits' in the types' range"""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    scale = min(1.0, temperature)
+    return [torch.randn(rows, generator=gen, device="cuda") * scale for _ in range(2)]
+
+
+# (rows, V): a row over eight CTAs; threads with several batches; a row a CTA
+SHAPES = [(16, 20011), (8, 40000), (1400, 6007)]
+
+
+@pytest.mark.parametrize("rows,V", SHAPES)
+@pytest.mark.parametrize("dtype,value,temperature", MASKED)
+def test_finite_masks(lib, dtype, value, temperature, rows, V):
+    t = f32(temperature)
+    logits, tokens = masked_rows(dtype, value, rows, V)
+    r = lib.token_logprobs(logits, tokens, top=8, entropy=True, temperature=t)
+    check_forward(logits, tokens, t, 8, r)
+    plain = lib.token_logprobs(logits, tokens, temperature=t)
+    check_forward(logits, tokens, t, 0, plain)
+
+
+OFFSETS = [("f32", 1e8, 8.0), ("f32", -3e9, 256.0), ("f32", 1e20, 2.0 ** 43), ("f32", -1e30, 2.0 ** 76),
+           ("bf16", 1e8, 2.0 ** 19), ("bf16", -1e20, 2.0 ** 59), ("f16", 6e4, 32.0), ("f16", -6e4, 32.0)]
+
+
+def offset_rows(dtype, base, step, rows=12, V=5003):
+    """logits a few of the type's steps from each other, far from zero"""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    k = torch.randint(-8, 9, (rows, V), generator=gen, device="cuda")
+    k[::4] = 0  # rows of one value only
+    logits = (base + k.double() * step).to(DTYPES[dtype])
+    return logits, torch.randint(0, V, (rows,), generator=gen, device="cuda")
+
+
+@pytest.mark.parametrize("dtype,base,step", OFFSETS)
+@pytest.mark.parametrize("of_step", [0.01, 0.5, 4.0])
+def test_far_from_zero(lib, dtype, base, step, of_step):
+    """the distribution of offsets of some `step`s at temperatures about as large"""
+    t = f32(step * of_step)
+    logits, tokens = offset_rows(dtype, base, step)
+    r = lib.token_logprobs(logits, tokens, top=8, entropy=True, temperature=t)
+    check_forward(logits, tokens, t, 8, r)
+
+
+COLD = [1e-3, 1e-6, 1e-9, 1e-12, 1e-30]
+
+
+def tied_rows(dtype, rows=10, V=9001):
+    """ordinary logits, the largest of them n times in the n-th row"""
+    logits, tokens = make(31, rows, V, DTYPES[dtype])
+    for n in range(rows):
+        logits[n, torch.arange(n + 1, device="cuda") * 811] = 17.75
+    tokens[::2] = 0
+    return logits, tokens
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("temperature", COLD)
+def test_cold(lib, dtype, temperature):
+    t = f32(temperature)
+    logits, tokens = tied_rows(dtype)
+    r = lib.token_logprobs(logits, tokens, top=12, entropy=True, temperature=t)
+    check_forward(logits, tokens, t, 12, r)
+    n = torch.arange(1, 11, device="cuda").double()
+    if t < 1e-5:
+        assert bool(((r.entropy.double() - torch.log(n)).abs() <= 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [1.0, 1.5, 3.0, 2e38, 3.4e38])
+def test_differences_beyond_the_range(lib, dtype, temperature):
+    """largest and lowest values side by side: their difference has no fp32 value, its product with 1 / T has"""
+    t, low = f32(temperature), LOWEST[dtype]
+    logits, tokens = make(77, 6, 3001, DTYPES[dtype])
+    logits[0] = low
+    logits[0, 7::3] = -low
+    logits[1, ::2] = low
+    logits[1, 1::2] = -low
+    logits[2] = low
+    logits[2, 2222] = -low
+    logits[3] = -low
+    logits[4, ::5] = low
+    tokens[:4] = torch.tensor([8, 1, 2222, 0], device="cuda")
+    r = lib.token_logprobs(logits, tokens, top=5, entropy=True, temperature=t)
+    check_forward(logits, tokens, t, 5, r)
