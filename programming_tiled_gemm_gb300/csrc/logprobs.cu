@@ -570,7 +570,8 @@ struct LogprobsGradParams {
     int64_t ld;
     int V, blocks;  // blocks of a row
     const int64_t* tokens;
-    float inv_t, c;
+    float inv_t;
+    Scale by;
     const float* stats;
     const float* entropy;
     const float* dlogprobs;
@@ -581,12 +582,8 @@ struct LogprobsGradParams {
 
 constexpr int GRAD_FLY = 4;
 
-// m c as it rounds, and whether it is out of the exponents' range
-__device__ __forceinline__ float rounded(float m, float c) { return fminf(fmaxf(m * c, -1e38f), 1e38f); }
-__device__ __forceinline__ bool is_far(float m, float c) { return fabsf(m) < INFINITY && fabsf(m) * c >= 1e29f; }
-
 // dz_j = (g (delta_jt - p_j) - h p_j (ln p_j + H)) / T = p_j (A + B log2 p_j) + delta_jt g / T,
-// log2 p_j = (z_j c - R) - L, L = ln S' / ln 2 + (m c - R)
+// log2 p_j = t_j - ln S / ln 2
 template <typename D, bool ENT>
 __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradParams p)
 {
@@ -599,27 +596,26 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradPara
     const T* row = static_cast<const T*>(p.logits) + r * p.ld;
     T* out = static_cast<T*>(p.dlogits) + r * p.ldd;
     const int64_t tok = p.tokens[r];
-    const float m = p.stats[2 * r], ln_s = p.stats[2 * r + 1], c = p.c;
+    const float m = p.stats[2 * r], ln_s = p.stats[2 * r + 1];
+    const Scale by = p.by;
     const bool have = tok >= 0 && tok < p.V;
     const float g = have && p.dlogprobs ? p.dlogprobs[r] : 0.f, h = ENT ? p.dentropy[r] : 0.f;
     const bool zero = (g == 0.f && h == 0.f) || (m == -INFINITY && ln_s == ln_s);
     const float B = -h * p.inv_t * LN2, A = ENT ? -(g + h * p.entropy[r]) * p.inv_t : -g * p.inv_t;
     const float gt = g * p.inv_t;
     const int t = have ? (int)tok : -1;
-    const float ref = rounded(m, c), log_s = ln_s * LOG2E + __fmaf_rn(m, c, -ref);
-    const bool far = is_far(m, c);
+    const float ref = reference(m, by.h), log_s = ln_s * LOG2E;
     const auto grad = [&](float z, int j) {
         if (zero) return 0.f;
         if (ln_s != ln_s) return ln_s;  // a row with NaN
-        float l = __fmaf_rn(z, c, -ref) - log_s;
-        if (far) l = z == m ? -ln_s * LOG2E : -INFINITY;
+        const float l = __fmaf_rn(__fmaf_rn(z, by.h, -ref), by.c, -log_s);
         const float e = ex2(l);
         const float v = ENT ? e * (A + B * fmaxf(l, FLOOR)) : e * A;
         return j == t ? v + gt : v;
     };
     const int head = head_of<D>(row, p.V), vecs = (p.V - head) / PER;
     const bool aligned = ((reinterpret_cast<uintptr_t>(out + head)) & 15) == 0;
-    if (!aligned || far || ln_s != ln_s) {
+    if (!aligned || ln_s != ln_s) {
         const int n = (p.V + p.blocks - 1) / p.blocks, j1 = min(p.V, (part + 1) * n);
         for (int j = part * n + (int)threadIdx.x; j < j1; j += THREADS)
             out[j] = D::put(grad(zero ? 0.f : D::get(row[j]), j));
@@ -631,7 +627,8 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradPara
     if (zero) {
         for (int v = v0 + (int)threadIdx.x; v < v1; v += THREADS) __stcs(dst + v, make_uint4(0, 0, 0, 0));
     } else {
-        const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref), log2 = make_float2(-log_s, -log_s);
+        const float2 h2 = make_float2(by.h, by.h), c2 = make_float2(by.c, by.c);
+        const float2 ref2 = make_float2(-ref, -ref), log2 = make_float2(-log_s, -log_s);
         const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
         for (int v = v0 + (int)threadIdx.x; v < v1; v += GRAD_FLY * THREADS) {
             uint4 in[GRAD_FLY];
@@ -645,7 +642,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradPara
                 D::unpack(in[u], z);
 #pragma unroll
                 for (int j = 0; j < PER; j += 2) {
-                    float2 l = __fadd2_rn(__ffma2_rn(make_float2(z[j], z[j + 1]), c2, ref2), log2);
+                    float2 l = __ffma2_rn(__ffma2_rn(make_float2(z[j], z[j + 1]), h2, ref2), c2, log2);
                     const float2 e = make_float2(ex2(l.x), ex2(l.y));
                     float2 w = A2;
                     if (ENT) {
@@ -745,7 +742,7 @@ int launch_logprobs_grad(const LogprobsGradArgs& a, cudaStream_t s, int* launche
     p.blocks = (a.V + batch - 1) / batch;
     p.tokens = a.tokens;
     p.inv_t = 1.f / a.temperature;
-    p.c = (float)(1.4426950408889634 / a.temperature);
+    p.by = scale_of(a.temperature);
     p.stats = a.stats, p.entropy = a.entropy;
     p.dlogprobs = a.dlogprobs, p.dentropy = a.dentropy;
     p.dlogits = a.dlogits, p.ldd = a.ldd;

@@ -56,12 +56,6 @@ def masked_rows(dtype, value, rows, V):
     return logits, tokens
 
 
-def gains(rows, temperature):
-    """gradients that leave the logits' in the types' range"""
-    gen = torch.Generator(device="cuda").manual_seed(rows)
-    scale = min(1.0, temperature)
-    return [torch.randn(rows, generator=gen, device="cuda") * scale for _ in range(2)]
-
 
 # (rows, V): a row over eight CTAs; threads with several batches; a row a CTA
 SHAPES = [(16, 20011), (8, 40000), (1400, 6007)]
@@ -125,11 +119,12 @@ def test_cold(lib, dtype, temperature):
         assert bool(((r.entropy.double() - torch.log(n)).abs() <= 2.0 ** -20).all())
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("temperature", [1.0, 1.5, 3.0, 2e38, 3.4e38])
-def test_differences_beyond_the_range(lib, dtype, temperature):
+HOT = [1.0, 1.5, 3.0, 2e38, 3.4e38]
+
+
+def rows_of_extremes(dtype):
     """largest and lowest values side by side: their difference has no fp32 value, its product with 1 / T has"""
-    t, low = f32(temperature), LOWEST[dtype]
+    low = LOWEST[dtype]
     logits, tokens = make(77, 6, 3001, DTYPES[dtype])
     logits[0] = low
     logits[0, 7::3] = -low
@@ -140,5 +135,62 @@ def test_differences_beyond_the_range(lib, dtype, temperature):
     logits[3] = -low
     logits[4, ::5] = low
     tokens[:4] = torch.tensor([8, 1, 2222, 0], device="cuda")
+    return logits, tokens
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", HOT)
+def test_differences_beyond_the_range(lib, dtype, temperature):
+    t = f32(temperature)
+    logits, tokens = rows_of_extremes(dtype)
     r = lib.token_logprobs(logits, tokens, top=5, entropy=True, temperature=t)
     check_forward(logits, tokens, t, 5, r)
+
+
+def check_gradients(lib, logits, tokens, t, r):
+    gen = torch.Generator(device="cuda").manual_seed(len(logits))
+    # (no larger than the temperature: the logits' gradients stay in the types' range)
+    gain, dh = (torch.randn(len(logits), generator=gen, device="cuda") * min(1.0, t) for _ in range(2))
+    for g_, h_ in ((gain, dh), (gain, None)):
+        dl = lib.token_logprobs_backward(g_, logits, tokens, r, dentropy=h_, temperature=t)
+        assert not bool(dl.isnan().any())
+        check_backward(logits, tokens, t, g_, h_, dl)
+
+
+@pytest.mark.parametrize("rows,V", SHAPES[:2])
+@pytest.mark.parametrize("dtype,value,temperature", MASKED)
+def test_gradient_of_finite_masks(lib, dtype, value, temperature, rows, V):
+    t = f32(temperature)
+    logits, tokens = masked_rows(dtype, value, rows, V)
+    check_gradients(lib, logits, tokens, t, lib.token_logprobs(logits, tokens, entropy=True, temperature=t))
+
+
+@pytest.mark.parametrize("dtype,base,step", OFFSETS)
+@pytest.mark.parametrize("of_step", [0.01, 0.5, 4.0])
+def test_gradient_far_from_zero(lib, dtype, base, step, of_step):
+    t = f32(step * of_step)
+    logits, tokens = offset_rows(dtype, base, step)
+    check_gradients(lib, logits, tokens, t, lib.token_logprobs(logits, tokens, entropy=True, temperature=t))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("temperature", COLD)
+def test_gradient_of_ties_in_the_cold(lib, dtype, temperature):
+    """n equal largest logits have 1 / n each, however cold"""
+    t = f32(temperature)
+    logits, tokens = tied_rows(dtype)
+    r = lib.token_logprobs(logits, tokens, entropy=True, temperature=t)
+    check_gradients(lib, logits, tokens, t, r)
+    dl = lib.token_logprobs_backward(torch.full((10,), -t, device="cuda"), logits, torch.full_like(tokens, 5), r,
+                                     temperature=t)
+    if t < 1e-5:
+        share = 1.0 / torch.arange(1, 11, device="cuda")
+        assert bool(((dl[:, 0].float() - share).abs() <= share * (torch.finfo(dl.dtype).eps / 2 + 2.0 ** -19)).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", HOT)
+def test_gradient_of_differences_beyond_the_range(lib, dtype, temperature):
+    t = f32(temperature)
+    logits, tokens = rows_of_extremes(dtype)
+    check_gradients(lib, logits, tokens, t, lib.token_logprobs(logits, tokens, entropy=True, temperature=t))
