@@ -500,8 +500,8 @@ int moe_layer(gemm_handle_t h, const moe_layer_args* args, void* stream);
  * -inf only has entropy 0, no alternatives and, where a token is given, logprob -inf.  A row that holds
  * NaN or +inf: NaN, and no alternatives.
  * logits, logprobs, entropy, stats and top_logprobs are aligned to their elements, tokens and
- * top_tokens to 8 bytes (GEMM_ERR_ALIGNMENT).  temperature must be positive and finite, with a
- * finite reciprocal, V >= 1, 0 <= top (GEMM_ERR_INVALID_ARG) <= 32 (GEMM_ERR_UNSUPPORTED).
+ * top_tokens to 8 bytes (GEMM_ERR_ALIGNMENT).  temperature must be positive and finite, with 1 / (T ln 2)
+ * finite in fp32 (from 4.24e-39 on), V >= 1, 0 <= top (GEMM_ERR_INVALID_ARG) <= 32 (GEMM_ERR_UNSUPPORTED).
  * top == 0: top_logprobs and top_tokens are ignored.  rows == 0: nothing is done.
  * The pages have no counterpart to it. */
 int token_logprobs(gemm_handle_t h, int64_t rows, int64_t V, const void* logits, int64_t ld, int dtype,

@@ -67,7 +67,9 @@ int check_logprobs(gemm_handle_t h, int64_t rows, int64_t V, const void* logits,
                    const int64_t* tokens, float temperature, const float* stats)
 {
     if (!h || rows < 0 || V < 1 || !known_dtype(dtype)) return GEMM_ERR_INVALID_ARG;
-    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature)) return GEMM_ERR_INVALID_ARG;
+    // (the kernels multiply by 1 / (T ln 2), which is infinite before 1 / T is)
+    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite((float)(1.4426950408889634 / temperature)))
+        return GEMM_ERR_INVALID_ARG;
     if (V > (1 << 30) || rows > kLim32) return GEMM_ERR_UNSUPPORTED;
     if (bad_matrix(logits, rows, V, ld) || (rows > 0 && (!tokens || !stats))) return GEMM_ERR_INVALID_ARG;
     if (misaligned(logits, size_of(dtype)) || misaligned(tokens, 8) || misaligned(stats, 4)) return GEMM_ERR_ALIGNMENT;

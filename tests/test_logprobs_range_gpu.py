@@ -194,3 +194,29 @@ def test_gradient_of_differences_beyond_the_range(lib, dtype, temperature):
     t = f32(temperature)
     logits, tokens = rows_of_extremes(dtype)
     check_gradients(lib, logits, tokens, t, lib.token_logprobs(logits, tokens, entropy=True, temperature=t))
+
+
+@pytest.mark.parametrize("temperature", [2.95e-39, 3.5e-39, 4.23e-39])
+def test_temperatures_without_a_finite_exponent_scale_are_refused(lib, g, temperature):
+    """1 / T is finite there, 1 / (T ln 2) is not"""
+    t = f32(temperature)
+    logits, tokens = make(1, 4, 100, torch.float32)
+    ok = lib.token_logprobs(logits, tokens)
+    n = lib.launch_count()
+    with pytest.raises(g.GemmError) as e:
+        lib.token_logprobs(logits, tokens, temperature=t)
+    assert e.value.status == g.GEMM_ERR_INVALID_ARG
+    with pytest.raises(g.GemmError) as e:
+        lib.token_logprobs_backward(None, logits, tokens, ok, temperature=t)
+    assert e.value.status == g.GEMM_ERR_INVALID_ARG
+    assert lib.launch_count() == n
+
+
+@pytest.mark.parametrize("temperature", [4.3e-39, 8.4e-39, 1e-38])
+def test_smallest_temperatures(lib, temperature):
+    """the largest logits share all, the others come to nothing; rows of zeros among them"""
+    t = f32(temperature)
+    logits, tokens = tied_rows("f32")
+    logits[3] = 0.0
+    r = lib.token_logprobs(logits, tokens, top=12, entropy=True, temperature=t)
+    check_forward(logits, tokens, t, 12, r)
