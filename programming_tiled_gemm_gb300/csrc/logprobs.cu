@@ -603,6 +603,9 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradPara
     const bool zero = (g == 0.f && h == 0.f) || (m == -INFINITY && ln_s == ln_s);
     const float B = -h * p.inv_t * LN2, A = ENT ? -(g + h * p.entropy[r]) * p.inv_t : -g * p.inv_t;
     const float gt = g * p.inv_t;
+    // g / T or h / T about as large as fp32's values go (B times an exponent no less): 1 / T comes last then, as p may
+    // bring the product back, to 0 above all
+    const bool large = !(fabsf(A) < 1e33f && fabsf(B) < 1e33f && fabsf(gt) < 1e33f);
     const int t = have ? (int)tok : -1;
     const float ref = reference(m, by.h), log_s = ln_s * LOG2E;
     const auto grad = [&](float z, int j) {
@@ -610,12 +613,16 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(LogprobsGradPara
         if (ln_s != ln_s) return ln_s;  // a row with NaN
         const float l = __fmaf_rn(__fmaf_rn(z, by.h, -ref), by.c, -log_s);
         const float e = ex2(l);
+        if (large) {
+            const float v = -e * g - (ENT ? e * h * (p.entropy[r] + LN2 * fmaxf(l, FLOOR)) : 0.f);
+            return (j == t ? v + g : v) * p.inv_t;
+        }
         const float v = ENT ? e * (A + B * fmaxf(l, FLOOR)) : e * A;
         return j == t ? v + gt : v;
     };
     const int head = head_of<D>(row, p.V), vecs = (p.V - head) / PER;
     const bool aligned = ((reinterpret_cast<uintptr_t>(out + head)) & 15) == 0;
-    if (!aligned || ln_s != ln_s) {
+    if (!aligned || large || ln_s != ln_s) {
         const int n = (p.V + p.blocks - 1) / p.blocks, j1 = min(p.V, (part + 1) * n);
         for (int j = part * n + (int)threadIdx.x; j < j1; j += THREADS)
             out[j] = D::put(grad(zero ? 0.f : D::get(row[j]), j));

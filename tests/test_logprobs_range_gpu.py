@@ -220,3 +220,31 @@ def test_smallest_temperatures(lib, temperature):
     logits[3] = 0.0
     r = lib.token_logprobs(logits, tokens, top=12, entropy=True, temperature=t)
     check_forward(logits, tokens, t, 12, r)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature,size", [(1e-38, 10.0), (1e-30, 3e8), (5e-39, 1.0), (1e-20, 1e30)])
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradient_where_g_over_t_overflows(lib, dtype, temperature, size, entropy):
+    """g / T has no fp32 value; g p / T is 0 nearly everywhere, and may be in range at the largest logits.
+    Equal to the formula as it rounds to the type, or off by the exponential's and the products' errors, 2^-19
+    (the entropy's part is a difference of two such), and the type's own rounding."""
+    t = f32(temperature)
+    logits, tokens = tied_rows(dtype)
+    rows = len(logits)
+    r = lib.token_logprobs(logits, tokens, entropy=True, temperature=t)
+    gain = torch.linspace(-1.0, 1.0, rows, device="cuda") * size
+    dh = gain.flip(0) if entropy else None
+    dl = lib.token_logprobs_backward(gain, logits, tokens, r, dentropy=dh, temperature=t)
+    n = torch.arange(1, rows + 1, device="cuda").double()[:, None]
+    p = (logits == 17.75).double() / n
+    delta = torch.zeros_like(p).scatter_(1, tokens[:, None], 1.0)
+    want = gain.double()[:, None] * (delta - p) / t  # (n equal ones: ln p + H = 0)
+    tol = 2.0 ** -19 * (gain.double().abs()[:, None] * (delta + p) + (dh.double().abs()[:, None] * p if entropy else 0)) / t
+    tol = tol + torch.finfo(dl.dtype).eps / 2 * want.abs()
+    top = torch.finfo(dl.dtype).max
+    got = dl.double()
+    over = want.abs() - tol > top  # (no value of the type)
+    assert bool(torch.where(over, got == want.sign() * math.inf, (got - want).abs() <= tol).logical_or(
+        (want.abs() + tol > top) & (got == want.sign() * math.inf)).all())
+    assert not bool(dl.isnan().any()) and bool((dl[p == 0][delta[p == 0] == 0] == 0).all())
