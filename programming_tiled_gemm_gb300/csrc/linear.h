@@ -19,6 +19,9 @@ enum LinMode { kLinFwd = 0, kLinDx = 1, kLinDw = 2 };
 // Low-rank adapters beside a forward product: row m adds s_i (X[m] A_i) B_i, i = adapters[m].
 constexpr int kMaxAdapterRank = 128;
 constexpr int kMaxAdapters = 8192;     // (which of them are used: a bit each in shared memory)
+constexpr int64_t kMaxAdaptedK = 16384;  // (one accumulator over all of K)
+// (adapters.cu looks at up to 4096 row numbers past the last, in 32 bits)
+constexpr int64_t kMaxAdaptedRows = ((int64_t)1 << 31) - (1 << 17);
 constexpr int kAdapterParts = 32;      // of a used adapter's B, which have a byte of `bad` each
 struct LinAdapt {
     int n, r, rs;  // adapters, their rank, and the rank to 16, 32, 64 or 128: a row's length in `u`

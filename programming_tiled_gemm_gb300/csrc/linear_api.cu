@@ -53,8 +53,8 @@ bool bad_stride(int64_t groups, int64_t K, int64_t ld, int64_t stride)
 int check_adapters(const gemm_linear_args* a, const gemm_adapter_args* d, int64_t Nw)
 {
     if (d->n < 0 || d->r < 1 || a->groups != 0 || a->Z) return GEMM_ERR_INVALID_ARG;
-    // (adapters.cu looks at up to 4096 row numbers past the last, in 32 bits)
-    if (a->y_dtype != a->dtype || a->K > 16384 || a->M > kLim32 - (1 << 16) || d->n > kMaxAdapters || d->r > kMaxAdapterRank)
+    if (a->y_dtype != a->dtype || a->K > kMaxAdaptedK || a->M > kMaxAdaptedRows || d->n > kMaxAdapters ||
+        d->r > kMaxAdapterRank)
         return GEMM_ERR_UNSUPPORTED;
     if (d->n == 0 || a->M == 0 || a->N == 0) return GEMM_OK;
     if (!d->adapters || bad_matrix(d->A, a->K, d->r, d->lda) || bad_matrix(d->B, d->r, Nw, d->ldb) ||
