@@ -330,7 +330,8 @@ typedef struct gemm_adapter_args {
  *   Y[m] = act(X[m] W + scales[i] (X[m] A_i) B_i + bias) + R[m],  i = adapters[m].
  *   n adapters of rank r: A [n][K][r] (adapter i at i * a_stride elements), B [n][r][Nw] (b_stride), of
  *   type dtype; scales fp32 [n] or NULL (ones); adapters [M] device memory, read by the kernels in any order
- *   of rows; a row with an index outside 0 .. n-1 (as -1) has none.  n == 0: gemm_linear.
+ *   of rows; a row with an index outside 0 .. n-1 (as -1) has none.  n == 0: gemm_linear without groups and Z,
+ *   in its own limits; nothing else of `adapters` is looked at.
  * U = scales[i] X A_i is rounded to dtype once, as the second product's operand (relative to the adapter's
  * part 2^-9 in bf16, 2^-12 in fp16, where |U| above 65504 is infinite); everything else is summed in fp32
  * with X W in one accumulator and rounded once.  Two launches, the first small.

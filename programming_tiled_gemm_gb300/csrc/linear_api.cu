@@ -52,11 +52,12 @@ bool bad_stride(int64_t groups, int64_t K, int64_t ld, int64_t stride)
 // What gemm_linear_adapted checks of its adapters.
 int check_adapters(const gemm_linear_args* a, const gemm_adapter_args* d, int64_t Nw)
 {
-    if (d->n < 0 || d->r < 1 || a->groups != 0 || a->Z) return GEMM_ERR_INVALID_ARG;
+    if (d->n < 0 || (d->n > 0 && d->r < 1) || a->groups != 0 || a->Z) return GEMM_ERR_INVALID_ARG;
+    if (d->n == 0) return GEMM_OK;
     if (a->y_dtype != a->dtype || a->K > kMaxAdaptedK || a->M > kMaxAdaptedRows || d->n > kMaxAdapters ||
         d->r > kMaxAdapterRank)
         return GEMM_ERR_UNSUPPORTED;
-    if (d->n == 0 || a->M == 0 || a->N == 0) return GEMM_OK;
+    if (a->M == 0 || a->N == 0) return GEMM_OK;
     if (!d->adapters || bad_matrix(d->A, a->K, d->r, d->lda) || bad_matrix(d->B, d->r, Nw, d->ldb) ||
         bad_stride(d->n, a->K, d->lda, d->a_stride) || (d->n > 1 && d->a_stride < (a->K - 1) * d->lda + d->r) ||
         bad_stride(d->n, d->r, d->ldb, d->b_stride) || (d->n > 1 && d->b_stride < (d->r - 1) * d->ldb + Nw))

@@ -63,3 +63,23 @@ def test_other_limits(g, call):
     assert call(n=8193, adapters=off) == g.GEMM_ERR_UNSUPPORTED
     assert call(r=128, lda=128, adapters=off, **wide) == g.GEMM_ERR_ALIGNMENT
     assert call(r=129, lda=136, adapters=off, **wide) == g.GEMM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("M,K,f32", [(3, 64, False), (3, 16400, False), (40, 20000, False), (40, 64, True), (2, 64, True)])
+def test_without_adapters_it_is_the_linear_layer(g, lib, M, K, f32):
+    """n = 0 and nothing else in the adapters' structure: K and types that only the layer itself takes"""
+    gen = torch.Generator(device="cuda").manual_seed(K + M)
+    x, w = (torch.randn(*s, generator=gen, device="cuda").to(BF16) for s in ((M, K), (K, 72)))
+    out_dtype = torch.float32 if f32 else BF16
+    want = lib.linear(x, w, out_dtype=out_dtype)
+    got = torch.full_like(want, 3.0)
+    la = g.LinearArgs(M=M, K=K, N=72, X=x.data_ptr(), ldx=K, W=w.data_ptr(), ldw=72, Y=got.data_ptr(), ldy=72,
+                      dtype=g.GEMM_BF16, y_dtype=g.GEMM_F32 if f32 else g.GEMM_BF16)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert g.gemm_linear_adapted(lib.handle, la, g.AdapterArgs(), stream) == g.GEMM_OK
+    assert torch.equal(got, want)
+    if not f32:  # and through the binding, with a stack of no adapters
+        for r in (0, 16):
+            none = torch.empty(0, K, r, device="cuda", dtype=BF16), torch.empty(0, r, 72, device="cuda", dtype=BF16)
+            ids = torch.full((M,), -1, device="cuda", dtype=torch.int32)
+            assert torch.equal(lib.adapted_linear(x, w, none[0], none[1], ids), want)
