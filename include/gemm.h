@@ -333,7 +333,7 @@ typedef struct gemm_adapter_args {
  *   of rows; a row with an index outside 0 .. n-1 (as -1) has none.  n == 0: gemm_linear without groups and Z,
  *   in its own limits; nothing else of `adapters` is looked at.
  * U = scales[i] X A_i is rounded to dtype once, as the second product's operand (relative to the adapter's
- * part 2^-9 in bf16, 2^-12 in fp16, where |U| above 65504 is infinite); everything else is summed in fp32
+ * part 2^-8 in bf16, 2^-11 in fp16, where |U| above 65504 is infinite); everything else is summed in fp32
  * with X W in one accumulator and rounded once.  Two launches, the first small.
  * Infinities and NaN in a row of X stay in that row.  An adapter whose A or B holds some reaches its own rows
  * only, which become NaN where it falls, or in all columns.
@@ -474,7 +474,10 @@ typedef struct moe_layer_args {
  *   b1, b2 and R may be NULL; R may be Y itself.  A token without picks is R (or 0).
  * The activation's results are rounded to dtype once, as the second product's operand (GEMM_F16: beyond
  * 65504 infinite); the picks' products and their sum, in the order of j, are held in fp32 and rounded
- * once.  Only the picked experts' weights are read.  Deterministic.
+ * once.  A product's sum over all of D or F runs in four fp32 accumulators, without the restarts every 1024 of
+ * gemm_linear's fp32 results: with y_dtype GEMM_F32 and D or F above 4096 the calls named are nearer.
+ * Only the picked experts' weights are read.  Deterministic.
+ * For few tokens: with more than some 16 to 32 (the more experts, the fewer) those calls are faster.
  * X, W1 and W2 must be 16-byte aligned with leading dimensions (and strides) multiples of 8, F a
  * multiple of 8 for GEMM_ACT_SWIGLU; the others aligned to their elements (GEMM_ERR_ALIGNMENT).
  * GEMM_ERR_UNSUPPORTED for GEMM_F32 operands, T > 64 (use the calls named above), k > 32, E > 1024,
@@ -516,7 +519,9 @@ int token_logprobs(gemm_handle_t h, int64_t rows, int64_t V, const void* logits,
  * may be the logits themselves (the same address and leading dimension), not a part of them.
  * Rows whose g and h are both 0 get zeros without being read, rows of -inf only get zeros, rows
  * that hold NaN or +inf get NaN.  GEMM_F16: p g below 2^-25 is 0; scale the loss accordingly.
- * Alignment, limits and errors as in token_logprobs.
+ * A dlogits whose rows lie to 16-byte boundaries as the logits' do is written by 16 bytes, any other by
+ * elements (three times as long).
+ * Alignment, limits and errors as in token_logprobs, and rows * ceil(V / 4096) < 2^31.
  * The pages have no counterpart to it. */
 int token_logprobs_backward(gemm_handle_t h, int64_t rows, int64_t V, const void* logits, int64_t ld, int dtype,
                             const int64_t* tokens, float temperature, const float* stats, const float* entropy,

@@ -25,9 +25,11 @@
 //
 // Bound by memory where the rows fill the SMs, next by the exponentials (16 a cycle and SM: two thirds of the
 // reading's time at 16 bits); short calls by latency.  Measured (GPU time; bf16 where not said otherwise):
-//   4096 x 131072: forward 158 us, 6.8 TB/s; with 1 or 20 alternatives 193 and 229; the gradient 309, 6.95 TB/s
-//   1000 x 50257 with entropy: 27 us, 3.7 TB/s (one wave of CTAs, 12 batches a thread), its gradient 34, 5.9 TB/s
-//   64 x 131072 with entropy: 8.7 us; with 20 alternatives 15.6; 1 x 32000 fp32: 4.9 and 10.5
+//   4096 x 131072: forward 157 us, 6.8 TB/s (with entropy 163); with 20 alternatives 228; the gradient 304, 7.1 TB/s
+//   1000 x 50257 with entropy: 26 us, 3.9 TB/s (one wave of CTAs, 12 batches a thread); its gradient 33, 6.1 TB/s (31
+//   behind the forward pass, which leaves a part of the logits in L2); into rows of another alignment 119
+//   64 x 131072 with entropy: 7.7 us; with 20 alternatives 15.0; 1 x 32000 fp32 with entropy and 5 alternatives: 7.8
+// z c - R, R the rounded m c, instead of the difference: 4096 x 131072 160 us, with entropy 162, 1000 x 50257 25.2.
 // Dropped: every logit offered to sorted lists as the row goes by (64 x 131072, 20 alternatives: 51 us); one maximum a
 // thread as the unit (its 16 bytes cost whole sectors again: 4096 x 131072 286 us); units ranked by counting (241, and
 // 144 instead of 109 for the best of 4096 x 32000 fp32); persistent blocks for the gradient (552 instead of 494 both
@@ -728,7 +730,7 @@ int launch_logprobs(const LogprobsArgs& a, int num_sms, cudaStream_t s, int* lau
         p.cluster *= 2;
     // Four warps a CTA: more of them are resident and less of the last wave is idle.  Eight where long rows
     // do not fill the SMs and the loads in flight count.  us with four and eight warps (bf16, entropy):
-    //   4000 x 12000 29 48, 2000 x 50257 43 52, 4096 x 131072 159 166; 1000 x 131072 55 47
+    //   4000 x 12000 28 45, 2000 x 50257 43 53, 4096 x 131072 162 168; 1000 x 131072 52 49
     const int few = THREADS / 2;
     p.threads = a.rows * p.cluster < 8 * (int64_t)num_sms && a.V / p.cluster > 1 << 16 ? THREADS : few;
     const cudaError_t e = a.dtype == GEMM_F32    ? launch_typed<LF32>(p, a.rows, s)
