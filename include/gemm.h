@@ -474,8 +474,7 @@ typedef struct moe_layer_args {
  *   b1, b2 and R may be NULL; R may be Y itself.  A token without picks is R (or 0).
  * The activation's results are rounded to dtype once, as the second product's operand (GEMM_F16: beyond
  * 65504 infinite); the picks' products and their sum, in the order of j, are held in fp32 and rounded
- * once.  A product's sum over all of D or F runs in four fp32 accumulators, without the restarts every 1024 of
- * gemm_linear's fp32 results: with y_dtype GEMM_F32 and D or F above 4096 the calls named are nearer.
+ * once; a product's sum starts anew every 4096 of D or F, and the parts are added in fp32.
  * Only the picked experts' weights are read.  Deterministic.
  * For few tokens: with more than some 16 to 32 (the more experts, the fewer) those calls are faster.
  * X, W1 and W2 must be 16-byte aligned with leading dimensions (and strides) multiples of 8, F a

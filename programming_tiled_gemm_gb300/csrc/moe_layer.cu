@@ -43,6 +43,10 @@ namespace {
 constexpr int MMA_WARPS = 8, WARPS = MMA_WARPS + 2, THREADS = 32 * WARPS;  // the last two load weights and rows
 constexpr int SLAB = kLayerSlab;  // columns of W an item
 constexpr int DEPTH = 128;        // of the reduced dimension a stage
+// Stages after which the sums are put aside, 4096 of the reduced dimension: an MMA truncates what it adds to, so that a
+// sum of one sign loses in proportion to its length (1.2e-5 of the result at F 16384, 3.9e-4 at 262144; with this 1.7e-6 at
+// either, and 8 experts of 4096 x 14336 take 444 us for 32 tokens instead of 437, 1 to 8 of 4096 x 4096 0.5 % more).
+constexpr int RESTART = 4096 / DEPTH;
 constexpr int W_BYTES = DEPTH * SLAB * 2;
 constexpr int ROW_BYTES = DEPTH * 2 + 16;  // of X or H a stage: rows 16 bytes apart in the banks
 constexpr int MAX_STAGES = 8;  // (an even number of them: each belongs to one half of the warps, which sees its every phase)
@@ -512,52 +516,58 @@ __global__ void __launch_bounds__(THREADS, 2) layer_kernel(const __grid_constant
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int a = item / p.slabs, slab = item - a * p.slabs;
         const int first = r.first[a], n_rows = r.first[a + 1] - first, tiles = (n_rows + 7) / 8;
-        float acc[MAX_TILES][2][4];  // even and odd steps of 16: an MMA takes 60 cycles to the next of its sum
+        for (int step0 = 0; step0 < steps; step0 += RESTART) {
+            float acc[MAX_TILES][2][4];  // even and odd steps of 16: an MMA takes 60 cycles to the next of its sum
 #pragma unroll
-        for (int t = 0; t < MAX_TILES; ++t)
+            for (int t = 0; t < MAX_TILES; ++t)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[t][i / 4][i % 4] = 0.f;
-        for (int step = 0; step < steps && !dead; ++step) {
-            if ((stage & 1) == kh) {
-                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, &abort_flag))) {
-                    gave_up(kDevTimeoutMma);
-                    dead = true;
-                    break;
+                for (int i = 0; i < 8; ++i) acc[t][i / 4][i % 4] = 0.f;
+            const int step1 = min(step0 + RESTART, steps);
+            for (int step = step0; step < step1 && !dead; ++step) {
+                if ((stage & 1) == kh) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full_bar[stage]), phase, p.limit_ns, &abort_flag))) {
+                        gave_up(kDevTimeoutMma);
+                        dead = true;
+                        break;
+                    }
+                    const uint32_t at_w = ring_w + stage * W_BYTES, at_x = ring_x + stage * x_bytes;
+                    switch (tiles) {
+                    case 1: products<GATED, BF16, 1>(acc, at_w, at_x, fg, lane); break;
+                    case 2: products<GATED, BF16, 2>(acc, at_w, at_x, fg, lane); break;
+                    case 3: products<GATED, BF16, 3>(acc, at_w, at_x, fg, lane); break;
+                    default: products<GATED, BF16, 4>(acc, at_w, at_x, fg, lane); break;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&empty_bar[stage]));
                 }
-                const uint32_t at_w = ring_w + stage * W_BYTES, at_x = ring_x + stage * x_bytes;
-                switch (tiles) {
-                case 1: products<GATED, BF16, 1>(acc, at_w, at_x, fg, lane); break;
-                case 2: products<GATED, BF16, 2>(acc, at_w, at_x, fg, lane); break;
-                case 3: products<GATED, BF16, 3>(acc, at_w, at_x, fg, lane); break;
-                default: products<GATED, BF16, 4>(acc, at_w, at_x, fg, lane); break;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&empty_bar[stage]));
+                if (++stage == p.stages) stage = 0, phase ^= 1;
             }
-            if (++stage == p.stages) stage = 0, phase ^= 1;
+#pragma unroll
+            for (int t = 0; t < MAX_TILES; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][0][i] += acc[t][1][i];
+            // the even and the odd stages, [row][column]; on top of the stretches before
+            const int f = fg * 16 + lane / 4, row = lane % 4 * 2;
+            if (kh == 1)
+#pragma unroll
+                for (int t = 0; t < MAX_TILES; ++t)
+                    if (t < tiles) {
+                        float* s = sums + (t * 8 + row) * PAD + f;
+                        if (step0 == 0)
+                            s[0] = acc[t][0][0], s[PAD] = acc[t][0][1], s[8] = acc[t][0][2], s[PAD + 8] = acc[t][0][3];
+                        else
+                            s[0] += acc[t][0][0], s[PAD] += acc[t][0][1], s[8] += acc[t][0][2], s[PAD + 8] += acc[t][0][3];
+                    }
+            named_barrier(1, 32 * MMA_WARPS);
+            if (kh == 0)
+#pragma unroll
+                for (int t = 0; t < MAX_TILES; ++t)
+                    if (t < tiles) {
+                        float* s = sums + (t * 8 + row) * PAD + f;
+                        s[0] += acc[t][0][0], s[PAD] += acc[t][0][1], s[8] += acc[t][0][2], s[PAD + 8] += acc[t][0][3];
+                    }
+            named_barrier(1, 32 * MMA_WARPS);
         }
-#pragma unroll
-        for (int t = 0; t < MAX_TILES; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][0][i] += acc[t][1][i];
-        // the even and the odd stages, [row][column]
-        const int f = fg * 16 + lane / 4, row = lane % 4 * 2;
-        if (kh == 1)
-#pragma unroll
-            for (int t = 0; t < MAX_TILES; ++t)
-                if (t < tiles) {
-                    float* s = sums + (t * 8 + row) * PAD + f;
-                    s[0] = acc[t][0][0], s[PAD] = acc[t][0][1], s[8] = acc[t][0][2], s[PAD + 8] = acc[t][0][3];
-                }
-        named_barrier(1, 32 * MMA_WARPS);
-        if (kh == 0)
-#pragma unroll
-            for (int t = 0; t < MAX_TILES; ++t)
-                if (t < tiles) {
-                    float* s = sums + (t * 8 + row) * PAD + f;
-                    s[0] += acc[t][0][0], s[PAD] += acc[t][0][1], s[8] += acc[t][0][2], s[PAD + 8] += acc[t][0][3];
-                }
-        named_barrier(1, 32 * MMA_WARPS);
         for (int q = threadIdx.x; q < n_rows * (COLS / 8) && !dead; q += 32 * MMA_WARPS) {
             const int i = q / (COLS / 8), c0 = q % (COLS / 8) * 8, pick = r.pick[first + i], col = slab * COLS + c0;
             if (!in_range(pick, p.T * p.k)) continue;
